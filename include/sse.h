@@ -351,6 +351,154 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
                            void *log_gate, void *router_logits, void *q_shared, void *k_shared,
                            void *workspace, size_t workspace_bytes, sse_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * sse_scan_forward / sse_scan_backward / sse_scan_step -- a gated linear
+ * recurrence with one float32 state per channel, the one-row member of the
+ * diagonal-gate family of sse_forward (eq. 6 with c = 1), over the same packed
+ * varlen batches.  Per sequence and channel, with a_t = exp(log_gate_t):
+ *   h_t = a_t h_{t-1} + s(a_t) x_t,     out_t = h_t
+ * The config's input_scale chooses s: SSE_INPUT_PLAIN s = 1;
+ * SSE_INPUT_COMPLEMENT s = 1 - a; SSE_INPUT_UNIT s = sqrt(1 - a^2) (keeps the
+ * variance of the state).  log_gate <= 0 (decays in [0, 1]; the log_gate and v
+ * of sse_front_end fit as they are); a log-gate of -infinity empties the
+ * state.  Positive log-gates are outside the method and not checked.  A NaN or
+ * an infinity stays in its own sequence and channel, from its token on.
+ *
+ *   x, log_gate, d_out   [total_tokens, width] in cfg->dtype.  x and log_gate
+ *                        take a row stride in elements (>= width, whole
+ *                        16-byte words), so slices of a wider projection need
+ *                        no copy; d_out and every output are packed.
+ *   initial_state        float32 [num_seqs, width], may be NULL (zero)
+ *   final_state          likewise, may be NULL (not written); may be
+ *                        initial_state itself.  An empty sequence's final
+ *                        state is its initial state.
+ *   checkpoints          float32 [sse_scan_checkpoint_rows(total_tokens),
+ *                        width], may be NULL (not written): the state before
+ *                        every 64th packed token, which the backward reads
+ *                        instead of repeating the forward.  Rows that no
+ *                        sequence passes through are left as they were.
+ * Backward, for L = <d_out, out> + <d_final_state, final_state>:
+ *   dh_t = d_out_t + a_{t+1} dh_{t+1};  dx_t = s(a_t) dh_t;
+ *   d_log_gate_t = dh_t (a_t h_{t-1} + s'(log_gate_t) x_t);
+ *   d_initial_state = a_1 dh_1
+ * with the states recomputed in float32 from the checkpoints.  With
+ * SSE_INPUT_UNIT, s' is unbounded at log_gate = 0 and taken as zero there.
+ * d_final_state and d_initial_state may be NULL; they do not overlap.
+ * Tokens at and past cu_seqlens[num_seqs] (a padded batch) belong to no
+ * sequence: their rows are not read and the outputs' rows stay as they were.
+ * All sums and states are float32, rounded once to cfg->dtype at the end, and
+ * formed in a fixed order (deterministic).  No workspace.
+ *
+ * sse_scan_step is one token of each of `batch` sequences: state
+ * float32 [batch, width] is replaced, out [batch, width].
+ *
+ * width is at most 65536 and width and the row strides are whole 16-byte words
+ * of cfg->dtype; total_tokens is below 2^30.
+ * ------------------------------------------------------------------------- */
+typedef enum { SSE_INPUT_PLAIN = 0, SSE_INPUT_COMPLEMENT = 1, SSE_INPUT_UNIT = 2 } sse_input_scale_t;
+
+typedef struct {
+    int32_t width;       /* channels: columns of every row */
+    int32_t input_scale; /* sse_input_scale_t */
+    int32_t dtype;       /* sse_dtype_t of the token tensors */
+} sse_scan_config_t;
+
+/* Rows of the checkpoints of total_tokens packed tokens (0 for bad sizes). */
+int64_t sse_scan_checkpoint_rows(int64_t total_tokens);
+
+sse_status_t sse_scan_forward(const sse_scan_config_t *cfg, const void *x, int64_t x_stride, const void *log_gate,
+                              int64_t gate_stride, const int32_t *cu_seqlens, int32_t num_seqs,
+                              int64_t total_tokens, const float *initial_state, float *final_state, void *out,
+                              float *checkpoints, sse_stream_t stream);
+
+sse_status_t sse_scan_backward(const sse_scan_config_t *cfg, const void *x, int64_t x_stride,
+                               const void *log_gate, int64_t gate_stride, const int32_t *cu_seqlens,
+                               int32_t num_seqs, int64_t total_tokens, const float *initial_state,
+                               const float *checkpoints, const void *d_out, const float *d_final_state, void *dx,
+                               void *d_log_gate, float *d_initial_state, sse_stream_t stream);
+
+sse_status_t sse_scan_step(const sse_scan_config_t *cfg, const void *x, int64_t x_stride, const void *log_gate,
+                           int64_t gate_stride, int32_t batch, float *state, void *out, sse_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * sse_block_norm / sse_block_norm_backward -- the norms before and after a
+ * block, with the block's output gate and the residual stream between them,
+ * in one pass over each token.  With o the output of a block (for example of
+ * sse_forward or sse_scan_forward, or of a projection behind them), z its
+ * gate, r the residual stream and
+ *   RMS_G(u; w) = w * u / sqrt(mean of u^2 over each G columns + eps):
+ *   r' = residual_scale * r
+ *      + branch_scale * channel_scale * act(z) * RMS_group(o; w_after)
+ *   x' = RMS_width(r'; w_before)
+ * r' is the residual stream behind the block and x' the input of the next one
+ * (the x of sse_front_end).  Each part is optional:
+ *   block_out NULL       no branch: r' = residual_scale * r
+ *   w_after NULL         no norm after: o enters as it is
+ *   cfg->gate NONE       no gate (gate NULL); else gate is required
+ *   channel_scale NULL   1 on every column
+ *   residual NULL        no residual stream: r' is the branch alone
+ *   w_before NULL        no norm before: next_in is NULL and not written
+ * block_out or residual is required; gate, w_after and channel_scale need
+ * block_out.  residual_out may be NULL where next_in is wanted.
+ *
+ *   block_out, gate, residual  [total_tokens, width] in cfg->dtype, each with
+ *                              its own row stride in elements (>= width,
+ *                              whole 16-byte words)
+ *   residual_out, next_in      [total_tokens, width] in cfg->dtype, packed.
+ *                              residual_out may be the residual itself when
+ *                              that is packed (an in-place residual stream).
+ *   w_after, channel_scale, w_before  float32 [width]
+ * group: columns of one norm after the block (a head's width; 0: the whole
+ * row); it divides width.  x' is formed from r' before r' is rounded.
+ *
+ * Backward: gradients of L = <d_residual_out, r'> + <d_next_in, x'>, the norm
+ * before taken at the residual_out that the forward stored (read with
+ * w_before only).  d_residual_out may be NULL (zero) where d_next_in is given;
+ * d_next_in is given exactly with w_before.  d_block_out is given exactly with
+ * block_out and d_gate exactly with gate; d_residual, d_w_after,
+ * d_channel_scale and d_w_before may be NULL (not written).  The weights'
+ * gradients are float32 [width], summed over the tokens in a fixed order
+ * (deterministic), zero when there are none; d_block_out, d_gate, d_residual
+ * and d_residual_out are packed.
+ * Workspace (backward only): sse_block_norm_backward_workspace_size bytes,
+ * 256-byte aligned, contents undefined on entry and exit.
+ *
+ * Sums are float32.  width is at most 16384 for SSE_BF16 and 8192 for SSE_F32;
+ * width, group and the row strides are whole 16-byte words of cfg->dtype; eps
+ * is positive; total_tokens is below 2^31.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    SSE_GATE_NONE = 0,
+    SSE_GATE_SILU = 1,    /* act(z) = z / (1 + exp(-z)) */
+    SSE_GATE_SIGMOID = 2, /* act(z) = 1 / (1 + exp(-z)) */
+    SSE_GATE_LINEAR = 3   /* act(z) = z */
+} sse_gate_t;
+
+typedef struct {
+    int32_t width;        /* columns of every row */
+    int32_t group;        /* columns of one norm after the block; 0 = width */
+    int32_t gate;         /* sse_gate_t */
+    float eps;            /* added to the mean square */
+    float residual_scale; /* factor of the residual stream */
+    float branch_scale;   /* factor of the block's branch */
+    int32_t dtype;        /* sse_dtype_t of the token tensors */
+} sse_norm_config_t;
+
+sse_status_t sse_block_norm(const sse_norm_config_t *cfg, int64_t total_tokens, const void *block_out,
+                            int64_t block_stride, const void *gate, int64_t gate_stride, const void *residual,
+                            int64_t residual_stride, const float *w_after, const float *channel_scale,
+                            const float *w_before, void *residual_out, void *next_in, sse_stream_t stream);
+
+size_t sse_block_norm_backward_workspace_size(const sse_norm_config_t *cfg, int64_t total_tokens);
+
+sse_status_t sse_block_norm_backward(const sse_norm_config_t *cfg, int64_t total_tokens, const void *block_out,
+                                     int64_t block_stride, const void *gate, int64_t gate_stride,
+                                     const void *residual_out, int64_t residual_stride, const float *w_after,
+                                     const float *channel_scale, const float *w_before, const void *d_residual_out,
+                                     const void *d_next_in, void *d_block_out, void *d_gate, void *d_residual,
+                                     float *d_w_after, float *d_channel_scale, float *d_w_before, void *workspace,
+                                     size_t workspace_bytes, sse_stream_t stream);
+
 /* Device-side status bits (bit mask), written by the kernels into the first
  * word of the workspace of sse_forward, sse_backward, sse_delta_forward and
  * sse_front_end (each call clears them first).

@@ -5,7 +5,9 @@ The functions named like the C entry points (``sse_route``, ``sse_forward``,
 stream handle) and only marshal arguments.  The ``route`` / ``forward`` /
 ``decode_step`` helpers take torch tensors, allocate outputs and the
 workspace with torch (device memory plumbing only) and call the C entry
-points on the current torch stream.  Every step of the layer runs in the
+points on the current torch stream.  The ``scan_*`` and ``block_norm*`` helpers
+also check the tensors' shapes, types, strides and device (SSEError with
+SSE_ERR_INVALID_ARG) and run on the tensors' device, whichever is current.  Every step of the layer runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback: if libsse.so is
 missing, loading raises.
 """
@@ -32,7 +34,15 @@ EXPORTED = ("sse_abi_version", "sse_status_string", "sse_route_workspace_size", 
             "sse_route_noalloc", "sse_forward_workspace_size", "sse_forward", "sse_forward_timed", "sse_decode_step",
             "sse_front_end_workspace_size", "sse_front_end", "sse_read_device_status",
             "sse_get_last_device_error", "sse_backward_workspace_size", "sse_backward",
-            "sse_delta_forward_workspace_size", "sse_delta_forward", "sse_delta_decode_step")
+            "sse_delta_forward_workspace_size", "sse_delta_forward", "sse_delta_decode_step",
+            "sse_scan_checkpoint_rows", "sse_scan_forward", "sse_scan_backward", "sse_scan_step",
+            "sse_block_norm", "sse_block_norm_backward_workspace_size", "sse_block_norm_backward")
+
+SSE_INPUT_PLAIN, SSE_INPUT_COMPLEMENT, SSE_INPUT_UNIT = 0, 1, 2
+_INPUT_SCALES = {"plain": SSE_INPUT_PLAIN, "complement": SSE_INPUT_COMPLEMENT, "unit": SSE_INPUT_UNIT}
+SSE_GATE_NONE, SSE_GATE_SILU, SSE_GATE_SIGMOID, SSE_GATE_LINEAR = 0, 1, 2, 3
+_GATES = {"none": SSE_GATE_NONE, "silu": SSE_GATE_SILU, "sigmoid": SSE_GATE_SIGMOID, "linear": SSE_GATE_LINEAR}
+SCAN_CHECKPOINT = 64  # packed tokens between two of the scan's stored states
 
 
 class sse_config_t(ctypes.Structure):
@@ -40,6 +50,16 @@ class sse_config_t(ctypes.Structure):
                 ("value_dim", ctypes.c_int32), ("num_partitions", ctypes.c_int32),
                 ("top_k", ctypes.c_int32), ("use_shared", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("dtype", ctypes.c_int32), ("algo", ctypes.c_int32)]
+
+
+class sse_scan_config_t(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("input_scale", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class sse_norm_config_t(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("group", ctypes.c_int32), ("gate", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
 
 
 class SSEError(RuntimeError):
@@ -100,6 +120,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sse_delta_forward.argtypes = [cfgp, P, P, P, P, P, P, P, P, P, i32, i64, P, P, P, P, P, P, sz, P]
     lib.sse_delta_decode_step.restype = ctypes.c_int
     lib.sse_delta_decode_step.argtypes = [cfgp, P, P, P, P, P, P, P, P, i32, P, P, P, P, P]
+    scanp, normp = ctypes.POINTER(sse_scan_config_t), ctypes.POINTER(sse_norm_config_t)
+    lib.sse_scan_checkpoint_rows.restype = i64
+    lib.sse_scan_checkpoint_rows.argtypes = [i64]
+    lib.sse_scan_forward.restype = ctypes.c_int
+    lib.sse_scan_forward.argtypes = [scanp, P, i64, P, i64, P, i32, i64, P, P, P, P, P]
+    lib.sse_scan_backward.restype = ctypes.c_int
+    lib.sse_scan_backward.argtypes = [scanp, P, i64, P, i64, P, i32, i64, P, P, P, P, P, P, P, P]
+    lib.sse_scan_step.restype = ctypes.c_int
+    lib.sse_scan_step.argtypes = [scanp, P, i64, P, i64, i32, P, P, P]
+    lib.sse_block_norm.restype = ctypes.c_int
+    lib.sse_block_norm.argtypes = [normp, i64, P, i64, P, i64, P, i64, P, P, P, P, P, P]
+    lib.sse_block_norm_backward_workspace_size.restype = sz
+    lib.sse_block_norm_backward_workspace_size.argtypes = [normp, i64]
+    lib.sse_block_norm_backward.restype = ctypes.c_int
+    lib.sse_block_norm_backward.argtypes = [normp, i64, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P, P, P, P,
+                                            sz, P]
     _lib = lib
     return lib
 
@@ -190,6 +226,48 @@ def sse_backward(cfg, q, k, v, log_gate, logits, q_shared, k_shared, cu_seqlens,
     return load().sse_backward(ctypes.byref(cfg), q, k, v, log_gate, logits, q_shared, k_shared, cu_seqlens,
                                num_seqs, total_tokens, initial_state, d_out, d_final_state, dq, dk, dv, d_log_gate,
                                d_logits, dq_shared, dk_shared, d_initial_state, workspace, workspace_bytes, stream)
+
+
+def sse_scan_checkpoint_rows(total_tokens: int) -> int:
+    return load().sse_scan_checkpoint_rows(total_tokens)
+
+
+def sse_scan_forward(cfg, x, x_stride, log_gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state,
+                     final_state, out, checkpoints, stream) -> int:
+    return load().sse_scan_forward(ctypes.byref(cfg), x, x_stride, log_gate, gate_stride, cu_seqlens, num_seqs,
+                                   total_tokens, initial_state, final_state, out, checkpoints, stream)
+
+
+def sse_scan_backward(cfg, x, x_stride, log_gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state,
+                      checkpoints, d_out, d_final_state, dx, d_log_gate, d_initial_state, stream) -> int:
+    return load().sse_scan_backward(ctypes.byref(cfg), x, x_stride, log_gate, gate_stride, cu_seqlens, num_seqs,
+                                    total_tokens, initial_state, checkpoints, d_out, d_final_state, dx, d_log_gate,
+                                    d_initial_state, stream)
+
+
+def sse_scan_step(cfg, x, x_stride, log_gate, gate_stride, batch, state, out, stream) -> int:
+    return load().sse_scan_step(ctypes.byref(cfg), x, x_stride, log_gate, gate_stride, batch, state, out, stream)
+
+
+def sse_block_norm(cfg, total_tokens, block_out, block_stride, gate, gate_stride, residual, residual_stride, w_after,
+                   channel_scale, w_before, residual_out, next_in, stream) -> int:
+    return load().sse_block_norm(ctypes.byref(cfg), total_tokens, block_out, block_stride, gate, gate_stride,
+                                 residual, residual_stride, w_after, channel_scale, w_before, residual_out, next_in,
+                                 stream)
+
+
+def sse_block_norm_backward_workspace_size(cfg: sse_norm_config_t, total_tokens: int) -> int:
+    return load().sse_block_norm_backward_workspace_size(ctypes.byref(cfg), total_tokens)
+
+
+def sse_block_norm_backward(cfg, total_tokens, block_out, block_stride, gate, gate_stride, residual_out,
+                            residual_stride, w_after, channel_scale, w_before, d_residual_out, d_next_in, d_block_out,
+                            d_gate, d_residual, d_w_after, d_channel_scale, d_w_before, workspace, workspace_bytes,
+                            stream) -> int:
+    return load().sse_block_norm_backward(ctypes.byref(cfg), total_tokens, block_out, block_stride, gate, gate_stride,
+                                          residual_out, residual_stride, w_after, channel_scale, w_before,
+                                          d_residual_out, d_next_in, d_block_out, d_gate, d_residual, d_w_after,
+                                          d_channel_scale, d_w_before, workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -389,6 +467,207 @@ def front_end(cfg, x, w_q, w_k, w_v, w_g, w_e, *, a_q=None, b_q=None, a_k=None, 
                          _ptr(outs["q_shared"]), _ptr(outs["k_shared"]), _ptr(workspace), workspace.numel(),
                          _stream()), "sse_front_end")
     return dict(outs, workspace=workspace)
+
+
+# ---------------------------------------------------------------------------
+# Gated linear recurrence and block norms: helpers that check their tensors
+# ---------------------------------------------------------------------------
+def make_scan_config(width, input_scale="plain", dtype="bf16") -> sse_scan_config_t:
+    return sse_scan_config_t(width, _INPUT_SCALES[input_scale] if isinstance(input_scale, str) else int(input_scale),
+                             {"bf16": SSE_BF16, "f32": SSE_F32}[dtype] if isinstance(dtype, str) else dtype)
+
+
+def make_norm_config(width, group=0, gate="none", eps=1e-6, residual_scale=1.0, branch_scale=1.0,
+                     dtype="bf16") -> sse_norm_config_t:
+    return sse_norm_config_t(width, group, _GATES[gate] if isinstance(gate, str) else int(gate), float(eps),
+                             float(residual_scale), float(branch_scale),
+                             {"bf16": SSE_BF16, "f32": SSE_F32}[dtype] if isinstance(dtype, str) else dtype)
+
+
+class _Args:
+    """Checks the tensors of one call against each other and remembers their device."""
+
+    def __init__(self, what: str, rows: int, width: int, dtype, device):
+        self.what, self.rows, self.width, self.dtype, self.device = what, rows, width, dtype, device
+
+    def refuse(self, why: str):
+        raise SSEError(SSE_ERR_INVALID_ARG, f"{self.what}: {why}")
+
+    def tokens(self, name: str, t, packed: bool = False):
+        """(pointer, row stride) of a token tensor: [rows, width], or [rows, heads, width of a head]."""
+        if t is None:
+            return None, self.width
+        if t.dtype != self.dtype or t.device != self.device:
+            self.refuse(f"{name} is {t.dtype} on {t.device}, not {self.dtype} on {self.device}")
+        shape = t.shape
+        if len(shape) < 2 or shape[0] != self.rows or t.numel() != self.rows * self.width:
+            self.refuse(f"{name} has shape {tuple(shape)}, not [{self.rows}, {self.width}]")
+        if t.is_contiguous():
+            return t.data_ptr(), self.width
+        if packed:
+            self.refuse(f"{name} is not contiguous")
+        stride = t.stride()
+        inner = 1
+        for n, s in zip(shape[:0:-1], stride[:0:-1]):  # the last dimensions: one packed row
+            if n != 1 and s != inner:
+                self.refuse(f"{name} has strides {stride}: the columns of a row are not packed")
+            inner *= n
+        if stride[0] < self.width and self.rows > 1:
+            self.refuse(f"{name} has row stride {stride[0]}, below its width {self.width}")
+        return t.data_ptr(), stride[0] if self.rows > 1 else self.width
+
+    def f32(self, name: str, t, *shape: int):
+        """Pointer of a packed float32 tensor."""
+        import torch
+        if t is None:
+            return None
+        if t.dtype != torch.float32 or t.device != self.device or t.shape != shape or not t.is_contiguous():
+            self.refuse(f"{name} is not a contiguous float32 {list(shape)} on {self.device}")
+        return t.data_ptr()
+
+    def run(self, call, *args):
+        """One C call on the tensors' device and its current stream."""
+        import torch
+        index = self.device.index
+        if index == torch.cuda.current_device():
+            status = call(*args, torch.cuda.current_stream(index).cuda_stream)
+        else:
+            with torch.cuda.device(index):
+                status = call(*args, torch.cuda.current_stream(index).cuda_stream)
+        _check(status, self.what)
+
+
+def _scan_args(what, cfg, x, cu_seqlens):
+    import torch
+    if not x.is_cuda or x.dim() < 2:
+        raise SSEError(SSE_ERR_INVALID_ARG, f"{what}: x is not a [tokens, width] CUDA tensor")
+    a = _Args(what, x.shape[0], cfg.width, _token_dtype(cfg), x.device)
+    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device or
+                                   cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
+        a.refuse(f"cu_seqlens is not a contiguous int32 [sequences + 1] on {x.device}")
+    return a
+
+
+def scan_forward(cfg, x, log_gate, cu_seqlens, *, initial_state=None, want_final_state=True, want_checkpoints=False,
+                 out=None, final_state=None, checkpoints=None):
+    """The gated linear recurrence (sse_scan_forward) over packed sequences;
+    x, log_gate [T, width] or [T, H, width / H].  Returns dict(out,
+    final_state, checkpoints); checkpoints are what scan_backward reads."""
+    import torch
+    a = _scan_args("sse_scan_forward", cfg, x, cu_seqlens)
+    T, S, W = a.rows, cu_seqlens.numel() - 1, cfg.width
+    px, sx = a.tokens("x", x)
+    pg, sg = a.tokens("log_gate", log_gate)
+    if out is None:
+        out = torch.empty(x.shape, dtype=a.dtype, device=a.device)
+    if final_state is None and want_final_state:
+        final_state = torch.empty((S, W), dtype=torch.float32, device=a.device)
+    rows = -(-T // SCAN_CHECKPOINT)
+    if checkpoints is None and want_checkpoints:
+        checkpoints = torch.empty((rows, W), dtype=torch.float32, device=a.device)
+    a.run(load().sse_scan_forward, ctypes.byref(cfg), px, sx, pg, sg, cu_seqlens.data_ptr(), S, T,
+          a.f32("initial_state", initial_state, S, W), a.f32("final_state", final_state, S, W),
+          a.tokens("out", out, packed=True)[0], a.f32("checkpoints", checkpoints, rows, W))
+    return {"out": out, "final_state": final_state, "checkpoints": checkpoints}
+
+
+def scan_backward(cfg, x, log_gate, cu_seqlens, checkpoints, d_out, *, initial_state=None, d_final_state=None,
+                  want_d_initial_state=True):
+    """Gradients of <d_out, out> + <d_final_state, final_state> of scan_forward
+    (sse_scan_backward); returns dict(dx, d_log_gate, d_initial_state)."""
+    import torch
+    a = _scan_args("sse_scan_backward", cfg, x, cu_seqlens)
+    T, S, W = a.rows, cu_seqlens.numel() - 1, cfg.width
+    px, sx = a.tokens("x", x)
+    pg, sg = a.tokens("log_gate", log_gate)
+    pd = a.tokens("d_out", d_out, packed=True)[0]
+    if checkpoints is None:
+        a.refuse("checkpoints is None: scan_forward(..., want_checkpoints=True) returns them")
+    dx = torch.empty(x.shape, dtype=a.dtype, device=a.device)
+    dg = torch.empty(log_gate.shape, dtype=a.dtype, device=a.device)
+    d_init = torch.empty((S, W), dtype=torch.float32, device=a.device) if want_d_initial_state else None
+    a.run(load().sse_scan_backward, ctypes.byref(cfg), px, sx, pg, sg, cu_seqlens.data_ptr(), S, T,
+          a.f32("initial_state", initial_state, S, W), a.f32("checkpoints", checkpoints, -(-T // SCAN_CHECKPOINT), W),
+          pd, a.f32("d_final_state", d_final_state, S, W), dx.data_ptr(), dg.data_ptr(), _ptr(d_init))
+    return {"dx": dx, "d_log_gate": dg, "d_initial_state": d_init}
+
+
+def scan_step(cfg, state, x, log_gate, *, out=None):
+    """One token of each sequence (sse_scan_step): x, log_gate [B, width];
+    ``state`` [B, width] float32 is updated in place.  Returns dict(out)."""
+    import torch
+    a = _scan_args("sse_scan_step", cfg, x, None)
+    px, sx = a.tokens("x", x)
+    pg, sg = a.tokens("log_gate", log_gate)
+    if state is None:
+        a.refuse("state is None")
+    if out is None:
+        out = torch.empty(x.shape, dtype=a.dtype, device=a.device)
+    a.run(load().sse_scan_step, ctypes.byref(cfg), px, sx, pg, sg, a.rows, a.f32("state", state, a.rows, cfg.width),
+          a.tokens("out", out, packed=True)[0])
+    return {"out": out}
+
+
+def _norm_args(what, cfg, first):
+    if first is None or not first.is_cuda or first.dim() < 2:
+        raise SSEError(SSE_ERR_INVALID_ARG, f"{what}: a [tokens, width] CUDA tensor is required")
+    return _Args(what, first.shape[0], cfg.width, _token_dtype(cfg), first.device)
+
+
+def block_norm(cfg, block_out=None, *, gate=None, residual=None, w_after=None, channel_scale=None, w_before=None,
+               residual_out=None, next_in=None, want_residual_out=True):
+    """The norms before and after a block with its gate and the residual
+    stream (sse_block_norm); token tensors [T, width] or [T, H, width / H].
+    Returns dict(residual_out, next_in); next_in is None without w_before."""
+    import torch
+    first = block_out if block_out is not None else residual
+    a = _norm_args("sse_block_norm", cfg, first)
+    po, so = a.tokens("block_out", block_out)
+    pz, sz = a.tokens("gate", gate)
+    pr, sr = a.tokens("residual", residual)
+    W = cfg.width
+    like = residual if residual is not None else first
+    if residual_out is None and want_residual_out:
+        residual_out = torch.empty(like.shape, dtype=a.dtype, device=a.device)
+    if next_in is None and w_before is not None:
+        next_in = torch.empty(like.shape, dtype=a.dtype, device=a.device)
+    a.run(load().sse_block_norm, ctypes.byref(cfg), a.rows, po, so, pz, sz, pr, sr, a.f32("w_after", w_after, W),
+          a.f32("channel_scale", channel_scale, W), a.f32("w_before", w_before, W),
+          a.tokens("residual_out", residual_out, packed=True)[0], a.tokens("next_in", next_in, packed=True)[0])
+    return {"residual_out": residual_out, "next_in": next_in}
+
+
+def block_norm_backward(cfg, d_residual_out, block_out=None, *, gate=None, w_after=None, channel_scale=None,
+                        w_before=None, residual_out=None, d_next_in=None, want_d_residual=True, workspace=None):
+    """Gradients of <d_residual_out, residual_out> + <d_next_in, next_in> of
+    block_norm (sse_block_norm_backward); residual_out is the forward's.
+    Returns dict(d_block_out, d_gate, d_residual, d_w_after, d_channel_scale,
+    d_w_before), None where the part is absent."""
+    import torch
+    first = d_residual_out if d_residual_out is not None else d_next_in
+    a = _norm_args("sse_block_norm_backward", cfg, first)
+    po, so = a.tokens("block_out", block_out)
+    pz, sz = a.tokens("gate", gate)
+    pr, sr = a.tokens("residual_out", residual_out)
+    W, T = cfg.width, a.rows
+
+    def like(t, wanted=True):
+        return torch.empty(t.shape, dtype=t.dtype, device=a.device) if t is not None and wanted else None
+
+    g = {"d_block_out": like(block_out), "d_gate": like(gate),
+         "d_residual": like(first, want_d_residual), "d_w_after": like(w_after),
+         "d_channel_scale": like(channel_scale), "d_w_before": like(w_before)}
+    if workspace is None:
+        n = load().sse_block_norm_backward_workspace_size(ctypes.byref(cfg), T)
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=a.device)
+    elif workspace.dtype != torch.uint8 or workspace.device != a.device or not workspace.is_contiguous():
+        a.refuse(f"workspace is not a contiguous uint8 tensor on {a.device}")
+    a.run(load().sse_block_norm_backward, ctypes.byref(cfg), T, po, so, pz, sz, pr, sr,
+          a.f32("w_after", w_after, W), a.f32("channel_scale", channel_scale, W), a.f32("w_before", w_before, W),
+          a.tokens("d_residual_out", d_residual_out, packed=True)[0], a.tokens("d_next_in", d_next_in, packed=True)[0],
+          _ptr(g["d_block_out"]), _ptr(g["d_gate"]), _ptr(g["d_residual"]), _ptr(g["d_w_after"]),
+          _ptr(g["d_channel_scale"]), _ptr(g["d_w_before"]), workspace.data_ptr(), workspace.numel())
+    return g
 
 
 def to_device(arr, device="cuda"):

@@ -625,6 +625,214 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
     return sse::launch_front_end(*cfg, f, s, &launches) == cudaSuccess ? SSE_OK : SSE_ERR_CUDA;
 }
 
+namespace {
+// A row stride: at least the row, in whole 16-byte words.
+bool stride_ok(int64_t stride, int32_t width, int esz) {
+    return stride >= width && stride < (int64_t(1) << 40) && (stride * esz) % 16 == 0;
+}
+
+sse_status_t check_scan(const sse_scan_config_t *cfg, int64_t total_tokens, int32_t num_seqs) {
+    if (!cfg) return SSE_ERR_INVALID_ARG;
+    if (cfg->width < 1 || (cfg->dtype != SSE_F32 && cfg->dtype != SSE_BF16)) return SSE_ERR_INVALID_ARG;
+    if (cfg->input_scale < SSE_INPUT_PLAIN || cfg->input_scale > SSE_INPUT_UNIT) return SSE_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_tokens < 0 || (num_seqs == 0 && total_tokens != 0)) return SSE_ERR_INVALID_ARG;
+    if (cfg->width > sse::kScanMaxWidth || cfg->width % (cfg->dtype == SSE_BF16 ? 8 : 4)) return SSE_ERR_UNSUPPORTED;
+    if (total_tokens >= (int64_t(1) << 30) || num_seqs >= (1 << 30)) return SSE_ERR_UNSUPPORTED;
+    return SSE_OK;
+}
+
+sse::ScanArgs scan_args(const void *x, int64_t x_stride, const void *log_gate, int64_t gate_stride,
+                        const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, const float *init) {
+    sse::ScanArgs a{};
+    a.x = x; a.log_gate = log_gate;
+    a.x_stride = x_stride; a.gate_stride = gate_stride;
+    a.cu_seqlens = cu_seqlens;
+    a.num_seqs = num_seqs;
+    a.total_tokens = (int32_t)total_tokens;
+    a.init = init;
+    return a;
+}
+}  // namespace
+
+int64_t sse_scan_checkpoint_rows(int64_t total_tokens) {
+    if (total_tokens < 0 || total_tokens >= (int64_t(1) << 30)) return 0;
+    return (total_tokens + sse::kScanCheckpoint - 1) / sse::kScanCheckpoint;
+}
+
+sse_status_t sse_scan_forward(const sse_scan_config_t *cfg, const void *x, int64_t x_stride, const void *log_gate,
+                              int64_t gate_stride, const int32_t *cu_seqlens, int32_t num_seqs,
+                              int64_t total_tokens, const float *initial_state, float *final_state, void *out,
+                              float *checkpoints, sse_stream_t stream) {
+    SSE_RANGE("sse_scan_forward");
+    const sse_status_t st = check_scan(cfg, total_tokens, num_seqs);
+    if (st != SSE_OK) return st;
+    const int esz = cfg->dtype == SSE_BF16 ? 2 : 4;
+    if (!cu_seqlens || (total_tokens > 0 && (!x || !log_gate || !out))) return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, cfg->width, esz) || !stride_ok(gate_stride, cfg->width, esz)) return SSE_ERR_INVALID_ARG;
+    for (const void *p : std::initializer_list<const void *>{x, log_gate, initial_state, final_state, out, checkpoints})
+        if (!aligned16(p)) return SSE_ERR_INVALID_ARG;
+    if (num_seqs == 0) return SSE_OK;
+    sse::ScanArgs a = scan_args(x, x_stride, log_gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state);
+    a.final_state = final_state;
+    a.out = out;
+    a.checkpoints = checkpoints;
+    return sse::launch_scan_forward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SSE_OK
+                                                                                                    : SSE_ERR_CUDA;
+}
+
+sse_status_t sse_scan_backward(const sse_scan_config_t *cfg, const void *x, int64_t x_stride,
+                               const void *log_gate, int64_t gate_stride, const int32_t *cu_seqlens,
+                               int32_t num_seqs, int64_t total_tokens, const float *initial_state,
+                               const float *checkpoints, const void *d_out, const float *d_final_state, void *dx,
+                               void *d_log_gate, float *d_initial_state, sse_stream_t stream) {
+    SSE_RANGE("sse_scan_backward");
+    const sse_status_t st = check_scan(cfg, total_tokens, num_seqs);
+    if (st != SSE_OK) return st;
+    const int esz = cfg->dtype == SSE_BF16 ? 2 : 4;
+    if (!cu_seqlens || (total_tokens > 0 && (!x || !log_gate || !checkpoints || !d_out || !dx || !d_log_gate)))
+        return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, cfg->width, esz) || !stride_ok(gate_stride, cfg->width, esz)) return SSE_ERR_INVALID_ARG;
+    for (const void *p : std::initializer_list<const void *>{x, log_gate, initial_state, checkpoints, d_out,
+                                                             d_final_state, dx, d_log_gate, d_initial_state})
+        if (!aligned16(p)) return SSE_ERR_INVALID_ARG;
+    if (num_seqs == 0) return SSE_OK;
+    sse::ScanArgs a = scan_args(x, x_stride, log_gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state);
+    a.checkpoints = const_cast<float *>(checkpoints);
+    a.d_out = d_out;
+    a.d_final = d_final_state;
+    a.dx = dx;
+    a.d_log_gate = d_log_gate;
+    a.d_init = d_initial_state;
+    return sse::launch_scan_backward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SSE_OK
+                                                                                                     : SSE_ERR_CUDA;
+}
+
+sse_status_t sse_scan_step(const sse_scan_config_t *cfg, const void *x, int64_t x_stride, const void *log_gate,
+                           int64_t gate_stride, int32_t batch, float *state, void *out, sse_stream_t stream) {
+    SSE_RANGE("sse_scan_step");
+    const sse_status_t st = check_scan(cfg, 0, batch);
+    if (st != SSE_OK) return st;
+    const int esz = cfg->dtype == SSE_BF16 ? 2 : 4;
+    if (batch > 0 && (!x || !log_gate || !state || !out)) return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, cfg->width, esz) || !stride_ok(gate_stride, cfg->width, esz)) return SSE_ERR_INVALID_ARG;
+    for (const void *p : std::initializer_list<const void *>{x, log_gate, state, out})
+        if (!aligned16(p)) return SSE_ERR_INVALID_ARG;
+    if (batch == 0) return SSE_OK;
+    sse::ScanArgs a = scan_args(x, x_stride, log_gate, gate_stride, nullptr, batch, batch, nullptr);
+    a.final_state = state;
+    a.out = out;
+    return sse::launch_scan_step(*cfg, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SSE_OK
+                                                                                                 : SSE_ERR_CUDA;
+}
+
+namespace {
+sse_status_t check_norm(const sse_norm_config_t *cfg, int64_t total_tokens) {
+    if (!cfg) return SSE_ERR_INVALID_ARG;
+    const sse_norm_config_t &c = *cfg;
+    if (c.width < 1 || c.group < 0 || (c.dtype != SSE_F32 && c.dtype != SSE_BF16)) return SSE_ERR_INVALID_ARG;
+    if (c.gate < SSE_GATE_NONE || c.gate > SSE_GATE_LINEAR || total_tokens < 0) return SSE_ERR_INVALID_ARG;
+    if (!(c.eps > 0.f) || !std::isfinite(c.eps) || !std::isfinite(c.residual_scale) || !std::isfinite(c.branch_scale))
+        return SSE_ERR_INVALID_ARG;
+    if (c.group > 0 && c.width % c.group) return SSE_ERR_INVALID_ARG;
+    const int vec = c.dtype == SSE_BF16 ? 8 : 4;
+    if (c.width % vec || c.group % vec || c.width > sse::block_norm_max_width(c.dtype)) return SSE_ERR_UNSUPPORTED;
+    if (total_tokens >= (int64_t(1) << 31)) return SSE_ERR_UNSUPPORTED;
+    return SSE_OK;
+}
+
+// The tensors of one call that belong together, and their strides.
+sse_status_t check_norm_inputs(const sse_norm_config_t &c, const void *block_out, int64_t block_stride, const void *gate,
+                               int64_t gate_stride, const void *r, int64_t r_stride, const float *w_after,
+                               const float *channel_scale) {
+    const int esz = c.dtype == SSE_BF16 ? 2 : 4;
+    if ((gate != nullptr) != (c.gate != SSE_GATE_NONE) || (!block_out && (gate || w_after || channel_scale)))
+        return SSE_ERR_INVALID_ARG;
+    if ((block_out && !stride_ok(block_stride, c.width, esz)) || (gate && !stride_ok(gate_stride, c.width, esz)) ||
+        (r && !stride_ok(r_stride, c.width, esz)))
+        return SSE_ERR_INVALID_ARG;
+    return SSE_OK;
+}
+}  // namespace
+
+sse_status_t sse_block_norm(const sse_norm_config_t *cfg, int64_t total_tokens, const void *block_out,
+                            int64_t block_stride, const void *gate, int64_t gate_stride, const void *residual,
+                            int64_t residual_stride, const float *w_after, const float *channel_scale,
+                            const float *w_before, void *residual_out, void *next_in, sse_stream_t stream) {
+    SSE_RANGE("sse_block_norm");
+    sse_status_t st = check_norm(cfg, total_tokens);
+    if (st != SSE_OK) return st;
+    if (total_tokens == 0) return SSE_OK;
+    if ((st = check_norm_inputs(*cfg, block_out, block_stride, gate, gate_stride, residual, residual_stride, w_after,
+                                channel_scale)) != SSE_OK)
+        return st;
+    if (!block_out && !residual) return SSE_ERR_INVALID_ARG;
+    if ((w_before != nullptr) != (next_in != nullptr) || (!residual_out && !next_in)) return SSE_ERR_INVALID_ARG;
+    for (const void *p : std::initializer_list<const void *>{block_out, gate, residual, w_after, channel_scale,
+                                                             w_before, residual_out, next_in})
+        if (!aligned16(p)) return SSE_ERR_INVALID_ARG;
+    // in place only element for element
+    if (residual_out && residual_out == residual && residual_stride != cfg->width) return SSE_ERR_INVALID_ARG;
+    sse::BlockNormArgs a{};
+    a.T = total_tokens;
+    a.o = block_out; a.o_stride = block_stride;
+    a.z = gate; a.z_stride = gate_stride;
+    a.r = residual; a.r_stride = residual_stride;
+    a.w_after = w_after; a.channel = channel_scale; a.w_before = w_before;
+    a.r_out = residual_out; a.next = next_in;
+    return sse::launch_block_norm(*cfg, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? SSE_OK
+                                                                                                  : SSE_ERR_CUDA;
+}
+
+size_t sse_block_norm_backward_workspace_size(const sse_norm_config_t *cfg, int64_t total_tokens) {
+    if (check_norm(cfg, total_tokens) != SSE_OK) return 0;
+    const size_t n = 2 * (size_t)sse::block_norm_partial_rows(*cfg, total_tokens) * cfg->width * sizeof(float);
+    return (std::max(n, size_t(256)) + 255) & ~size_t(255);
+}
+
+sse_status_t sse_block_norm_backward(const sse_norm_config_t *cfg, int64_t total_tokens, const void *block_out,
+                                     int64_t block_stride, const void *gate, int64_t gate_stride,
+                                     const void *residual_out, int64_t residual_stride, const float *w_after,
+                                     const float *channel_scale, const float *w_before, const void *d_residual_out,
+                                     const void *d_next_in, void *d_block_out, void *d_gate, void *d_residual,
+                                     float *d_w_after, float *d_channel_scale, float *d_w_before, void *workspace,
+                                     size_t workspace_bytes, sse_stream_t stream) {
+    SSE_RANGE("sse_block_norm_backward");
+    sse_status_t st = check_norm(cfg, total_tokens);
+    if (st != SSE_OK) return st;
+    if (total_tokens > 0) {
+        st = check_norm_inputs(*cfg, block_out, block_stride, gate, gate_stride, residual_out, residual_stride, w_after,
+                               channel_scale);
+        if (st != SSE_OK) return st;
+        if ((block_out != nullptr) != (d_block_out != nullptr) || (gate != nullptr) != (d_gate != nullptr))
+            return SSE_ERR_INVALID_ARG;
+        if ((w_before != nullptr) != (d_next_in != nullptr) || (w_before && !residual_out) ||
+            (!d_residual_out && !d_next_in))
+            return SSE_ERR_INVALID_ARG;
+    }
+    if ((d_w_after && !w_after) || (d_channel_scale && !channel_scale) || (d_w_before && !w_before))
+        return SSE_ERR_INVALID_ARG;
+    for (const void *p : std::initializer_list<const void *>{
+             block_out, gate, residual_out, w_after, channel_scale, w_before, d_residual_out, d_next_in, d_block_out,
+             d_gate, d_residual, d_w_after, d_channel_scale, d_w_before})
+        if (!aligned16(p)) return SSE_ERR_INVALID_ARG;
+    const size_t need = sse_block_norm_backward_workspace_size(cfg, total_tokens);
+    if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
+        return SSE_ERR_WORKSPACE;
+    sse::BlockNormArgs a{};
+    a.T = total_tokens;
+    a.o = block_out; a.o_stride = block_stride;
+    a.z = gate; a.z_stride = gate_stride;
+    a.r = residual_out; a.r_stride = residual_stride;
+    a.w_after = w_after; a.channel = channel_scale; a.w_before = w_before;
+    a.d_r_out = d_residual_out; a.d_next = d_next_in;
+    a.d_o = d_block_out; a.d_z = d_gate; a.d_r = d_residual;
+    a.d_w_after = d_w_after; a.d_channel = d_channel_scale; a.d_w_before = d_w_before;
+    a.partials = static_cast<float *>(workspace);
+    return sse::launch_block_norm_backward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? SSE_OK
+               : SSE_ERR_CUDA;
+}
+
 sse_status_t sse_read_device_status(void *workspace, int32_t *flags, sse_stream_t stream) {
     if (!workspace || !flags || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SSE_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -398,4 +398,49 @@ bool front_end_supported(const sse_config_t &cfg, int32_t hidden);
 // Adds the number of kernels it launched to *launches.
 cudaError_t launch_front_end(const sse_config_t &cfg, const FrontEndArgs &f, cudaStream_t stream, int *launches);
 
+// Gated linear recurrence (scan.cu); pointers as in sse_scan_forward /
+// sse_scan_backward / sse_scan_step.
+constexpr int kScanCheckpoint = 64;      // packed tokens between two stored states
+constexpr int kScanMaxWidth = 1 << 16;
+struct ScanArgs {
+    const void *x, *log_gate;
+    int64_t x_stride, gate_stride;  // elements between rows
+    const int32_t *cu_seqlens;
+    int32_t num_seqs, total_tokens;
+    const float *init;
+    float *final_state;
+    void *out;
+    float *checkpoints;  // written by the forward, read by the backward
+    // backward only
+    const void *d_out;
+    const float *d_final;
+    void *dx, *d_log_gate;
+    float *d_init;
+};
+cudaError_t launch_scan_forward(const sse_scan_config_t &cfg, const ScanArgs &a, cudaStream_t stream);
+cudaError_t launch_scan_backward(const sse_scan_config_t &cfg, const ScanArgs &a, cudaStream_t stream);
+// One token per sequence: a.num_seqs rows, a.final_state the states, in place.
+cudaError_t launch_scan_step(const sse_scan_config_t &cfg, const ScanArgs &a, cudaStream_t stream);
+
+// Norms around a block (block_norm.cu); pointers as in sse_block_norm and
+// sse_block_norm_backward.
+struct BlockNormArgs {
+    int64_t T;
+    const void *o, *z, *r;  // r: the residual (forward), the stored residual_out (backward)
+    int64_t o_stride, z_stride, r_stride;
+    const float *w_after, *channel, *w_before;
+    void *r_out, *next;
+    // backward only
+    const void *d_r_out, *d_next;
+    void *d_o, *d_z, *d_r;
+    float *d_w_after, *d_channel, *d_w_before;
+    float *partials;  // [2, partial rows, width]: column sums of each CTA
+};
+// Widest row the kernels hold in registers.
+inline int block_norm_max_width(int dtype) { return dtype == SSE_BF16 ? 16384 : 8192; }
+// Rows of column sums the backward leaves per weight gradient.
+int64_t block_norm_partial_rows(const sse_norm_config_t &cfg, int64_t T);
+cudaError_t launch_block_norm(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream);
+cudaError_t launch_block_norm_backward(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream);
+
 }  // namespace sse
