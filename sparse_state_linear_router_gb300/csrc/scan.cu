@@ -34,14 +34,13 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kMaxCluster = 8;  // the portable cluster size
+constexpr int kWorkers = 8;                   // warps that go through rows
+constexpr int kThreads = (kWorkers + 1) * 32;  // and the conductor
+constexpr int kRows = 8;                      // rows of a worker in one tile
+constexpr int kTile = kWorkers * kRows;
+constexpr int kMaxCluster = 8;                // the portable cluster size
 constexpr int kSms = 152;
-constexpr int kRowsFwd = 16;  // rows per warp and tile
-constexpr int kRowsBwd = 8;
-static_assert(kWarps * kRowsBwd == kScanCheckpoint, "the backward's tiles start at checkpoints");
-static_assert((kWarps * kRowsFwd) % kScanCheckpoint == 0, "checkpoints are at warps' first rows");
+static_assert(kTile == kScanCheckpoint, "tiles start at checkpoints");
 
 // ---------------------------------------------------------------------------
 // A lane's channels of one row: two bf16 (computed as a float32 pair) or one
@@ -105,17 +104,21 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN stays NaN
     return y;
 }
 
-// a = exp(la) = 2^(la log2 e).  The product's rounding error, |la| 2^-24 of the
-// result, is put back to first order: 2^(t + r) = 2^t (1 + r ln 2).  Below
-// e^-150 (the least float32 is e^-103) the result is 0; -infinity stops there.
+// a = exp(la) = 2^(la log2 e).  The product's rounding error is |la| 2^-24 of
+// the result: next to the bf16 gates' own steps nothing.  For float32 gates it is
+// put back to first order, 2^(t + r) = 2^t (1 + r ln 2); -infinity stops at
+// e^-150 (the least float32 is e^-103), where the result is 0.
 template <typename T> __device__ __forceinline__ typename Lane<T>::V decay(typename Lane<T>::V la) {
     using L = Lane<T>;
-    la = each(la, [](float x) { return max_nan(x, -150.f); });
-    const auto t = mul2(la, L::splat(1.44269504f));
-    auto r = fma2(la, L::splat(1.44269504f), each(t, [](float x) { return -x; }));
-    r = fma2(la, L::splat(1.92596303e-8f), r);  // log2 e - 1.44269504f
-    const auto a = each(t, [](float x) { return ex2(x); });
-    return fma2(a, mul2(r, L::splat(0.693147181f)), a);
+    if constexpr (sizeof(T) == 4) {
+        la = max_nan(la, -150.f);
+        const float t = la * 1.44269504f;
+        const float r = fmaf(la, 1.92596303e-8f, fmaf(la, 1.44269504f, -t));  // log2 e - 1.44269504f
+        const float a = ex2(t);
+        return fmaf(a, r * 0.693147181f, a);
+    } else {
+        return each(mul2(la, L::splat(1.44269504f)), [](float x) { return ex2(x); });
+    }
 }
 
 // 1 - exp(u) for u <= 0, e = exp(u): its Taylor series up to u^8 / 8! for u >
@@ -205,33 +208,70 @@ template <int ROWS> struct Edges {
     }
 };
 
-// ROWS rows of one token tensor, the lane's 4 bytes of each; zeros outside
-// [t0, t1) (decay 1, input 0: such rows change nothing).
-template <typename T, int ROWS>
-__device__ __forceinline__ void load_rows(uint32_t (&u)[ROWS], const void *base, int64_t stride, int col, int row0,
-                                          int t0, int t1, bool live) {
-    const T *q = static_cast<const T *>(base) + (int64_t)row0 * stride + col;
-    if (row0 >= t0 && row0 + ROWS <= t1) {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) u[i] = live ? __ldg(reinterpret_cast<const uint32_t *>(q + i * stride)) : 0u;
-    } else {
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            u[i] = live && row0 + i >= t0 && row0 + i < t1 ? __ldg(reinterpret_cast<const uint32_t *>(q + i * stride))
-                                                           : 0u;
+// ---------------------------------------------------------------------------
+// Staging of rows: each warp copies its own rows to shared memory a few tiles
+// ahead (16 bytes per lane, four rows per instruction) and waits for nobody
+// else.  Rows outside [t0, t1) are filled with zeros, which change nothing:
+// decay 1, input 0.
+// ---------------------------------------------------------------------------
+struct RowCopy {
+    const char *at;      // this lane's 16 bytes of the first four rows of the next tile to copy
+    int64_t four, step;  // bytes to four rows on, to the next tile
+    // base: the tensor's first row and column; row0: the first tile's first row; rows: to the next tile
+    __device__ __forceinline__ RowCopy(const void *base, int64_t stride_bytes, int64_t col_byte, int row0, int rows,
+                                       int lane) {
+        at = static_cast<const char *>(base) + (row0 + (lane >> 3)) * stride_bytes + col_byte;
+        four = 4 * stride_bytes;
+        step = rows * stride_bytes;
     }
+    // row0: the tile's first row; whole: all its rows are within [t0, t1)
+    __device__ __forceinline__ void copy(uint32_t dst, const void *base, int row0, int t0, int t1, bool whole, bool col_ok,
+                                         int lane) {
+#pragma unroll
+        for (int k = 0; k < kRows; k += 4) {
+            const char *src = at + (k / 4) * four;
+            bool ok = col_ok;
+            if (!whole) {
+                const int row = row0 + k + (lane >> 3);
+                ok = ok && row >= t0 && row < t1;
+            }
+            if (!ok) src = static_cast<const char *>(base);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16), "l"(src),
+                         "r"(ok ? 16 : 0) : "memory");
+        }
+        at += step;
+    }
+};
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups are in flight; then the whole warp's rows are there.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncwarp();
 }
 
-// What the warps and CTAs tell each other, in two buffers in turn: one step's
-// runs are read while the next step's are written.
+// ---------------------------------------------------------------------------
+// Exchange.  The eight workers of a CTA publish their rows' runs and go on
+// with the next tile; a ninth warp, the conductor, composes them, sends the
+// CTA's run to the cluster and meets the other conductors in the cluster's
+// barrier, whose two halves the workers pass a tile apart.  The conductor
+// stores nothing to global memory, so its release has little to wait for; the
+// workers' arrivals carry no data to other CTAs and are relaxed.
+// Buffers alternate: one step's runs are read while the next step's are written.
+// ---------------------------------------------------------------------------
 template <typename V> struct Exchange {
-    Run<V> warp[2][kWarps][32];
-    Run<V> cta[2][kMaxCluster][32];
-    uint32_t warp_reset[2][kWarps];
-    uint32_t cta_reset[2][kMaxCluster];
+    Run<V> warp[kWorkers][32];              // the workers' runs
+    Run<V> ahead[2][kWorkers][32];          // composed: the CTA's rows ahead of each worker
+    Run<V> cta[2][kMaxCluster][32];         // the runs of the cluster's CTAs
+    uint32_t warp_reset[kWorkers], ahead_reset[2], cta_reset[2][kMaxCluster];
 };
 
-// Bits of the warps (or CTAs) whose run holds a reset.
+__device__ __forceinline__ void workers_published() { asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void await_workers() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Bits of the n flags that are set.
 __device__ __forceinline__ uint32_t reset_bits(const uint32_t *flags, int n, int lane) {
     return __ballot_sync(0xffffffffu, lane < n && flags[lane] != 0);
 }
@@ -246,149 +286,216 @@ template <typename V> __device__ __forceinline__ void append(Run<V> &first, cons
     first.P = mul2(first.P, r.P);
 }
 
-// Hands this CTA's run to every CTA of the cluster (one warp calls it).
-template <typename V>
-__device__ __forceinline__ void tell_cluster(cg::cluster_group &cluster, Exchange<V> &ex, int buf, int rank, int csize,
-                                             const Run<V> &r, bool reset, int lane) {
-    for (int k = 0; k < csize; ++k) {
-        *cluster.map_shared_rank(&ex.cta[buf][rank][lane], k) = r;
-        if (lane == 0) *cluster.map_shared_rank(&ex.cta_reset[buf][rank], k) = reset;
+// The conductor's part of one step: the runs ahead of each worker (in the order
+// first worker to last, or last to first) and the CTA's run, sent to the cluster.
+template <bool REVERSE, typename V>
+__device__ __forceinline__ void conduct(cg::cluster_group &cluster, Exchange<V> &ex, int buf, int rank, int csize,
+                                        int lane, V one, V zero) {
+    const uint32_t resets = reset_bits(ex.warp_reset, kWorkers, lane);
+    Run<V> r[kWorkers], all{one, zero};
+#pragma unroll
+    for (int w = 0; w < kWorkers; ++w) r[w] = ex.warp[REVERSE ? kWorkers - 1 - w : w][lane];
+    uint32_t seen = 0, ahead = 0;
+#pragma unroll
+    for (int k = 0; k < kWorkers; ++k) {
+        const int w = REVERSE ? kWorkers - 1 - k : k;
+        ex.ahead[buf][w][lane] = all;
+        ahead |= seen << w;
+        const bool reset = (resets >> w) & 1u;
+        append(all, r[k], reset);
+        seen |= reset;
     }
+    if (lane == 0) ex.ahead_reset[buf] = ahead;
+    for (int k = 0; k < csize; ++k) *cluster.map_shared_rank(&ex.cta[buf][rank][lane], k) = all;
+    if (lane < csize) *cluster.map_shared_rank(&ex.cta_reset[buf][rank], lane) = seen;
 }
 
-// The state the CTA's tile starts from; `state` moves on past the cluster's tiles.
+// A worker's part: the state its rows start from; `state` moves on past the cluster's tiles.
 template <typename V>
-__device__ __forceinline__ V through_cluster(const Exchange<V> &ex, int buf, int rank, int csize, V &state, int lane) {
+__device__ __forceinline__ V start_of(const Exchange<V> &ex, int buf, int rank, int csize, int warp, int lane, V &state) {
     const uint32_t resets = reset_bits(ex.cta_reset[buf], csize, lane);
     V mine = state;
-    for (int k = 0; k < csize; ++k) {
-        if (k == rank) mine = state;
-        state = apply(ex.cta[buf][k][lane], state, (resets >> k) & 1u);
+    if (resets == 0) {
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+            if (k == rank) mine = state;
+            if (k < csize) {
+                const Run<V> r = ex.cta[buf][k][lane];
+                state = fma2(r.P, state, r.q);
+            }
+        }
+    } else {
+        for (int k = 0; k < csize; ++k) {
+            if (k == rank) mine = state;
+            state = apply(ex.cta[buf][k][lane], state, (resets >> k) & 1u);
+        }
     }
-    return mine;
+    return apply(ex.ahead[buf][warp][lane], mine, (ex.ahead_reset[buf] >> warp) & 1u);
 }
+
+// The tiles of one cluster.
+struct Span {
+    int t0, t1, tile0, tiles, steps;
+    __device__ __forceinline__ Span(const ScanArgs &p, int csize) {
+        t0 = range_start(p, blockIdx.y, gridDim.y);
+        t1 = range_start(p, blockIdx.y + 1, gridDim.y);
+        tile0 = t0 / kTile;
+        tiles = t1 > t0 ? (t1 + kTile - 1) / kTile - tile0 : 0;
+        steps = (tiles + csize - 1) / csize;
+    }
+};
 
 // ---------------------------------------------------------------------------
 // Forward.  grid.x: column x cluster rank, grid.y: ranges of the token axis.
 // ---------------------------------------------------------------------------
+template <typename V> struct ForwardRows {
+    V a[kRows], b[kRows];
+    uint32_t starts, ends;
+    int seq, row0;
+};
+
+constexpr int kStagesFwd = 4, kStagesBwd = 3;  // tiles of a warp's ring
+constexpr size_t kRowBytes = kRows * 128;      // one tensor's rows of a warp
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     using V = typename L::V;
-    constexpr int R = kRowsFwd;
+    extern __shared__ uint4 ring[];
     __shared__ Exchange<V> ex;
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = cluster.num_blocks(), rank = cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = ((int)(blockIdx.x / csize) * 32 + lane) * L::kCols;
+    const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
     const bool live = col < width;
-    if (csize > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");  // every CTA has started
+    const Span sp(p, csize);
+    cluster_arrive_relaxed();  // every CTA has started before the first run is sent
+    cluster_wait();
 
-    const int t0 = range_start(p, blockIdx.y, gridDim.y), t1 = range_start(p, blockIdx.y + 1, gridDim.y);
-    constexpr int kTile = kWarps * R;
-    const int tile0 = t0 / kTile;
-    const int tiles = t1 > t0 ? (t1 + kTile - 1) / kTile - tile0 : 0;
-    const int steps = (tiles + csize - 1) / csize;
-
-    uint32_t xr[R], gr[R];
-    int row0 = (tile0 + rank) * kTile + warp * R;
-    if (steps > 0) {
-        load_rows<T, R>(gr, p.log_gate, p.gate_stride, col, row0, t0, t1, live);
-        load_rows<T, R>(xr, p.x, p.x_stride, col, row0, t0, t1, live);
+    if (warp == kWorkers) {
+        for (int step = 0; step < sp.steps; ++step) {
+            await_workers();
+            conduct<false>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f));
+            cluster_arrive_release();
+            cluster_wait();
+        }
+        return;
     }
-    if (csize > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 
-    V state = L::splat(0.f);  // the state ahead of the cluster's tiles
-    Edges<R> ed;
+    uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesFwd * 2 * kRows * 32);
+    const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
+    const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
+    const int first_row = (sp.tile0 + rank) * kTile + warp * kRows;
+    RowCopy copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, csize * kTile, lane);
+    RowCopy copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, csize * kTile, lane);
+    auto load = [&](int step) {  // called for one step after the other
+        if (step < sp.steps) {
+            const uint32_t dst = ring_at + (step % kStagesFwd) * (2 * kRows * 128);
+            const int row0 = first_row + step * csize * kTile;
+            const bool whole = row0 >= sp.t0 && row0 + kRows <= sp.t1;
+            copy_g.copy(dst, p.log_gate, row0, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_x.copy(dst + kRows * 128, p.x, row0, sp.t0, sp.t1, whole, col_ok, lane);
+        }
+        copies_commit();
+    };
+
+    Edges<kRows> ed;
     ed.lo = ed.hi = 0;
-    for (int step = 0; step < steps; ++step) {
-        const int buf = step & 1;
-        V a[R], b[R];
+    Run<V> run;
+    // Decays, inputs and the run of one tile's rows.
+    auto first_pass = [&](ForwardRows<V> &r, int step) {
+        r.row0 = (sp.tile0 + rank + step * csize) * kTile + warp * kRows;
+        const uint32_t *src = mine + (step % kStagesFwd) * (2 * kRows * 32) + lane;
+        ed.find(p, r.row0, sp.t0, sp.t1, lane);
+        r.starts = ed.starts;
+        r.ends = ed.ends;
+        r.seq = ed.seq;
+        copies_wait<kStagesFwd - 1>();
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const V la = L::unpack(gr[i]);
-            a[i] = decay<T>(la);
-            b[i] = L::unpack(xr[i]);
-            if constexpr (MODE != SSE_INPUT_PLAIN) b[i] = mul2(b[i], input_factor<T, MODE>(la, a[i]));
+        for (int i = 0; i < kRows; ++i) {
+            const V la = L::unpack(src[i * 32]);
+            r.a[i] = decay<T>(la);
+            r.b[i] = L::unpack(src[(kRows + i) * 32]);
+            if constexpr (MODE != SSE_INPUT_PLAIN) r.b[i] = mul2(r.b[i], input_factor<T, MODE>(la, r.a[i]));
         }
-        const int next = row0 + csize * kTile;
-        if (step + 1 < steps) {
-            load_rows<T, R>(gr, p.log_gate, p.gate_stride, col, next, t0, t1, live);
-            load_rows<T, R>(xr, p.x, p.x_stride, col, next, t0, t1, live);
-        }
-        ed.find(p, row0, t0, t1, lane);
-        Run<V> run{L::splat(1.f), L::splat(0.f)};
-        if (ed.starts == 0) {
+        __syncwarp();  // every lane has read the slot
+        load(step + kStagesFwd);
+        run = Run<V>{L::splat(1.f), L::splat(0.f)};
+        if (r.starts == 0) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                run.q = fma2(a[i], run.q, b[i]);
-                run.P = mul2(run.P, a[i]);
+            for (int i = 0; i < kRows; ++i) {
+                run.q = fma2(r.a[i], run.q, r.b[i]);
+                run.P = mul2(run.P, r.a[i]);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                if ((ed.starts >> i) & 1u) {
+            for (int i = 0; i < kRows; ++i) {
+                if ((r.starts >> i) & 1u) {
                     // the initial state enters here and is not read again: it may be the final state's buffer
-                    const int s = __shfl_sync(0xffffffffu, ed.seq, i);
+                    const int s = __shfl_sync(0xffffffffu, r.seq, i);
                     const V init = p.init && live ? L::load_state(p.init + (int64_t)s * width + col) : L::splat(0.f);
-                    b[i] = fma2(a[i], init, b[i]);
-                    run.q = b[i];
+                    r.b[i] = fma2(r.a[i], init, r.b[i]);
+                    run.q = r.b[i];
                     run.P = L::splat(0.f);
                 } else {
-                    run.q = fma2(a[i], run.q, b[i]);
-                    run.P = mul2(run.P, a[i]);
+                    run.q = fma2(r.a[i], run.q, r.b[i]);
+                    run.P = mul2(run.P, r.a[i]);
                 }
             }
         }
-        ex.warp[buf][warp][lane] = run;
-        if (lane == 0) ex.warp_reset[buf][warp] = ed.starts;
-        __syncthreads();
-        const uint32_t resets = reset_bits(ex.warp_reset[buf], kWarps, lane);
-        Run<V> ahead{L::splat(1.f), L::splat(0.f)};  // the CTA's warps before this one
-        for (int w = 0; w < warp; ++w) append(ahead, ex.warp[buf][w][lane], (resets >> w) & 1u);
-        if (warp == kWarps - 1) {
-            Run<V> all = ahead;
-            append(all, run, ed.starts != 0);
-            if (csize > 1)
-                tell_cluster(cluster, ex, buf, rank, csize, all, resets != 0, lane);
-            else
-                ex.cta[buf][0][lane] = all, ex.cta_reset[buf][0] = resets != 0;
-        }
-        if (csize > 1) {
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        } else {
-            __syncthreads();
-        }
-        V h = through_cluster(ex, buf, rank, csize, state, lane);
-        h = apply(ahead, h, (resets & ((1u << warp) - 1u)) != 0);
-        if (p.checkpoints && live && row0 % kScanCheckpoint == 0 && row0 >= t0 && row0 < t1)
+    };
+    auto publish = [&](const ForwardRows<V> &r) {
+        ex.warp[warp][lane] = run;
+        if (lane == 0) ex.warp_reset[warp] = r.starts;
+        workers_published();
+        cluster_arrive_relaxed();
+    };
+    V state = L::splat(0.f);  // the state ahead of the cluster's tiles
+    // One step: the next tile's run while this one's is on its way, then this tile's states.
+    auto advance = [&](ForwardRows<V> &now, ForwardRows<V> &next, int step) {
+        const bool more = step + 1 < sp.steps;
+        if (more) first_pass(next, step + 1);
+        cluster_wait();
+        V h = start_of(ex, step & 1, rank, csize, warp, lane, state);
+        if (more) publish(next);
+        const int row0 = now.row0;
+        if (p.checkpoints && live && row0 % kScanCheckpoint == 0 && row0 >= sp.t0 && row0 < sp.t1)
             L::store_state(p.checkpoints + (int64_t)(row0 / kScanCheckpoint) * width + col, h);
         T *out = static_cast<T *>(p.out) + (int64_t)row0 * width + col;
-        if ((ed.starts | ed.ends) == 0 && row0 >= t0 && row0 + R <= t1) {
+        if ((now.starts | now.ends) == 0 && row0 >= sp.t0 && row0 + kRows <= sp.t1) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                h = fma2(a[i], h, b[i]);
+            for (int i = 0; i < kRows; ++i) {
+                h = fma2(now.a[i], h, now.b[i]);
                 if (live) *reinterpret_cast<uint32_t *>(out + (int64_t)i * width) = L::pack(h);
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                h = (ed.starts >> i) & 1u ? b[i] : fma2(a[i], h, b[i]);
-                if (live && row0 + i >= t0 && row0 + i < t1)
+            for (int i = 0; i < kRows; ++i) {
+                h = (now.starts >> i) & 1u ? now.b[i] : fma2(now.a[i], h, now.b[i]);
+                if (live && row0 + i >= sp.t0 && row0 + i < sp.t1)
                     *reinterpret_cast<uint32_t *>(out + (int64_t)i * width) = L::pack(h);
-                if ((ed.ends >> i) & 1u) {
-                    const int s = __shfl_sync(0xffffffffu, ed.seq, i);
+                if ((now.ends >> i) & 1u) {
+                    const int s = __shfl_sync(0xffffffffu, now.seq, i);
                     if (p.final_state && live) L::store_state(p.final_state + (int64_t)s * width + col, h);
                 }
             }
         }
-        row0 = next;
+    };
+    if (sp.steps > 0) {
+        ForwardRows<V> one, two;
+        for (int k = 0; k < kStagesFwd; ++k) load(k);
+        first_pass(one, 0);
+        publish(one);
+        for (int step = 0; step < sp.steps; step += 2) {
+            advance(one, two, step);
+            if (step + 1 < sp.steps) advance(two, one, step + 1);
+        }
     }
     // empty sequences keep their initial state
     if (p.final_state && live) {
-        const int n = gridDim.y * csize * kWarps;
-        for (int s = ((int)blockIdx.y * csize + rank) * kWarps + warp; s < p.num_seqs; s += n)
+        const int n = gridDim.y * csize * kWorkers;
+        for (int s = ((int)blockIdx.y * csize + rank) * kWorkers + warp; s < p.num_seqs; s += n)
             if (__ldg(p.cu_seqlens + s) >= __ldg(p.cu_seqlens + s + 1)) {
                 const int64_t i = (int64_t)s * width + col;
                 L::store_state(p.final_state + i, p.init ? L::load_state(p.init + i) : L::splat(0.f));
@@ -397,165 +504,207 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
 }
 
 // ---------------------------------------------------------------------------
-// Backward: the tiles from the last to the first.  A tile's states come from
-// its checkpoint and the CTA's own rows; what later tokens hand back,
-// e_t = a_t (d_out_t + e_{t+1}), is the same kind of run in the other
-// direction and goes through the cluster.
+// Backward: the tiles from the last to the first.  What later tokens hand back,
+// e_t = a_t (d_out_t + e_{t+1}), is the same kind of run in the other direction
+// and goes through the cluster; a tile's states come from its checkpoint and the
+// CTA's own rows, composed by the conductor in the same step.
 // ---------------------------------------------------------------------------
+template <typename V, int MODE> struct BackwardRows {
+    V a[kRows], s[MODE == SSE_INPUT_PLAIN ? 1 : kRows];
+    uint32_t starts, ends;
+    int seq, row0;
+};
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     using V = typename L::V;
-    constexpr int R = kRowsBwd;
-    __shared__ Exchange<V> ex;                   // adjoint runs
-    __shared__ Run<V> fwd[2][kWarps][32];        // state runs of the CTA's warps
-    __shared__ uint32_t fwd_reset[2][kWarps];
+    extern __shared__ uint4 ring[];
+    __shared__ Exchange<V> ex;                 // adjoint runs
+    __shared__ Run<V> fwd[kWorkers][32];       // the workers' state runs
+    __shared__ V before[2][kWorkers][32];      // the state ahead of each worker's rows
+    __shared__ uint32_t fwd_reset[kWorkers];
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = cluster.num_blocks(), rank = cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = ((int)(blockIdx.x / csize) * 32 + lane) * L::kCols;
+    const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
     const bool live = col < width;
-    if (csize > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const Span sp(p, csize);
+    const int last_tile = sp.tile0 + sp.tiles - 1 - rank;  // rank 0 has the last; below tile0 there are no rows
+    cluster_arrive_relaxed();
+    cluster_wait();
 
-    const int t0 = range_start(p, blockIdx.y, gridDim.y), t1 = range_start(p, blockIdx.y + 1, gridDim.y);
-    constexpr int kTile = kWarps * R;
-    const int tile0 = t0 / kTile;
-    const int tiles = t1 > t0 ? (t1 + kTile - 1) / kTile - tile0 : 0;
-    const int steps = (tiles + csize - 1) / csize;
-
-    uint32_t xr[R], gr[R], dr[R];
-    V check = L::splat(0.f);  // the state ahead of the tile
-    // rank 0 has the last tile; a tile below tile0 has no rows in [t0, t1)
-    auto load = [&](int tile) {
-        const int row = tile * kTile + warp * R;
-        load_rows<T, R>(gr, p.log_gate, p.gate_stride, col, row, t0, t1, live);
-        load_rows<T, R>(xr, p.x, p.x_stride, col, row, t0, t1, live);
-        load_rows<T, R>(dr, p.d_out, width, col, row, t0, t1, live);
-        check = live && tile * kTile > t0 ? L::load_state(p.checkpoints + (int64_t)tile * width + col) : L::splat(0.f);
-    };
-    int tile = tile0 + tiles - 1 - rank;
-    if (steps > 0) load(tile);
-    if (csize > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-
-    V adjoint = L::splat(0.f);  // what the tokens behind the cluster's tiles hand back
-    Edges<R> ed;
-    ed.lo = ed.hi = 0;
-    for (int step = 0; step < steps; ++step) {
-        const int buf = step & 1, row0 = tile * kTile + warp * R;
-        V a[R], h[R], s[MODE == SSE_INPUT_PLAIN ? 1 : R];  // h: first the inputs s x, then the states before each row
-        uint32_t x[R], d[R];
+    if (warp == kWorkers) {
+        auto checkpoint = [&](int step) {
+            const int tile = last_tile - step * csize;
+            return live && tile * kTile > sp.t0 ? L::load_state(p.checkpoints + (int64_t)tile * width + col)
+                                                : L::splat(0.f);
+        };
+        V check = sp.steps > 0 ? checkpoint(0) : L::splat(0.f);
+        for (int step = 0; step < sp.steps; ++step) {
+            V state = check;
+            if (step + 1 < sp.steps) check = checkpoint(step + 1);
+            await_workers();
+            conduct<true>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f));
+            const uint32_t resets = reset_bits(fwd_reset, kWorkers, lane);
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const V la = L::unpack(gr[i]);
-            a[i] = decay<T>(la);
-            x[i] = xr[i];
-            d[i] = dr[i];
-            h[i] = L::unpack(x[i]);
+            for (int w = 0; w < kWorkers; ++w) {
+                before[step & 1][w][lane] = state;
+                state = apply(fwd[w][lane], state, (resets >> w) & 1u);
+            }
+            cluster_arrive_release();
+            cluster_wait();
+        }
+        return;
+    }
+
+    uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesBwd * 3 * kRows * 32);
+    const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
+    const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
+    auto slot = [&](int step) { return mine + (step % kStagesBwd) * (3 * kRows * 32); };
+    auto row_of = [&](int step) { return (last_tile - step * csize) * kTile + warp * kRows; };
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
+    RowCopy copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, row_of(0), -csize * kTile, lane);
+    RowCopy copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, row_of(0), -csize * kTile, lane);
+    RowCopy copy_d(p.d_out, (int64_t)width * (int)sizeof(T), col_byte, row_of(0), -csize * kTile, lane);
+    auto load = [&](int step) {  // called for one step after the other
+        if (step < sp.steps) {
+            const uint32_t dst = ring_at + (step % kStagesBwd) * (3 * kRows * 128);
+            const int row0 = row_of(step);
+            const bool whole = row0 >= sp.t0 && row0 + kRows <= sp.t1;
+            copy_g.copy(dst, p.log_gate, row0, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_x.copy(dst + kRows * 128, p.x, row0, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_d.copy(dst + 2 * kRows * 128, p.d_out, row0, sp.t0, sp.t1, whole, col_ok, lane);
+        }
+        copies_commit();
+    };
+
+    Edges<kRows> ed;
+    ed.lo = ed.hi = 0;
+    Run<V> run, back;
+    auto first_state = [&](int seq, int i) {
+        const int q = __shfl_sync(0xffffffffu, seq, i);
+        return p.init && live ? L::load_state(p.init + (int64_t)q * width + col) : L::splat(0.f);
+    };
+    auto last_adjoint = [&](int seq, int i) {
+        const int q = __shfl_sync(0xffffffffu, seq, i);
+        return p.d_final && live ? L::load_state(p.d_final + (int64_t)q * width + col) : L::splat(0.f);
+    };
+    auto first_pass = [&](BackwardRows<V, MODE> &r, int step) {
+        r.row0 = row_of(step);
+        const uint32_t *src = slot(step) + lane;
+        ed.find(p, r.row0, sp.t0, sp.t1, lane);
+        r.starts = ed.starts;
+        r.ends = ed.ends;
+        r.seq = ed.seq;
+        copies_wait<kStagesBwd - 2>();
+        V b[kRows], d[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const V la = L::unpack(src[i * 32]);
+            r.a[i] = decay<T>(la);
+            b[i] = L::unpack(src[(kRows + i) * 32]);
+            d[i] = L::unpack(src[(2 * kRows + i) * 32]);
             if constexpr (MODE != SSE_INPUT_PLAIN) {
-                s[i] = input_factor<T, MODE>(la, a[i]);
-                h[i] = mul2(h[i], s[i]);
+                r.s[i] = input_factor<T, MODE>(la, r.a[i]);
+                b[i] = mul2(b[i], r.s[i]);
             }
         }
-        V state = check;
-        if (step + 1 < steps) load(tile - csize);
-        ed.find(p, row0, t0, t1, lane);
-        const uint32_t starts = ed.starts, ends = ed.ends;
-        auto first_state = [&](int i) {
-            const int sq = __shfl_sync(0xffffffffu, ed.seq, i);
-            return p.init && live ? L::load_state(p.init + (int64_t)sq * width + col) : L::splat(0.f);
-        };
-        auto last_adjoint = [&](int i) {
-            const int sq = __shfl_sync(0xffffffffu, ed.seq, i);
-            return p.d_final && live ? L::load_state(p.d_final + (int64_t)sq * width + col) : L::splat(0.f);
-        };
-        Run<V> run{L::splat(1.f), L::splat(0.f)}, back{L::splat(1.f), L::splat(0.f)};
-        if ((starts | ends) == 0) {
+        run = back = Run<V>{L::splat(1.f), L::splat(0.f)};
+        if ((r.starts | r.ends) == 0) {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                run.q = fma2(a[i], run.q, h[i]);
-                run.P = mul2(run.P, a[i]);
-                const int j = R - 1 - i;
-                back.q = mul2(a[j], add2(L::unpack(d[j]), back.q));
+            for (int i = 0; i < kRows; ++i) {
+                run.q = fma2(r.a[i], run.q, b[i]);
+                run.P = mul2(run.P, r.a[i]);
+                const int j = kRows - 1 - i;
+                back.q = mul2(r.a[j], add2(d[j], back.q));
             }
             back.P = run.P;
         } else {
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                run.q = fma2(a[i], (starts >> i) & 1u ? first_state(i) : run.q, h[i]);
-                run.P = mul2(run.P, a[i]);
-                const int j = R - 1 - i;
-                back.q = mul2(a[j], add2(L::unpack(d[j]), (ends >> j) & 1u ? last_adjoint(j) : back.q));
+            for (int i = 0; i < kRows; ++i) {
+                run.q = fma2(r.a[i], (r.starts >> i) & 1u ? first_state(r.seq, i) : run.q, b[i]);
+                run.P = mul2(run.P, r.a[i]);
+                const int j = kRows - 1 - i;
+                back.q = mul2(r.a[j], add2(d[j], (r.ends >> j) & 1u ? last_adjoint(r.seq, j) : back.q));
             }
             back.P = run.P;
-            if (starts) run.P = L::splat(0.f);
-            if (ends) back.P = L::splat(0.f);
+            if (r.starts) run.P = L::splat(0.f);
+            if (r.ends) back.P = L::splat(0.f);
         }
-        fwd[buf][warp][lane] = run;
-        ex.warp[buf][warp][lane] = back;
+    };
+    auto publish = [&](const BackwardRows<V, MODE> &r) {
+        fwd[warp][lane] = run;
+        ex.warp[warp][lane] = back;
         if (lane == 0) {
-            fwd_reset[buf][warp] = starts;
-            ex.warp_reset[buf][warp] = ends;
+            fwd_reset[warp] = r.starts;
+            ex.warp_reset[warp] = r.ends;
         }
-        __syncthreads();
-        const uint32_t fresets = reset_bits(fwd_reset[buf], kWarps, lane);
-        const uint32_t bresets = reset_bits(ex.warp_reset[buf], kWarps, lane);
-        Run<V> behind{L::splat(1.f), L::splat(0.f)};  // the CTA's warps of later rows
-        for (int w = kWarps - 1; w > warp; --w) append(behind, ex.warp[buf][w][lane], (bresets >> w) & 1u);
-        if (warp == 0) {
-            Run<V> all = behind;
-            append(all, back, ends != 0);
-            if (csize > 1)
-                tell_cluster(cluster, ex, buf, rank, csize, all, bresets != 0, lane);
-            else
-                ex.cta[buf][0][lane] = all, ex.cta_reset[buf][0] = bresets != 0;
-        }
-        if (csize > 1)
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-        // the states before each row, while the cluster gathers
-        for (int w = 0; w < warp; ++w) state = apply(fwd[buf][w][lane], state, (fresets >> w) & 1u);
+        workers_published();
+        cluster_arrive_relaxed();
+    };
+    V adjoint = L::splat(0.f);  // what the tokens behind the cluster's tiles hand back
+    auto advance = [&](BackwardRows<V, MODE> &now, BackwardRows<V, MODE> &next, int step) {
+        const bool more = step + 1 < sp.steps;
+        if (more) first_pass(next, step + 1);
+        cluster_wait();
+        V e = start_of(ex, step & 1, rank, csize, warp, lane, adjoint);
+        V state = before[step & 1][warp][lane];
+        if (more) publish(next);
+        const uint32_t *src = slot(step) + lane;
+        V h[kRows];  // the state before each row
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const V in = h[i];
-            if ((starts >> i) & 1u) state = first_state(i);
+        for (int i = 0; i < kRows; ++i) {
+            if ((now.starts >> i) & 1u) state = first_state(now.seq, i);
             h[i] = state;
-            state = fma2(a[i], state, in);
+            V b = L::unpack(src[(kRows + i) * 32]);
+            if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, now.s[i]);
+            state = fma2(now.a[i], state, b);
         }
-        if (csize > 1)
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        else
-            __syncthreads();
-        V e = through_cluster(ex, buf, rank, csize, adjoint, lane);
-        e = apply(behind, e, (bresets >> (warp + 1)) != 0);
+        const int row0 = now.row0;
         const int64_t at = (int64_t)row0 * width + col;
         T *dx = static_cast<T *>(p.dx) + at, *dg = static_cast<T *>(p.d_log_gate) + at;
-        const bool whole = row0 >= t0 && row0 + R <= t1;
+        const bool whole = row0 >= sp.t0 && row0 + kRows <= sp.t1;
 #pragma unroll
-        for (int j = R - 1; j >= 0; --j) {
-            if ((ends >> j) & 1u) e = last_adjoint(j);
-            const V dh = add2(L::unpack(d[j]), e);
-            e = mul2(a[j], dh);
-            V gx = dh, slope = mul2(a[j], h[j]);
+        for (int j = kRows - 1; j >= 0; --j) {
+            if ((now.ends >> j) & 1u) e = last_adjoint(now.seq, j);
+            const V dh = add2(L::unpack(src[(2 * kRows + j) * 32]), e);
+            e = mul2(now.a[j], dh);
+            V gx = dh, slope = mul2(now.a[j], h[j]);
             if constexpr (MODE != SSE_INPUT_PLAIN) {
-                gx = mul2(dh, s[j]);
+                gx = mul2(dh, now.s[j]);
                 const V ds = MODE == SSE_INPUT_COMPLEMENT
-                                 ? each(a[j], [](float v) { return -v; })
-                                 : each(a[j], s[j], [](float v, float f) { return f > 0.f ? __fdividef(-v * v, f) : 0.f; });
-                slope = fma2(ds, L::unpack(x[j]), slope);
+                                 ? each(now.a[j], [](float v) { return -v; })
+                                 : each(now.a[j], now.s[j],
+                                        [](float v, float f) { return f > 0.f ? __fdividef(-v * v, f) : 0.f; });
+                slope = fma2(ds, L::unpack(src[(kRows + j) * 32]), slope);
             }
-            if (live && (whole || (row0 + j >= t0 && row0 + j < t1))) {
+            if (live && (whole || (row0 + j >= sp.t0 && row0 + j < sp.t1))) {
                 *reinterpret_cast<uint32_t *>(dx + (int64_t)j * width) = L::pack(gx);
                 *reinterpret_cast<uint32_t *>(dg + (int64_t)j * width) = L::pack(mul2(dh, slope));
             }
-            if ((starts >> j) & 1u) {
-                const int sq = __shfl_sync(0xffffffffu, ed.seq, j);
-                if (p.d_init && live) L::store_state(p.d_init + (int64_t)sq * width + col, e);
+            if ((now.starts >> j) & 1u) {
+                const int q = __shfl_sync(0xffffffffu, now.seq, j);
+                if (p.d_init && live) L::store_state(p.d_init + (int64_t)q * width + col, e);
             }
         }
-        tile -= csize;
+        __syncwarp();  // every lane has read the slot
+        load(step + kStagesBwd);
+    };
+    if (sp.steps > 0) {
+        BackwardRows<V, MODE> one, two;
+        for (int k = 0; k < kStagesBwd - 1; ++k) load(k);
+        first_pass(one, 0);
+        load(kStagesBwd - 1);
+        publish(one);
+        for (int step = 0; step < sp.steps; step += 2) {
+            advance(one, two, step);
+            if (step + 1 < sp.steps) advance(two, one, step + 1);
+        }
     }
     if (p.d_init && live) {  // empty sequences hand the final state's gradient through
-        const int n = gridDim.y * csize * kWarps;
-        for (int q = ((int)blockIdx.y * csize + rank) * kWarps + warp; q < p.num_seqs; q += n)
+        const int n = gridDim.y * csize * kWorkers;
+        for (int q = ((int)blockIdx.y * csize + rank) * kWorkers + warp; q < p.num_seqs; q += n)
             if (__ldg(p.cu_seqlens + q) >= __ldg(p.cu_seqlens + q + 1)) {
                 const int64_t i = (int64_t)q * width + col;
                 L::store_state(p.d_init + i, p.d_final ? L::load_state(p.d_final + i) : L::splat(0.f));
@@ -607,8 +756,7 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     // columns leave, but no more tiles than there are; with fewer columns the
     // token axis is split into ranges of whole sequences as well.
     const int columns = (width + 32 * Lane<T>::kCols - 1) / (32 * Lane<T>::kCols);
-    const int tile = kWarps * (what == kForward ? kRowsFwd : kRowsBwd);
-    const int64_t tiles = ((int64_t)a.total_tokens + tile - 1) / tile;
+    const int64_t tiles = ((int64_t)a.total_tokens + kTile - 1) / kTile;
     int csize = 2 * kSms / columns;
     csize = csize > kMaxCluster ? kMaxCluster : csize < 1 ? 1 : csize;
     if (csize > tiles) csize = tiles < 1 ? 1 : (int)tiles;
@@ -616,7 +764,12 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     if (ranges > a.num_seqs) ranges = a.num_seqs;
     if (ranges > tiles / csize) ranges = tiles / csize;
     if (ranges < 1) ranges = 1;
+    const auto kernel = what == kForward ? scan_forward_kernel<T, MODE> : scan_backward_kernel<T, MODE>;
+    const size_t smem = kWorkers * kRowBytes * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = smem;
     cfg.gridDim = dim3(columns * csize, (unsigned)ranges);
     cfg.blockDim = kThreads;
     cfg.stream = stream;
@@ -625,8 +778,7 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     attr[0].val.clusterDim = {(unsigned)csize, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, what == kForward ? scan_forward_kernel<T, MODE> : scan_backward_kernel<T, MODE>, a,
-                              width);
+    return cudaLaunchKernelEx(&cfg, kernel, a, width);
 }
 
 template <typename T>
