@@ -36,11 +36,11 @@ namespace cg = cooperative_groups;
 
 constexpr int kWorkers = 8;                   // warps that go through rows
 constexpr int kThreads = (kWorkers + 1) * 32;  // and the conductor
-constexpr int kRows = 8;                      // rows of a worker in one tile
-constexpr int kTile = kWorkers * kRows;
+constexpr int kRowsFwd = 16, kRowsBwd = 8;    // rows of a worker in one tile
 constexpr int kMaxCluster = 8;                // the portable cluster size
 constexpr int kSms = 152;
-static_assert(kTile == kScanCheckpoint, "tiles start at checkpoints");
+static_assert(kWorkers * kRowsBwd % kScanCheckpoint == 0 && kScanCheckpoint % kRowsFwd == 0,
+              "checkpoints lie at workers' first rows, and the backward's tiles at checkpoints");
 
 // ---------------------------------------------------------------------------
 // A lane's channels of one row: two bf16 (computed as a float32 pair) or one
@@ -121,21 +121,20 @@ template <typename T> __device__ __forceinline__ typename Lane<T>::V decay(typen
     }
 }
 
-// 1 - exp(u) for u <= 0, e = exp(u): its Taylor series up to u^8 / 8! for u >
-// -1/2 (the next term is 10^-8 of the sum), where 1 - e would cancel.
+// 1 - exp(u) for u <= 0, e = exp(u).  For u > -1/2, where 1 - e would cancel,
+// -u times the Chebyshev interpolation of degree 5 of (exp(u) - 1) / u on
+// [-1/2, 0] (1.5e-9 off, 6e-8 with float32 roundings).
 template <typename T>
 __device__ __forceinline__ typename Lane<T>::V one_minus_exp(typename Lane<T>::V u, typename Lane<T>::V e) {
     using L = Lane<T>;
-    auto p = L::splat(-1.f / 40320);
-    p = fma2(p, u, L::splat(-1.f / 5040));
-    p = fma2(p, u, L::splat(-1.f / 720));
-    p = fma2(p, u, L::splat(-1.f / 120));
-    p = fma2(p, u, L::splat(-1.f / 24));
-    p = fma2(p, u, L::splat(-1.f / 6));
-    p = fma2(p, u, L::splat(-1.f / 2));
+    auto p = L::splat(-0.0011234042f);
+    p = fma2(p, u, L::splat(-0.008189614f));
+    p = fma2(p, u, L::splat(-0.041630074f));
+    p = fma2(p, u, L::splat(-0.16666242f));
+    p = fma2(p, u, L::splat(-0.49999982f));
     p = fma2(p, u, L::splat(-1.f));
     p = mul2(p, u);
-    return each(u, p, e, [](float x, float series, float ex) { return x > -0.5f ? series : 1.f - ex; });
+    return each(u, p, e, [](float x, float near0, float ex) { return x > -0.5f ? near0 : 1.f - ex; });
 }
 
 // The input factor s(a) of MODE (sse_input_scale_t; not for PLAIN).
@@ -214,7 +213,7 @@ template <int ROWS> struct Edges {
 // else.  Rows outside [t0, t1) are filled with zeros, which change nothing:
 // decay 1, input 0.
 // ---------------------------------------------------------------------------
-struct RowCopy {
+template <int ROWS> struct RowCopy {
     const char *at;      // this lane's 16 bytes of the first four rows of the next tile to copy
     int64_t four, step;  // bytes to four rows on, to the next tile
     // base: the tensor's first row and column; row0: the first tile's first row; rows: to the next tile
@@ -227,17 +226,17 @@ struct RowCopy {
     // row0: the tile's first row; whole: all its rows are within [t0, t1)
     __device__ __forceinline__ void copy(uint32_t dst, const void *base, int row0, int t0, int t1, bool whole, bool col_ok,
                                          int lane) {
+        const char *src = at;
 #pragma unroll
-        for (int k = 0; k < kRows; k += 4) {
-            const char *src = at + (k / 4) * four;
+        for (int k = 0; k < ROWS; k += 4) {
             bool ok = col_ok;
             if (!whole) {
                 const int row = row0 + k + (lane >> 3);
                 ok = ok && row >= t0 && row < t1;
             }
-            if (!ok) src = static_cast<const char *>(base);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16), "l"(src),
-                         "r"(ok ? 16 : 0) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16),
+                         "l"(ok ? src : static_cast<const char *>(base)), "r"(ok ? 16 : 0) : "memory");
+            src += four;
         }
         at += step;
     }
@@ -249,24 +248,52 @@ template <int N> __device__ __forceinline__ void copies_wait() {
     __syncwarp();
 }
 
-// ---------------------------------------------------------------------------
-// Exchange.  The eight workers of a CTA publish their rows' runs and go on
-// with the next tile; a ninth warp, the conductor, composes them, sends the
-// CTA's run to the cluster and meets the other conductors in the cluster's
-// barrier, whose two halves the workers pass a tile apart.  The conductor
-// stores nothing to global memory, so its release has little to wait for; the
-// workers' arrivals carry no data to other CTAs and are relaxed.
-// Buffers alternate: one step's runs are read while the next step's are written.
-// ---------------------------------------------------------------------------
-template <typename V> struct Exchange {
-    Run<V> warp[kWorkers][32];              // the workers' runs
-    Run<V> ahead[2][kWorkers][32];          // composed: the CTA's rows ahead of each worker
-    Run<V> cta[2][kMaxCluster][32];         // the runs of the cluster's CTAs
-    uint32_t warp_reset[kWorkers], ahead_reset[2], cta_reset[2][kMaxCluster];
+// A worker's results go back through the slot they were made from, each word in
+// the place of the input it replaces, and out in 16-byte words.
+template <int ROWS> struct RowStore {
+    char *at;
+    int64_t four, step;
+    __device__ __forceinline__ RowStore(void *base, int64_t stride_bytes, int64_t col_byte, int row0, int rows, int lane) {
+        at = static_cast<char *>(base) + (row0 + (lane >> 3)) * stride_bytes + col_byte;
+        four = 4 * stride_bytes;
+        step = rows * stride_bytes;
+    }
+    __device__ __forceinline__ void store(const uint32_t *src, int row0, int t0, int t1, bool whole, bool col_ok, int lane) {
+        char *dst = at;
+#pragma unroll
+        for (int k = 0; k < ROWS; k += 4) {
+            bool ok = col_ok;
+            if (!whole) {
+                const int row = row0 + k + (lane >> 3);
+                ok = ok && row >= t0 && row < t1;
+            }
+            const uint4 u = *reinterpret_cast<const uint4 *>(src + k * 32 + lane * 4);
+            if (ok) *reinterpret_cast<uint4 *>(dst) = u;
+            dst += four;
+        }
+        at += step;
+    }
 };
 
-__device__ __forceinline__ void workers_published() { asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ void await_workers() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+// ---------------------------------------------------------------------------
+// Exchange.  The workers of a CTA publish their rows' runs and go on with the
+// next tile; a ninth warp, the conductor, composes them, sends the CTA's run to
+// the cluster, meets the other conductors in the cluster's barrier and leaves
+// each worker the state its rows start from.  The conductor stores nothing to
+// global memory, so its release has little to wait for; the workers' arrivals
+// carry no data to other CTAs and are relaxed.
+// ---------------------------------------------------------------------------
+template <typename V> struct Exchange {
+    Run<V> warp[kWorkers][32];       // the workers' runs
+    Run<V> cta[2][kMaxCluster][32];  // the runs of the cluster's CTAs, two steps in turn
+    V start[kWorkers][32];           // what each worker's rows start from; read before the worker's next arrival
+    uint32_t warp_reset[kWorkers], cta_reset[2][kMaxCluster];
+};
+
+__device__ __forceinline__ void runs_published() { asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void await_runs() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void starts_published() { asm volatile("barrier.cta.arrive 2, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ void await_starts() { asm volatile("barrier.cta.sync 2, %0;" ::"n"(kThreads) : "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -280,61 +307,56 @@ __device__ __forceinline__ uint32_t reset_bits(const uint32_t *flags, int n, int
 template <typename V> __device__ __forceinline__ V apply(const Run<V> &r, V h, bool reset) {
     return reset ? r.q : fma2(r.P, h, r.q);
 }
-// `first`, then r; `reset`: r holds a reset.
-template <typename V> __device__ __forceinline__ void append(Run<V> &first, const Run<V> &r, bool reset) {
-    first.q = apply(r, first.q, reset);
-    first.P = mul2(first.P, r.P);
-}
 
-// The conductor's part of one step: the runs ahead of each worker (in the order
-// first worker to last, or last to first) and the CTA's run, sent to the cluster.
-template <bool REVERSE, typename V>
+// The conductor's part of one step, between the workers' runs and their
+// starts; `meanwhile` runs while the cluster gathers.  REVERSE: the last worker
+// comes first.  `state` moves past the cluster's tiles.
+template <bool REVERSE, typename V, typename F>
 __device__ __forceinline__ void conduct(cg::cluster_group &cluster, Exchange<V> &ex, int buf, int rank, int csize,
-                                        int lane, V one, V zero) {
+                                        int lane, V one, V zero, V &state, F meanwhile) {
     const uint32_t resets = reset_bits(ex.warp_reset, kWorkers, lane);
     Run<V> r[kWorkers], all{one, zero};
 #pragma unroll
-    for (int w = 0; w < kWorkers; ++w) r[w] = ex.warp[REVERSE ? kWorkers - 1 - w : w][lane];
-    uint32_t seen = 0, ahead = 0;
+    for (int k = 0; k < kWorkers; ++k) r[k] = ex.warp[REVERSE ? kWorkers - 1 - k : k][lane];
 #pragma unroll
     for (int k = 0; k < kWorkers; ++k) {
-        const int w = REVERSE ? kWorkers - 1 - k : k;
-        ex.ahead[buf][w][lane] = all;
-        ahead |= seen << w;
-        const bool reset = (resets >> w) & 1u;
-        append(all, r[k], reset);
-        seen |= reset;
+        all.q = apply(r[k], all.q, (resets >> (REVERSE ? kWorkers - 1 - k : k)) & 1u);
+        all.P = mul2(all.P, r[k].P);
     }
-    if (lane == 0) ex.ahead_reset[buf] = ahead;
     for (int k = 0; k < csize; ++k) *cluster.map_shared_rank(&ex.cta[buf][rank][lane], k) = all;
-    if (lane < csize) *cluster.map_shared_rank(&ex.cta_reset[buf][rank], lane) = seen;
-}
-
-// A worker's part: the state its rows start from; `state` moves on past the cluster's tiles.
-template <typename V>
-__device__ __forceinline__ V start_of(const Exchange<V> &ex, int buf, int rank, int csize, int warp, int lane, V &state) {
-    const uint32_t resets = reset_bits(ex.cta_reset[buf], csize, lane);
+    if (lane < csize) *cluster.map_shared_rank(&ex.cta_reset[buf][rank], lane) = resets;
+    cluster_arrive_release();
+    meanwhile();
+    cluster_wait();
+    const uint32_t cta_resets = reset_bits(ex.cta_reset[buf], csize, lane);
     V mine = state;
-    if (resets == 0) {
+    if (cta_resets == 0) {
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
             if (k == rank) mine = state;
             if (k < csize) {
-                const Run<V> r = ex.cta[buf][k][lane];
-                state = fma2(r.P, state, r.q);
+                const Run<V> c = ex.cta[buf][k][lane];
+                state = fma2(c.P, state, c.q);
             }
         }
     } else {
         for (int k = 0; k < csize; ++k) {
             if (k == rank) mine = state;
-            state = apply(ex.cta[buf][k][lane], state, (resets >> k) & 1u);
+            state = apply(ex.cta[buf][k][lane], state, (cta_resets >> k) & 1u);
         }
     }
-    return apply(ex.ahead[buf][warp][lane], mine, (ex.ahead_reset[buf] >> warp) & 1u);
+#pragma unroll
+    for (int k = 0; k < kWorkers; ++k) {
+        const int w = REVERSE ? kWorkers - 1 - k : k;
+        ex.start[w][lane] = mine;
+        mine = apply(r[k], mine, (resets >> w) & 1u);
+    }
+    starts_published();
 }
 
 // The tiles of one cluster.
-struct Span {
+template <int ROWS> struct Span {
+    static constexpr int kTile = kWorkers * ROWS;
     int t0, t1, tile0, tiles, steps;
     __device__ __forceinline__ Span(const ScanArgs &p, int csize) {
         t0 = range_start(p, blockIdx.y, gridDim.y);
@@ -345,22 +367,27 @@ struct Span {
     }
 };
 
-// ---------------------------------------------------------------------------
-// Forward.  grid.x: column x cluster rank, grid.y: ranges of the token axis.
-// ---------------------------------------------------------------------------
-template <typename V> struct ForwardRows {
-    V a[kRows], b[kRows];
+// Sequence edges among the rows of a worker's tile.
+struct Marks {
     uint32_t starts, ends;
     int seq, row0;
+    bool whole;  // every row is within [t0, t1)
 };
 
-constexpr int kStagesFwd = 4, kStagesBwd = 3;  // tiles of a warp's ring
-constexpr size_t kRowBytes = kRows * 128;      // one tensor's rows of a warp
+constexpr int kStagesFwd = 3, kStagesBwd = 3;  // tiles of a worker's ring
 
+// ---------------------------------------------------------------------------
+// Forward.  grid.x: column x cluster rank, grid.y: ranges of the token axis.
+// Each tile's rows are gone through twice from shared memory, once for their
+// run and once from their start; the decays are made twice, which is cheaper
+// than the registers that would hold them.
+// ---------------------------------------------------------------------------
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     using V = typename L::V;
+    constexpr int kRows = kRowsFwd, kTile = kWorkers * kRows;
+    constexpr int kSlotWords = kRows * 32, kSlotBytes = kSlotWords * 4;  // one tensor's rows of a worker
     extern __shared__ uint4 ring[];
     __shared__ Exchange<V> ex;
     cg::cluster_group cluster = cg::this_cluster();
@@ -368,128 +395,139 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
     const bool live = col < width;
-    const Span sp(p, csize);
+    const Span<kRows> sp(p, csize);
     cluster_arrive_relaxed();  // every CTA has started before the first run is sent
     cluster_wait();
 
     if (warp == kWorkers) {
+        V state = L::splat(0.f);  // the state ahead of the cluster's tiles
         for (int step = 0; step < sp.steps; ++step) {
-            await_workers();
-            conduct<false>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f));
-            cluster_arrive_release();
-            cluster_wait();
+            await_runs();
+            conduct<false>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f), state, [] {});
         }
         return;
     }
 
-    uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesFwd * 2 * kRows * 32);
+    uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesFwd * 2 * kSlotWords);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
     const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
     const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
-    const int first_row = (sp.tile0 + rank) * kTile + warp * kRows;
-    RowCopy copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, csize * kTile, lane);
-    RowCopy copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, csize * kTile, lane);
+    const int first_row = (sp.tile0 + rank) * kTile + warp * kRows, stride = csize * kTile;
+    RowCopy<kRows> copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, stride, lane);
+    RowCopy<kRows> copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, stride, lane);
+    RowStore<kRows> store_out(p.out, (int64_t)width * (int)sizeof(T), col_byte, first_row, stride, lane);
+    int load_slot = 0, load_row = first_row;
     auto load = [&](int step) {  // called for one step after the other
         if (step < sp.steps) {
-            const uint32_t dst = ring_at + (step % kStagesFwd) * (2 * kRows * 128);
-            const int row0 = first_row + step * csize * kTile;
-            const bool whole = row0 >= sp.t0 && row0 + kRows <= sp.t1;
-            copy_g.copy(dst, p.log_gate, row0, sp.t0, sp.t1, whole, col_ok, lane);
-            copy_x.copy(dst + kRows * 128, p.x, row0, sp.t0, sp.t1, whole, col_ok, lane);
+            const uint32_t dst = ring_at + load_slot * (2 * kSlotBytes);
+            const bool whole = load_row >= sp.t0 && load_row + kRows <= sp.t1;
+            copy_g.copy(dst, p.log_gate, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_x.copy(dst + kSlotBytes, p.x, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            load_slot = load_slot + 1 == kStagesFwd ? 0 : load_slot + 1;
+            load_row += stride;
         }
         copies_commit();
+    };
+    auto first_state = [&](int seq, int i) {
+        const int s = __shfl_sync(0xffffffffu, seq, i);
+        return p.init && live ? L::load_state(p.init + (int64_t)s * width + col) : L::splat(0.f);
+    };
+    // a and s x of row i of a slot
+    auto step_of = [&](const uint32_t *src, int i, V &a, V &b) {
+        const V la = L::unpack(src[i * 32]);
+        a = decay<T>(la);
+        b = L::unpack(src[kSlotWords + i * 32]);
+        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
     };
 
     Edges<kRows> ed;
     ed.lo = ed.hi = 0;
-    Run<V> run;
-    // Decays, inputs and the run of one tile's rows.
-    auto first_pass = [&](ForwardRows<V> &r, int step) {
-        r.row0 = (sp.tile0 + rank + step * csize) * kTile + warp * kRows;
-        const uint32_t *src = mine + (step % kStagesFwd) * (2 * kRows * 32) + lane;
-        ed.find(p, r.row0, sp.t0, sp.t1, lane);
-        r.starts = ed.starts;
-        r.ends = ed.ends;
-        r.seq = ed.seq;
-        copies_wait<kStagesFwd - 1>();
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const V la = L::unpack(src[i * 32]);
-            r.a[i] = decay<T>(la);
-            r.b[i] = L::unpack(src[(kRows + i) * 32]);
-            if constexpr (MODE != SSE_INPUT_PLAIN) r.b[i] = mul2(r.b[i], input_factor<T, MODE>(la, r.a[i]));
-        }
-        __syncwarp();  // every lane has read the slot
-        load(step + kStagesFwd);
+    // Publishes the run of one tile's rows.  `entry`: the initial state that enters at the last start among them.
+    auto first_pass = [&](Marks &m, V &entry, Run<V> &run, int row0, const uint32_t *src) {
+        ed.find(p, row0, sp.t0, sp.t1, lane);
+        m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1};
         run = Run<V>{L::splat(1.f), L::splat(0.f)};
-        if (r.starts == 0) {
+        if (m.starts == 0) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                run.q = fma2(r.a[i], run.q, r.b[i]);
-                run.P = mul2(run.P, r.a[i]);
+                V a, b;
+                step_of(src, i, a, b);
+                run.q = fma2(a, run.q, b);
+                run.P = mul2(run.P, a);
             }
         } else {
-#pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                if ((r.starts >> i) & 1u) {
-                    // the initial state enters here and is not read again: it may be the final state's buffer
-                    const int s = __shfl_sync(0xffffffffu, r.seq, i);
-                    const V init = p.init && live ? L::load_state(p.init + (int64_t)s * width + col) : L::splat(0.f);
-                    r.b[i] = fma2(r.a[i], init, r.b[i]);
-                    run.q = r.b[i];
-                    run.P = L::splat(0.f);
-                } else {
-                    run.q = fma2(r.a[i], run.q, r.b[i]);
-                    run.P = mul2(run.P, r.a[i]);
-                }
+                V a, b;
+                step_of(src, i, a, b);
+                if ((m.starts >> i) & 1u) run.q = entry = first_state(m.seq, i);
+                run.q = fma2(a, run.q, b);
             }
+            run.P = L::splat(0.f);
         }
     };
-    auto publish = [&](const ForwardRows<V> &r) {
+    auto publish = [&](const Marks &m, const Run<V> &run) {
         ex.warp[warp][lane] = run;
-        if (lane == 0) ex.warp_reset[warp] = r.starts;
-        workers_published();
+        if (lane == 0) ex.warp_reset[warp] = m.starts;
+        runs_published();
         cluster_arrive_relaxed();
     };
-    V state = L::splat(0.f);  // the state ahead of the cluster's tiles
-    // One step: the next tile's run while this one's is on its way, then this tile's states.
-    auto advance = [&](ForwardRows<V> &now, ForwardRows<V> &next, int step) {
-        const bool more = step + 1 < sp.steps;
-        if (more) first_pass(next, step + 1);
-        cluster_wait();
-        V h = start_of(ex, step & 1, rank, csize, warp, lane, state);
-        if (more) publish(next);
-        const int row0 = now.row0;
-        if (p.checkpoints && live && row0 % kScanCheckpoint == 0 && row0 >= sp.t0 && row0 < sp.t1)
-            L::store_state(p.checkpoints + (int64_t)(row0 / kScanCheckpoint) * width + col, h);
-        T *out = static_cast<T *>(p.out) + (int64_t)row0 * width + col;
-        if ((now.starts | now.ends) == 0 && row0 >= sp.t0 && row0 + kRows <= sp.t1) {
+    auto second_pass = [&](const Marks &m, const V &entry, V h, uint32_t *src) {
+        if (p.checkpoints && live && m.row0 % kScanCheckpoint == 0 && m.row0 >= sp.t0 && m.row0 < sp.t1)
+            L::store_state(p.checkpoints + (int64_t)(m.row0 / kScanCheckpoint) * width + col, h);
+        if ((m.starts | m.ends) == 0) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                h = fma2(now.a[i], h, now.b[i]);
-                if (live) *reinterpret_cast<uint32_t *>(out + (int64_t)i * width) = L::pack(h);
+                V a, b;
+                step_of(src, i, a, b);
+                h = fma2(a, h, b);
+                src[kSlotWords + i * 32] = L::pack(h);
             }
         } else {
-#pragma unroll
+            const int last = 31 - __clz(m.starts);
             for (int i = 0; i < kRows; ++i) {
-                h = (now.starts >> i) & 1u ? now.b[i] : fma2(now.a[i], h, now.b[i]);
-                if (live && row0 + i >= sp.t0 && row0 + i < sp.t1)
-                    *reinterpret_cast<uint32_t *>(out + (int64_t)i * width) = L::pack(h);
-                if ((now.ends >> i) & 1u) {
-                    const int s = __shfl_sync(0xffffffffu, now.seq, i);
+                V a, b;
+                step_of(src, i, a, b);
+                // Where the final state is written over the initial one, another worker may have done so by now for
+                // the sequence that leaves these rows, so its initial state was kept; the others end among these rows.
+                if ((m.starts >> i) & 1u) h = i == last ? entry : first_state(m.seq, i);
+                h = fma2(a, h, b);
+                src[kSlotWords + i * 32] = L::pack(h);
+                if ((m.ends >> i) & 1u) {
+                    const int s = __shfl_sync(0xffffffffu, m.seq, i);
                     if (p.final_state && live) L::store_state(p.final_state + (int64_t)s * width + col, h);
                 }
             }
         }
+        __syncwarp();
+        store_out.store(src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
+        __syncwarp();  // the slot is free
     };
     if (sp.steps > 0) {
-        ForwardRows<V> one, two;
+        Marks now, next;
+        V entry = L::splat(0.f), next_entry = entry;
+        Run<V> run;
+        int slot = 0, row0 = first_row;
         for (int k = 0; k < kStagesFwd; ++k) load(k);
-        first_pass(one, 0);
-        publish(one);
-        for (int step = 0; step < sp.steps; step += 2) {
-            advance(one, two, step);
-            if (step + 1 < sp.steps) advance(two, one, step + 1);
+        copies_wait<kStagesFwd - 1>();
+        first_pass(now, entry, run, row0, mine + lane);
+        publish(now, run);
+        for (int step = 0; step < sp.steps; ++step) {
+            const bool more = step + 1 < sp.steps;
+            const int next_slot = slot + 1 == kStagesFwd ? 0 : slot + 1;
+            if (more) {
+                row0 += stride;
+                copies_wait<kStagesFwd - 2>();
+                first_pass(next, next_entry, run, row0, mine + next_slot * (2 * kSlotWords) + lane);
+            }
+            await_starts();
+            const V h = ex.start[warp][lane];
+            cluster_wait();
+            if (more) publish(next, run);
+            second_pass(now, entry, h, mine + slot * (2 * kSlotWords) + lane);
+            load(step + kStagesFwd);
+            now = next;
+            entry = next_entry;
+            slot = next_slot;
         }
     }
     // empty sequences keep their initial state
@@ -509,79 +547,78 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
 // and goes through the cluster; a tile's states come from its checkpoint and the
 // CTA's own rows, composed by the conductor in the same step.
 // ---------------------------------------------------------------------------
-template <typename V, int MODE> struct BackwardRows {
-    V a[kRows], s[MODE == SSE_INPUT_PLAIN ? 1 : kRows];
-    uint32_t starts, ends;
-    int seq, row0;
-};
-
 template <typename T, int MODE>
 __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     using V = typename L::V;
+    constexpr int kRows = kRowsBwd, kTile = kWorkers * kRows;
+    constexpr int kSlotWords = kRows * 32, kSlotBytes = kSlotWords * 4;  // one tensor's rows of a worker
     extern __shared__ uint4 ring[];
     __shared__ Exchange<V> ex;                 // adjoint runs
     __shared__ Run<V> fwd[kWorkers][32];       // the workers' state runs
-    __shared__ V before[2][kWorkers][32];      // the state ahead of each worker's rows
+    __shared__ V before[kWorkers][32];         // the state ahead of each worker's rows
     __shared__ uint32_t fwd_reset[kWorkers];
     cg::cluster_group cluster = cg::this_cluster();
     const int csize = cluster.num_blocks(), rank = cluster.block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
     const bool live = col < width;
-    const Span sp(p, csize);
+    const Span<kRows> sp(p, csize);
     const int last_tile = sp.tile0 + sp.tiles - 1 - rank;  // rank 0 has the last; below tile0 there are no rows
     cluster_arrive_relaxed();
     cluster_wait();
 
     if (warp == kWorkers) {
         auto checkpoint = [&](int step) {
-            const int tile = last_tile - step * csize;
-            return live && tile * kTile > sp.t0 ? L::load_state(p.checkpoints + (int64_t)tile * width + col)
-                                                : L::splat(0.f);
+            const int row = (last_tile - step * csize) * kTile;
+            return live && row > sp.t0 ? L::load_state(p.checkpoints + (int64_t)(row / kScanCheckpoint) * width + col)
+                                       : L::splat(0.f);
         };
         V check = sp.steps > 0 ? checkpoint(0) : L::splat(0.f);
+        V adjoint = L::splat(0.f);  // what the tokens behind the cluster's tiles hand back
         for (int step = 0; step < sp.steps; ++step) {
             V state = check;
             if (step + 1 < sp.steps) check = checkpoint(step + 1);
-            await_workers();
-            conduct<true>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f));
-            const uint32_t resets = reset_bits(fwd_reset, kWorkers, lane);
+            await_runs();
+            conduct<true>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f), adjoint, [&] {
+                const uint32_t resets = reset_bits(fwd_reset, kWorkers, lane);
 #pragma unroll
-            for (int w = 0; w < kWorkers; ++w) {
-                before[step & 1][w][lane] = state;
-                state = apply(fwd[w][lane], state, (resets >> w) & 1u);
-            }
-            cluster_arrive_release();
-            cluster_wait();
+                for (int w = 0; w < kWorkers; ++w) {
+                    before[w][lane] = state;
+                    state = apply(fwd[w][lane], state, (resets >> w) & 1u);
+                }
+            });
         }
         return;
     }
 
-    uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesBwd * 3 * kRows * 32);
+    uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesBwd * 3 * kSlotWords);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
     const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
     const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
-    auto slot = [&](int step) { return mine + (step % kStagesBwd) * (3 * kRows * 32); };
-    auto row_of = [&](int step) { return (last_tile - step * csize) * kTile + warp * kRows; };
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
-    RowCopy copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, row_of(0), -csize * kTile, lane);
-    RowCopy copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, row_of(0), -csize * kTile, lane);
-    RowCopy copy_d(p.d_out, (int64_t)width * (int)sizeof(T), col_byte, row_of(0), -csize * kTile, lane);
+    const int first_row = last_tile * kTile + warp * kRows, stride = csize * kTile;
+    const int64_t packed = (int64_t)width * (int)sizeof(T);
+    RowCopy<kRows> copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, -stride, lane);
+    RowCopy<kRows> copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, -stride, lane);
+    RowCopy<kRows> copy_d(p.d_out, packed, col_byte, first_row, -stride, lane);
+    RowStore<kRows> store_dx(p.dx, packed, col_byte, first_row, -stride, lane);
+    RowStore<kRows> store_dg(p.d_log_gate, packed, col_byte, first_row, -stride, lane);
+    int load_slot = 0, load_row = first_row;
     auto load = [&](int step) {  // called for one step after the other
         if (step < sp.steps) {
-            const uint32_t dst = ring_at + (step % kStagesBwd) * (3 * kRows * 128);
-            const int row0 = row_of(step);
-            const bool whole = row0 >= sp.t0 && row0 + kRows <= sp.t1;
-            copy_g.copy(dst, p.log_gate, row0, sp.t0, sp.t1, whole, col_ok, lane);
-            copy_x.copy(dst + kRows * 128, p.x, row0, sp.t0, sp.t1, whole, col_ok, lane);
-            copy_d.copy(dst + 2 * kRows * 128, p.d_out, row0, sp.t0, sp.t1, whole, col_ok, lane);
+            const uint32_t dst = ring_at + load_slot * (3 * kSlotBytes);
+            const bool whole = load_row >= sp.t0 && load_row + kRows <= sp.t1;
+            copy_g.copy(dst, p.log_gate, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_x.copy(dst + kSlotBytes, p.x, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_d.copy(dst + 2 * kSlotBytes, p.d_out, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            load_slot = load_slot + 1 == kStagesBwd ? 0 : load_slot + 1;
+            load_row -= stride;
         }
         copies_commit();
     };
 
     Edges<kRows> ed;
     ed.lo = ed.hi = 0;
-    Run<V> run, back;
     auto first_state = [&](int seq, int i) {
         const int q = __shfl_sync(0xffffffffu, seq, i);
         return p.init && live ? L::load_state(p.init + (int64_t)q * width + col) : L::splat(0.f);
@@ -590,116 +627,111 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         const int q = __shfl_sync(0xffffffffu, seq, i);
         return p.d_final && live ? L::load_state(p.d_final + (int64_t)q * width + col) : L::splat(0.f);
     };
-    auto first_pass = [&](BackwardRows<V, MODE> &r, int step) {
-        r.row0 = row_of(step);
-        const uint32_t *src = slot(step) + lane;
-        ed.find(p, r.row0, sp.t0, sp.t1, lane);
-        r.starts = ed.starts;
-        r.ends = ed.ends;
-        r.seq = ed.seq;
-        copies_wait<kStagesBwd - 2>();
-        V b[kRows], d[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const V la = L::unpack(src[i * 32]);
-            r.a[i] = decay<T>(la);
-            b[i] = L::unpack(src[(kRows + i) * 32]);
-            d[i] = L::unpack(src[(2 * kRows + i) * 32]);
-            if constexpr (MODE != SSE_INPUT_PLAIN) {
-                r.s[i] = input_factor<T, MODE>(la, r.a[i]);
-                b[i] = mul2(b[i], r.s[i]);
-            }
-        }
+    // The tile's state run and, since a run of decays is the same both ways, its
+    // adjoint run in one sweep: q_back = sum over rows of (a_first ... a_row) d_row.
+    auto first_pass = [&](Marks &m, Run<V> &run, Run<V> &back, int row0, const uint32_t *src) {
+        ed.find(p, row0, sp.t0, sp.t1, lane);
+        m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1};
         run = back = Run<V>{L::splat(1.f), L::splat(0.f)};
-        if ((r.starts | r.ends) == 0) {
+        if ((m.starts | m.ends) == 0) {
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                run.q = fma2(r.a[i], run.q, b[i]);
-                run.P = mul2(run.P, r.a[i]);
-                const int j = kRows - 1 - i;
-                back.q = mul2(r.a[j], add2(d[j], back.q));
+                const V la = L::unpack(src[i * 32]), a = decay<T>(la);
+                V b = L::unpack(src[kSlotWords + i * 32]);
+                if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
+                run.q = fma2(a, run.q, b);
+                run.P = mul2(run.P, a);
+                back.q = fma2(run.P, L::unpack(src[2 * kSlotWords + i * 32]), back.q);
             }
             back.P = run.P;
         } else {
-#pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                run.q = fma2(r.a[i], (r.starts >> i) & 1u ? first_state(r.seq, i) : run.q, b[i]);
-                run.P = mul2(run.P, r.a[i]);
-                const int j = kRows - 1 - i;
-                back.q = mul2(r.a[j], add2(d[j], (r.ends >> j) & 1u ? last_adjoint(r.seq, j) : back.q));
+                const V la = L::unpack(src[i * 32]), a = decay<T>(la);
+                V b = L::unpack(src[kSlotWords + i * 32]);
+                if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
+                run.q = fma2(a, (m.starts >> i) & 1u ? first_state(m.seq, i) : run.q, b);
+                run.P = mul2(run.P, a);
             }
-            back.P = run.P;
-            if (r.starts) run.P = L::splat(0.f);
-            if (r.ends) back.P = L::splat(0.f);
+            for (int j = kRows - 1; j >= 0; --j) {
+                const V a = decay<T>(L::unpack(src[j * 32])), d = L::unpack(src[2 * kSlotWords + j * 32]);
+                back.q = mul2(a, add2(d, (m.ends >> j) & 1u ? last_adjoint(m.seq, j) : back.q));
+            }
+            back.P = m.ends ? L::splat(0.f) : run.P;
+            if (m.starts) run.P = L::splat(0.f);
         }
     };
-    auto publish = [&](const BackwardRows<V, MODE> &r) {
+    auto publish = [&](const Marks &m, const Run<V> &run, const Run<V> &back) {
         fwd[warp][lane] = run;
         ex.warp[warp][lane] = back;
         if (lane == 0) {
-            fwd_reset[warp] = r.starts;
-            ex.warp_reset[warp] = r.ends;
+            fwd_reset[warp] = m.starts;
+            ex.warp_reset[warp] = m.ends;
         }
-        workers_published();
+        runs_published();
         cluster_arrive_relaxed();
     };
-    V adjoint = L::splat(0.f);  // what the tokens behind the cluster's tiles hand back
-    auto advance = [&](BackwardRows<V, MODE> &now, BackwardRows<V, MODE> &next, int step) {
-        const bool more = step + 1 < sp.steps;
-        if (more) first_pass(next, step + 1);
-        cluster_wait();
-        V e = start_of(ex, step & 1, rank, csize, warp, lane, adjoint);
-        V state = before[step & 1][warp][lane];
-        if (more) publish(next);
-        const uint32_t *src = slot(step) + lane;
+    auto second_pass = [&](const Marks &m, V state, V e, uint32_t *src) {
         V h[kRows];  // the state before each row
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            if ((now.starts >> i) & 1u) state = first_state(now.seq, i);
+            if ((m.starts >> i) & 1u) state = first_state(m.seq, i);
             h[i] = state;
-            V b = L::unpack(src[(kRows + i) * 32]);
-            if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, now.s[i]);
-            state = fma2(now.a[i], state, b);
+            const V la = L::unpack(src[i * 32]), a = decay<T>(la);
+            V b = L::unpack(src[kSlotWords + i * 32]);
+            if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
+            state = fma2(a, state, b);
         }
-        const int row0 = now.row0;
-        const int64_t at = (int64_t)row0 * width + col;
-        T *dx = static_cast<T *>(p.dx) + at, *dg = static_cast<T *>(p.d_log_gate) + at;
-        const bool whole = row0 >= sp.t0 && row0 + kRows <= sp.t1;
 #pragma unroll
         for (int j = kRows - 1; j >= 0; --j) {
-            if ((now.ends >> j) & 1u) e = last_adjoint(now.seq, j);
-            const V dh = add2(L::unpack(src[(2 * kRows + j) * 32]), e);
-            e = mul2(now.a[j], dh);
-            V gx = dh, slope = mul2(now.a[j], h[j]);
+            if ((m.ends >> j) & 1u) e = last_adjoint(m.seq, j);
+            const V la = L::unpack(src[j * 32]), a = decay<T>(la);
+            const V dh = add2(L::unpack(src[2 * kSlotWords + j * 32]), e);
+            e = mul2(a, dh);
+            V gx = dh, slope = mul2(a, h[j]);
             if constexpr (MODE != SSE_INPUT_PLAIN) {
-                gx = mul2(dh, now.s[j]);
+                const V s = input_factor<T, MODE>(la, a);
+                gx = mul2(dh, s);
                 const V ds = MODE == SSE_INPUT_COMPLEMENT
-                                 ? each(now.a[j], [](float v) { return -v; })
-                                 : each(now.a[j], now.s[j],
-                                        [](float v, float f) { return f > 0.f ? __fdividef(-v * v, f) : 0.f; });
-                slope = fma2(ds, L::unpack(src[(kRows + j) * 32]), slope);
+                                 ? each(a, [](float v) { return -v; })
+                                 : each(a, s, [](float v, float f) { return f > 0.f ? __fdividef(-v * v, f) : 0.f; });
+                slope = fma2(ds, L::unpack(src[kSlotWords + j * 32]), slope);
             }
-            if (live && (whole || (row0 + j >= sp.t0 && row0 + j < sp.t1))) {
-                *reinterpret_cast<uint32_t *>(dx + (int64_t)j * width) = L::pack(gx);
-                *reinterpret_cast<uint32_t *>(dg + (int64_t)j * width) = L::pack(mul2(dh, slope));
-            }
-            if ((now.starts >> j) & 1u) {
-                const int q = __shfl_sync(0xffffffffu, now.seq, j);
+            src[kSlotWords + j * 32] = L::pack(gx);
+            src[2 * kSlotWords + j * 32] = L::pack(mul2(dh, slope));
+            if ((m.starts >> j) & 1u) {
+                const int q = __shfl_sync(0xffffffffu, m.seq, j);
                 if (p.d_init && live) L::store_state(p.d_init + (int64_t)q * width + col, e);
             }
         }
-        __syncwarp();  // every lane has read the slot
-        load(step + kStagesBwd);
+        __syncwarp();
+        store_dx.store(src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
+        store_dg.store(src - lane + 2 * kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
+        __syncwarp();  // the slot is free
     };
     if (sp.steps > 0) {
-        BackwardRows<V, MODE> one, two;
-        for (int k = 0; k < kStagesBwd - 1; ++k) load(k);
-        first_pass(one, 0);
-        load(kStagesBwd - 1);
-        publish(one);
-        for (int step = 0; step < sp.steps; step += 2) {
-            advance(one, two, step);
-            if (step + 1 < sp.steps) advance(two, one, step + 1);
+        Marks now, next;
+        Run<V> run, back;
+        int slot = 0, row0 = first_row;
+        for (int k = 0; k < kStagesBwd; ++k) load(k);
+        copies_wait<kStagesBwd - 1>();
+        first_pass(now, run, back, row0, mine + lane);
+        publish(now, run, back);
+        for (int step = 0; step < sp.steps; ++step) {
+            const bool more = step + 1 < sp.steps;
+            const int next_slot = slot + 1 == kStagesBwd ? 0 : slot + 1;
+            if (more) {
+                row0 -= stride;
+                copies_wait<kStagesBwd - 2>();
+                first_pass(next, run, back, row0, mine + next_slot * (3 * kSlotWords) + lane);
+            }
+            await_starts();
+            const V e = ex.start[warp][lane], state = before[warp][lane];
+            cluster_wait();
+            if (more) publish(next, run, back);
+            second_pass(now, state, e, mine + slot * (3 * kSlotWords) + lane);
+            load(step + kStagesBwd);
+            now = next;
+            slot = next_slot;
         }
     }
     if (p.d_init && live) {  // empty sequences hand the final state's gradient through
@@ -756,7 +788,8 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     // columns leave, but no more tiles than there are; with fewer columns the
     // token axis is split into ranges of whole sequences as well.
     const int columns = (width + 32 * Lane<T>::kCols - 1) / (32 * Lane<T>::kCols);
-    const int64_t tiles = ((int64_t)a.total_tokens + kTile - 1) / kTile;
+    const int rows = what == kForward ? kRowsFwd : kRowsBwd, tile = kWorkers * rows;
+    const int64_t tiles = ((int64_t)a.total_tokens + tile - 1) / tile;
     int csize = 2 * kSms / columns;
     csize = csize > kMaxCluster ? kMaxCluster : csize < 1 ? 1 : csize;
     if (csize > tiles) csize = tiles < 1 ? 1 : (int)tiles;
@@ -765,7 +798,7 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     if (ranges > tiles / csize) ranges = tiles / csize;
     if (ranges < 1) ranges = 1;
     const auto kernel = what == kForward ? scan_forward_kernel<T, MODE> : scan_backward_kernel<T, MODE>;
-    const size_t smem = kWorkers * kRowBytes * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
+    const size_t smem = (size_t)tile * 128 * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
