@@ -104,6 +104,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN stays NaN
     return y;
 }
 
+__device__ __forceinline__ float rsqrt_ftz(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // a = exp(la) = 2^(la log2 e).  The product's rounding error is |la| 2^-24 of
 // the result: next to the bf16 gates' own steps nothing.  For float32 gates it is
 // put back to first order, 2^(t + r) = 2^t (1 + r ln 2); -infinity stops at
@@ -137,14 +143,21 @@ __device__ __forceinline__ typename Lane<T>::V one_minus_exp(typename Lane<T>::V
     return each(u, p, e, [](float x, float near0, float ex) { return x > -0.5f ? near0 : 1.f - ex; });
 }
 
-// The input factor s(a) of MODE (sse_input_scale_t; not for PLAIN).
-template <typename T, int MODE>
-__device__ __forceinline__ typename Lane<T>::V input_factor(typename Lane<T>::V la, typename Lane<T>::V a) {
+// The input factor s(a) of MODE (sse_input_scale_t; not for PLAIN), and with
+// GRAD its derivative by the log-gate.
+template <typename T, int MODE, bool GRAD = false>
+__device__ __forceinline__ typename Lane<T>::V input_factor(typename Lane<T>::V la, typename Lane<T>::V a,
+                                                            typename Lane<T>::V *slope = nullptr) {
+    using L = Lane<T>;
     if constexpr (MODE == SSE_INPUT_COMPLEMENT) {
+        if constexpr (GRAD) *slope = mul2(a, L::splat(-1.f));
         return one_minus_exp<T>(la, a);
     } else {
-        const auto s2 = one_minus_exp<T>(add2(la, la), mul2(a, a));
-        return each(s2, [](float v) { return v * rsqrtf(fmaxf(v, 1e-37f)); });  // 0 at 0
+        const auto a2 = mul2(a, a), s2 = one_minus_exp<T>(add2(la, la), a2);
+        // 1 / s, and 0 for s = 0: no input enters there and its slope is taken as 0
+        const auto r = each(s2, [](float v) { return rsqrt_ftz(fmaxf(v, 1e-37f)); });
+        if constexpr (GRAD) *slope = mul2(mul2(a2, L::splat(-1.f)), each(s2, r, [](float v, float i) { return v > 0.f ? i : v; }));
+        return mul2(s2, r);
     }
 }
 
@@ -308,23 +321,61 @@ template <typename V> __device__ __forceinline__ V apply(const Run<V> &r, V h, b
     return reset ? r.q : fma2(r.P, h, r.q);
 }
 
+// Where this CTA's runs go in the cluster's CTAs (a conductor's registers).
+template <typename V> struct Outbox {
+    uint32_t run[kMaxCluster], reset;
+    __device__ __forceinline__ Outbox(Exchange<V> &ex, int rank, int csize, int lane) {
+        const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&ex.cta[0][rank][lane]);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(run[k]) : "r"(mine), "r"(k < csize ? k : 0));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(reset)
+            : "r"((uint32_t)__cvta_generic_to_shared(&ex.cta_reset[0][rank])), "r"(lane < csize ? lane : 0));
+    }
+    __device__ __forceinline__ void send(int buf, int csize, int lane, const Run<V> &r, uint32_t resets) const {
+        const uint32_t off = buf * (uint32_t)sizeof(Exchange<V>::cta[0]);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k)
+            if (k < csize) {
+                if constexpr (sizeof(V) == 8) {
+                    const float2 u = f2_get(r.P), v = f2_get(r.q);
+                    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(run[k] + off), "f"(u.x), "f"(u.y),
+                                 "f"(v.x), "f"(v.y) : "memory");
+                } else {
+                    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(run[k] + off), "f"(r.P), "f"(r.q)
+                                 : "memory");
+                }
+            }
+        if (lane < csize)
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(reset + buf * (uint32_t)sizeof(Exchange<V>::cta_reset[0])),
+                         "r"(resets) : "memory");
+    }
+};
+
 // The conductor's part of one step, between the workers' runs and their
 // starts; `meanwhile` runs while the cluster gathers.  REVERSE: the last worker
-// comes first.  `state` moves past the cluster's tiles.
+// comes first.  `state` moves past the cluster's tiles.  Its length is what the
+// cluster waits for, so steps without a reset take the short way.
 template <bool REVERSE, typename V, typename F>
-__device__ __forceinline__ void conduct(cg::cluster_group &cluster, Exchange<V> &ex, int buf, int rank, int csize,
-                                        int lane, V one, V zero, V &state, F meanwhile) {
+__device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, int buf, int rank, int csize, int lane,
+                                        V &state, F meanwhile) {
     const uint32_t resets = reset_bits(ex.warp_reset, kWorkers, lane);
-    Run<V> r[kWorkers], all{one, zero};
+    Run<V> r[kWorkers];
 #pragma unroll
     for (int k = 0; k < kWorkers; ++k) r[k] = ex.warp[REVERSE ? kWorkers - 1 - k : k][lane];
+    Run<V> all = r[0];
+    if (resets == 0) {
 #pragma unroll
-    for (int k = 0; k < kWorkers; ++k) {
-        all.q = apply(r[k], all.q, (resets >> (REVERSE ? kWorkers - 1 - k : k)) & 1u);
-        all.P = mul2(all.P, r[k].P);
+        for (int k = 1; k < kWorkers; ++k) {
+            all.q = fma2(r[k].P, all.q, r[k].q);
+            all.P = mul2(all.P, r[k].P);
+        }
+    } else {
+#pragma unroll
+        for (int k = 1; k < kWorkers; ++k)
+            all.q = apply(r[k], all.q, (resets >> (REVERSE ? kWorkers - 1 - k : k)) & 1u);
     }
-    for (int k = 0; k < csize; ++k) *cluster.map_shared_rank(&ex.cta[buf][rank][lane], k) = all;
-    if (lane < csize) *cluster.map_shared_rank(&ex.cta_reset[buf][rank], lane) = resets;
+    out.send(buf, csize, lane, all, resets);
     cluster_arrive_release();
     meanwhile();
     cluster_wait();
@@ -339,17 +390,22 @@ __device__ __forceinline__ void conduct(cg::cluster_group &cluster, Exchange<V> 
                 state = fma2(c.P, state, c.q);
             }
         }
+#pragma unroll
+        for (int k = 0; k < kWorkers; ++k) {
+            ex.start[REVERSE ? kWorkers - 1 - k : k][lane] = mine;
+            mine = fma2(r[k].P, mine, r[k].q);
+        }
     } else {
         for (int k = 0; k < csize; ++k) {
             if (k == rank) mine = state;
             state = apply(ex.cta[buf][k][lane], state, (cta_resets >> k) & 1u);
         }
-    }
 #pragma unroll
-    for (int k = 0; k < kWorkers; ++k) {
-        const int w = REVERSE ? kWorkers - 1 - k : k;
-        ex.start[w][lane] = mine;
-        mine = apply(r[k], mine, (resets >> w) & 1u);
+        for (int k = 0; k < kWorkers; ++k) {
+            const int w = REVERSE ? kWorkers - 1 - k : k;
+            ex.start[w][lane] = mine;
+            mine = apply(r[k], mine, (resets >> w) & 1u);
+        }
     }
     starts_published();
 }
@@ -390,8 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     constexpr int kSlotWords = kRows * 32, kSlotBytes = kSlotWords * 4;  // one tensor's rows of a worker
     extern __shared__ uint4 ring[];
     __shared__ Exchange<V> ex;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int csize = cluster.num_blocks(), rank = cluster.block_rank();
+    const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
     const bool live = col < width;
@@ -400,10 +455,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     cluster_wait();
 
     if (warp == kWorkers) {
+        const Outbox<V> out(ex, rank, csize, lane);
         V state = L::splat(0.f);  // the state ahead of the cluster's tiles
         for (int step = 0; step < sp.steps; ++step) {
             await_runs();
-            conduct<false>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f), state, [] {});
+            conduct<false>(out, ex, step & 1, rank, csize, lane, state, [] {});
         }
         return;
     }
@@ -558,8 +614,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
     __shared__ Run<V> fwd[kWorkers][32];       // the workers' state runs
     __shared__ V before[kWorkers][32];         // the state ahead of each worker's rows
     __shared__ uint32_t fwd_reset[kWorkers];
-    cg::cluster_group cluster = cg::this_cluster();
-    const int csize = cluster.num_blocks(), rank = cluster.block_rank();
+    const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
     const bool live = col < width;
@@ -574,13 +629,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
             return live && row > sp.t0 ? L::load_state(p.checkpoints + (int64_t)(row / kScanCheckpoint) * width + col)
                                        : L::splat(0.f);
         };
+        const Outbox<V> out(ex, rank, csize, lane);
         V check = sp.steps > 0 ? checkpoint(0) : L::splat(0.f);
         V adjoint = L::splat(0.f);  // what the tokens behind the cluster's tiles hand back
         for (int step = 0; step < sp.steps; ++step) {
             V state = check;
             if (step + 1 < sp.steps) check = checkpoint(step + 1);
             await_runs();
-            conduct<true>(cluster, ex, step & 1, rank, csize, lane, L::splat(1.f), L::splat(0.f), adjoint, [&] {
+            conduct<true>(out, ex, step & 1, rank, csize, lane, adjoint, [&] {
                 const uint32_t resets = reset_bits(fwd_reset, kWorkers, lane);
 #pragma unroll
                 for (int w = 0; w < kWorkers; ++w) {
@@ -671,33 +727,34 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         cluster_arrive_relaxed();
     };
     auto second_pass = [&](const Marks &m, V state, V e, uint32_t *src) {
-        V h[kRows];  // the state before each row
+        // forwards for the states, then backwards: dh = d + e, dx = s dh, d_log_gate = dh (a h_before + s' x)
+        V a[kRows], s[MODE == SSE_INPUT_PLAIN ? 1 : kRows], slope[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             if ((m.starts >> i) & 1u) state = first_state(m.seq, i);
-            h[i] = state;
-            const V la = L::unpack(src[i * 32]), a = decay<T>(la);
+            const V la = L::unpack(src[i * 32]);
             V b = L::unpack(src[kSlotWords + i * 32]);
-            if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
-            state = fma2(a, state, b);
+            a[i] = decay<T>(la);
+            if constexpr (MODE == SSE_INPUT_PLAIN) {
+                slope[i] = mul2(a[i], state);
+                state = add2(slope[i], b);
+            } else {
+                V ds;
+                s[i] = input_factor<T, MODE, true>(la, a[i], &ds);
+                slope[i] = mul2(a[i], state);
+                state = fma2(s[i], b, slope[i]);
+                slope[i] = fma2(ds, b, slope[i]);
+            }
         }
 #pragma unroll
         for (int j = kRows - 1; j >= 0; --j) {
             if ((m.ends >> j) & 1u) e = last_adjoint(m.seq, j);
-            const V la = L::unpack(src[j * 32]), a = decay<T>(la);
             const V dh = add2(L::unpack(src[2 * kSlotWords + j * 32]), e);
-            e = mul2(a, dh);
-            V gx = dh, slope = mul2(a, h[j]);
-            if constexpr (MODE != SSE_INPUT_PLAIN) {
-                const V s = input_factor<T, MODE>(la, a);
-                gx = mul2(dh, s);
-                const V ds = MODE == SSE_INPUT_COMPLEMENT
-                                 ? each(a, [](float v) { return -v; })
-                                 : each(a, s, [](float v, float f) { return f > 0.f ? __fdividef(-v * v, f) : 0.f; });
-                slope = fma2(ds, L::unpack(src[kSlotWords + j * 32]), slope);
-            }
+            e = mul2(a[j], dh);
+            V gx = dh;
+            if constexpr (MODE != SSE_INPUT_PLAIN) gx = mul2(dh, s[j]);
             src[kSlotWords + j * 32] = L::pack(gx);
-            src[2 * kSlotWords + j * 32] = L::pack(mul2(dh, slope));
+            src[2 * kSlotWords + j * 32] = L::pack(mul2(dh, slope[j]));
             if ((m.starts >> j) & 1u) {
                 const int q = __shfl_sync(0xffffffffu, m.seq, j);
                 if (p.d_init && live) L::store_state(p.d_init + (int64_t)q * width + col, e);
