@@ -12,9 +12,13 @@
 //          dc = branch_scale w_after C;  dw_before_j = sum of dx' r_hat
 //
 // Bound by HBM: about 16 to 40 operations per element against 4 to 16 bytes.
-// Each row is read once into registers, 16 bytes per thread and tensor, by a
-// team of threads that covers it; sums over the row or a group of it go
-// through shuffles and one word per warp of shared memory.
+// A team of threads covers a row, 16 bytes per thread and tensor, and goes from
+// row to row; each thread copies its own words of the rows ahead to shared
+// memory asynchronously (no barrier: nobody else reads them), so the loads of
+// the next rows are in flight while this one is summed.  Sums over the row go
+// through shuffles and one word per warp of shared memory; sums over a group of
+// columns through shuffles where the group is a power of two of lanes.
+#include "f32x2.cuh"
 #include "sse_internal.cuh"
 
 namespace sse {
@@ -25,49 +29,75 @@ constexpr int kSms = 152;
 // How the sum of squares of the norm after the block is shared.
 enum { kGroupNone, kGroupRow, kGroupShuffle, kGroupShared };
 
+// One 16-byte word of a row as float32 pairs.
 template <typename T> struct Row {
-    static constexpr int kE = 16 / sizeof(T);  // elements of one 16-byte word
-    static __device__ __forceinline__ uint4 load(const void *base, int64_t i) {
-        return *reinterpret_cast<const uint4 *>(static_cast<const T *>(base) + i);
-    }
-    static __device__ __forceinline__ void unpack(uint4 u, float *f) {
+    static constexpr int kE = 16 / sizeof(T);  // elements
+    static constexpr int kP = kE / 2;          // pairs
+    static __device__ __forceinline__ void unpack(uint4 u, F2 (&f)[kP]) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            if (sizeof(T) == 2)
-                f[i] = __uint_as_float(i & 1 ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+        for (int i = 0; i < kP; ++i) {
+            if constexpr (sizeof(T) == 2)
+                f[i] = f2_bits(w[i] << 16, w[i] & 0xffff0000u);
             else
-                f[i] = __uint_as_float(w[i]);
+                f[i] = f2_bits(w[2 * i], w[2 * i + 1]);
         }
     }
-    static __device__ __forceinline__ void store(void *base, int64_t i, const float *f) {
+    static __device__ __forceinline__ void store(void *base, int64_t i, const F2 (&f)[kP]) {
         uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (sizeof(T) == 2) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+        for (int k = 0; k < kP; ++k) {
+            const float2 v = f2_get(f[k]);
+            if constexpr (sizeof(T) == 2) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v.x, v.y);
                 w[k] = *reinterpret_cast<const uint32_t *>(&b);
             } else {
-                w[k] = __float_as_uint(f[k]);
+                w[2 * k] = __float_as_uint(v.x);
+                w[2 * k + 1] = __float_as_uint(v.y);
             }
         }
         *reinterpret_cast<uint4 *>(static_cast<T *>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
-// act(z); with GRAD also its derivative.
-template <bool GRAD> __device__ __forceinline__ float act(int gate, float z, float &d) {
-    if (gate == SSE_GATE_LINEAR) {
-        if (GRAD) d = 1.f;
-        return z;
+__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+
+// 1 / (1 + exp(-z))
+__device__ __forceinline__ F2 sigmoid2(F2 z) {
+    const float2 t = f2_get(mul2(z, both(-1.44269504f)));
+    float ex, ey, x, y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(t.y));
+    const float2 u = f2_get(add2(f2(ex, ey), both(1.f)));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(u.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(u.y));
+    return f2(x, y);
+}
+
+// act(z) of one word in the place of z, and with GRAD its derivative.
+template <bool GRAD, int P> __device__ __forceinline__ void act(int gate, F2 (&z)[P], F2 (&d)[P]) {
+    if (gate == SSE_GATE_SILU) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const F2 s = sigmoid2(z[i]);
+            if (GRAD) d[i] = mul2(s, fma2(z[i], fma2(s, both(-1.f), both(1.f)), both(1.f)));
+            z[i] = mul2(z[i], s);
+        }
+    } else if (gate == SSE_GATE_SIGMOID) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            z[i] = sigmoid2(z[i]);
+            if (GRAD) d[i] = mul2(z[i], fma2(z[i], both(-1.f), both(1.f)));
+        }
+    } else if (GRAD) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = both(1.f);
     }
-    const float s = __fdividef(1.f, 1.f + __expf(-z));
-    if (gate == SSE_GATE_SIGMOID) {
-        if (GRAD) d = s * (1.f - s);
-        return s;
-    }
-    if (GRAD) d = s * fmaf(z, 1.f - s, 1.f);
-    return z * s;
+}
+
+__device__ __forceinline__ float fold(F2 v) {
+    const float2 f = f2_get(v);
+    return f.x + f.y;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -79,20 +109,35 @@ __device__ __forceinline__ float warp_sum(float v) {
 // The team of one row: blockDim.x threads (whole warps), blockDim.y rows per
 // CTA.  Every thread of the CTA makes the same calls (they synchronize).
 struct Team {
-    float *warp_words;  // [2][rows][32]: this row's words, two buffers in turn
+    float *warp_words;  // [2][rows][2][32]: this row's words, two buffers in turn; zero behind the last warp
     float *vec_words;   // [rows][words of a row]: kGroupShared only
     int turn;
-    // Sum of one value per thread over the team.
-    __device__ __forceinline__ float row_sum(float v) {
-        v = warp_sum(v);
-        const int warps = blockDim.x >> 5;
-        if (warps == 1) return v;
-        float *w = warp_words + (turn * blockDim.y + threadIdx.y) * 32;
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) w[threadIdx.x >> 5] = v;
+    __device__ __forceinline__ void clear() {  // before the first sum
+        for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 4 * 32 * (int)blockDim.y; i += blockDim.x * blockDim.y)
+            warp_words[i] = 0.f;
         __syncthreads();
-        const int lane = threadIdx.x & 31;
-        return warp_sum(lane < warps ? w[lane] : 0.f);
+    }
+    __device__ __forceinline__ float gather(const float *w) const {
+        float s = 0.f;
+        for (int k = 0; k < (int)blockDim.x >> 5; k += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(w + k);
+            s += (v.x + v.y) + (v.z + v.w);
+        }
+        return s;
+    }
+    // Sums of N (1 or 2) values per thread over the team.
+    template <int N> __device__ __forceinline__ void row_sum(float (&v)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
+        if (blockDim.x == 32) return;
+        float *w = warp_words + (turn * blockDim.y + threadIdx.y) * 64;
+        turn ^= 1;
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int i = 0; i < N; ++i) w[i * 32 + (threadIdx.x >> 5)] = v[i];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = gather(w + i * 32);
     }
 };
 
@@ -104,9 +149,10 @@ __device__ __forceinline__ void group_sum(Team &tm, int mode, int gw, int nv, fl
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) s += v[i];
-        s = tm.row_sum(s);
+        float t[1] = {s};
+        tm.row_sum<1>(t);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) v[i] = s;
+        for (int i = 0; i < VPT; ++i) v[i] = t[0];
     } else if (mode == kGroupShuffle) {  // a power of two of neighbouring lanes
         for (int o = gw >> 1; o > 0; o >>= 1)
 #pragma unroll
@@ -136,175 +182,258 @@ __device__ __forceinline__ void group_sum(Team &tm, int mode, int gw, int nv, fl
 struct NormShape {
     int width, nv;       // columns and 16-byte words of a row
     int mode, gw;        // group mode, words of a group
+    int stages;          // rows of a thread's ring
     int gate;
     float eps, rs, bs;
     float inv_width, inv_group;
 };
 
-// coef = branch_scale c w_after of the thread's columns
+// A thread's ring of rows: `tensors` tensors x VPT words per row.  The slot of a
+// row is free again when its words have been taken to registers.
+template <typename T, int VPT> struct Ring {
+    uint32_t at;          // this thread's first word in shared memory
+    int words, stages;    // words of one stage in the CTA's ring, stages
+    int threads;
+    __device__ __forceinline__ Ring(const void *smem, int tensors, int n_stages) {
+        threads = blockDim.x * blockDim.y;
+        at = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
+        words = tensors * VPT * threads;
+        stages = n_stages;
+    }
+    __device__ __forceinline__ uint32_t slot(int stage, int tensor, int i) const {
+        return at + (stage * words + (tensor * VPT + i) * threads) * 16;
+    }
+    // Copies the thread's words of one tensor's row (zeros past its end).
+    __device__ __forceinline__ void fetch(int stage, int tensor, const void *base, int64_t first, int nv, bool live) const {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = threadIdx.x + i * blockDim.x;
+            const bool ok = live && j < nv;
+            const T *src = static_cast<const T *>(base) + (ok ? first + j * Row<T>::kE : 0);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot(stage, tensor, i)), "l"(src),
+                         "r"(ok ? 16 : 0) : "memory");
+        }
+    }
+    __device__ __forceinline__ uint4 take(int stage, int tensor, int i) const {
+        uint4 u;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot(stage, tensor, i)) : "memory");
+        return u;
+    }
+};
+__device__ __forceinline__ void fetches_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits for the oldest of `stages` groups.
+__device__ __forceinline__ void fetches_wait(int stages) {
+    if (stages == 3)
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (stages == 2)
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// coef = branch_scale c w_after of the thread's columns, and w_before
 template <typename T, int VPT>
-__device__ __forceinline__ void load_coef(const BlockNormArgs &a, const NormShape &n, float (&coef)[VPT][Row<T>::kE],
-                                          float (&wb)[VPT][Row<T>::kE]) {
-    constexpr int E = Row<T>::kE;
+__device__ __forceinline__ void load_coef(const BlockNormArgs &a, const NormShape &n, F2 (&coef)[VPT][Row<T>::kP],
+                                          F2 (&wb)[VPT][Row<T>::kP]) {
+    constexpr int E = Row<T>::kE, P = Row<T>::kP;
+    auto times = [](F2 (&c)[P], const float *w) {
+#pragma unroll
+        for (int k = 0; k < P; k += 2) {
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(w + 2 * k));
+            c[k] = mul2(c[k], f2(v.x, v.y));
+            c[k + 1] = mul2(c[k + 1], f2(v.z, v.w));
+        }
+    };
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            coef[i][e] = n.bs;
-            wb[i][e] = 0.f;
+        for (int k = 0; k < P; ++k) {
+            coef[i][k] = both(n.bs);
+            wb[i][k] = both(1.f);
         }
         if (j < n.nv) {
-#pragma unroll
-            for (int e = 0; e < E; e += 4) {
-                if (a.w_after) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(a.w_after + j * E + e));
-                    coef[i][e] *= w.x; coef[i][e + 1] *= w.y; coef[i][e + 2] *= w.z; coef[i][e + 3] *= w.w;
-                }
-                if (a.channel) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(a.channel + j * E + e));
-                    coef[i][e] *= w.x; coef[i][e + 1] *= w.y; coef[i][e + 2] *= w.z; coef[i][e + 3] *= w.w;
-                }
-                if (a.w_before) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(a.w_before + j * E + e));
-                    wb[i][e] = w.x; wb[i][e + 1] = w.y; wb[i][e + 2] = w.z; wb[i][e + 3] = w.w;
-                }
-            }
+            if (a.w_after) times(coef[i], a.w_after + j * E);
+            if (a.channel) times(coef[i], a.channel + j * E);
+            if (a.w_before) times(wb[i], a.w_before + j * E);
         }
     }
 }
 
-template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_forward_kernel(BlockNormArgs a, NormShape n) {
-    constexpr int E = Row<T>::kE;
-    extern __shared__ float smem[];
-    Team tm{smem, smem + 2 * blockDim.y * 32, 0};
-    float coef[VPT][E], wb[VPT][E];
+template <typename T, int VPT, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs a, NormShape n) {
+    constexpr int E = Row<T>::kE, P = Row<T>::kP;
+    extern __shared__ uint4 smem[];
+    const int has_o = a.o != nullptr, has_z = a.z != nullptr, has_r = a.r != nullptr;
+    const Ring<T, VPT> ring(smem, has_o + has_z + has_r, n.stages);
+    Team tm;
+    tm.warp_words = reinterpret_cast<float *>(smem + ring.words * n.stages);
+    tm.vec_words = tm.warp_words + 4 * 32 * blockDim.y;
+    tm.turn = 0;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y;
+    auto fetch = [&](int stage, int64_t row) {
+        const bool live = row < a.T;
+        if (has_o) ring.fetch(stage, 0, a.o, row * a.o_stride, n.nv, live);
+        if (has_z) ring.fetch(stage, has_o, a.z, row * a.z_stride, n.nv, live);
+        if (has_r) ring.fetch(stage, has_o + has_z, a.r, row * a.r_stride, n.nv, live);
+        fetches_commit();
+    };
+    for (int k = 0; k < n.stages; ++k) fetch(k, first + k * step + threadIdx.y);
+    F2 coef[VPT][P], wb[VPT][P];
     load_coef<T, VPT>(a, n, coef, wb);
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < a.T; base += step) {
+    tm.clear();
+    int stage = 0;
+    for (int64_t base = first; base < a.T; base += step) {
         const int64_t row = base + threadIdx.y;
         const bool live = row < a.T;
-        float u[VPT][E], z[VPT][E], r[VPT][E];
+        F2 u[VPT][P];
+        uint4 uz[VPT], ur[VPT];
+        fetches_wait(n.stages);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            uint4 uo = make_uint4(0, 0, 0, 0), uz = uo, ur = uo;
-            if (live && j < n.nv) {
-                if (a.o) uo = Row<T>::load(a.o, row * a.o_stride + j * E);
-                if (a.z) uz = Row<T>::load(a.z, row * a.z_stride + j * E);
-                if (a.r) ur = Row<T>::load(a.r, row * a.r_stride + j * E);
-            }
-            Row<T>::unpack(uo, u[i]);
-            Row<T>::unpack(uz, z[i]);
-            Row<T>::unpack(ur, r[i]);
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            Row<T>::unpack(has_o ? ring.take(stage, 0, i) : none, u[i]);
+            uz[i] = has_z ? ring.take(stage, has_o, i) : none;
+            ur[i] = has_r ? ring.take(stage, has_o + has_z, i) : none;
         }
+        fetch(stage, row + n.stages * step);
+        stage = stage + 1 == n.stages ? 0 : stage + 1;
         if (n.mode != kGroupNone) {
             float ss[VPT];
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                ss[i] = 0.f;
+                F2 t = both(0.f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) ss[i] = fmaf(u[i][e], u[i][e], ss[i]);
+                for (int k = 0; k < P; ++k) t = fma2(u[i][k], u[i][k], t);
+                ss[i] = fold(t);
             }
             group_sum<VPT>(tm, n.mode, n.gw, n.nv, ss);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const float rstd = rsqrtf(fmaf(ss[i], n.inv_group, n.eps));
+                const F2 rstd = both(rsqrtf(fmaf(ss[i], n.inv_group, n.eps)));
 #pragma unroll
-                for (int e = 0; e < E; ++e) u[i][e] *= rstd;
+                for (int k = 0; k < P; ++k) u[i][k] = mul2(u[i][k], rstd);
             }
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int j = threadIdx.x + i * blockDim.x;
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float d, v = coef[i][e] * u[i][e];
-                if (n.gate != SSE_GATE_NONE) v *= act<false>(n.gate, z[i][e], d);
-                u[i][e] = a.r ? (a.o ? fmaf(n.rs, r[i][e], v) : n.rs * r[i][e]) : v;
+            for (int k = 0; k < P; ++k) u[i][k] = mul2(u[i][k], coef[i][k]);
+            if (has_z) {
+                F2 z[P], none[P];
+                Row<T>::unpack(uz[i], z);
+                act<false>(n.gate, z, none);
+#pragma unroll
+                for (int k = 0; k < P; ++k) u[i][k] = mul2(u[i][k], z[k]);
+            }
+            if (has_r) {
+                F2 r[P];
+                Row<T>::unpack(ur[i], r);
+#pragma unroll
+                for (int k = 0; k < P; ++k)
+                    u[i][k] = has_o ? fma2(both(n.rs), r[k], u[i][k]) : mul2(both(n.rs), r[k]);
             }
             if (a.r_out && live && j < n.nv) Row<T>::store(a.r_out, row * n.width + j * E, u[i]);
         }
         if (a.next) {
-            float ss = 0.f;
+            F2 t = both(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < E; ++e) ss = fmaf(u[i][e], u[i][e], ss);
-            const float rstd = rsqrtf(fmaf(tm.row_sum(ss), n.inv_width, n.eps));
+                for (int k = 0; k < P; ++k) t = fma2(u[i][k], u[i][k], t);
+            float sum[1] = {fold(t)};
+            tm.row_sum<1>(sum);
+            const F2 rstd = both(rsqrtf(fmaf(sum[0], n.inv_width, n.eps)));
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const int j = threadIdx.x + i * blockDim.x;
 #pragma unroll
-                for (int e = 0; e < E; ++e) u[i][e] *= rstd * wb[i][e];
+                for (int k = 0; k < P; ++k) u[i][k] = mul2(mul2(u[i][k], rstd), wb[i][k]);
                 if (live && j < n.nv) Row<T>::store(a.next, row * n.width + j * E, u[i]);
             }
         }
     }
 }
 
-template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, NormShape n) {
-    constexpr int E = Row<T>::kE;
-    extern __shared__ float smem[];
-    Team tm{smem, smem + 2 * blockDim.y * 32, 0};
-    float coef[VPT][E], wb[VPT][E];
+template <typename T, int VPT, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) norm_backward_kernel(BlockNormArgs a, NormShape n) {
+    constexpr int E = Row<T>::kE, P = Row<T>::kP;
+    extern __shared__ uint4 smem[];
+    const int has_o = a.o != nullptr, has_z = a.z != nullptr, has_d = a.d_r_out != nullptr, has_n = a.d_next != nullptr;
+    const int at_z = has_o, at_d = has_o + has_z, at_n = at_d + has_d;  // the tensors' places in a stage
+    const Ring<T, VPT> ring(smem, at_n + 2 * has_n, n.stages);
+    Team tm;
+    tm.warp_words = reinterpret_cast<float *>(smem + ring.words * n.stages);
+    tm.vec_words = tm.warp_words + 4 * 32 * blockDim.y;
+    tm.turn = 0;
+    const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y;
+    auto fetch = [&](int stage, int64_t row) {
+        const bool live = row < a.T;
+        if (has_n) {
+            ring.fetch(stage, at_n, a.r, row * a.r_stride, n.nv, live);
+            ring.fetch(stage, at_n + 1, a.d_next, row * n.width, n.nv, live);
+        }
+        if (has_d) ring.fetch(stage, at_d, a.d_r_out, row * n.width, n.nv, live);
+        if (has_o) ring.fetch(stage, 0, a.o, row * a.o_stride, n.nv, live);
+        if (has_z) ring.fetch(stage, at_z, a.z, row * a.z_stride, n.nv, live);
+        fetches_commit();
+    };
+    for (int k = 0; k < n.stages; ++k) fetch(k, first + k * step + threadIdx.y);
+    F2 coef[VPT][P], wb[VPT][P];
     load_coef<T, VPT>(a, n, coef, wb);
-    float sum_c[VPT][E], sum_b[VPT][E];  // C_j and dw_before of the thread's columns
+    tm.clear();
+    F2 sum_c[VPT][P], sum_b[VPT][P];  // C_j and dw_before of the thread's columns
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum_c[i][e] = sum_b[i][e] = 0.f;
-    const int64_t step = (int64_t)gridDim.x * blockDim.y;
-    for (int64_t base = (int64_t)blockIdx.x * blockDim.y; base < a.T; base += step) {
+        for (int k = 0; k < P; ++k) sum_c[i][k] = sum_b[i][k] = both(0.f);
+    int stage = 0;
+    for (int64_t base = first; base < a.T; base += step) {
         const int64_t row = base + threadIdx.y;
         const bool live = row < a.T;
-        float d[VPT][E], o[VPT][E], z[VPT][E];
-        uint4 ur[VPT], un[VPT];
+        F2 d[VPT][P];
+        uint4 uo[VPT], uz[VPT], ur[VPT], un[VPT];
+        fetches_wait(n.stages);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            uint4 uo = make_uint4(0, 0, 0, 0), uz = uo, ud = uo;
-            ur[i] = un[i] = uo;
-            if (live && j < n.nv) {
-                if (a.o) uo = Row<T>::load(a.o, row * a.o_stride + j * E);
-                if (a.z) uz = Row<T>::load(a.z, row * a.z_stride + j * E);
-                if (a.d_r_out) ud = Row<T>::load(a.d_r_out, row * n.width + j * E);
-                if (a.d_next) {
-                    ur[i] = Row<T>::load(a.r, row * a.r_stride + j * E);
-                    un[i] = Row<T>::load(a.d_next, row * n.width + j * E);
-                }
-            }
-            Row<T>::unpack(uo, o[i]);
-            Row<T>::unpack(uz, z[i]);
-            Row<T>::unpack(ud, d[i]);
+            const uint4 none = make_uint4(0, 0, 0, 0);
+            uo[i] = has_o ? ring.take(stage, 0, i) : none;
+            uz[i] = has_z ? ring.take(stage, at_z, i) : none;
+            Row<T>::unpack(has_d ? ring.take(stage, at_d, i) : none, d[i]);
+            ur[i] = has_n ? ring.take(stage, at_n, i) : none;
+            un[i] = has_n ? ring.take(stage, at_n + 1, i) : none;
         }
-        if (a.d_next) {
-            float ss = 0.f, dot = 0.f;
+        fetch(stage, row + n.stages * step);
+        stage = stage + 1 == n.stages ? 0 : stage + 1;
+        if (has_n) {
+            F2 ss = both(0.f), dot = both(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                float r[E], g[E];
+                F2 r[P], g[P];
                 Row<T>::unpack(ur[i], r);
                 Row<T>::unpack(un[i], g);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    ss = fmaf(r[e], r[e], ss);
-                    dot = fmaf(g[e] * wb[i][e], r[e], dot);
+                for (int k = 0; k < P; ++k) {
+                    ss = fma2(r[k], r[k], ss);
+                    dot = fma2(mul2(g[k], wb[i][k]), r[k], dot);
                 }
             }
-            const float rstd = rsqrtf(fmaf(tm.row_sum(ss), n.inv_width, n.eps));
-            const float mean = tm.row_sum(dot) * rstd * n.inv_width;
+            float sums[2] = {fold(ss), fold(dot)};
+            tm.row_sum<2>(sums);
+            const float rstd = rsqrtf(fmaf(sums[0], n.inv_width, n.eps));
+            const F2 minus_mean = both(-(sums[1] * rstd * n.inv_width)), rr = both(rstd);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                float r[E], g[E];
+                F2 r[P], g[P];
                 Row<T>::unpack(ur[i], r);
                 Row<T>::unpack(un[i], g);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float hat = r[e] * rstd;
-                    sum_b[i][e] = fmaf(g[e], hat, sum_b[i][e]);
-                    d[i][e] = fmaf(rstd, fmaf(g[e], wb[i][e], -hat * mean), d[i][e]);
+                for (int k = 0; k < P; ++k) {
+                    const F2 hat = mul2(r[k], rr);
+                    sum_b[i][k] = fma2(g[k], hat, sum_b[i][k]);
+                    d[i][k] = fma2(rr, fma2(hat, minus_mean, mul2(g[k], wb[i][k])), d[i][k]);
                 }
             }
         }
@@ -312,22 +441,27 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
         for (int i = 0; i < VPT; ++i) {
             const int j = threadIdx.x + i * blockDim.x;
             if (a.d_r && live && j < n.nv) {
-                float v[E];
+                F2 v[P];
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[e] = n.rs * d[i][e];
+                for (int k = 0; k < P; ++k) v[k] = mul2(both(n.rs), d[i][k]);
                 Row<T>::store(a.d_r, row * n.width + j * E, v);
             }
         }
-        if (!a.o) continue;
+        if (!has_o) continue;
+        F2 o[VPT][P];
         float rstd[VPT], dot[VPT];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) rstd[i] = 1.f;
+        for (int i = 0; i < VPT; ++i) {
+            Row<T>::unpack(uo[i], o[i]);
+            rstd[i] = 1.f;
+        }
         if (n.mode != kGroupNone) {
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                rstd[i] = 0.f;
+                F2 t = both(0.f);
 #pragma unroll
-                for (int e = 0; e < E; ++e) rstd[i] = fmaf(o[i][e], o[i][e], rstd[i]);
+                for (int k = 0; k < P; ++k) t = fma2(o[i][k], o[i][k], t);
+                rstd[i] = fold(t);
             }
             group_sum<VPT>(tm, n.mode, n.gw, n.nv, rstd);
 #pragma unroll
@@ -336,28 +470,36 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int j = threadIdx.x + i * blockDim.x;
-            float dz[E];
-            dot[i] = 0.f;
+            F2 av[P], da[P];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float da = 0.f, av = 1.f;
-                o[i][e] *= rstd[i];
-                if (n.gate != SSE_GATE_NONE) av = act<true>(n.gate, z[i][e], da);
-                const float p = d[i][e] * coef[i][e];
-                sum_c[i][e] = fmaf(d[i][e] * av, o[i][e], sum_c[i][e]);
-                dz[e] = p * o[i][e] * da;
-                d[i][e] = p * av;
-                dot[i] = fmaf(d[i][e], o[i][e], dot[i]);
+            for (int k = 0; k < P; ++k) o[i][k] = mul2(o[i][k], both(rstd[i]));
+            if (has_z) {
+                Row<T>::unpack(uz[i], av);
+                act<true>(n.gate, av, da);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    da[k] = mul2(mul2(mul2(d[i][k], coef[i][k]), o[i][k]), da[k]);
+                    d[i][k] = mul2(d[i][k], av[k]);
+                }
+                if (live && j < n.nv) Row<T>::store(a.d_z, row * n.width + j * E, da);
             }
-            if (a.d_z && live && j < n.nv) Row<T>::store(a.d_z, row * n.width + j * E, dz);
+            F2 t = both(0.f);
+#pragma unroll
+            for (int k = 0; k < P; ++k) {
+                sum_c[i][k] = fma2(d[i][k], o[i][k], sum_c[i][k]);
+                d[i][k] = mul2(d[i][k], coef[i][k]);
+                t = fma2(d[i][k], o[i][k], t);
+            }
+            dot[i] = fold(t);
         }
         if (n.mode != kGroupNone) {
             group_sum<VPT>(tm, n.mode, n.gw, n.nv, dot);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i) {
+                const F2 minus_mean = both(-dot[i] * n.inv_group), rr = both(rstd[i]);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    d[i][e] = rstd[i] * fmaf(-o[i][e], dot[i] * n.inv_group, d[i][e]);
+                for (int k = 0; k < P; ++k) d[i][k] = mul2(rr, fma2(o[i][k], minus_mean, d[i][k]));
+            }
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
@@ -373,13 +515,11 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
         const int j = threadIdx.x + i * blockDim.x;
         if (j < n.nv) {
 #pragma unroll
-            for (int e = 0; e < E; e += 4) {
+            for (int k = 0; k < P; ++k) {
                 if (a.d_w_after || a.d_channel)
-                    *reinterpret_cast<float4 *>(a.partials + mine * n.width + j * E + e) =
-                        make_float4(sum_c[i][e], sum_c[i][e + 1], sum_c[i][e + 2], sum_c[i][e + 3]);
+                    *reinterpret_cast<float2 *>(a.partials + mine * n.width + j * E + 2 * k) = f2_get(sum_c[i][k]);
                 if (a.d_w_before)
-                    *reinterpret_cast<float4 *>(a.partials + (rows + mine) * n.width + j * E + e) =
-                        make_float4(sum_b[i][e], sum_b[i][e + 1], sum_b[i][e + 2], sum_b[i][e + 3]);
+                    *reinterpret_cast<float2 *>(a.partials + (rows + mine) * n.width + j * E + 2 * k) = f2_get(sum_b[i][k]);
             }
         }
     }
@@ -419,10 +559,11 @@ __global__ void __launch_bounds__(1024) norm_weight_grads_kernel(BlockNormArgs a
 struct NormPlan {
     NormShape n;
     int vpt, threads, rows;  // words per thread, threads of a row, rows per CTA
-    size_t smem;
+    int per_sm;              // CTAs on an SM
+    size_t team_bytes;       // shared memory of the sums
 };
 
-NormPlan plan_norm(const sse_norm_config_t &c, bool after) {
+NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
     NormPlan p{};
     const int E = c.dtype == SSE_BF16 ? 8 : 4;
     const int group = c.group ? c.group : c.width;
@@ -440,50 +581,61 @@ NormPlan plan_norm(const sse_norm_config_t &c, bool after) {
     p.vpt = p.n.nv > 1024 ? 2 : 1;
     p.threads = ((p.n.nv + p.vpt - 1) / p.vpt + 31) / 32 * 32;
     p.rows = p.threads >= 256 ? 1 : 256 / p.threads;
-    p.smem = sizeof(float) * (2 * 32 * p.rows + (p.n.mode == kGroupShared ? p.rows * p.n.nv : 0));
+    // registers: 64 per thread forward, 80 backward (64 above 512 threads)
+    const int most = backward ? 768 : 1024;
+    p.per_sm = most / (p.threads * p.rows);
+    if (p.per_sm < 1) p.per_sm = 1;
+    p.team_bytes = sizeof(float) * (4 * 32 * p.rows + (p.n.mode == kGroupShared ? p.rows * p.n.nv : 0));
     return p;
 }
 
 int norm_grid(const NormPlan &p, int64_t T) {
-    const int64_t need = (T + p.rows - 1) / p.rows;
-    const int64_t most = (int64_t)kSms * (p.threads * p.rows <= 256 ? 4 : p.threads <= 512 ? 2 : 1);
+    const int64_t need = (T + p.rows - 1) / p.rows, most = (int64_t)kSms * p.per_sm;
     return (int)(need < most ? need : most);
 }
 
-template <typename T, int VPT, int MAXT>
-cudaError_t launch_t(const NormPlan &p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    const dim3 block(p.threads, p.rows);
-    const int grid = norm_grid(p, a.T);
-    if (backward)
-        norm_backward_kernel<T, VPT, MAXT><<<grid, block, p.smem, stream>>>(a, p.n);
-    else
-        norm_forward_kernel<T, VPT, MAXT><<<grid, block, p.smem, stream>>>(a, p.n);
+template <typename T, int VPT, int MAXT, int FWD, int BWD>
+cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, int tensors, cudaStream_t stream) {
+    // three rows ahead where the SM's shared memory holds them, else two or one
+    const size_t row_bytes = (size_t)tensors * VPT * p.threads * p.rows * 16, room = size_t(220) * 1024 / p.per_sm;
+    p.n.stages = 3;
+    while (p.n.stages > 1 && p.n.stages * row_bytes + p.team_bytes > room) --p.n.stages;
+    const size_t smem = p.n.stages * row_bytes + p.team_bytes;
+    const auto kernel = backward ? norm_backward_kernel<T, VPT, MAXT, BWD> : norm_forward_kernel<T, VPT, MAXT, FWD>;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<norm_grid(p, a.T), dim3(p.threads, p.rows), smem, stream>>>(a, p.n);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_rows(const NormPlan &p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    if (p.vpt == 2) return launch_t<T, 2, 1024>(p, a, backward, stream);
-    if (p.threads * p.rows <= 256) return launch_t<T, 1, 256>(p, a, backward, stream);
-    if (p.threads <= 512) return launch_t<T, 1, 512>(p, a, backward, stream);
-    return launch_t<T, 1, 1024>(p, a, backward, stream);
+    const int tensors = (a.o != nullptr) + (a.z != nullptr) +
+                        (backward ? (a.d_r_out != nullptr) + 2 * (a.d_next != nullptr) : (a.r != nullptr));
+    if (p.vpt == 2) return launch_t<T, 2, 1024, 1, 1>(p, a, backward, tensors, stream);
+    if (p.threads * p.rows <= 256) return launch_t<T, 1, 256, 4, 3>(p, a, backward, tensors, stream);
+    if (p.threads <= 384) return launch_t<T, 1, 384, 2, 2>(p, a, backward, tensors, stream);
+    if (p.threads <= 512) return launch_t<T, 1, 512, 2, 1>(p, a, backward, tensors, stream);
+    return launch_t<T, 1, 1024, 1, 1>(p, a, backward, tensors, stream);
 }
 
 }  // namespace
 
 int64_t block_norm_partial_rows(const sse_norm_config_t &cfg, int64_t T) {
-    const NormPlan p = plan_norm(cfg, true);
+    const NormPlan p = plan_norm(cfg, true, true);
     return (int64_t)norm_grid(p, T) * p.rows;
 }
 
 cudaError_t launch_block_norm(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream) {
-    const NormPlan p = plan_norm(cfg, a.w_after != nullptr);
+    const NormPlan p = plan_norm(cfg, a.w_after != nullptr, false);
     return cfg.dtype == SSE_BF16 ? launch_rows<__nv_bfloat16>(p, a, false, stream)
                                  : launch_rows<float>(p, a, false, stream);
 }
 
 cudaError_t launch_block_norm_backward(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream) {
-    const NormPlan p = plan_norm(cfg, a.w_after != nullptr);
+    const NormPlan p = plan_norm(cfg, a.w_after != nullptr, true);
     if (a.T > 0) {
         const cudaError_t e = cfg.dtype == SSE_BF16 ? launch_rows<__nv_bfloat16>(p, a, true, stream)
                                                     : launch_rows<float>(p, a, true, stream);
