@@ -43,7 +43,7 @@ template <typename T> struct Row {
                 f[i] = f2_bits(w[2 * i], w[2 * i + 1]);
         }
     }
-    static __device__ __forceinline__ void store(void *base, int64_t i, const F2 (&f)[kP]) {
+    static __device__ __forceinline__ void store(char *at, const F2 (&f)[kP]) {
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < kP; ++k) {
@@ -56,7 +56,7 @@ template <typename T> struct Row {
                 w[2 * k + 1] = __float_as_uint(v.y);
             }
         }
-        *reinterpret_cast<uint4 *>(static_cast<T *>(base) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4 *>(at) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
@@ -95,6 +95,11 @@ template <bool GRAD, int P> __device__ __forceinline__ void act(int gate, F2 (&z
     }
 }
 
+__device__ __forceinline__ float rsqrt_ftz(float x) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float fold(F2 v) {
     const float2 f = f2_get(v);
     return f.x + f.y;
@@ -112,7 +117,10 @@ struct Team {
     float *warp_words;  // [2][rows][2][32]: this row's words, two buffers in turn; zero behind the last warp
     float *vec_words;   // [rows][words of a row]: kGroupShared only
     int turn;
-    __device__ __forceinline__ void clear() {  // before the first sum
+    __device__ __forceinline__ Team(uint4 *smem, uint32_t sums_at, uint32_t words_at) {
+        warp_words = reinterpret_cast<float *>(reinterpret_cast<char *>(smem) + sums_at);
+        vec_words = reinterpret_cast<float *>(reinterpret_cast<char *>(smem) + words_at);
+        turn = 0;
         for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 4 * 32 * (int)blockDim.y; i += blockDim.x * blockDim.y)
             warp_words[i] = 0.f;
         __syncthreads();
@@ -154,9 +162,11 @@ __device__ __forceinline__ void group_sum(Team &tm, int mode, int gw, int nv, fl
 #pragma unroll
         for (int i = 0; i < VPT; ++i) v[i] = t[0];
     } else if (mode == kGroupShuffle) {  // a power of two of neighbouring lanes
-        for (int o = gw >> 1; o > 0; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        for (int o = 16; o > 0; o >>= 1)
+            if (o < gw)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
     } else {
         float *w = tm.vec_words + threadIdx.y * nv;
         __syncthreads();  // the sums of the call before have been read
@@ -182,46 +192,71 @@ __device__ __forceinline__ void group_sum(Team &tm, int mode, int gw, int nv, fl
 struct NormShape {
     int width, nv;       // columns and 16-byte words of a row
     int mode, gw;        // group mode, words of a group
-    int stages;          // rows of a thread's ring
+    // The launch's layout, here so that it takes no registers.
+    int stages;                                // rows of a thread's ring
+    uint32_t word, stage_bytes, vec;           // bytes between a thread's words in the ring, between stages, in a row
+    uint32_t coef_at, sums_at, words_at;       // shared memory: coefficients, Team's words
+    int64_t stride[5], packed;                 // bytes of a row in each fetched tensor and in a packed one
     int gate;
     float eps, rs, bs;
     float inv_width, inv_group;
 };
 
-// A thread's ring of rows: `tensors` tensors x VPT words per row.  The slot of a
-// row is free again when its words have been taken to registers.
-template <typename T, int VPT> struct Ring {
-    uint32_t at;          // this thread's first word in shared memory
-    int words, stages;    // words of one stage in the CTA's ring, stages
-    int threads;
-    __device__ __forceinline__ Ring(const void *smem, int tensors, int n_stages) {
-        threads = blockDim.x * blockDim.y;
+// A thread's ring of rows: TENSORS x VPT words per row, each thread's own.  The
+// slot of a row is free again when its words have been taken to registers.
+// Words past the row's end, rows past the last one and absent tensors read as
+// zeros.
+template <int TENSORS, int VPT> struct Ring {
+    uint32_t at;  // this thread's first word
+    const void *const (&base)[TENSORS];  // null: absent
+
+    __device__ __forceinline__ Ring(const NormShape &n, const void *const (&tensors)[TENSORS]) : base(tensors) {
+        extern __shared__ uint4 smem[];
         at = (uint32_t)__cvta_generic_to_shared(smem) + (threadIdx.y * blockDim.x + threadIdx.x) * 16;
-        words = tensors * VPT * threads;
-        stages = n_stages;
-    }
-    __device__ __forceinline__ uint32_t slot(int stage, int tensor, int i) const {
-        return at + (stage * words + (tensor * VPT + i) * threads) * 16;
-    }
-    // Copies the thread's words of one tensor's row (zeros past its end).
-    __device__ __forceinline__ void fetch(int stage, int tensor, const void *base, int64_t first, int nv, bool live) const {
+        for (int s = 0; s < n.stages; ++s)  // the words that no fetch writes
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            const bool ok = live && j < nv;
-            const T *src = static_cast<const T *>(base) + (ok ? first + j * Row<T>::kE : 0);
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot(stage, tensor, i)), "l"(src),
-                         "r"(ok ? 16 : 0) : "memory");
-        }
+            for (int t = 0; t < TENSORS; ++t)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (!base[t] || !col_ok(n, i)) clear(at + s * n.stage_bytes + (t * VPT + i) * n.word);
     }
-    __device__ __forceinline__ uint4 take(int stage, int tensor, int i) const {
+    static __device__ __forceinline__ bool col_ok(const NormShape &n, int i) {
+        return (int)threadIdx.x + i * (int)blockDim.x < n.nv;
+    }
+    static __device__ __forceinline__ void clear(uint32_t dst) {
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+    }
+    __device__ __forceinline__ void fetch(const NormShape &n, int stage, int64_t row, bool row_ok) {
+        const uint32_t dst = at + stage * n.stage_bytes;
+#pragma unroll
+        for (int t = 0; t < TENSORS; ++t) {
+            if (!base[t]) continue;
+            if (row_ok) {
+                const char *src = static_cast<const char *>(base[t]) + row * n.stride[t] + threadIdx.x * 16;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i)
+                    if (col_ok(n, i))
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (t * VPT + i) * n.word),
+                                     "l"(src + i * n.vec) : "memory");
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) clear(dst + (t * VPT + i) * n.word);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ uint4 take(const NormShape &n, int stage, int t, int i) const {
         uint4 u;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(slot(stage, tensor, i)) : "memory");
+                     : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "r"(at + stage * n.stage_bytes + (t * VPT + i) * n.word) : "memory");
         return u;
     }
 };
-__device__ __forceinline__ void fetches_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// This thread's word of a row of a packed output.
+__device__ __forceinline__ char *word_of(void *base, const NormShape &n, int64_t row, int i) {
+    return static_cast<char *>(base) + row * n.packed + threadIdx.x * 16 + i * n.vec;
+}
 // Waits for the oldest of `stages` groups.
 __device__ __forceinline__ void fetches_wait(int stages) {
     if (stages == 3)
@@ -263,41 +298,33 @@ __device__ __forceinline__ void load_coef(const BlockNormArgs &a, const NormShap
 
 template <typename T, int VPT, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs a, NormShape n) {
-    constexpr int E = Row<T>::kE, P = Row<T>::kP;
+    constexpr int P = Row<T>::kP;
     extern __shared__ uint4 smem[];
-    const int has_o = a.o != nullptr, has_z = a.z != nullptr, has_r = a.r != nullptr;
-    const Ring<T, VPT> ring(smem, has_o + has_z + has_r, n.stages);
-    Team tm;
-    tm.warp_words = reinterpret_cast<float *>(smem + ring.words * n.stages);
-    tm.vec_words = tm.warp_words + 4 * 32 * blockDim.y;
-    tm.turn = 0;
-    const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y;
-    auto fetch = [&](int stage, int64_t row) {
-        const bool live = row < a.T;
-        if (has_o) ring.fetch(stage, 0, a.o, row * a.o_stride, n.nv, live);
-        if (has_z) ring.fetch(stage, has_o, a.z, row * a.z_stride, n.nv, live);
-        if (has_r) ring.fetch(stage, has_o + has_z, a.r, row * a.r_stride, n.nv, live);
-        fetches_commit();
-    };
-    for (int k = 0; k < n.stages; ++k) fetch(k, first + k * step + threadIdx.y);
+    const bool has_o = a.o != nullptr, has_z = a.z != nullptr, has_r = a.r != nullptr;
+    const int64_t on = (int64_t)gridDim.x * blockDim.y, row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    // rows of this team, and of the CTA's first (the others have as many or one less)
+    const int mine = row0 < a.T ? (int)((a.T - 1 - row0) / on) + 1 : 0;
+    const int most = (int)((a.T - 1 - (int64_t)blockIdx.x * blockDim.y) / on) + 1;
+    const void *const tensors[3] = {a.o, a.z, a.r};
+    Ring<3, VPT> ring(n, tensors);
+    for (int k = 0; k < n.stages; ++k) ring.fetch(n, k, row0 + k * on, k < mine);
     F2 coef[VPT][P], wb[VPT][P];
     load_coef<T, VPT>(a, n, coef, wb);
-    tm.clear();
+    Team tm(smem, n.sums_at, n.words_at);
     int stage = 0;
-    for (int64_t base = first; base < a.T; base += step) {
-        const int64_t row = base + threadIdx.y;
-        const bool live = row < a.T;
+    int64_t row = row0;
+    for (int k = 0; k < most; ++k, row += on) {
+        const bool live = k < mine;
         F2 u[VPT][P];
         uint4 uz[VPT], ur[VPT];
         fetches_wait(n.stages);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const uint4 none = make_uint4(0, 0, 0, 0);
-            Row<T>::unpack(has_o ? ring.take(stage, 0, i) : none, u[i]);
-            uz[i] = has_z ? ring.take(stage, has_o, i) : none;
-            ur[i] = has_r ? ring.take(stage, has_o + has_z, i) : none;
+            Row<T>::unpack(ring.take(n, stage, 0, i), u[i]);
+            uz[i] = ring.take(n, stage, 1, i);
+            ur[i] = ring.take(n, stage, 2, i);
         }
-        fetch(stage, row + n.stages * step);
+        ring.fetch(n, stage, row + n.stages * on, k + n.stages < mine);
         stage = stage + 1 == n.stages ? 0 : stage + 1;
         if (n.mode != kGroupNone) {
             float ss[VPT];
@@ -311,14 +338,13 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs 
             group_sum<VPT>(tm, n.mode, n.gw, n.nv, ss);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const F2 rstd = both(rsqrtf(fmaf(ss[i], n.inv_group, n.eps)));
+                const F2 rstd = both(rsqrt_ftz(fmaf(ss[i], n.inv_group, n.eps)));
 #pragma unroll
                 for (int k = 0; k < P; ++k) u[i][k] = mul2(u[i][k], rstd);
             }
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
 #pragma unroll
             for (int k = 0; k < P; ++k) u[i][k] = mul2(u[i][k], coef[i][k]);
             if (has_z) {
@@ -335,7 +361,8 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs 
                 for (int k = 0; k < P; ++k)
                     u[i][k] = has_o ? fma2(both(n.rs), r[k], u[i][k]) : mul2(both(n.rs), r[k]);
             }
-            if (a.r_out && live && j < n.nv) Row<T>::store(a.r_out, row * n.width + j * E, u[i]);
+            if (a.r_out && live && ring.col_ok(n, i))
+                Row<T>::store(word_of(a.r_out, n, row, i), u[i]);
         }
         if (a.next) {
             F2 t = both(0.f);
@@ -345,171 +372,205 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs 
                 for (int k = 0; k < P; ++k) t = fma2(u[i][k], u[i][k], t);
             float sum[1] = {fold(t)};
             tm.row_sum<1>(sum);
-            const F2 rstd = both(rsqrtf(fmaf(sum[0], n.inv_width, n.eps)));
+            const F2 rstd = both(rsqrt_ftz(fmaf(sum[0], n.inv_width, n.eps)));
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                const int j = threadIdx.x + i * blockDim.x;
 #pragma unroll
                 for (int k = 0; k < P; ++k) u[i][k] = mul2(mul2(u[i][k], rstd), wb[i][k]);
-                if (live && j < n.nv) Row<T>::store(a.next, row * n.width + j * E, u[i]);
+                if (live && ring.col_ok(n, i)) Row<T>::store(word_of(a.next, n, row, i), u[i]);
             }
         }
     }
 }
 
+// The backward's coefficients: registers hold the column sums instead.  One word
+// per thread: both vectors in shared memory, a word's 16-byte pieces nv apart (no
+// bank conflicts).  Two words per thread: there is no room beside the ring, and
+// they are read from global memory.
+template <typename T, int VPT> struct Coefs {
+    static constexpr int E = Row<T>::kE, P = Row<T>::kP;
+    const float4 *smem;  // [2][E / 4][nv]: coef, w_before
+    int nv;
+    __device__ __forceinline__ void fill(const BlockNormArgs &a, const NormShape &n, float4 *at) {
+        smem = at;
+        nv = n.nv;
+        if (VPT > 1) return;
+        const int threads = blockDim.x * blockDim.y;
+        for (int q = threadIdx.y * blockDim.x + threadIdx.x; q < n.nv * (E / 4); q += threads) {
+            const int j = q / (E / 4), h = q % (E / 4);
+            float4 c, b;
+            load(a, n, j, h, c, b);
+            at[h * n.nv + j] = c;
+            at[(E / 4 + h) * n.nv + j] = b;
+        }
+    }
+    static __device__ __forceinline__ void load(const BlockNormArgs &a, const NormShape &n, int j, int h, float4 &c,
+                                                float4 &b) {
+        const int at = j * E + 4 * h;
+        c = make_float4(n.bs, n.bs, n.bs, n.bs);
+        b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.w_after) {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(a.w_after + at));
+            c.x *= w.x; c.y *= w.y; c.z *= w.z; c.w *= w.w;
+        }
+        if (a.channel) {
+            const float4 w = __ldg(reinterpret_cast<const float4 *>(a.channel + at));
+            c.x *= w.x; c.y *= w.y; c.z *= w.z; c.w *= w.w;
+        }
+        if (a.w_before) b = __ldg(reinterpret_cast<const float4 *>(a.w_before + at));
+    }
+    // which: 0 coef, 1 w_before
+    __device__ __forceinline__ void get(const BlockNormArgs &a, const NormShape &n, int which, int j, F2 (&f)[P]) const {
+        if (j >= nv) j = nv - 1;  // a word past the row meets zeros
+#pragma unroll
+        for (int h = 0; h < E / 4; ++h) {
+            float4 v;
+            if constexpr (VPT == 1) {
+                v = smem[(which * (E / 4) + h) * nv + j];
+            } else {
+                float4 c, b;
+                load(a, n, j, h, c, b);
+                v = which ? b : c;
+            }
+            f[2 * h] = f2(v.x, v.y);
+            f[2 * h + 1] = f2(v.z, v.w);
+        }
+    }
+};
+
 template <typename T, int VPT, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) norm_backward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int E = Row<T>::kE, P = Row<T>::kP;
     extern __shared__ uint4 smem[];
-    const int has_o = a.o != nullptr, has_z = a.z != nullptr, has_d = a.d_r_out != nullptr, has_n = a.d_next != nullptr;
-    const int at_z = has_o, at_d = has_o + has_z, at_n = at_d + has_d;  // the tensors' places in a stage
-    const Ring<T, VPT> ring(smem, at_n + 2 * has_n, n.stages);
-    Team tm;
-    tm.warp_words = reinterpret_cast<float *>(smem + ring.words * n.stages);
-    tm.vec_words = tm.warp_words + 4 * 32 * blockDim.y;
-    tm.turn = 0;
-    const int64_t step = (int64_t)gridDim.x * blockDim.y, first = (int64_t)blockIdx.x * blockDim.y;
-    auto fetch = [&](int stage, int64_t row) {
-        const bool live = row < a.T;
-        if (has_n) {
-            ring.fetch(stage, at_n, a.r, row * a.r_stride, n.nv, live);
-            ring.fetch(stage, at_n + 1, a.d_next, row * n.width, n.nv, live);
-        }
-        if (has_d) ring.fetch(stage, at_d, a.d_r_out, row * n.width, n.nv, live);
-        if (has_o) ring.fetch(stage, 0, a.o, row * a.o_stride, n.nv, live);
-        if (has_z) ring.fetch(stage, at_z, a.z, row * a.z_stride, n.nv, live);
-        fetches_commit();
-    };
-    for (int k = 0; k < n.stages; ++k) fetch(k, first + k * step + threadIdx.y);
-    F2 coef[VPT][P], wb[VPT][P];
-    load_coef<T, VPT>(a, n, coef, wb);
-    tm.clear();
+    const bool has_o = a.o != nullptr, has_z = a.z != nullptr, has_n = a.d_next != nullptr;
+    const int64_t on = (int64_t)gridDim.x * blockDim.y, row0 = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    // rows of this team, and of the CTA's first (the others have as many or one less)
+    const int mine = row0 < a.T ? (int)((a.T - 1 - row0) / on) + 1 : 0;
+    const int most = (int)((a.T - 1 - (int64_t)blockIdx.x * blockDim.y) / on) + 1;
+    const void *const tensors[5] = {a.o, a.z, a.d_r_out, has_n ? a.r : nullptr, a.d_next};
+    Ring<5, VPT> ring(n, tensors);
+    for (int k = 0; k < n.stages; ++k) ring.fetch(n, k, row0 + k * on, k < mine);
+    Coefs<T, VPT> co;
+    co.fill(a, n, reinterpret_cast<float4 *>(reinterpret_cast<char *>(smem) + n.coef_at));
+    Team tm(smem, n.sums_at, n.words_at);
     F2 sum_c[VPT][P], sum_b[VPT][P];  // C_j and dw_before of the thread's columns
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
         for (int k = 0; k < P; ++k) sum_c[i][k] = sum_b[i][k] = both(0.f);
     int stage = 0;
-    for (int64_t base = first; base < a.T; base += step) {
-        const int64_t row = base + threadIdx.y;
-        const bool live = row < a.T;
+    int64_t row = row0;
+    for (int k = 0; k < most; ++k, row += on) {
+        const bool live = k < mine;
         F2 d[VPT][P];
-        uint4 uo[VPT], uz[VPT], ur[VPT], un[VPT];
         fetches_wait(n.stages);
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const uint4 none = make_uint4(0, 0, 0, 0);
-            uo[i] = has_o ? ring.take(stage, 0, i) : none;
-            uz[i] = has_z ? ring.take(stage, at_z, i) : none;
-            Row<T>::unpack(has_d ? ring.take(stage, at_d, i) : none, d[i]);
-            ur[i] = has_n ? ring.take(stage, at_n, i) : none;
-            un[i] = has_n ? ring.take(stage, at_n + 1, i) : none;
-        }
-        fetch(stage, row + n.stages * step);
-        stage = stage + 1 == n.stages ? 0 : stage + 1;
+        float rstd_row = 0.f, minus_mean = 0.f;
         if (has_n) {
             F2 ss = both(0.f), dot = both(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
-                F2 r[P], g[P];
-                Row<T>::unpack(ur[i], r);
-                Row<T>::unpack(un[i], g);
+                F2 r[P], g[P], w[P];
+                Row<T>::unpack(ring.take(n, stage, 3, i), r);
+                Row<T>::unpack(ring.take(n, stage, 4, i), g);
+                co.get(a, n, 1, threadIdx.x + i * blockDim.x, w);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
                     ss = fma2(r[k], r[k], ss);
-                    dot = fma2(mul2(g[k], wb[i][k]), r[k], dot);
+                    dot = fma2(mul2(g[k], w[k]), r[k], dot);
                 }
             }
             float sums[2] = {fold(ss), fold(dot)};
             tm.row_sum<2>(sums);
-            const float rstd = rsqrtf(fmaf(sums[0], n.inv_width, n.eps));
-            const F2 minus_mean = both(-(sums[1] * rstd * n.inv_width)), rr = both(rstd);
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                F2 r[P], g[P];
-                Row<T>::unpack(ur[i], r);
-                Row<T>::unpack(un[i], g);
-#pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    const F2 hat = mul2(r[k], rr);
-                    sum_b[i][k] = fma2(g[k], hat, sum_b[i][k]);
-                    d[i][k] = fma2(rr, fma2(hat, minus_mean, mul2(g[k], wb[i][k])), d[i][k]);
-                }
-            }
+            rstd_row = rsqrt_ftz(fmaf(sums[0], n.inv_width, n.eps));
+            minus_mean = -(sums[1] * rstd_row * n.inv_width);
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            if (a.d_r && live && j < n.nv) {
+            Row<T>::unpack(ring.take(n, stage, 2, i), d[i]);
+            if (has_n) {
+                F2 r[P], g[P], w[P];
+                Row<T>::unpack(ring.take(n, stage, 3, i), r);
+                Row<T>::unpack(ring.take(n, stage, 4, i), g);
+                co.get(a, n, 1, threadIdx.x + i * blockDim.x, w);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    const F2 hat = mul2(r[k], both(rstd_row));
+                    sum_b[i][k] = fma2(g[k], hat, sum_b[i][k]);
+                    d[i][k] = fma2(both(rstd_row), fma2(hat, both(minus_mean), mul2(g[k], w[k])), d[i][k]);
+                }
+            }
+            if (a.d_r && live && ring.col_ok(n, i)) {
                 F2 v[P];
 #pragma unroll
                 for (int k = 0; k < P; ++k) v[k] = mul2(both(n.rs), d[i][k]);
-                Row<T>::store(a.d_r, row * n.width + j * E, v);
+                Row<T>::store(word_of(a.d_r, n, row, i), v);
             }
         }
-        if (!has_o) continue;
-        F2 o[VPT][P];
-        float rstd[VPT], dot[VPT];
+        if (has_o) {
+            float rstd[VPT], dot[VPT];
+            if (n.mode != kGroupNone) {
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            Row<T>::unpack(uo[i], o[i]);
-            rstd[i] = 1.f;
-        }
-        if (n.mode != kGroupNone) {
+                for (int i = 0; i < VPT; ++i) {
+                    F2 o[P], t = both(0.f);
+                    Row<T>::unpack(ring.take(n, stage, 0, i), o);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) t = fma2(o[k], o[k], t);
+                    rstd[i] = fold(t);
+                }
+                group_sum<VPT>(tm, n.mode, n.gw, n.nv, rstd);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) rstd[i] = rsqrt_ftz(fmaf(rstd[i], n.inv_group, n.eps));
+            } else {
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) rstd[i] = 1.f;
+            }
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
+                F2 o[P], c[P];
+                Row<T>::unpack(ring.take(n, stage, 0, i), o);
+                co.get(a, n, 0, threadIdx.x + i * blockDim.x, c);
+#pragma unroll
+                for (int k = 0; k < P; ++k) o[k] = mul2(o[k], both(rstd[i]));
+                if (has_z) {
+                    F2 av[P], da[P];
+                    Row<T>::unpack(ring.take(n, stage, 1, i), av);
+                    act<true>(n.gate, av, da);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        da[k] = mul2(mul2(mul2(d[i][k], c[k]), o[k]), da[k]);
+                        d[i][k] = mul2(d[i][k], av[k]);
+                    }
+                    if (live && ring.col_ok(n, i)) Row<T>::store(word_of(a.d_z, n, row, i), da);
+                }
                 F2 t = both(0.f);
 #pragma unroll
-                for (int k = 0; k < P; ++k) t = fma2(o[i][k], o[i][k], t);
-                rstd[i] = fold(t);
-            }
-            group_sum<VPT>(tm, n.mode, n.gw, n.nv, rstd);
-#pragma unroll
-            for (int i = 0; i < VPT; ++i) rstd[i] = rsqrtf(fmaf(rstd[i], n.inv_group, n.eps));
-        }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            F2 av[P], da[P];
-#pragma unroll
-            for (int k = 0; k < P; ++k) o[i][k] = mul2(o[i][k], both(rstd[i]));
-            if (has_z) {
-                Row<T>::unpack(uz[i], av);
-                act<true>(n.gate, av, da);
-#pragma unroll
                 for (int k = 0; k < P; ++k) {
-                    da[k] = mul2(mul2(mul2(d[i][k], coef[i][k]), o[i][k]), da[k]);
-                    d[i][k] = mul2(d[i][k], av[k]);
+                    sum_c[i][k] = fma2(d[i][k], o[k], sum_c[i][k]);
+                    d[i][k] = mul2(d[i][k], c[k]);
+                    t = fma2(d[i][k], o[k], t);
                 }
-                if (live && j < n.nv) Row<T>::store(a.d_z, row * n.width + j * E, da);
+                dot[i] = fold(t);
             }
-            F2 t = both(0.f);
+            if (n.mode != kGroupNone) {
+                group_sum<VPT>(tm, n.mode, n.gw, n.nv, dot);
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                sum_c[i][k] = fma2(d[i][k], o[i][k], sum_c[i][k]);
-                d[i][k] = mul2(d[i][k], coef[i][k]);
-                t = fma2(d[i][k], o[i][k], t);
+                for (int i = 0; i < VPT; ++i) {
+                    // d = rstd (d - o_hat mean), o_hat = o rstd
+                    const F2 f = both(-dot[i] * n.inv_group * rstd[i]);
+                    F2 o[P];
+                    Row<T>::unpack(ring.take(n, stage, 0, i), o);
+#pragma unroll
+                    for (int k = 0; k < P; ++k) d[i][k] = mul2(both(rstd[i]), fma2(o[k], f, d[i][k]));
+                }
             }
-            dot[i] = fold(t);
-        }
-        if (n.mode != kGroupNone) {
-            group_sum<VPT>(tm, n.mode, n.gw, n.nv, dot);
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const F2 minus_mean = both(-dot[i] * n.inv_group), rr = both(rstd[i]);
-#pragma unroll
-                for (int k = 0; k < P; ++k) d[i][k] = mul2(rr, fma2(o[i][k], minus_mean, d[i][k]));
-            }
+            for (int i = 0; i < VPT; ++i)
+                if (live && ring.col_ok(n, i)) Row<T>::store(word_of(a.d_o, n, row, i), d[i]);
         }
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int j = threadIdx.x + i * blockDim.x;
-            if (live && j < n.nv) Row<T>::store(a.d_o, row * n.width + j * E, d[i]);
-        }
+        ring.fetch(n, stage, row + n.stages * on, k + n.stages < mine);
+        stage = stage + 1 == n.stages ? 0 : stage + 1;
     }
     // column sums of this team: one partial row of each
-    const int64_t rows = (int64_t)gridDim.x * blockDim.y;
-    const int64_t mine = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int j = threadIdx.x + i * blockDim.x;
@@ -517,9 +578,9 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward_kernel(BlockNormArgs
 #pragma unroll
             for (int k = 0; k < P; ++k) {
                 if (a.d_w_after || a.d_channel)
-                    *reinterpret_cast<float2 *>(a.partials + mine * n.width + j * E + 2 * k) = f2_get(sum_c[i][k]);
+                    *reinterpret_cast<float2 *>(a.partials + row0 * n.width + j * E + 2 * k) = f2_get(sum_c[i][k]);
                 if (a.d_w_before)
-                    *reinterpret_cast<float2 *>(a.partials + (rows + mine) * n.width + j * E + 2 * k) = f2_get(sum_b[i][k]);
+                    *reinterpret_cast<float2 *>(a.partials + (on + row0) * n.width + j * E + 2 * k) = f2_get(sum_b[i][k]);
             }
         }
     }
@@ -560,7 +621,7 @@ struct NormPlan {
     NormShape n;
     int vpt, threads, rows;  // words per thread, threads of a row, rows per CTA
     int per_sm;              // CTAs on an SM
-    size_t team_bytes;       // shared memory of the sums
+    size_t team_bytes;       // shared memory of the sums and the backward's coefficients
 };
 
 NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
@@ -581,11 +642,12 @@ NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
     p.vpt = p.n.nv > 1024 ? 2 : 1;
     p.threads = ((p.n.nv + p.vpt - 1) / p.vpt + 31) / 32 * 32;
     p.rows = p.threads >= 256 ? 1 : 256 / p.threads;
-    // registers: 64 per thread forward, 80 backward (64 above 512 threads)
-    const int most = backward ? 768 : 1024;
+    // registers: 64 per thread forward, 96 to 128 backward (64 above 512 threads)
+    const int most = backward ? 576 : 1024;
     p.per_sm = most / (p.threads * p.rows);
     if (p.per_sm < 1) p.per_sm = 1;
-    p.team_bytes = sizeof(float) * (4 * 32 * p.rows + (p.n.mode == kGroupShared ? p.rows * p.n.nv : 0));
+    p.team_bytes = sizeof(float) * (4 * 32 * p.rows + (p.n.mode == kGroupShared ? p.rows * p.n.nv : 0)) +
+                   (backward && p.vpt == 1 ? size_t(2) * c.width * sizeof(float) : 0);
     return p;
 }
 
@@ -595,9 +657,9 @@ int norm_grid(const NormPlan &p, int64_t T) {
 }
 
 template <typename T, int VPT, int MAXT, int FWD, int BWD>
-cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, int tensors, cudaStream_t stream) {
+cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
     // three rows ahead where the SM's shared memory holds them, else two or one
-    const size_t row_bytes = (size_t)tensors * VPT * p.threads * p.rows * 16, room = size_t(220) * 1024 / p.per_sm;
+    const size_t row_bytes = size_t(backward ? 5 : 3) * VPT * p.threads * p.rows * 16, room = size_t(220) * 1024 / p.per_sm;
     p.n.stages = 3;
     while (p.n.stages > 1 && p.n.stages * row_bytes + p.team_bytes > room) --p.n.stages;
     const size_t smem = p.n.stages * row_bytes + p.team_bytes;
@@ -606,19 +668,26 @@ cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, int tens
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
+    const int64_t width = p.n.width, strides[5] = {a.o_stride, a.z_stride, backward ? width : a.r_stride, a.r_stride, width};
+    for (int t = 0; t < 5; ++t) p.n.stride[t] = strides[t] * (int64_t)sizeof(T);
+    p.n.packed = width * (int64_t)sizeof(T);
+    p.n.word = p.threads * p.rows * 16;
+    p.n.stage_bytes = (uint32_t)row_bytes;
+    p.n.vec = p.threads * 16;
+    p.n.coef_at = (uint32_t)(p.n.stages * row_bytes);
+    p.n.sums_at = p.n.coef_at + (backward && VPT == 1 ? 2 * p.n.width * (uint32_t)sizeof(float) : 0);
+    p.n.words_at = p.n.sums_at + 4 * 32 * p.rows * (uint32_t)sizeof(float);
     kernel<<<norm_grid(p, a.T), dim3(p.threads, p.rows), smem, stream>>>(a, p.n);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_rows(const NormPlan &p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    const int tensors = (a.o != nullptr) + (a.z != nullptr) +
-                        (backward ? (a.d_r_out != nullptr) + 2 * (a.d_next != nullptr) : (a.r != nullptr));
-    if (p.vpt == 2) return launch_t<T, 2, 1024, 1, 1>(p, a, backward, tensors, stream);
-    if (p.threads * p.rows <= 256) return launch_t<T, 1, 256, 4, 3>(p, a, backward, tensors, stream);
-    if (p.threads <= 384) return launch_t<T, 1, 384, 2, 2>(p, a, backward, tensors, stream);
-    if (p.threads <= 512) return launch_t<T, 1, 512, 2, 1>(p, a, backward, tensors, stream);
-    return launch_t<T, 1, 1024, 1, 1>(p, a, backward, tensors, stream);
+    if (p.vpt == 2) return launch_t<T, 2, 1024, 1, 1>(p, a, backward, stream);
+    if (p.threads * p.rows <= 256) return launch_t<T, 1, 256, 4, 2>(p, a, backward, stream);
+    if (p.threads <= 384) return launch_t<T, 1, 384, 2, 2>(p, a, backward, stream);
+    if (p.threads <= 512) return launch_t<T, 1, 512, 2, 1>(p, a, backward, stream);
+    return launch_t<T, 1, 1024, 1, 1>(p, a, backward, stream);
 }
 
 }  // namespace
