@@ -235,9 +235,9 @@ template <int TENSORS, int VPT> struct Ring {
                 const char *src = static_cast<const char *>(base[t]) + row * n.stride[t] + threadIdx.x * 16;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
-                    if (col_ok(n, i))
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + (t * VPT + i) * n.word),
-                                     "l"(src + i * n.vec) : "memory");
+                    asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p cp.async.cg.shared.global [%0], [%1], 16;\n}"
+                                 ::"r"(dst + (t * VPT + i) * n.word), "l"(src + i * n.vec), "r"((uint32_t)col_ok(n, i))
+                                 : "memory");
             } else {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) clear(dst + (t * VPT + i) * n.word);
@@ -296,8 +296,8 @@ __device__ __forceinline__ void load_coef(const BlockNormArgs &a, const NormShap
     }
 }
 
-template <typename T, int VPT, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs a, NormShape n) {
+template <typename T, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_forward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int P = Row<T>::kP;
     extern __shared__ uint4 smem[];
     const bool has_o = a.o != nullptr, has_z = a.z != nullptr, has_r = a.r != nullptr;
@@ -383,18 +383,18 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_forward_kernel(BlockNormArgs 
     }
 }
 
-// The backward's coefficients: registers hold the column sums instead.  One word
-// per thread: both vectors in shared memory, a word's 16-byte pieces nv apart (no
-// bank conflicts).  Two words per thread: there is no room beside the ring, and
-// they are read from global memory.
-template <typename T, int VPT> struct Coefs {
+// The backward's coefficients: registers hold the column sums instead.  Both
+// vectors in shared memory, a word's 16-byte pieces nv apart (no bank conflicts);
+// the widest rows (SMEM false) leave no room for them beside the ring, and read
+// them from global memory.
+template <typename T, bool SMEM> struct Coefs {
     static constexpr int E = Row<T>::kE, P = Row<T>::kP;
     const float4 *smem;  // [2][E / 4][nv]: coef, w_before
     int nv;
     __device__ __forceinline__ void fill(const BlockNormArgs &a, const NormShape &n, float4 *at) {
         smem = at;
         nv = n.nv;
-        if (VPT > 1) return;
+        if (!SMEM) return;
         const int threads = blockDim.x * blockDim.y;
         for (int q = threadIdx.y * blockDim.x + threadIdx.x; q < n.nv * (E / 4); q += threads) {
             const int j = q / (E / 4), h = q % (E / 4);
@@ -425,7 +425,7 @@ template <typename T, int VPT> struct Coefs {
 #pragma unroll
         for (int h = 0; h < E / 4; ++h) {
             float4 v;
-            if constexpr (VPT == 1) {
+            if constexpr (SMEM) {
                 v = smem[(which * (E / 4) + h) * nv + j];
             } else {
                 float4 c, b;
@@ -438,8 +438,8 @@ template <typename T, int VPT> struct Coefs {
     }
 };
 
-template <typename T, int VPT, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) norm_backward_kernel(BlockNormArgs a, NormShape n) {
+template <typename T, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int E = Row<T>::kE, P = Row<T>::kP;
     extern __shared__ uint4 smem[];
     const bool has_o = a.o != nullptr, has_z = a.z != nullptr, has_n = a.d_next != nullptr;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(MAXT, MINB) norm_backward_kernel(BlockNormArgs
     const void *const tensors[5] = {a.o, a.z, a.d_r_out, has_n ? a.r : nullptr, a.d_next};
     Ring<5, VPT> ring(n, tensors);
     for (int k = 0; k < n.stages; ++k) ring.fetch(n, k, row0 + k * on, k < mine);
-    Coefs<T, VPT> co;
+    Coefs<T, MAXT <= 512> co;
     co.fill(a, n, reinterpret_cast<float4 *>(reinterpret_cast<char *>(smem) + n.coef_at));
     Team tm(smem, n.sums_at, n.words_at);
     F2 sum_c[VPT][P], sum_b[VPT][P];  // C_j and dw_before of the thread's columns
@@ -621,7 +621,8 @@ struct NormPlan {
     NormShape n;
     int vpt, threads, rows;  // words per thread, threads of a row, rows per CTA
     int per_sm;              // CTAs on an SM
-    size_t team_bytes;       // shared memory of the sums and the backward's coefficients
+    uint32_t row_bytes, coef_bytes, sum_bytes;  // shared memory: a row in the ring, the coefficients, the sums' words
+    size_t smem;
 };
 
 NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
@@ -639,15 +640,23 @@ NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
     p.n.bs = c.branch_scale;
     p.n.inv_width = 1.f / c.width;
     p.n.inv_group = 1.f / group;
-    p.vpt = p.n.nv > 1024 ? 2 : 1;
+    // Two words per thread: the control flow of a row is shared by both.
+    p.vpt = p.n.nv <= 32 ? 1 : 2;
     p.threads = ((p.n.nv + p.vpt - 1) / p.vpt + 31) / 32 * 32;
-    p.rows = p.threads >= 256 ? 1 : 256 / p.threads;
-    // registers: 64 per thread forward, 96 to 128 backward (64 above 512 threads)
-    const int most = backward ? 576 : 1024;
-    p.per_sm = most / (p.threads * p.rows);
+    p.rows = p.threads >= 128 ? 1 : 128 / p.threads;
+    p.coef_bytes = backward && p.threads <= 512 ? 2 * c.width * (uint32_t)sizeof(float) : 0;
+    p.sum_bytes = sizeof(float) * 4 * 32 * p.rows;
+    p.row_bytes = (backward ? 5 : 3) * p.vpt * p.threads * p.rows * 16;
+    const size_t fixed = p.coef_bytes + p.sum_bytes + (p.n.mode == kGroupShared ? sizeof(float) * p.rows * p.n.nv : 0);
+    // As many CTAs on an SM as its registers hold (up to 128 per thread; 64 in CTAs of more than 512), with room for
+    // two rows of each; then up to three.
+    const size_t room = 220 * 1024;
+    p.per_sm = 512 / (p.threads * p.rows);
+    while (p.per_sm > 1 && p.per_sm * (2 * p.row_bytes + fixed) > room) --p.per_sm;
     if (p.per_sm < 1) p.per_sm = 1;
-    p.team_bytes = sizeof(float) * (4 * 32 * p.rows + (p.n.mode == kGroupShared ? p.rows * p.n.nv : 0)) +
-                   (backward && p.vpt == 1 ? size_t(2) * c.width * sizeof(float) : 0);
+    p.n.stages = 3;
+    while (p.n.stages > 1 && p.per_sm * (p.n.stages * p.row_bytes + fixed) > room) --p.n.stages;
+    p.smem = p.n.stages * p.row_bytes + fixed;
     return p;
 }
 
@@ -656,38 +665,31 @@ int norm_grid(const NormPlan &p, int64_t T) {
     return (int)(need < most ? need : most);
 }
 
-template <typename T, int VPT, int MAXT, int FWD, int BWD>
+template <typename T, int VPT, int MAXT>
 cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    // three rows ahead where the SM's shared memory holds them, else two or one
-    const size_t row_bytes = size_t(backward ? 5 : 3) * VPT * p.threads * p.rows * 16, room = size_t(220) * 1024 / p.per_sm;
-    p.n.stages = 3;
-    while (p.n.stages > 1 && p.n.stages * row_bytes + p.team_bytes > room) --p.n.stages;
-    const size_t smem = p.n.stages * row_bytes + p.team_bytes;
-    const auto kernel = backward ? norm_backward_kernel<T, VPT, MAXT, BWD> : norm_forward_kernel<T, VPT, MAXT, FWD>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto kernel = backward ? norm_backward_kernel<T, VPT, MAXT> : norm_forward_kernel<T, VPT, MAXT>;
+    if (p.smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
         if (e != cudaSuccess) return e;
     }
     const int64_t width = p.n.width, strides[5] = {a.o_stride, a.z_stride, backward ? width : a.r_stride, a.r_stride, width};
     for (int t = 0; t < 5; ++t) p.n.stride[t] = strides[t] * (int64_t)sizeof(T);
     p.n.packed = width * (int64_t)sizeof(T);
     p.n.word = p.threads * p.rows * 16;
-    p.n.stage_bytes = (uint32_t)row_bytes;
+    p.n.stage_bytes = p.row_bytes;
     p.n.vec = p.threads * 16;
-    p.n.coef_at = (uint32_t)(p.n.stages * row_bytes);
-    p.n.sums_at = p.n.coef_at + (backward && VPT == 1 ? 2 * p.n.width * (uint32_t)sizeof(float) : 0);
-    p.n.words_at = p.n.sums_at + 4 * 32 * p.rows * (uint32_t)sizeof(float);
-    kernel<<<norm_grid(p, a.T), dim3(p.threads, p.rows), smem, stream>>>(a, p.n);
+    p.n.coef_at = p.n.stages * p.row_bytes;
+    p.n.sums_at = p.n.coef_at + p.coef_bytes;
+    p.n.words_at = p.n.sums_at + p.sum_bytes;
+    kernel<<<norm_grid(p, a.T), dim3(p.threads, p.rows), p.smem, stream>>>(a, p.n);
     return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_rows(const NormPlan &p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    if (p.vpt == 2) return launch_t<T, 2, 1024, 1, 1>(p, a, backward, stream);
-    if (p.threads * p.rows <= 256) return launch_t<T, 1, 256, 4, 2>(p, a, backward, stream);
-    if (p.threads <= 384) return launch_t<T, 1, 384, 2, 2>(p, a, backward, stream);
-    if (p.threads <= 512) return launch_t<T, 1, 512, 2, 1>(p, a, backward, stream);
-    return launch_t<T, 1, 1024, 1, 1>(p, a, backward, stream);
+    if (p.vpt == 1) return launch_t<T, 1, 128>(p, a, backward, stream);
+    if (p.threads <= 512) return launch_t<T, 2, 512>(p, a, backward, stream);
+    return launch_t<T, 2, 1024>(p, a, backward, stream);
 }
 
 }  // namespace
