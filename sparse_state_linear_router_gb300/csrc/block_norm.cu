@@ -226,10 +226,11 @@ template <int TENSORS, int VPT> struct Ring {
     static __device__ __forceinline__ void clear(uint32_t dst) {
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
     }
-    __device__ __forceinline__ void fetch(const NormShape &n, int stage, int64_t row, bool row_ok) {
+    // Tensors T0 to T1 of one row, as one group of copies.
+    template <int T0, int T1> __device__ __forceinline__ void fetch(const NormShape &n, int stage, int64_t row, bool row_ok) {
         const uint32_t dst = at + stage * n.stage_bytes;
 #pragma unroll
-        for (int t = 0; t < TENSORS; ++t) {
+        for (int t = T0; t < T1; ++t) {
             if (!base[t]) continue;
             if (row_ok) {
                 const char *src = static_cast<const char *>(base[t]) + row * n.stride[t] + threadIdx.x * 16;
@@ -257,14 +258,14 @@ template <int TENSORS, int VPT> struct Ring {
 __device__ __forceinline__ char *word_of(void *base, const NormShape &n, int64_t row, int i) {
     return static_cast<char *>(base) + row * n.packed + threadIdx.x * 16 + i * n.vec;
 }
-// Waits for the oldest of `stages` groups.
-__device__ __forceinline__ void fetches_wait(int stages) {
+// Waits for the oldest of `stages` rows' groups, GROUPS to a row.
+template <int GROUPS> __device__ __forceinline__ void fetches_wait(int stages) {
     if (stages == 3)
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(3 * GROUPS - 1) : "memory");
     else if (stages == 2)
-        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(2 * GROUPS - 1) : "memory");
     else
-        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(GROUPS - 1) : "memory");
 }
 
 // coef = branch_scale c w_after of the thread's columns, and w_before
@@ -297,7 +298,7 @@ __device__ __forceinline__ void load_coef(const BlockNormArgs &a, const NormShap
 }
 
 template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_forward_kernel(BlockNormArgs a, NormShape n) {
+__global__ void __launch_bounds__(MAXT, VPT == 1 ? 8 : 1) norm_forward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int P = Row<T>::kP;
     extern __shared__ uint4 smem[];
     const bool has_o = a.o != nullptr, has_z = a.z != nullptr, has_r = a.r != nullptr;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(BlockNormArgs a, Nor
     const int most = (int)((a.T - 1 - (int64_t)blockIdx.x * blockDim.y) / on) + 1;
     const void *const tensors[3] = {a.o, a.z, a.r};
     Ring<3, VPT> ring(n, tensors);
-    for (int k = 0; k < n.stages; ++k) ring.fetch(n, k, row0 + k * on, k < mine);
+    for (int k = 0; k < n.stages; ++k) ring.template fetch<0, 3>(n, k, row0 + k * on, k < mine);
     F2 coef[VPT][P], wb[VPT][P];
     load_coef<T, VPT>(a, n, coef, wb);
     Team tm(smem, n.sums_at, n.words_at);
@@ -317,14 +318,14 @@ __global__ void __launch_bounds__(MAXT) norm_forward_kernel(BlockNormArgs a, Nor
         const bool live = k < mine;
         F2 u[VPT][P];
         uint4 uz[VPT], ur[VPT];
-        fetches_wait(n.stages);
+        fetches_wait<1>(n.stages);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             Row<T>::unpack(ring.take(n, stage, 0, i), u[i]);
             uz[i] = ring.take(n, stage, 1, i);
             ur[i] = ring.take(n, stage, 2, i);
         }
-        ring.fetch(n, stage, row + n.stages * on, k + n.stages < mine);
+        ring.template fetch<0, 3>(n, stage, row + n.stages * on, k + n.stages < mine);
         stage = stage + 1 == n.stages ? 0 : stage + 1;
         if (n.mode != kGroupNone) {
             float ss[VPT];
@@ -439,7 +440,7 @@ template <typename T, bool SMEM> struct Coefs {
 };
 
 template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, NormShape n) {
+__global__ void __launch_bounds__(MAXT, VPT == 1 ? 5 : 1) norm_backward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int E = Row<T>::kE, P = Row<T>::kP;
     extern __shared__ uint4 smem[];
     const bool has_o = a.o != nullptr, has_z = a.z != nullptr, has_n = a.d_next != nullptr;
@@ -447,9 +448,13 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
     // rows of this team, and of the CTA's first (the others have as many or one less)
     const int mine = row0 < a.T ? (int)((a.T - 1 - row0) / on) + 1 : 0;
     const int most = (int)((a.T - 1 - (int64_t)blockIdx.x * blockDim.y) / on) + 1;
-    const void *const tensors[5] = {a.o, a.z, a.d_r_out, has_n ? a.r : nullptr, a.d_next};
+    // the first three make dr', and their place in the ring is free again while the last two are at work
+    const void *const tensors[5] = {a.d_r_out, has_n ? a.r : nullptr, a.d_next, a.o, a.z};
     Ring<5, VPT> ring(n, tensors);
-    for (int k = 0; k < n.stages; ++k) ring.fetch(n, k, row0 + k * on, k < mine);
+    for (int k = 0; k < n.stages; ++k) {
+        ring.template fetch<0, 3>(n, k, row0 + k * on, k < mine);
+        ring.template fetch<3, 5>(n, k, row0 + k * on, k < mine);
+    }
     Coefs<T, MAXT <= 512> co;
     co.fill(a, n, reinterpret_cast<float4 *>(reinterpret_cast<char *>(smem) + n.coef_at));
     Team tm(smem, n.sums_at, n.words_at);
@@ -463,15 +468,15 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
     for (int k = 0; k < most; ++k, row += on) {
         const bool live = k < mine;
         F2 d[VPT][P];
-        fetches_wait(n.stages);
+        fetches_wait<2>(n.stages);
         float rstd_row = 0.f, minus_mean = 0.f;
         if (has_n) {
             F2 ss = both(0.f), dot = both(0.f);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 F2 r[P], g[P], w[P];
-                Row<T>::unpack(ring.take(n, stage, 3, i), r);
-                Row<T>::unpack(ring.take(n, stage, 4, i), g);
+                Row<T>::unpack(ring.take(n, stage, 1, i), r);
+                Row<T>::unpack(ring.take(n, stage, 2, i), g);
                 co.get(a, n, 1, threadIdx.x + i * blockDim.x, w);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
@@ -486,11 +491,11 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
         }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            Row<T>::unpack(ring.take(n, stage, 2, i), d[i]);
+            Row<T>::unpack(ring.take(n, stage, 0, i), d[i]);
             if (has_n) {
                 F2 r[P], g[P], w[P];
-                Row<T>::unpack(ring.take(n, stage, 3, i), r);
-                Row<T>::unpack(ring.take(n, stage, 4, i), g);
+                Row<T>::unpack(ring.take(n, stage, 1, i), r);
+                Row<T>::unpack(ring.take(n, stage, 2, i), g);
                 co.get(a, n, 1, threadIdx.x + i * blockDim.x, w);
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
@@ -506,13 +511,15 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
                 Row<T>::store(word_of(a.d_r, n, row, i), v);
             }
         }
+        ring.template fetch<0, 3>(n, stage, row + n.stages * on, k + n.stages < mine);
+        fetches_wait<2>(n.stages);
         if (has_o) {
             float rstd[VPT], dot[VPT];
             if (n.mode != kGroupNone) {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     F2 o[P], t = both(0.f);
-                    Row<T>::unpack(ring.take(n, stage, 0, i), o);
+                    Row<T>::unpack(ring.take(n, stage, 3, i), o);
 #pragma unroll
                     for (int k = 0; k < P; ++k) t = fma2(o[k], o[k], t);
                     rstd[i] = fold(t);
@@ -527,13 +534,13 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 F2 o[P], c[P];
-                Row<T>::unpack(ring.take(n, stage, 0, i), o);
+                Row<T>::unpack(ring.take(n, stage, 3, i), o);
                 co.get(a, n, 0, threadIdx.x + i * blockDim.x, c);
 #pragma unroll
                 for (int k = 0; k < P; ++k) o[k] = mul2(o[k], both(rstd[i]));
                 if (has_z) {
                     F2 av[P], da[P];
-                    Row<T>::unpack(ring.take(n, stage, 1, i), av);
+                    Row<T>::unpack(ring.take(n, stage, 4, i), av);
                     act<true>(n.gate, av, da);
 #pragma unroll
                     for (int k = 0; k < P; ++k) {
@@ -558,7 +565,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
                     // d = rstd (d - o_hat mean), o_hat = o rstd
                     const F2 f = both(-dot[i] * n.inv_group * rstd[i]);
                     F2 o[P];
-                    Row<T>::unpack(ring.take(n, stage, 0, i), o);
+                    Row<T>::unpack(ring.take(n, stage, 3, i), o);
 #pragma unroll
                     for (int k = 0; k < P; ++k) d[i][k] = mul2(both(rstd[i]), fma2(o[k], f, d[i][k]));
                 }
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(MAXT) norm_backward_kernel(BlockNormArgs a, No
             for (int i = 0; i < VPT; ++i)
                 if (live && ring.col_ok(n, i)) Row<T>::store(word_of(a.d_o, n, row, i), d[i]);
         }
-        ring.fetch(n, stage, row + n.stages * on, k + n.stages < mine);
+        ring.template fetch<3, 5>(n, stage, row + n.stages * on, k + n.stages < mine);
         stage = stage + 1 == n.stages ? 0 : stage + 1;
     }
     // column sums of this team: one partial row of each
@@ -648,11 +655,11 @@ NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
     p.sum_bytes = sizeof(float) * 4 * 32 * p.rows;
     p.row_bytes = (backward ? 5 : 3) * p.vpt * p.threads * p.rows * 16;
     const size_t fixed = p.coef_bytes + p.sum_bytes + (p.n.mode == kGroupShared ? sizeof(float) * p.rows * p.n.nv : 0);
-    // As many CTAs on an SM as its registers hold (up to 128 per thread; 64 in CTAs of more than 512), with room for
-    // two rows of each; then up to three.
+    // As many CTAs on an SM as its registers and shared memory hold (up to 128 registers per thread with two words, 64
+    // and 96 with one), then up to three rows of each.
     const size_t room = 220 * 1024;
-    p.per_sm = 512 / (p.threads * p.rows);
-    while (p.per_sm > 1 && p.per_sm * (2 * p.row_bytes + fixed) > room) --p.per_sm;
+    p.per_sm = (p.vpt == 2 ? 512 : backward ? 640 : 1024) / (p.threads * p.rows);
+    while (p.per_sm > 1 && p.per_sm * (p.row_bytes + fixed) > room) --p.per_sm;
     if (p.per_sm < 1) p.per_sm = 1;
     p.n.stages = 3;
     while (p.n.stages > 1 && p.per_sm * (p.n.stages * p.row_bytes + fixed) > room) --p.n.stages;
@@ -672,8 +679,9 @@ cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStre
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
         if (e != cudaSuccess) return e;
     }
-    const int64_t width = p.n.width, strides[5] = {a.o_stride, a.z_stride, backward ? width : a.r_stride, a.r_stride, width};
-    for (int t = 0; t < 5; ++t) p.n.stride[t] = strides[t] * (int64_t)sizeof(T);
+    const int64_t width = p.n.width, fwd[5] = {a.o_stride, a.z_stride, a.r_stride, 0, 0},
+                  bwd[5] = {width, a.r_stride, width, a.o_stride, a.z_stride};
+    for (int t = 0; t < 5; ++t) p.n.stride[t] = (backward ? bwd : fwd)[t] * (int64_t)sizeof(T);
     p.n.packed = width * (int64_t)sizeof(T);
     p.n.word = p.threads * p.rows * 16;
     p.n.stage_bytes = p.row_bytes;
