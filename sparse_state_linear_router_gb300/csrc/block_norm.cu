@@ -126,9 +126,10 @@ struct Team {
         __syncthreads();
     }
     __device__ __forceinline__ float gather(const float *w) const {
-        float s = 0.f;
-        for (int k = 0; k < (int)blockDim.x >> 5; k += 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(w + k);
+        float4 v = *reinterpret_cast<const float4 *>(w);
+        float s = (v.x + v.y) + (v.z + v.w);
+        for (int k = 4; k < (int)blockDim.x >> 5; k += 4) {
+            v = *reinterpret_cast<const float4 *>(w + k);
             s += (v.x + v.y) + (v.z + v.w);
         }
         return s;
@@ -194,7 +195,8 @@ struct NormShape {
     int mode, gw;        // group mode, words of a group
     // The launch's layout, here so that it takes no registers.
     int stages;                                // rows of a thread's ring
-    uint32_t word, stage_bytes, vec;           // bytes between a thread's words in the ring, between stages, in a row
+    uint32_t stage_bytes, vec;                 // bytes of a stage of the ring; between a thread's words of a row
+    uint32_t slot[5], word;                    // a tensor's place in a stage (absent ones share one of zeros), its words
     uint32_t coef_at, sums_at, words_at;       // shared memory: coefficients, Team's words
     int64_t stride[5], packed;                 // bytes of a row in each fetched tensor and in a packed one
     int gate;
@@ -218,7 +220,7 @@ template <int TENSORS, int VPT> struct Ring {
             for (int t = 0; t < TENSORS; ++t)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
-                    if (!base[t] || !col_ok(n, i)) clear(at + s * n.stage_bytes + (t * VPT + i) * n.word);
+                    if (!base[t] || !col_ok(n, i)) clear(at + s * n.stage_bytes + n.slot[t] + i * n.word);
     }
     static __device__ __forceinline__ bool col_ok(const NormShape &n, int i) {
         return (int)threadIdx.x + i * (int)blockDim.x < n.nv;
@@ -237,11 +239,11 @@ template <int TENSORS, int VPT> struct Ring {
 #pragma unroll
                 for (int i = 0; i < VPT; ++i)
                     asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %2, 0;\n@p cp.async.cg.shared.global [%0], [%1], 16;\n}"
-                                 ::"r"(dst + (t * VPT + i) * n.word), "l"(src + i * n.vec), "r"((uint32_t)col_ok(n, i))
+                                 ::"r"(dst + n.slot[t] + i * n.word), "l"(src + i * n.vec), "r"((uint32_t)col_ok(n, i))
                                  : "memory");
             } else {
 #pragma unroll
-                for (int i = 0; i < VPT; ++i) clear(dst + (t * VPT + i) * n.word);
+                for (int i = 0; i < VPT; ++i) clear(dst + n.slot[t] + i * n.word);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -250,7 +252,7 @@ template <int TENSORS, int VPT> struct Ring {
         uint4 u;
         asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                     : "r"(at + stage * n.stage_bytes + (t * VPT + i) * n.word) : "memory");
+                     : "r"(at + stage * n.stage_bytes + n.slot[t] + i * n.word) : "memory");
         return u;
     }
 };
@@ -632,8 +634,14 @@ struct NormPlan {
     size_t smem;
 };
 
-NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
+int most_per_sm(const NormPlan &p, bool backward) {
+    const int n = (p.vpt == 2 ? 512 : backward ? 640 : 1024) / (p.threads * p.rows);
+    return n < 1 ? 1 : n;
+}
+
+NormPlan plan_norm(const sse_norm_config_t &c, const BlockNormArgs &a, bool backward) {
     NormPlan p{};
+    const bool after = a.w_after != nullptr;
     const int E = c.dtype == SSE_BF16 ? 8 : 4;
     const int group = c.group ? c.group : c.width;
     p.n.width = c.width;
@@ -653,14 +661,21 @@ NormPlan plan_norm(const sse_norm_config_t &c, bool after, bool backward) {
     p.rows = p.threads >= 128 ? 1 : 128 / p.threads;
     p.coef_bytes = backward && p.threads <= 512 ? 2 * c.width * (uint32_t)sizeof(float) : 0;
     p.sum_bytes = sizeof(float) * 4 * 32 * p.rows;
-    p.row_bytes = (backward ? 5 : 3) * p.vpt * p.threads * p.rows * 16;
+    // a stage of the ring: the tensors that the call has, and words of zeros for the others
+    const void *const fwd[5] = {a.o, a.z, a.r}, *const bwd[5] = {a.d_r_out, a.d_next ? a.r : nullptr, a.d_next, a.o, a.z};
+    p.n.word = p.threads * p.rows * 16;
+    uint32_t present = 0;
+    for (int t = 0; t < (backward ? 5 : 3); ++t)
+        if ((backward ? bwd : fwd)[t]) p.n.slot[t] = present++ * p.vpt * p.n.word;
+    for (int t = 0; t < (backward ? 5 : 3); ++t)
+        if (!(backward ? bwd : fwd)[t]) p.n.slot[t] = present * p.vpt * p.n.word;
+    p.row_bytes = (present + (present < (backward ? 5 : 3))) * p.vpt * p.n.word;
     const size_t fixed = p.coef_bytes + p.sum_bytes + (p.n.mode == kGroupShared ? sizeof(float) * p.rows * p.n.nv : 0);
     // As many CTAs on an SM as its registers and shared memory hold (up to 128 registers per thread with two words, 64
     // and 96 with one), then up to three rows of each.
     const size_t room = 220 * 1024;
-    p.per_sm = (p.vpt == 2 ? 512 : backward ? 640 : 1024) / (p.threads * p.rows);
+    p.per_sm = most_per_sm(p, backward);
     while (p.per_sm > 1 && p.per_sm * (p.row_bytes + fixed) > room) --p.per_sm;
-    if (p.per_sm < 1) p.per_sm = 1;
     p.n.stages = 3;
     while (p.n.stages > 1 && p.per_sm * (p.n.stages * p.row_bytes + fixed) > room) --p.n.stages;
     p.smem = p.n.stages * p.row_bytes + fixed;
@@ -683,7 +698,6 @@ cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStre
                   bwd[5] = {width, a.r_stride, width, a.o_stride, a.z_stride};
     for (int t = 0; t < 5; ++t) p.n.stride[t] = (backward ? bwd : fwd)[t] * (int64_t)sizeof(T);
     p.n.packed = width * (int64_t)sizeof(T);
-    p.n.word = p.threads * p.rows * 16;
     p.n.stage_bytes = p.row_bytes;
     p.n.vec = p.threads * 16;
     p.n.coef_at = p.n.stages * p.row_bytes;
@@ -703,18 +717,20 @@ cudaError_t launch_rows(const NormPlan &p, const BlockNormArgs &a, bool backward
 }  // namespace
 
 int64_t block_norm_partial_rows(const sse_norm_config_t &cfg, int64_t T) {
-    const NormPlan p = plan_norm(cfg, true, true);
+    // at most: a call's own plan has as many CTAs on an SM or fewer
+    NormPlan p = plan_norm(cfg, BlockNormArgs{}, true);
+    p.per_sm = most_per_sm(p, true);
     return (int64_t)norm_grid(p, T) * p.rows;
 }
 
 cudaError_t launch_block_norm(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream) {
-    const NormPlan p = plan_norm(cfg, a.w_after != nullptr, false);
+    const NormPlan p = plan_norm(cfg, a, false);
     return cfg.dtype == SSE_BF16 ? launch_rows<__nv_bfloat16>(p, a, false, stream)
                                  : launch_rows<float>(p, a, false, stream);
 }
 
 cudaError_t launch_block_norm_backward(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream) {
-    const NormPlan p = plan_norm(cfg, a.w_after != nullptr, true);
+    const NormPlan p = plan_norm(cfg, a, true);
     if (a.T > 0) {
         const cudaError_t e = cfg.dtype == SSE_BF16 ? launch_rows<__nv_bfloat16>(p, a, true, stream)
                                                     : launch_rows<float>(p, a, true, stream);
