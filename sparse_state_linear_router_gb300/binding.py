@@ -294,8 +294,19 @@ def _check(status: int, what: str):
         raise SSEError(status, what)
 
 
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _token_dtype(cfg):
-    import torch
+    torch = _torch()
     return torch.bfloat16 if cfg.dtype == SSE_BF16 else torch.float32
 
 
@@ -484,68 +495,88 @@ def make_norm_config(width, group=0, gate="none", eps=1e-6, residual_scale=1.0, 
                              {"bf16": SSE_BF16, "f32": SSE_F32}[dtype] if isinstance(dtype, str) else dtype)
 
 
-class _Args:
-    """Checks the tensors of one call against each other and remembers their device."""
-
-    def __init__(self, what: str, rows: int, width: int, dtype, device):
-        self.what, self.rows, self.width, self.dtype, self.device = what, rows, width, dtype, device
-
-    def refuse(self, why: str):
-        raise SSEError(SSE_ERR_INVALID_ARG, f"{self.what}: {why}")
-
-    def tokens(self, name: str, t, packed: bool = False):
-        """(pointer, row stride) of a token tensor: [rows, width], or [rows, heads, width of a head]."""
-        if t is None:
-            return None, self.width
-        if t.dtype != self.dtype or t.device != self.device:
-            self.refuse(f"{name} is {t.dtype} on {t.device}, not {self.dtype} on {self.device}")
-        shape = t.shape
-        if len(shape) < 2 or shape[0] != self.rows or t.numel() != self.rows * self.width:
-            self.refuse(f"{name} has shape {tuple(shape)}, not [{self.rows}, {self.width}]")
-        if t.is_contiguous():
-            return t.data_ptr(), self.width
-        if packed:
-            self.refuse(f"{name} is not contiguous")
-        stride = t.stride()
-        inner = 1
-        for n, s in zip(shape[:0:-1], stride[:0:-1]):  # the last dimensions: one packed row
-            if n != 1 and s != inner:
-                self.refuse(f"{name} has strides {stride}: the columns of a row are not packed")
-            inner *= n
-        if stride[0] < self.width and self.rows > 1:
-            self.refuse(f"{name} has row stride {stride[0]}, below its width {self.width}")
-        return t.data_ptr(), stride[0] if self.rows > 1 else self.width
-
-    def f32(self, name: str, t, *shape: int):
-        """Pointer of a packed float32 tensor."""
-        import torch
-        if t is None:
-            return None
-        if t.dtype != torch.float32 or t.device != self.device or t.shape != shape or not t.is_contiguous():
-            self.refuse(f"{name} is not a contiguous float32 {list(shape)} on {self.device}")
-        return t.data_ptr()
-
-    def run(self, call, *args):
-        """One C call on the tensors' device and its current stream."""
-        import torch
-        index = self.device.index
-        if index == torch.cuda.current_device():
-            status = call(*args, torch.cuda.current_stream(index).cuda_stream)
-        else:
-            with torch.cuda.device(index):
-                status = call(*args, torch.cuda.current_stream(index).cuda_stream)
-        _check(status, self.what)
+def _refuse(what: str, why: str):
+    raise SSEError(SSE_ERR_INVALID_ARG, f"{what}: {why}")
 
 
-def _scan_args(what, cfg, x, cu_seqlens):
-    import torch
-    if not x.is_cuda or x.dim() < 2:
-        raise SSEError(SSE_ERR_INVALID_ARG, f"{what}: x is not a [tokens, width] CUDA tensor")
-    a = _Args(what, x.shape[0], cfg.width, _token_dtype(cfg), x.device)
-    if cu_seqlens is not None and (cu_seqlens.dtype != torch.int32 or cu_seqlens.device != x.device or
-                                   cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
-        a.refuse(f"cu_seqlens is not a contiguous int32 [sequences + 1] on {x.device}")
-    return a
+def _refuse_tokens(what, name, t, rows, width, dtype, device):
+    if t.dtype != dtype or t.device != device:
+        _refuse(what, f"{name} is {t.dtype} on {t.device}, not {dtype} on {device}")
+    _refuse(what, f"{name} has shape {tuple(t.shape)}, not [{rows}, {width}] or [{rows}, heads, {width} / heads]")
+
+
+def _rows(what, name, t, rows, width, dtype, device):
+    """(pointer, row stride) of a token tensor [rows, width] or [rows, heads, width / heads] whose rows are packed."""
+    if t is None:
+        return None, width
+    if t.dtype is not dtype or t.device != device or t.numel() != rows * width or t.dim() < 2 or t.shape[0] != rows:
+        _refuse_tokens(what, name, t, rows, width, dtype, device)
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    stride = t.stride()
+    inner = 1
+    for n, s in zip(t.shape[:0:-1], stride[:0:-1]):
+        if n != 1 and s != inner:
+            _refuse(what, f"{name} has strides {stride}: the columns of a row are not packed")
+        inner *= n
+    if rows <= 1:
+        return t.data_ptr(), width
+    if stride[0] < width:
+        _refuse(what, f"{name} has row stride {stride[0]}, below its width {width}")
+    return t.data_ptr(), stride[0]
+
+
+def _packed(what, name, t, rows, width, dtype, device):
+    """Pointer of a contiguous token tensor."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.device != device or t.numel() != rows * width or t.dim() < 2 or t.shape[0] != rows:
+        _refuse_tokens(what, name, t, rows, width, dtype, device)
+    if not t.is_contiguous():
+        _refuse(what, f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+def _floats(what, name, t, shape, device):
+    """Pointer of a contiguous float32 tensor."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not _torch().float32 or t.device != device or not t.is_contiguous():
+        _refuse(what, f"{name} is not a contiguous float32 {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _on_device(what, device, call, *args):
+    """One C call on the tensors' device and its current stream, whichever device is current."""
+    cuda = _torch().cuda
+    index = device.index
+    if index == cuda.current_device():
+        status = call(*args, cuda.current_stream(index).cuda_stream)
+    else:
+        with cuda.device(index):
+            status = call(*args, cuda.current_stream(index).cuda_stream)
+    if status != SSE_OK:
+        raise SSEError(status, what)
+
+
+def _first(what, t):
+    """Rows, device and type check of the tensor that the others are compared with."""
+    if t is None or not t.is_cuda or t.dim() < 2:
+        _refuse(what, "a [tokens, width] CUDA tensor is required")
+    return t.shape[0], t.device
+
+
+def _sequences(what, cu_seqlens, device):
+    if (cu_seqlens.dtype is not _torch().int32 or cu_seqlens.device != device or cu_seqlens.dim() != 1 or
+            cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
+        _refuse(what, f"cu_seqlens is not a contiguous int32 [sequences + 1] on {device}")
+    return cu_seqlens.numel() - 1
+
+
+def _like(t):
+    """A packed tensor of t's shape and type."""
+    torch = _torch()
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def scan_forward(cfg, x, log_gate, cu_seqlens, *, initial_state=None, want_final_state=True, want_checkpoints=False,
@@ -553,21 +584,25 @@ def scan_forward(cfg, x, log_gate, cu_seqlens, *, initial_state=None, want_final
     """The gated linear recurrence (sse_scan_forward) over packed sequences;
     x, log_gate [T, width] or [T, H, width / H].  Returns dict(out,
     final_state, checkpoints); checkpoints are what scan_backward reads."""
-    import torch
-    a = _scan_args("sse_scan_forward", cfg, x, cu_seqlens)
-    T, S, W = a.rows, cu_seqlens.numel() - 1, cfg.width
-    px, sx = a.tokens("x", x)
-    pg, sg = a.tokens("log_gate", log_gate)
+    torch, what = _torch(), "sse_scan_forward"
+    T, dev = _first(what, x)
+    S, W, dt = _sequences(what, cu_seqlens, dev), cfg.width, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    pg, sg = _rows(what, "log_gate", log_gate, T, W, dt, dev)
+    pi = _floats(what, "initial_state", initial_state, (S, W), dev)
+    po, pf, pc = (_packed(what, "out", out, T, W, dt, dev), _floats(what, "final_state", final_state, (S, W), dev),
+                  _floats(what, "checkpoints", checkpoints, (-(-T // SCAN_CHECKPOINT), W), dev))
     if out is None:
-        out = torch.empty(x.shape, dtype=a.dtype, device=a.device)
+        out = _like(x)
+        po = out.data_ptr()
     if final_state is None and want_final_state:
-        final_state = torch.empty((S, W), dtype=torch.float32, device=a.device)
-    rows = -(-T // SCAN_CHECKPOINT)
+        final_state = torch.empty((S, W), dtype=torch.float32, device=dev)
+        pf = final_state.data_ptr()
     if checkpoints is None and want_checkpoints:
-        checkpoints = torch.empty((rows, W), dtype=torch.float32, device=a.device)
-    a.run(load().sse_scan_forward, ctypes.byref(cfg), px, sx, pg, sg, cu_seqlens.data_ptr(), S, T,
-          a.f32("initial_state", initial_state, S, W), a.f32("final_state", final_state, S, W),
-          a.tokens("out", out, packed=True)[0], a.f32("checkpoints", checkpoints, rows, W))
+        checkpoints = torch.empty((-(-T // SCAN_CHECKPOINT), W), dtype=torch.float32, device=dev)
+        pc = checkpoints.data_ptr()
+    _on_device(what, dev, load().sse_scan_forward, ctypes.byref(cfg), px, sx, pg, sg, cu_seqlens.data_ptr(), S, T, pi,
+               pf, po, pc)
     return {"out": out, "final_state": final_state, "checkpoints": checkpoints}
 
 
@@ -575,43 +610,41 @@ def scan_backward(cfg, x, log_gate, cu_seqlens, checkpoints, d_out, *, initial_s
                   want_d_initial_state=True):
     """Gradients of <d_out, out> + <d_final_state, final_state> of scan_forward
     (sse_scan_backward); returns dict(dx, d_log_gate, d_initial_state)."""
-    import torch
-    a = _scan_args("sse_scan_backward", cfg, x, cu_seqlens)
-    T, S, W = a.rows, cu_seqlens.numel() - 1, cfg.width
-    px, sx = a.tokens("x", x)
-    pg, sg = a.tokens("log_gate", log_gate)
-    pd = a.tokens("d_out", d_out, packed=True)[0]
+    torch, what = _torch(), "sse_scan_backward"
+    T, dev = _first(what, x)
+    S, W, dt = _sequences(what, cu_seqlens, dev), cfg.width, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    pg, sg = _rows(what, "log_gate", log_gate, T, W, dt, dev)
+    pd = _packed(what, "d_out", d_out, T, W, dt, dev)
     if checkpoints is None:
-        a.refuse("checkpoints is None: scan_forward(..., want_checkpoints=True) returns them")
-    dx = torch.empty(x.shape, dtype=a.dtype, device=a.device)
-    dg = torch.empty(log_gate.shape, dtype=a.dtype, device=a.device)
-    d_init = torch.empty((S, W), dtype=torch.float32, device=a.device) if want_d_initial_state else None
-    a.run(load().sse_scan_backward, ctypes.byref(cfg), px, sx, pg, sg, cu_seqlens.data_ptr(), S, T,
-          a.f32("initial_state", initial_state, S, W), a.f32("checkpoints", checkpoints, -(-T // SCAN_CHECKPOINT), W),
-          pd, a.f32("d_final_state", d_final_state, S, W), dx.data_ptr(), dg.data_ptr(), _ptr(d_init))
+        _refuse(what, "checkpoints is None: scan_forward(..., want_checkpoints=True) returns them")
+    pc = _floats(what, "checkpoints", checkpoints, (-(-T // SCAN_CHECKPOINT), W), dev)
+    dx, dg = _like(x), _like(log_gate)
+    d_init = torch.empty((S, W), dtype=torch.float32, device=dev) if want_d_initial_state else None
+    _on_device(what, dev, load().sse_scan_backward, ctypes.byref(cfg), px, sx, pg, sg, cu_seqlens.data_ptr(), S, T,
+               _floats(what, "initial_state", initial_state, (S, W), dev), pc, pd,
+               _floats(what, "d_final_state", d_final_state, (S, W), dev), dx.data_ptr(), dg.data_ptr(), _ptr(d_init))
     return {"dx": dx, "d_log_gate": dg, "d_initial_state": d_init}
 
 
 def scan_step(cfg, state, x, log_gate, *, out=None):
     """One token of each sequence (sse_scan_step): x, log_gate [B, width];
     ``state`` [B, width] float32 is updated in place.  Returns dict(out)."""
-    import torch
-    a = _scan_args("sse_scan_step", cfg, x, None)
-    px, sx = a.tokens("x", x)
-    pg, sg = a.tokens("log_gate", log_gate)
+    what = "sse_scan_step"
+    B, dev = _first(what, x)
+    W, dt = cfg.width, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, B, W, dt, dev)
+    pg, sg = _rows(what, "log_gate", log_gate, B, W, dt, dev)
     if state is None:
-        a.refuse("state is None")
+        _refuse(what, "state is None")
+    ps = _floats(what, "state", state, (B, W), dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=a.dtype, device=a.device)
-    a.run(load().sse_scan_step, ctypes.byref(cfg), px, sx, pg, sg, a.rows, a.f32("state", state, a.rows, cfg.width),
-          a.tokens("out", out, packed=True)[0])
+        out = _like(x)
+        po = out.data_ptr()
+    else:
+        po = _packed(what, "out", out, B, W, dt, dev)
+    _on_device(what, dev, load().sse_scan_step, ctypes.byref(cfg), px, sx, pg, sg, B, ps, po)
     return {"out": out}
-
-
-def _norm_args(what, cfg, first):
-    if first is None or not first.is_cuda or first.dim() < 2:
-        raise SSEError(SSE_ERR_INVALID_ARG, f"{what}: a [tokens, width] CUDA tensor is required")
-    return _Args(what, first.shape[0], cfg.width, _token_dtype(cfg), first.device)
 
 
 def block_norm(cfg, block_out=None, *, gate=None, residual=None, w_after=None, channel_scale=None, w_before=None,
@@ -619,21 +652,25 @@ def block_norm(cfg, block_out=None, *, gate=None, residual=None, w_after=None, c
     """The norms before and after a block with its gate and the residual
     stream (sse_block_norm); token tensors [T, width] or [T, H, width / H].
     Returns dict(residual_out, next_in); next_in is None without w_before."""
-    import torch
-    first = block_out if block_out is not None else residual
-    a = _norm_args("sse_block_norm", cfg, first)
-    po, so = a.tokens("block_out", block_out)
-    pz, sz = a.tokens("gate", gate)
-    pr, sr = a.tokens("residual", residual)
-    W = cfg.width
-    like = residual if residual is not None else first
+    what = "sse_block_norm"
+    like = residual if residual is not None else block_out
+    T, dev = _first(what, like)
+    W, dt = cfg.width, _token_dtype(cfg)
+    po, so = _rows(what, "block_out", block_out, T, W, dt, dev)
+    pz, sz = _rows(what, "gate", gate, T, W, dt, dev)
+    pr, sr = _rows(what, "residual", residual, T, W, dt, dev)
+    wa = _floats(what, "w_after", w_after, (W,), dev)
+    wc = _floats(what, "channel_scale", channel_scale, (W,), dev)
+    wb = _floats(what, "w_before", w_before, (W,), dev)
+    pt, pn = (_packed(what, "residual_out", residual_out, T, W, dt, dev),
+              _packed(what, "next_in", next_in, T, W, dt, dev))
     if residual_out is None and want_residual_out:
-        residual_out = torch.empty(like.shape, dtype=a.dtype, device=a.device)
+        residual_out = _like(like)
+        pt = residual_out.data_ptr()
     if next_in is None and w_before is not None:
-        next_in = torch.empty(like.shape, dtype=a.dtype, device=a.device)
-    a.run(load().sse_block_norm, ctypes.byref(cfg), a.rows, po, so, pz, sz, pr, sr, a.f32("w_after", w_after, W),
-          a.f32("channel_scale", channel_scale, W), a.f32("w_before", w_before, W),
-          a.tokens("residual_out", residual_out, packed=True)[0], a.tokens("next_in", next_in, packed=True)[0])
+        next_in = _like(like)
+        pn = next_in.data_ptr()
+    _on_device(what, dev, load().sse_block_norm, ctypes.byref(cfg), T, po, so, pz, sz, pr, sr, wa, wc, wb, pt, pn)
     return {"residual_out": residual_out, "next_in": next_in}
 
 
@@ -643,30 +680,30 @@ def block_norm_backward(cfg, d_residual_out, block_out=None, *, gate=None, w_aft
     block_norm (sse_block_norm_backward); residual_out is the forward's.
     Returns dict(d_block_out, d_gate, d_residual, d_w_after, d_channel_scale,
     d_w_before), None where the part is absent."""
-    import torch
+    torch, what = _torch(), "sse_block_norm_backward"
     first = d_residual_out if d_residual_out is not None else d_next_in
-    a = _norm_args("sse_block_norm_backward", cfg, first)
-    po, so = a.tokens("block_out", block_out)
-    pz, sz = a.tokens("gate", gate)
-    pr, sr = a.tokens("residual_out", residual_out)
-    W, T = cfg.width, a.rows
-
-    def like(t, wanted=True):
-        return torch.empty(t.shape, dtype=t.dtype, device=a.device) if t is not None and wanted else None
-
-    g = {"d_block_out": like(block_out), "d_gate": like(gate),
-         "d_residual": like(first, want_d_residual), "d_w_after": like(w_after),
-         "d_channel_scale": like(channel_scale), "d_w_before": like(w_before)}
+    T, dev = _first(what, first)
+    W, dt = cfg.width, _token_dtype(cfg)
+    po, so = _rows(what, "block_out", block_out, T, W, dt, dev)
+    pz, sz = _rows(what, "gate", gate, T, W, dt, dev)
+    pr, sr = _rows(what, "residual_out", residual_out, T, W, dt, dev)
+    pd = _packed(what, "d_residual_out", d_residual_out, T, W, dt, dev)
+    pn = _packed(what, "d_next_in", d_next_in, T, W, dt, dev)
+    wa = _floats(what, "w_after", w_after, (W,), dev)
+    wc = _floats(what, "channel_scale", channel_scale, (W,), dev)
+    wb = _floats(what, "w_before", w_before, (W,), dev)
+    g = {"d_block_out": None if block_out is None else _like(block_out), "d_gate": None if gate is None else _like(gate),
+         "d_residual": _like(first) if want_d_residual else None,
+         "d_w_after": None if w_after is None else _like(w_after),
+         "d_channel_scale": None if channel_scale is None else _like(channel_scale),
+         "d_w_before": None if w_before is None else _like(w_before)}
     if workspace is None:
         n = load().sse_block_norm_backward_workspace_size(ctypes.byref(cfg), T)
-        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=a.device)
-    elif workspace.dtype != torch.uint8 or workspace.device != a.device or not workspace.is_contiguous():
-        a.refuse(f"workspace is not a contiguous uint8 tensor on {a.device}")
-    a.run(load().sse_block_norm_backward, ctypes.byref(cfg), T, po, so, pz, sz, pr, sr,
-          a.f32("w_after", w_after, W), a.f32("channel_scale", channel_scale, W), a.f32("w_before", w_before, W),
-          a.tokens("d_residual_out", d_residual_out, packed=True)[0], a.tokens("d_next_in", d_next_in, packed=True)[0],
-          _ptr(g["d_block_out"]), _ptr(g["d_gate"]), _ptr(g["d_residual"]), _ptr(g["d_w_after"]),
-          _ptr(g["d_channel_scale"]), _ptr(g["d_w_before"]), workspace.data_ptr(), workspace.numel())
+        workspace = torch.empty(max(n, 256), dtype=torch.uint8, device=dev)
+    elif workspace.dtype is not torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        _refuse(what, f"workspace is not a contiguous uint8 tensor on {dev}")
+    _on_device(what, dev, load().sse_block_norm_backward, ctypes.byref(cfg), T, po, so, pz, sz, pr, sr, wa, wc, wb, pd,
+               pn, *map(_ptr, g.values()), workspace.data_ptr(), workspace.numel())
     return g
 
 
