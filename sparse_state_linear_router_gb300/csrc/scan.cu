@@ -726,12 +726,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         runs_published();
         cluster_arrive_relaxed();
     };
-    auto second_pass = [&](const Marks &m, V state, V e, uint32_t *src) {
+    // EDGES: sequences begin or end among the rows.
+    auto rows_of = [&](auto edges, const Marks &m, V state, V e, uint32_t *src) {
+        constexpr bool EDGES = decltype(edges)::value;
         // forwards for the states, then backwards: dh = d + e, dx = s dh, d_log_gate = dh (a h_before + s' x)
         V a[kRows], s[MODE == SSE_INPUT_PLAIN ? 1 : kRows], slope[kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            if ((m.starts >> i) & 1u) state = first_state(m.seq, i);
+            if (EDGES && ((m.starts >> i) & 1u)) state = first_state(m.seq, i);
             const V la = L::unpack(src[i * 32]);
             V b = L::unpack(src[kSlotWords + i * 32]);
             a[i] = decay<T>(la);
@@ -748,18 +750,24 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         }
 #pragma unroll
         for (int j = kRows - 1; j >= 0; --j) {
-            if ((m.ends >> j) & 1u) e = last_adjoint(m.seq, j);
+            if (EDGES && ((m.ends >> j) & 1u)) e = last_adjoint(m.seq, j);
             const V dh = add2(L::unpack(src[2 * kSlotWords + j * 32]), e);
             e = mul2(a[j], dh);
             V gx = dh;
             if constexpr (MODE != SSE_INPUT_PLAIN) gx = mul2(dh, s[j]);
             src[kSlotWords + j * 32] = L::pack(gx);
             src[2 * kSlotWords + j * 32] = L::pack(mul2(dh, slope[j]));
-            if ((m.starts >> j) & 1u) {
+            if (EDGES && ((m.starts >> j) & 1u)) {
                 const int q = __shfl_sync(0xffffffffu, m.seq, j);
                 if (p.d_init && live) L::store_state(p.d_init + (int64_t)q * width + col, e);
             }
         }
+    };
+    auto second_pass = [&](const Marks &m, V state, V e, uint32_t *src) {
+        if ((m.starts | m.ends) == 0)
+            rows_of(std::false_type{}, m, state, e, src);
+        else
+            rows_of(std::true_type{}, m, state, e, src);
         __syncwarp();
         store_dx.store(src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
         store_dg.store(src - lane + 2 * kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
