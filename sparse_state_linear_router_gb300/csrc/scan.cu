@@ -127,11 +127,10 @@ template <typename T> __device__ __forceinline__ typename Lane<T>::V decay(typen
     }
 }
 
-// 1 - exp(u) for u <= 0, e = exp(u).  For u > -1/2, where 1 - e would cancel,
-// -u times the Chebyshev interpolation of degree 5 of (exp(u) - 1) / u on
-// [-1/2, 0] (1.5e-9 off, 6e-8 with float32 roundings).
-template <typename T>
-__device__ __forceinline__ typename Lane<T>::V one_minus_exp(typename Lane<T>::V u, typename Lane<T>::V e) {
+// 1 - exp(u) for -1/2 <= u <= 0: -u times the Chebyshev interpolation of degree
+// 5 of (exp(u) - 1) / u on that interval (1.5e-9 off, 6e-8 with float32
+// roundings).  1 - exp(u) formed from exp(u) would cancel here.
+template <typename T> __device__ __forceinline__ typename Lane<T>::V one_minus_exp_near0(typename Lane<T>::V u) {
     using L = Lane<T>;
     auto p = L::splat(-0.0011234042f);
     p = fma2(p, u, L::splat(-0.008189614f));
@@ -139,27 +138,55 @@ __device__ __forceinline__ typename Lane<T>::V one_minus_exp(typename Lane<T>::V
     p = fma2(p, u, L::splat(-0.16666242f));
     p = fma2(p, u, L::splat(-0.49999982f));
     p = fma2(p, u, L::splat(-1.f));
-    p = mul2(p, u);
-    return each(u, p, e, [](float x, float near0, float ex) { return x > -0.5f ? near0 : 1.f - ex; });
+    return mul2(p, u);
 }
 
-// The input factor s(a) of MODE (sse_input_scale_t; not for PLAIN), and with
-// GRAD its derivative by the log-gate.
-template <typename T, int MODE, bool GRAD = false>
-__device__ __forceinline__ typename Lane<T>::V input_factor(typename Lane<T>::V la, typename Lane<T>::V a,
-                                                            typename Lane<T>::V *slope = nullptr) {
+// A row's decay a, input factor s(a) and, with GRAD, ds/dla.  NEAR0: every
+// log-gate of the warp's rows is in [-1/2, 0], where one series gives 1 - a and
+// with it a, without an exponential or a select.
+template <typename T, int MODE, bool NEAR0, bool GRAD = false>
+__device__ __forceinline__ void factors(typename Lane<T>::V la, typename Lane<T>::V &a, typename Lane<T>::V &s,
+                                        typename Lane<T>::V *slope = nullptr) {
     using L = Lane<T>;
-    if constexpr (MODE == SSE_INPUT_COMPLEMENT) {
-        if constexpr (GRAD) *slope = mul2(a, L::splat(-1.f));
-        return one_minus_exp<T>(la, a);
+    const auto one = L::splat(1.f), minus = L::splat(-1.f);
+    if constexpr (MODE == SSE_INPUT_PLAIN) {
+        a = decay<T>(la);
+    } else if constexpr (MODE == SSE_INPUT_COMPLEMENT) {
+        if constexpr (NEAR0) {
+            s = one_minus_exp_near0<T>(la);
+            a = fma2(s, minus, one);
+        } else {
+            a = decay<T>(la);
+            s = each(la, one_minus_exp_near0<T>(la), a, [](float x, float near0, float e) { return x > -0.5f ? near0 : 1.f - e; });
+        }
+        if constexpr (GRAD) *slope = mul2(a, minus);
     } else {
-        const auto a2 = mul2(a, a), s2 = one_minus_exp<T>(add2(la, la), a2);
-        // 1 / s, and 0 for s = 0: no input enters there and its slope is taken as 0
-        const auto r = each(s2, [](float v) { return rsqrt_ftz(fmaxf(v, 1e-37f)); });
-        if constexpr (GRAD) *slope = mul2(mul2(a2, L::splat(-1.f)), each(s2, r, [](float v, float i) { return v > 0.f ? i : v; }));
-        return mul2(s2, r);
+        typename L::V s2;  // 1 - a^2
+        if constexpr (NEAR0) {
+            const auto c = one_minus_exp_near0<T>(la);
+            a = fma2(c, minus, one);
+            s2 = mul2(c, add2(one, a));
+        } else {
+            a = decay<T>(la);
+            const auto u = add2(la, la);
+            s2 = each(u, one_minus_exp_near0<T>(u), mul2(a, a), [](float x, float near0, float e) { return x > -0.5f ? near0 : 1.f - e; });
+        }
+        // r = 1 / s; 10^-37 keeps it finite where s is 0: no input enters there, and s r makes its slope 0 too
+        const auto r = each(add2(s2, L::splat(1e-37f)), [](float v) { return rsqrt_ftz(v); });
+        s = mul2(s2, r);
+        if constexpr (GRAD) *slope = mul2(mul2(mul2(a, a), mul2(r, minus)), mul2(s, r));
     }
 }
+
+// A word's largest log-gate magnitude so far, as bits: larger bits of a negative
+// number are further from 0.
+__device__ __forceinline__ uint32_t further(uint32_t x, uint32_t y, __nv_bfloat16) { return __vmaxu2(x, y); }
+__device__ __forceinline__ uint32_t further(uint32_t x, uint32_t y, float) { return x > y ? x : y; }
+// Whether all are in [-1/2, 0].
+__device__ __forceinline__ bool near0(uint32_t bits, __nv_bfloat16) {
+    return (bits & 0xffffu) <= 0xbf00u && (bits >> 16) <= 0xbf00u;
+}
+__device__ __forceinline__ bool near0(uint32_t bits, float) { return bits <= 0xbf000000u; }
 
 // A run's composition.
 template <typename V> struct Run {
@@ -428,6 +455,7 @@ struct Marks {
     uint32_t starts, ends;
     int seq, row0;
     bool whole;  // every row is within [t0, t1)
+    bool near0;  // every log-gate is in [-1/2, 0]
 };
 
 constexpr int kStagesFwd = 3, kStagesBwd = 3;  // tiles of a worker's ring
@@ -489,32 +517,45 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         return p.init && live ? L::load_state(p.init + (int64_t)s * width + col) : L::splat(0.f);
     };
     // a and s x of row i of a slot
-    auto step_of = [&](const uint32_t *src, int i, V &a, V &b) {
-        const V la = L::unpack(src[i * 32]);
-        a = decay<T>(la);
+    auto step_of = [&](auto near, const uint32_t *src, int i, V &a, V &b) {
+        V s;
+        factors<T, MODE, decltype(near)::value>(L::unpack(src[i * 32]), a, s);
         b = L::unpack(src[kSlotWords + i * 32]);
-        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
+        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, s);
+    };
+    auto all_near0 = [&](const uint32_t *src) {
+        if constexpr (MODE == SSE_INPUT_PLAIN) return false;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) bits = further(bits, src[i * 32], T());
+        return (bool)__all_sync(0xffffffffu, near0(bits, T()));
     };
 
     Edges<kRows> ed;
     ed.lo = ed.hi = 0;
-    // Publishes the run of one tile's rows.  `entry`: the initial state that enters at the last start among them.
+    auto run_of = [&](auto near, Run<V> &run, const uint32_t *src) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            V a, b;
+            step_of(near, src, i, a, b);
+            run.q = fma2(a, run.q, b);
+            run.P = mul2(run.P, a);
+        }
+    };
+    // The run of one tile's rows.  `entry`: the initial state that enters at the last start among them.
     auto first_pass = [&](Marks &m, V &entry, Run<V> &run, int row0, const uint32_t *src) {
         ed.find(p, row0, sp.t0, sp.t1, lane);
-        m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1};
+        m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1, all_near0(src)};
         run = Run<V>{L::splat(1.f), L::splat(0.f)};
         if (m.starts == 0) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                V a, b;
-                step_of(src, i, a, b);
-                run.q = fma2(a, run.q, b);
-                run.P = mul2(run.P, a);
-            }
+            if (m.near0)
+                run_of(std::true_type{}, run, src);
+            else
+                run_of(std::false_type{}, run, src);
         } else {
             for (int i = 0; i < kRows; ++i) {
                 V a, b;
-                step_of(src, i, a, b);
+                step_of(std::false_type{}, src, i, a, b);
                 if ((m.starts >> i) & 1u) run.q = entry = first_state(m.seq, i);
                 run.q = fma2(a, run.q, b);
             }
@@ -527,22 +568,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         runs_published();
         cluster_arrive_relaxed();
     };
+    auto states_of = [&](auto near, V h, uint32_t *src) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            V a, b;
+            step_of(near, src, i, a, b);
+            h = fma2(a, h, b);
+            src[kSlotWords + i * 32] = L::pack(h);
+        }
+    };
     auto second_pass = [&](const Marks &m, const V &entry, V h, uint32_t *src) {
         if (p.checkpoints && live && m.row0 % kScanCheckpoint == 0 && m.row0 >= sp.t0 && m.row0 < sp.t1)
             L::store_state(p.checkpoints + (int64_t)(m.row0 / kScanCheckpoint) * width + col, h);
         if ((m.starts | m.ends) == 0) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                V a, b;
-                step_of(src, i, a, b);
-                h = fma2(a, h, b);
-                src[kSlotWords + i * 32] = L::pack(h);
-            }
+            if (m.near0)
+                states_of(std::true_type{}, h, src);
+            else
+                states_of(std::false_type{}, h, src);
         } else {
             const int last = 31 - __clz(m.starts);
             for (int i = 0; i < kRows; ++i) {
                 V a, b;
-                step_of(src, i, a, b);
+                step_of(std::false_type{}, src, i, a, b);
                 // Where the final state is written over the initial one, another worker may have done so by now for
                 // the sequence that leaves these rows, so its initial state was kept; the others end among these rows.
                 if ((m.starts >> i) & 1u) h = i == last ? entry : first_state(m.seq, i);
@@ -683,28 +730,46 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         const int q = __shfl_sync(0xffffffffu, seq, i);
         return p.d_final && live ? L::load_state(p.d_final + (int64_t)q * width + col) : L::splat(0.f);
     };
+    auto all_near0 = [&](const uint32_t *src) {
+        if constexpr (MODE == SSE_INPUT_PLAIN) return false;
+        uint32_t bits = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) bits = further(bits, src[i * 32], T());
+        return (bool)__all_sync(0xffffffffu, near0(bits, T()));
+    };
+    // a and s x of row i of a slot
+    auto step_of = [&](auto near, const uint32_t *src, int i, V &a, V &b) {
+        V s;
+        factors<T, MODE, decltype(near)::value>(L::unpack(src[i * 32]), a, s);
+        b = L::unpack(src[kSlotWords + i * 32]);
+        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, s);
+    };
     // The tile's state run and, since a run of decays is the same both ways, its
     // adjoint run in one sweep: q_back = sum over rows of (a_first ... a_row) d_row.
+    auto runs_of = [&](auto near, Run<V> &run, Run<V> &back, const uint32_t *src) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            V a, b;
+            step_of(near, src, i, a, b);
+            run.q = fma2(a, run.q, b);
+            run.P = mul2(run.P, a);
+            back.q = fma2(run.P, L::unpack(src[2 * kSlotWords + i * 32]), back.q);
+        }
+        back.P = run.P;
+    };
     auto first_pass = [&](Marks &m, Run<V> &run, Run<V> &back, int row0, const uint32_t *src) {
         ed.find(p, row0, sp.t0, sp.t1, lane);
-        m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1};
+        m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1, all_near0(src)};
         run = back = Run<V>{L::splat(1.f), L::splat(0.f)};
         if ((m.starts | m.ends) == 0) {
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const V la = L::unpack(src[i * 32]), a = decay<T>(la);
-                V b = L::unpack(src[kSlotWords + i * 32]);
-                if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
-                run.q = fma2(a, run.q, b);
-                run.P = mul2(run.P, a);
-                back.q = fma2(run.P, L::unpack(src[2 * kSlotWords + i * 32]), back.q);
-            }
-            back.P = run.P;
+            if (m.near0)
+                runs_of(std::true_type{}, run, back, src);
+            else
+                runs_of(std::false_type{}, run, back, src);
         } else {
             for (int i = 0; i < kRows; ++i) {
-                const V la = L::unpack(src[i * 32]), a = decay<T>(la);
-                V b = L::unpack(src[kSlotWords + i * 32]);
-                if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
+                V a, b;
+                step_of(std::false_type{}, src, i, a, b);
                 run.q = fma2(a, (m.starts >> i) & 1u ? first_state(m.seq, i) : run.q, b);
                 run.P = mul2(run.P, a);
             }
@@ -727,24 +792,23 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         cluster_arrive_relaxed();
     };
     // EDGES: sequences begin or end among the rows.
-    auto rows_of = [&](auto edges, const Marks &m, V state, V e, uint32_t *src) {
+    auto rows_of = [&](auto edges, auto near, const Marks &m, V state, V e, uint32_t *src) {
         constexpr bool EDGES = decltype(edges)::value;
         // forwards for the states, then backwards: dh = d + e, dx = s dh, d_log_gate = dh (a h_before + s' x)
-        V a[kRows], s[MODE == SSE_INPUT_PLAIN ? 1 : kRows], slope[kRows];
+        V a[kRows], slope[kRows];
+        [[maybe_unused]] V s[MODE == SSE_INPUT_PLAIN ? 1 : kRows];
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             if (EDGES && ((m.starts >> i) & 1u)) state = first_state(m.seq, i);
-            const V la = L::unpack(src[i * 32]);
-            V b = L::unpack(src[kSlotWords + i * 32]);
-            a[i] = decay<T>(la);
+            const V b = L::unpack(src[kSlotWords + i * 32]);
+            V si, ds;
+            factors<T, MODE, decltype(near)::value, true>(L::unpack(src[i * 32]), a[i], si, &ds);
+            slope[i] = mul2(a[i], state);
             if constexpr (MODE == SSE_INPUT_PLAIN) {
-                slope[i] = mul2(a[i], state);
                 state = add2(slope[i], b);
             } else {
-                V ds;
-                s[i] = input_factor<T, MODE, true>(la, a[i], &ds);
-                slope[i] = mul2(a[i], state);
-                state = fma2(s[i], b, slope[i]);
+                s[i] = si;
+                state = fma2(si, b, slope[i]);
                 slope[i] = fma2(ds, b, slope[i]);
             }
         }
@@ -764,10 +828,12 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         }
     };
     auto second_pass = [&](const Marks &m, V state, V e, uint32_t *src) {
-        if ((m.starts | m.ends) == 0)
-            rows_of(std::false_type{}, m, state, e, src);
+        if ((m.starts | m.ends) != 0)
+            rows_of(std::true_type{}, std::false_type{}, m, state, e, src);
+        else if (m.near0)
+            rows_of(std::false_type{}, std::true_type{}, m, state, e, src);
         else
-            rows_of(std::true_type{}, m, state, e, src);
+            rows_of(std::false_type{}, std::false_type{}, m, state, e, src);
         __syncwarp();
         store_dx.store(src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
         store_dg.store(src - lane + 2 * kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
@@ -828,9 +894,9 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs p, int width, i
     uint32_t o[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const V la = L::unpack(g[k]), a = decay<T>(la);
-        V b = L::unpack(x[k]);
-        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, input_factor<T, MODE>(la, a));
+        V a, s, b = L::unpack(x[k]);
+        factors<T, MODE, false>(L::unpack(g[k]), a, s);
+        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, s);
         h[k] = fma2(a, h[k], b);
         L::store_state(state + k * L::kCols, h[k]);
         o[k] = L::pack(h[k]);
