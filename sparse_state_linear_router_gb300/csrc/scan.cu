@@ -38,7 +38,6 @@ constexpr int kWorkers = 8;                   // warps that go through rows
 constexpr int kThreads = (kWorkers + 1) * 32;  // and the conductor
 constexpr int kRowsFwd = 16, kRowsBwd = 8;    // rows of a worker in one tile
 constexpr int kMaxCluster = 8;                // the portable cluster size
-constexpr int kSms = 152;
 static_assert(kWorkers * kRowsBwd % kScanCheckpoint == 0 && kScanCheckpoint % kRowsFwd == 0,
               "checkpoints lie at workers' first rows, and the backward's tiles at checkpoints");
 
@@ -208,15 +207,16 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int S, int t) {
     return lo;
 }
 
-// The packed tokens of one cluster: from the first sequence start at or after
-// the range's share of the tokens to that of the next range.
+// The packed tokens of one cluster: from the sequence start nearest to the
+// range's share of the tokens to that of the next range.
 __device__ __forceinline__ int range_start(const ScanArgs &p, int r, int ranges) {
     const int T = p.total_tokens, S = p.num_seqs;
     if (r >= ranges) return clamp_token(__ldg(p.cu_seqlens + S), T);
     if (r == 0) return clamp_token(__ldg(p.cu_seqlens), T);
     const int t = (int)((int64_t)T * r / ranges);
-    const int s = sequence_of(p.cu_seqlens, S, t - 1) + 1;  // the first with cu[s] >= t
-    return clamp_token(__ldg(p.cu_seqlens + (s < S ? s : S)), T);
+    const int s = sequence_of(p.cu_seqlens, S, t);
+    const int lo = __ldg(p.cu_seqlens + (s < 0 ? 0 : s)), hi = __ldg(p.cu_seqlens + (s < S ? s + 1 : S));
+    return clamp_token(t - lo <= hi - t ? lo : hi, T);
 }
 
 // Where sequences begin and end among the rows of a warp.
@@ -906,6 +906,30 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs p, int width, i
 
 enum What { kForward, kBackward, kStep };
 
+// Cluster size and ranges of the token axis: as many CTAs as the GPU holds at a
+// time, two per SM (a second wave of clusters would double the time: at 2560
+// channels and 20000 tokens, 40 clusters of 7 took 99 us where 40 of 6 take 72).  More ranges of
+// whole sequences split the tokens less evenly than more CTAs of one cluster
+// (counted as half a sequence per range), so they serve narrow rows.
+void choose_clusters(int columns, int64_t tiles, int num_seqs, int &csize, int &ranges) {
+    // Clusters of 1 to 8 CTAs that an idle GPU held, less a few: 304, 152, 97, 74, 58, 46, 38, 36.
+    static const int held[kMaxCluster + 1] = {0, 304, 148, 93, 71, 55, 44, 36, 34};
+    double best = 0;
+    for (int c = kMaxCluster; c >= 1; --c) {
+        if ((c > 1 && columns > held[c]) || (c > 1 && c > tiles)) continue;
+        int64_t r = held[c] / columns;
+        if (r > num_seqs) r = num_seqs;
+        if (r > tiles / c) r = tiles / c;
+        if (r < 1) r = 1;
+        const double ctas = (double)columns * c * r / (r > 1 ? 1 + 0.5 * r / num_seqs : 1);
+        if (ctas > best) {
+            best = ctas;
+            csize = c;
+            ranges = (int)r;
+        }
+    }
+}
+
 template <typename T, int MODE>
 cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t stream) {
     if (what == kStep) {
@@ -915,26 +939,18 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
         scan_step_kernel<T, MODE><<<(unsigned)blocks, 128, 0, stream>>>(a, width, words);
         return cudaGetLastError();
     }
-    // As many CTAs as the GPU holds (two per SM): the cluster takes what the
-    // columns leave, but no more tiles than there are; with fewer columns the
-    // token axis is split into ranges of whole sequences as well.
     const int columns = (width + 32 * Lane<T>::kCols - 1) / (32 * Lane<T>::kCols);
     const int rows = what == kForward ? kRowsFwd : kRowsBwd, tile = kWorkers * rows;
     const int64_t tiles = ((int64_t)a.total_tokens + tile - 1) / tile;
-    int csize = 2 * kSms / columns;
-    csize = csize > kMaxCluster ? kMaxCluster : csize < 1 ? 1 : csize;
-    if (csize > tiles) csize = tiles < 1 ? 1 : (int)tiles;
-    int64_t ranges = 2 * kSms / (columns * csize);
-    if (ranges > a.num_seqs) ranges = a.num_seqs;
-    if (ranges > tiles / csize) ranges = tiles / csize;
-    if (ranges < 1) ranges = 1;
+    int csize = 1, ranges = 1;
+    choose_clusters(columns, tiles, a.num_seqs, csize, ranges);
     const auto kernel = what == kForward ? scan_forward_kernel<T, MODE> : scan_backward_kernel<T, MODE>;
     const size_t smem = (size_t)tile * 128 * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.dynamicSmemBytes = smem;
-    cfg.gridDim = dim3(columns * csize, (unsigned)ranges);
+    cfg.gridDim = dim3(columns * csize, ranges);
     cfg.blockDim = kThreads;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
