@@ -263,24 +263,38 @@ template <int ROWS> struct RowCopy {
         four = 4 * stride_bytes;
         step = rows * stride_bytes;
     }
-    // row0: the tile's first row; whole: all its rows are within [t0, t1)
+    // row0: the tile's first row; whole: all its rows are within [t0, t1).  Lanes past the row's end copy nothing: their
+    // words start as zeros, and zeros are what rows of zeros leave in them.
     __device__ __forceinline__ void copy(uint32_t dst, const void *base, int row0, int t0, int t1, bool whole, bool col_ok,
                                          int lane) {
         const char *src = at;
+        if (whole) {
+            if (col_ok) {
 #pragma unroll
-        for (int k = 0; k < ROWS; k += 4) {
-            bool ok = col_ok;
-            if (!whole) {
-                const int row = row0 + k + (lane >> 3);
-                ok = ok && row >= t0 && row < t1;
+                for (int k = 0; k < ROWS; k += 4) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 128 + lane * 16), "l"(src) : "memory");
+                    src += four;
+                }
             }
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16),
-                         "l"(ok ? src : static_cast<const char *>(base)), "r"(ok ? 16 : 0) : "memory");
-            src += four;
+        } else {
+#pragma unroll
+            for (int k = 0; k < ROWS; k += 4) {
+                const int row = row0 + k + (lane >> 3);
+                const bool ok = col_ok && row >= t0 && row < t1;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16),
+                             "l"(ok ? src : static_cast<const char *>(base)), "r"(ok ? 16 : 0) : "memory");
+                src += four;
+            }
         }
         at += step;
     }
 };
+// Zeros in a worker's ring of `words` 16-byte words, for the lanes that copy nothing.
+__device__ __forceinline__ void clear_ring(uint32_t *mine, int words, bool col_ok, int lane) {
+    if (!col_ok)
+        for (int k = lane; k < words; k += 32) reinterpret_cast<uint4 *>(mine)[k] = make_uint4(0, 0, 0, 0);
+    __syncwarp();
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Waits until at most N of this thread's groups are in flight; then the whole warp's rows are there.
 template <int N> __device__ __forceinline__ void copies_wait() {
@@ -496,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
     const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
     const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
+    clear_ring(mine, kStagesFwd * 2 * kSlotBytes / 16, col_ok, lane);
     const int first_row = (sp.tile0 + rank) * kTile + warp * kRows, stride = csize * kTile;
     RowCopy<kRows> copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, stride, lane);
     RowCopy<kRows> copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, stride, lane);
@@ -699,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
     const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
     const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
+    clear_ring(mine, kStagesBwd * 3 * kSlotBytes / 16, col_ok, lane);
     const int first_row = last_tile * kTile + warp * kRows, stride = csize * kTile;
     const int64_t packed = (int64_t)width * (int)sizeof(T);
     RowCopy<kRows> copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, -stride, lane);
@@ -908,9 +924,11 @@ enum What { kForward, kBackward, kStep };
 
 // Cluster size and ranges of the token axis: as many CTAs as the GPU holds at a
 // time, two per SM (a second wave of clusters would double the time: at 2560
-// channels and 20000 tokens, 40 clusters of 7 took 99 us where 40 of 6 take 72).  More ranges of
-// whole sequences split the tokens less evenly than more CTAs of one cluster
-// (counted as half a sequence per range), so they serve narrow rows.
+// channels and 20000 tokens, 40 clusters of 7 took 99 us where 40 of 6 take 72).
+// Larger clusters wait longer for each other (72000 x 2048 channels in 16 even
+// sequences: 192, 176, 168, 161 us with 8, 4, 2, 1 CTAs in 1, 2, 4, 8 ranges);
+// more ranges of whole sequences split uneven lengths less evenly (sequences cut
+// at random: the largest of R ranges is R^2 / 4S over its share; counted half).
 void choose_clusters(int columns, int64_t tiles, int num_seqs, int &csize, int &ranges) {
     // Clusters of 1 to 8 CTAs that an idle GPU held, less a few: 304, 152, 97, 74, 58, 46, 38, 36.
     static const int held[kMaxCluster + 1] = {0, 304, 148, 93, 71, 55, 44, 36, 34};
@@ -921,9 +939,9 @@ void choose_clusters(int columns, int64_t tiles, int num_seqs, int &csize, int &
         if (r > num_seqs) r = num_seqs;
         if (r > tiles / c) r = tiles / c;
         if (r < 1) r = 1;
-        const double ctas = (double)columns * c * r / (r > 1 ? 1 + 0.5 * r / num_seqs : 1);
-        if (ctas > best) {
-            best = ctas;
+        const double rate = (double)columns * c * r / ((1 + 0.025 * c) * (r > 1 ? 1 + 0.125 * r * r / num_seqs : 1));
+        if (rate > best) {
+            best = rate;
             csize = c;
             ranges = (int)r;
         }
