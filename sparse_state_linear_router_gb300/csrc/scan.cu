@@ -253,42 +253,31 @@ template <int ROWS> struct Edges {
 // else.  Rows outside [t0, t1) are filled with zeros, which change nothing:
 // decay 1, input 0.
 // ---------------------------------------------------------------------------
-template <int ROWS> struct RowCopy {
-    const char *at;      // this lane's 16 bytes of the first four rows of the next tile to copy
-    int64_t four, step;  // bytes to four rows on, to the next tile
-    // base: the tensor's first row and column; row0: the first tile's first row; rows: to the next tile
-    __device__ __forceinline__ RowCopy(const void *base, int64_t stride_bytes, int64_t col_byte, int row0, int rows,
-                                       int lane) {
-        at = static_cast<const char *>(base) + (row0 + (lane >> 3)) * stride_bytes + col_byte;
-        four = 4 * stride_bytes;
-        step = rows * stride_bytes;
-    }
-    // row0: the tile's first row; whole: all its rows are within [t0, t1).  Lanes past the row's end copy nothing: their
-    // words start as zeros, and zeros are what rows of zeros leave in them.
-    __device__ __forceinline__ void copy(uint32_t dst, const void *base, int row0, int t0, int t1, bool whole, bool col_ok,
-                                         int lane) {
-        const char *src = at;
-        if (whole) {
-            if (col_ok) {
+// row0: the tile's first row; whole: all its rows are within [t0, t1).  Lanes
+// past the row's end copy nothing: their words start as zeros, and zeros are
+// what rows of zeros leave in them.  (Addresses are formed anew for each tile:
+// running pointers for every tensor took 30 registers.)
+template <int ROWS>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const void *base, int64_t stride, int col_byte, int row0, int t0,
+                                          int t1, bool whole, bool col_ok, int lane) {
+    const char *src = static_cast<const char *>(base) + (row0 + (lane >> 3)) * stride + col_byte;
+    if (whole) {
+        if (col_ok) {
 #pragma unroll
-                for (int k = 0; k < ROWS; k += 4) {
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 128 + lane * 16), "l"(src) : "memory");
-                    src += four;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < ROWS; k += 4) {
-                const int row = row0 + k + (lane >> 3);
-                const bool ok = col_ok && row >= t0 && row < t1;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16),
-                             "l"(ok ? src : static_cast<const char *>(base)), "r"(ok ? 16 : 0) : "memory");
-                src += four;
-            }
+            for (int k = 0; k < ROWS; k += 4)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 128 + lane * 16), "l"(src + k * stride)
+                             : "memory");
         }
-        at += step;
+    } else {
+#pragma unroll
+        for (int k = 0; k < ROWS; k += 4) {
+            const int row = row0 + k + (lane >> 3);
+            const bool ok = col_ok && row >= t0 && row < t1;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + k * 128 + lane * 16),
+                         "l"(ok ? src + k * stride : static_cast<const char *>(base)), "r"(ok ? 16 : 0) : "memory");
+        }
     }
-};
+}
 // Zeros in a worker's ring of `words` 16-byte words, for the lanes that copy nothing.
 __device__ __forceinline__ void clear_ring(uint32_t *mine, int words, bool col_ok, int lane) {
     if (!col_ok)
@@ -304,30 +293,21 @@ template <int N> __device__ __forceinline__ void copies_wait() {
 
 // A worker's results go back through the slot they were made from, each word in
 // the place of the input it replaces, and out in 16-byte words.
-template <int ROWS> struct RowStore {
-    char *at;
-    int64_t four, step;
-    __device__ __forceinline__ RowStore(void *base, int64_t stride_bytes, int64_t col_byte, int row0, int rows, int lane) {
-        at = static_cast<char *>(base) + (row0 + (lane >> 3)) * stride_bytes + col_byte;
-        four = 4 * stride_bytes;
-        step = rows * stride_bytes;
-    }
-    __device__ __forceinline__ void store(const uint32_t *src, int row0, int t0, int t1, bool whole, bool col_ok, int lane) {
-        char *dst = at;
+template <int ROWS>
+__device__ __forceinline__ void store_rows(void *base, int64_t stride, int col_byte, const uint32_t *src, int row0, int t0,
+                                           int t1, bool whole, bool col_ok, int lane) {
+    char *dst = static_cast<char *>(base) + (row0 + (lane >> 3)) * stride + col_byte;
 #pragma unroll
-        for (int k = 0; k < ROWS; k += 4) {
-            bool ok = col_ok;
-            if (!whole) {
-                const int row = row0 + k + (lane >> 3);
-                ok = ok && row >= t0 && row < t1;
-            }
-            const uint4 u = *reinterpret_cast<const uint4 *>(src + k * 32 + lane * 4);
-            if (ok) *reinterpret_cast<uint4 *>(dst) = u;
-            dst += four;
+    for (int k = 0; k < ROWS; k += 4) {
+        bool ok = col_ok;
+        if (!whole) {
+            const int row = row0 + k + (lane >> 3);
+            ok = ok && row >= t0 && row < t1;
         }
-        at += step;
+        const uint4 u = *reinterpret_cast<const uint4 *>(src + k * 32 + lane * 4);
+        if (ok) *reinterpret_cast<uint4 *>(dst + k * stride) = u;
     }
-};
+}
 
 // ---------------------------------------------------------------------------
 // Exchange.  The workers of a CTA publish their rows' runs and go on with the
@@ -509,19 +489,18 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesFwd * 2 * kSlotWords);
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
     const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
-    const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
+    const int col_byte = col0 * (int)sizeof(T) + (lane & 7) * 16;
     clear_ring(mine, kStagesFwd * 2 * kSlotBytes / 16, col_ok, lane);
     const int first_row = (sp.tile0 + rank) * kTile + warp * kRows, stride = csize * kTile;
-    RowCopy<kRows> copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, stride, lane);
-    RowCopy<kRows> copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, stride, lane);
-    RowStore<kRows> store_out(p.out, (int64_t)width * (int)sizeof(T), col_byte, first_row, stride, lane);
+    const int64_t packed = (int64_t)width * (int)sizeof(T);
     int load_slot = 0, load_row = first_row;
     auto load = [&](int step) {  // called for one step after the other
         if (step < sp.steps) {
             const uint32_t dst = ring_at + load_slot * (2 * kSlotBytes);
             const bool whole = load_row >= sp.t0 && load_row + kRows <= sp.t1;
-            copy_g.copy(dst, p.log_gate, load_row, sp.t0, sp.t1, whole, col_ok, lane);
-            copy_x.copy(dst + kSlotBytes, p.x, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_rows<kRows>(dst, p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, load_row, sp.t0, sp.t1, whole, col_ok,
+                             lane);
+            copy_rows<kRows>(dst + kSlotBytes, p.x, p.x_stride * (int)sizeof(T), col_byte, load_row, sp.t0, sp.t1, whole, col_ok, lane);
             load_slot = load_slot + 1 == kStagesFwd ? 0 : load_slot + 1;
             load_row += stride;
         }
@@ -617,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
             }
         }
         __syncwarp();
-        store_out.store(src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
+        store_rows<kRows>(p.out, packed, col_byte, src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
         __syncwarp();  // the slot is free
     };
     if (sp.steps > 0) {
@@ -713,23 +692,19 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
     uint32_t *mine = reinterpret_cast<uint32_t *>(ring) + warp * (kStagesBwd * 3 * kSlotWords);
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(mine);
     const bool col_ok = col0 + (lane & 7) * (16 / (int)sizeof(T)) < width;
-    const int64_t col_byte = (int64_t)col0 * sizeof(T) + (lane & 7) * 16;
+    const int col_byte = col0 * (int)sizeof(T) + (lane & 7) * 16;
     clear_ring(mine, kStagesBwd * 3 * kSlotBytes / 16, col_ok, lane);
     const int first_row = last_tile * kTile + warp * kRows, stride = csize * kTile;
     const int64_t packed = (int64_t)width * (int)sizeof(T);
-    RowCopy<kRows> copy_g(p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, first_row, -stride, lane);
-    RowCopy<kRows> copy_x(p.x, p.x_stride * (int)sizeof(T), col_byte, first_row, -stride, lane);
-    RowCopy<kRows> copy_d(p.d_out, packed, col_byte, first_row, -stride, lane);
-    RowStore<kRows> store_dx(p.dx, packed, col_byte, first_row, -stride, lane);
-    RowStore<kRows> store_dg(p.d_log_gate, packed, col_byte, first_row, -stride, lane);
     int load_slot = 0, load_row = first_row;
     auto load = [&](int step) {  // called for one step after the other
         if (step < sp.steps) {
             const uint32_t dst = ring_at + load_slot * (3 * kSlotBytes);
             const bool whole = load_row >= sp.t0 && load_row + kRows <= sp.t1;
-            copy_g.copy(dst, p.log_gate, load_row, sp.t0, sp.t1, whole, col_ok, lane);
-            copy_x.copy(dst + kSlotBytes, p.x, load_row, sp.t0, sp.t1, whole, col_ok, lane);
-            copy_d.copy(dst + 2 * kSlotBytes, p.d_out, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_rows<kRows>(dst, p.log_gate, p.gate_stride * (int)sizeof(T), col_byte, load_row, sp.t0, sp.t1, whole, col_ok,
+                             lane);
+            copy_rows<kRows>(dst + kSlotBytes, p.x, p.x_stride * (int)sizeof(T), col_byte, load_row, sp.t0, sp.t1, whole, col_ok, lane);
+            copy_rows<kRows>(dst + 2 * kSlotBytes, p.d_out, packed, col_byte, load_row, sp.t0, sp.t1, whole, col_ok, lane);
             load_slot = load_slot + 1 == kStagesBwd ? 0 : load_slot + 1;
             load_row -= stride;
         }
@@ -851,8 +826,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         else
             rows_of(std::false_type{}, std::false_type{}, m, state, e, src);
         __syncwarp();
-        store_dx.store(src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
-        store_dg.store(src - lane + 2 * kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
+        store_rows<kRows>(p.dx, packed, col_byte, src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
+        store_rows<kRows>(p.d_log_gate, packed, col_byte, src - lane + 2 * kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
         __syncwarp();  // the slot is free
     };
     if (sp.steps > 0) {
