@@ -383,7 +383,8 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
  *   d_initial_state = a_1 dh_1
  * with the states recomputed in float32 from the checkpoints.  With
  * SSE_INPUT_UNIT, s' is unbounded at log_gate = 0 and taken as zero there.
- * d_final_state and d_initial_state may be NULL; they do not overlap.
+ * d_final_state and d_initial_state may be NULL.  Apart from final_state,
+ * outputs do not overlap inputs.
  * Tokens at and past cu_seqlens[num_seqs] (a padded batch) belong to no
  * sequence: their rows are not read and the outputs' rows stay as they were.
  * All sums and states are float32, rounded once to cfg->dtype at the end, and
@@ -463,9 +464,11 @@ sse_status_t sse_scan_step(const sse_scan_config_t *cfg, const void *x, int64_t 
  * Workspace (backward only): sse_block_norm_backward_workspace_size bytes,
  * 256-byte aligned, contents undefined on entry and exit.
  *
- * Sums are float32.  width is at most 16384 for SSE_BF16 and 8192 for SSE_F32;
- * width, group and the row strides are whole 16-byte words of cfg->dtype; eps
- * is positive; total_tokens is below 2^31.
+ * Sums are float32: values whose squares leave its range (above 1.8e19) are
+ * outside.  Apart from residual_out, outputs do not overlap inputs.  width is at
+ * most 16384 for SSE_BF16 and 8192 for SSE_F32; width, group and the row strides
+ * are whole 16-byte words of cfg->dtype; eps is a positive normal number;
+ * total_tokens is below 2^31.
  * ------------------------------------------------------------------------- */
 typedef enum {
     SSE_GATE_NONE = 0,

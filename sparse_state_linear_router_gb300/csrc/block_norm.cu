@@ -12,12 +12,18 @@
 //          dc = branch_scale w_after C;  dw_before_j = sum of dx' r_hat
 //
 // Bound by HBM: about 16 to 40 operations per element against 4 to 16 bytes.
-// A team of threads covers a row, 16 bytes per thread and tensor, and goes from
-// row to row; each thread copies its own words of the rows ahead to shared
-// memory asynchronously (no barrier: nobody else reads them), so the loads of
-// the next rows are in flight while this one is summed.  Sums over the row go
-// through shuffles and one word per warp of shared memory; sums over a group of
-// columns through shuffles where the group is a power of two of lanes.
+// A team of threads covers a row, two 16-byte words per thread (one for rows up
+// to 512 bytes), and goes from row to row; each thread copies its own words of
+// the rows ahead to shared memory asynchronously (no barrier: nobody else reads
+// them), so the next rows' loads are in flight while this one is summed.  Sums
+// over the row go through shuffles and one word per warp of shared memory; sums
+// over a group of columns through shuffles where the group is a power of two of
+// lanes.  Arithmetic is on float32 pairs.  Measured on a GB300, bf16, against
+// the bytes at 6.77 TB/s: per-head norm and gate of 32768 x 2048 67 us (floor
+// 59.5); norm, scale, residual and next norm of 16384 x 2304 54 us (44.6);
+// backward of head norm, gate, residual and next norm of 32768 x 2048 189 us
+// (158.6).  One word per thread left the same backward at 254 us: the control
+// flow of a row (about 150 of 600 instructions per word) is shared by two words.
 #include "f32x2.cuh"
 #include "sse_internal.cuh"
 

@@ -2,26 +2,35 @@
 // state per channel: forward, backward and one step.
 //
 // A run of steps composes to h -> P h + q (P the product of its decays, q what
-// it makes of a zero state), and runs compose in order, so a long sequence is
+// it makes of a zero state), and runs compose in order.  So a long sequence is
 // split over warps and CTAs: each makes its rows' (P, q), the runs ahead are
 // composed to the state the rows start from, and the rows are gone through
-// again from that state.  Rows stay in registers between the two, so HBM is
+// again from that state.  Rows stay in shared memory between the two, so HBM is
 // read once and written once.
 //
-//  - A lane has 4 bytes of a row (two bf16 channels, or one float32), a warp
-//    one 128-byte line of each of kRows consecutive rows, a CTA 8 x kRows rows.
-//  - The CTAs of a cluster take consecutive tiles of the same 128-byte column
-//    and hand their (P, q) to each other through distributed shared memory;
-//    then the cluster moves on by its size.  Nothing waits on global memory, no
-//    workspace, and the order of every product and sum is fixed.
+//  - A lane has 4 bytes of a row (two bf16 channels as a float32 pair, or one
+//    float32), a warp ("worker") one 128-byte line of each of 16 (backward: 8)
+//    consecutive rows, a CTA eight workers' rows: its tile.
+//  - The CTAs of a cluster take consecutive tiles of the same 128-byte column,
+//    hand their (P, q) to each other through distributed shared memory and move
+//    on by the cluster's size.  The workers make the next tile's run while a
+//    ninth warp (the conductor) composes and exchanges this one's.  Nothing
+//    waits on global memory, there is no workspace, and the order of every
+//    product and sum is fixed.
 //  - The batch's packed token axis is one axis: a sequence's first row starts
-//    from its own initial state (a reset: P = 0), its last one writes the final
-//    state, so uneven lengths cost nothing.  A reset is a select and no
-//    product with zero: a NaN of one sequence does not reach the next.
-//  - Loads of the next tile are issued before the cluster's barrier.
+//    from its own initial state (a reset), its last one writes the final state,
+//    so uneven lengths cost nothing.  A reset is a select and no product with
+//    zero: a NaN of one sequence does not reach the next.
+//  - Rows come by asynchronous copies up to three tiles ahead, in 16-byte
+//    words, and leave in 16-byte words from the place of the inputs they replace.
 //
-// Bound by HBM: 6 bytes and about 20 (plain) to 45 (unit) instructions per two
-// bf16 channels forward, 10 bytes backward.
+// Measured on a GB300 (72000 tokens x 2048 channels in bf16, one sequence; HBM
+// floor at 6.77 TB/s): forward 131 us, took 175 us with s = 1 and 301 us with
+// s = sqrt(1 - a^2); backward 218 us, took 299 us and 477 us.  One sequence per
+// cluster of 8 waits for the exchange (a step of 1024 rows in 2.5 us); with
+// s = sqrt(1 - a^2) the arithmetic (about 65 instructions per two channels and
+// row, twice through the rows) is the longer part.  An earlier form with the rows
+// in registers and every warp composing for itself took 413 us (s = 1).
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -54,11 +63,6 @@ template <typename F> __device__ __forceinline__ F2 each(F2 x, F f) {
     return f2(f(v.x), f(v.y));
 }
 template <typename F> __device__ __forceinline__ float each(float x, F f) { return f(x); }
-template <typename F> __device__ __forceinline__ F2 each(F2 x, F2 y, F f) {
-    const float2 v = f2_get(x), w = f2_get(y);
-    return f2(f(v.x, w.x), f(v.y, w.y));
-}
-template <typename F> __device__ __forceinline__ float each(float x, float y, F f) { return f(x, y); }
 template <typename F> __device__ __forceinline__ F2 each(F2 x, F2 y, F2 z, F f) {
     const float2 v = f2_get(x), w = f2_get(y), u = f2_get(z);
     return f2(f(v.x, w.x, u.x), f(v.y, w.y, u.y));

@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <limits>
 
 #include "sse_internal.cuh"
 
@@ -731,7 +732,7 @@ sse_status_t check_norm(const sse_norm_config_t *cfg, int64_t total_tokens) {
     const sse_norm_config_t &c = *cfg;
     if (c.width < 1 || c.group < 0 || (c.dtype != SSE_F32 && c.dtype != SSE_BF16)) return SSE_ERR_INVALID_ARG;
     if (c.gate < SSE_GATE_NONE || c.gate > SSE_GATE_LINEAR || total_tokens < 0) return SSE_ERR_INVALID_ARG;
-    if (!(c.eps > 0.f) || !std::isfinite(c.eps) || !std::isfinite(c.residual_scale) || !std::isfinite(c.branch_scale))
+    if (!(c.eps >= std::numeric_limits<float>::min()) || !std::isfinite(c.eps) || !std::isfinite(c.residual_scale) || !std::isfinite(c.branch_scale))
         return SSE_ERR_INVALID_ARG;
     if (c.group > 0 && c.width % c.group) return SSE_ERR_INVALID_ARG;
     const int vec = c.dtype == SSE_BF16 ? 8 : 4;

@@ -86,7 +86,7 @@ def test_norm_refuses(b):
     assert _norm(b, mk(8196, dtype="f32"), os=8196, rs=8196) == U
     assert _norm(b, mk(64, gate=4)) == I
     assert _norm(b, mk(64, dtype=3)) == I
-    for eps in (0.0, -1.0, float("nan"), float("inf")):
+    for eps in (0.0, -1.0, 1e-40, float("nan"), float("inf")):
         assert _norm(b, mk(64, eps=eps)) == I
     assert _norm(b, mk(64, residual_scale=float("nan"))) == I
     assert _norm(b, mk(64, branch_scale=float("inf"))) == I
