@@ -460,11 +460,18 @@ constexpr int kStagesFwd = 3, kStagesBwd = 3;  // tiles of a worker's ring
 
 // ---------------------------------------------------------------------------
 // Forward.  grid.x: column x cluster rank, grid.y: ranges of the token axis.
-// Each tile's rows are gone through twice from shared memory, once for their
-// run and once from their start; the decays are made twice, which is cheaper
-// than the registers that would hold them.
+// Each tile's rows are gone through twice, once for their run and once from
+// their start.  Two forms:
+//  - HOLD false: the next tile's run is made while this one's is exchanged, and
+//    the second pass makes the decays and inputs again from shared memory;
+//  - HOLD true: they stay in registers between the passes, and only the SM's
+//    other CTA is at work during the exchange.  For input factors that cost more
+//    than the wait, where each SM has two CTAs.
+// 72000 tokens x 2048 channels, one sequence: s = 1 175 against 191 us (HOLD),
+// s = sqrt(1 - a^2) 301 against 240 us; at 512 channels, where an SM has one CTA
+// at most, 150 against 189 us.
 // ---------------------------------------------------------------------------
-template <typename T, int MODE>
+template <typename T, int MODE, bool HOLD>
 __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     using V = typename L::V;
@@ -514,13 +521,6 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         const int s = __shfl_sync(0xffffffffu, seq, i);
         return p.init && live ? L::load_state(p.init + (int64_t)s * width + col) : L::splat(0.f);
     };
-    // a and s x of row i of a slot
-    auto step_of = [&](auto near, const uint32_t *src, int i, V &a, V &b) {
-        V s;
-        factors<T, MODE, decltype(near)::value>(L::unpack(src[i * 32]), a, s);
-        b = L::unpack(src[kSlotWords + i * 32]);
-        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, s);
-    };
     auto all_near0 = [&](const uint32_t *src) {
         if constexpr (MODE == SSE_INPUT_PLAIN) return false;
         uint32_t bits = 0;
@@ -528,34 +528,73 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         for (int i = 0; i < kRows; ++i) bits = further(bits, src[i * 32], T());
         return (bool)__all_sync(0xffffffffu, near0(bits, T()));
     };
+    // a and s x of row i of a slot
+    auto make_row = [&](auto near, const uint32_t *src, int i, V &a, V &b) {
+        V s;
+        factors<T, MODE, decltype(near)::value>(L::unpack(src[i * 32]), a, s);
+        b = L::unpack(src[kSlotWords + i * 32]);
+        if constexpr (MODE != SSE_INPUT_PLAIN) b = mul2(b, s);
+    };
+    V held_a[HOLD ? kRows : 1], held_b[HOLD ? kRows : 1];
+    auto hold_rows = [&](auto near, const uint32_t *src) {
+#pragma unroll
+        for (int i = 0; i < (HOLD ? kRows : 0); ++i) make_row(near, src, i, held_a[i], held_b[i]);
+    };
+    auto row_of = [&](auto near, const uint32_t *src, int i, V &a, V &b) {
+        if constexpr (HOLD) {
+            a = held_a[i];
+            b = held_b[i];
+        } else {
+            make_row(near, src, i, a, b);
+        }
+    };
 
     Edges<kRows> ed;
     ed.lo = ed.hi = 0;
+    // The run of one tile's rows.  `entry`: the initial state that enters at the last start among them (HOLD: it goes
+    // into the row's held input).
     auto run_of = [&](auto near, Run<V> &run, const uint32_t *src) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             V a, b;
-            step_of(near, src, i, a, b);
+            row_of(near, src, i, a, b);
             run.q = fma2(a, run.q, b);
             run.P = mul2(run.P, a);
         }
     };
-    // The run of one tile's rows.  `entry`: the initial state that enters at the last start among them.
     auto first_pass = [&](Marks &m, V &entry, Run<V> &run, int row0, const uint32_t *src) {
         ed.find(p, row0, sp.t0, sp.t1, lane);
         m = Marks{ed.starts, ed.ends, ed.seq, row0, row0 >= sp.t0 && row0 + kRows <= sp.t1, all_near0(src)};
+        if constexpr (HOLD) {
+            if (m.near0)
+                hold_rows(std::true_type{}, src);
+            else
+                hold_rows(std::false_type{}, src);
+        }
         run = Run<V>{L::splat(1.f), L::splat(0.f)};
         if (m.starts == 0) {
-            if (m.near0)
+            if (!HOLD && m.near0)
                 run_of(std::true_type{}, run, src);
             else
                 run_of(std::false_type{}, run, src);
         } else {
+#pragma unroll(HOLD ? kRows : 1)
             for (int i = 0; i < kRows; ++i) {
                 V a, b;
-                step_of(std::false_type{}, src, i, a, b);
-                if ((m.starts >> i) & 1u) run.q = entry = first_state(m.seq, i);
-                run.q = fma2(a, run.q, b);
+                row_of(std::false_type{}, src, i, a, b);
+                if ((m.starts >> i) & 1u) {
+                    // Read here and not again for the sequence that leaves these rows: where the final state is written
+                    // over the initial one, another worker may have done so by the second pass.
+                    if constexpr (HOLD) {
+                        held_b[i] = fma2(a, first_state(m.seq, i), b);
+                        run.q = held_b[i];
+                    } else {
+                        entry = first_state(m.seq, i);
+                        run.q = fma2(a, entry, b);
+                    }
+                } else {
+                    run.q = fma2(a, run.q, b);
+                }
             }
             run.P = L::splat(0.f);
         }
@@ -570,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
             V a, b;
-            step_of(near, src, i, a, b);
+            row_of(near, src, i, a, b);
             h = fma2(a, h, b);
             src[kSlotWords + i * 32] = L::pack(h);
         }
@@ -579,19 +618,23 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         if (p.checkpoints && live && m.row0 % kScanCheckpoint == 0 && m.row0 >= sp.t0 && m.row0 < sp.t1)
             L::store_state(p.checkpoints + (int64_t)(m.row0 / kScanCheckpoint) * width + col, h);
         if ((m.starts | m.ends) == 0) {
-            if (m.near0)
+            if (!HOLD && m.near0)
                 states_of(std::true_type{}, h, src);
             else
                 states_of(std::false_type{}, h, src);
         } else {
-            const int last = 31 - __clz(m.starts);
+            [[maybe_unused]] const int last = 31 - __clz(m.starts);
+#pragma unroll(HOLD ? kRows : 1)
             for (int i = 0; i < kRows; ++i) {
                 V a, b;
-                step_of(std::false_type{}, src, i, a, b);
-                // Where the final state is written over the initial one, another worker may have done so by now for
-                // the sequence that leaves these rows, so its initial state was kept; the others end among these rows.
-                if ((m.starts >> i) & 1u) h = i == last ? entry : first_state(m.seq, i);
-                h = fma2(a, h, b);
+                row_of(std::false_type{}, src, i, a, b);
+                const bool start = (m.starts >> i) & 1u;
+                if constexpr (HOLD) {
+                    h = start ? b : fma2(a, h, b);
+                } else {
+                    if (start) h = i == last ? entry : first_state(m.seq, i);  // the others end among these rows
+                    h = fma2(a, h, b);
+                }
                 src[kSlotWords + i * 32] = L::pack(h);
                 if ((m.ends >> i) & 1u) {
                     const int s = __shfl_sync(0xffffffffu, m.seq, i);
@@ -603,32 +646,49 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         store_rows<kRows>(p.out, packed, col_byte, src - lane + kSlotWords, m.row0, sp.t0, sp.t1, m.whole, col_ok, lane);
         __syncwarp();  // the slot is free
     };
-    if (sp.steps > 0) {
-        Marks now, next;
-        V entry = L::splat(0.f), next_entry = entry;
-        Run<V> run;
-        int slot = 0, row0 = first_row;
-        for (int k = 0; k < kStagesFwd; ++k) load(k);
+    auto slot = [&](int at) { return mine + at * (2 * kSlotWords) + lane; };
+    auto take_start = [&] {
+        await_starts();
+        const V h = ex.start[warp][lane];
+        cluster_wait();
+        return h;
+    };
+    Marks now;
+    V entry = L::splat(0.f);
+    Run<V> run;
+    for (int k = 0; k < kStagesFwd; ++k) load(k);
+    if constexpr (HOLD) {
+        int at = 0, row0 = first_row;
+        for (int step = 0; step < sp.steps; ++step, row0 += stride) {
+            copies_wait<kStagesFwd - 1>();
+            first_pass(now, entry, run, row0, slot(at));
+            publish(now, run);
+            const V h = take_start();
+            second_pass(now, entry, h, slot(at));
+            load(step + kStagesFwd);
+            at = at + 1 == kStagesFwd ? 0 : at + 1;
+        }
+    } else if (sp.steps > 0) {
+        Marks next;
+        V next_entry = entry;
         copies_wait<kStagesFwd - 1>();
-        first_pass(now, entry, run, row0, mine + lane);
+        first_pass(now, entry, run, first_row, slot(0));
         publish(now, run);
+        int at = 0;
         for (int step = 0; step < sp.steps; ++step) {
             const bool more = step + 1 < sp.steps;
-            const int next_slot = slot + 1 == kStagesFwd ? 0 : slot + 1;
+            const int next_at = at + 1 == kStagesFwd ? 0 : at + 1;
             if (more) {
-                row0 += stride;
                 copies_wait<kStagesFwd - 2>();
-                first_pass(next, next_entry, run, row0, mine + next_slot * (2 * kSlotWords) + lane);
+                first_pass(next, next_entry, run, now.row0 + stride, slot(next_at));
             }
-            await_starts();
-            const V h = ex.start[warp][lane];
-            cluster_wait();
+            const V h = take_start();
             if (more) publish(next, run);
-            second_pass(now, entry, h, mine + slot * (2 * kSlotWords) + lane);
+            second_pass(now, entry, h, slot(at));
             load(step + kStagesFwd);
             now = next;
             entry = next_entry;
-            slot = next_slot;
+            at = next_at;
         }
     }
     // empty sequences keep their initial state
@@ -941,7 +1001,11 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     const int64_t tiles = ((int64_t)a.total_tokens + tile - 1) / tile;
     int csize = 1, ranges = 1;
     choose_clusters(columns, tiles, a.num_seqs, csize, ranges);
-    const auto kernel = what == kForward ? scan_forward_kernel<T, MODE> : scan_backward_kernel<T, MODE>;
+    constexpr bool kHeavy = MODE != SSE_INPUT_PLAIN;
+    const bool hold = kHeavy && columns * csize * ranges >= 192;  // two CTAs on a quarter of the SMs or more
+    const auto kernel = what == kBackward ? scan_backward_kernel<T, MODE>
+                        : hold            ? scan_forward_kernel<T, MODE, kHeavy>
+                                          : scan_forward_kernel<T, MODE, false>;
     const size_t smem = (size_t)tile * 128 * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
