@@ -312,6 +312,29 @@ def test_many_rows():
         assert torch.equal(zero[k], none[k])
 
 
+def test_calls_side_by_side():
+    """Different calls in flight on several streams at once, each with its own workspace: nothing is shared."""
+    sets = [make(700 + 50 * i, 256 * (i + 1), "bf16", seed=20 + i) for i in range(4)]
+    cfgs = [config(256 * (i + 1), "bf16", 64, "silu") for i in range(4)]
+    want = [run(c, cfg) for c, cfg in zip(sets, cfgs)]
+    streams = [torch.cuda.Stream() for _ in sets]
+    from sparse_state_linear_router_gb300 import binding
+    got = []
+    for c, cfg, st in zip(sets, cfgs, streams):
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            f = binding.block_norm(cfg, c["o"], gate=c["z"], residual=c["r"], w_after=c["a"], channel_scale=c["c"],
+                                   w_before=c["b"])
+            g = binding.block_norm_backward(cfg, c["dr"], c["o"], gate=c["z"], w_after=c["a"], channel_scale=c["c"],
+                                            w_before=c["b"], residual_out=c["at"], d_next_in=c["dn"])
+            got.append((f, g))
+    torch.cuda.synchronize()
+    for (f, g), (wf, wg) in zip(got, want):
+        for a, b in ((f, wf), (g, wg)):
+            for k in a:
+                assert torch.equal(a[k], b[k])
+
+
 def test_graph_replays_on_new_inputs_and_other_streams():
     from sparse_state_linear_router_gb300 import binding
     T, W = 333, 512

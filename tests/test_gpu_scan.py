@@ -374,6 +374,66 @@ def test_wide_rows(dtype="bf16"):
     check(sub, "complement", dtype, {k: f[k][:, pick] for k in ("out", "final_state")}, {k: b[k][:, pick] for k in b})
 
 
+def _pick(c, f, b, cols):
+    sub = {k: (c[k][:, cols] if k in ("x", "la", "d_out", "init", "d_final") else c[k]) for k in c}
+    return sub, {k: f[k][:, cols] for k in ("out", "final_state")}, {k: b[k][:, cols] for k in b}
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype,width", [("bf16", 2048), ("f32", 1024)])
+def test_enough_columns_to_fill_the_gpu(dtype, width, mode):
+    """Widths whose clusters fill the GPU (the form that keeps rows in registers, for the costly input factors): ragged
+    lengths with several starts and ends in one tile, emptied and kept states, the final state over the initial one."""
+    lens = [2600, 0, 5, 700, 1, 1, 130, 9, 3, 250]
+    c = make(lens, width, dtype, seed=18)
+    c["la"][7::41, 3] = float("-inf")
+    c["la"][5::37, 5] = 0.0
+    c["la"][4000:, 64:128] = -3.0   # a column whose log-gates leave [-1/2, 0] in its last tiles only
+    f, b = run(c, mode, dtype)
+    cols = [0, 3, 5, 31, 32, 63, 64, 100, 500, width - 1]
+    sub, sub_f, sub_b = _pick(c, f, b, cols)
+    check(sub, mode, dtype, sub_f, sub_b)
+    from sparse_state_linear_router_gb300 import binding
+    state = c["init"].clone()
+    cfg = binding.make_scan_config(width, mode, dtype)
+    got = binding.scan_forward(cfg, c["x"], c["la"], c["cu"], initial_state=state, final_state=state)
+    torch.cuda.synchronize()
+    assert torch.equal(got["out"], f["out"]) and torch.equal(state, f["final_state"])
+    c["x"][2605 + 350, 70] = float("nan")   # in the sequence of 700
+    bad, bad_b = run(c, mode, dtype)
+    same = torch.ones(sum(lens), width, dtype=torch.bool, device="cuda")
+    same[2955:3305, 70] = False
+    assert torch.equal(bad["out"][same], f["out"][same])
+    assert not bool(torch.isfinite(bad["out"][2955:3305, 70]).any())
+    same[2955, 70] = False
+    assert torch.equal(bad_b["d_log_gate"][same], b["d_log_gate"][same])
+    assert torch.equal(bad_b["dx"], b["dx"])
+
+
+def test_calls_side_by_side(dtype="bf16"):
+    """Different calls in flight on several streams at once: nothing is shared."""
+    from sparse_state_linear_router_gb300 import binding
+    sets = [make([900 + 100 * i, 7, 0, 333], 256 * (i + 1), dtype, seed=30 + i) for i in range(4)]
+    want = [run(c, "unit", dtype) for c in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    got = []
+    for _ in range(3):
+        got = []
+        for c, st in zip(sets, streams):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                cfg = binding.make_scan_config(c["x"].shape[1], "unit", dtype)
+                f = binding.scan_forward(cfg, c["x"], c["la"], c["cu"], initial_state=c["init"], want_checkpoints=True)
+                b = binding.scan_backward(cfg, c["x"], c["la"], c["cu"], f["checkpoints"], c["d_out"],
+                                          initial_state=c["init"], d_final_state=c["d_final"])
+                got.append((f, b))
+        torch.cuda.synchronize()
+    for (f, b), (wf, wb) in zip(got, want):
+        assert torch.equal(f["out"], wf["out"]) and torch.equal(f["final_state"], wf["final_state"])
+        for k in b:
+            assert torch.equal(b[k], wb[k])
+
+
 def test_graph_replays_on_new_inputs_and_other_streams(dtype="bf16"):
     from sparse_state_linear_router_gb300 import binding
     W, lens = 320, [800, 3, 0, 211]
