@@ -585,6 +585,7 @@ __global__ void __launch_bounds__(MAXT, VPT == 1 ? 5 : 1) norm_backward_kernel(B
         ring.template fetch<3, 5>(n, stage, row + n.stages * on, k + n.stages < mine);
         stage = stage + 1 == n.stages ? 0 : stage + 1;
     }
+    griddep_launch_dependents();
     // column sums of this team: one partial row of each
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -601,33 +602,33 @@ __global__ void __launch_bounds__(MAXT, VPT == 1 ? 5 : 1) norm_backward_kernel(B
     }
 }
 
-// The weights' gradients from the partial rows, in a fixed order: 32 columns
-// per CTA, 32 interleaved runs of rows, then their sum.
+// The weights' gradients from the partial rows, in a fixed order: 32 columns of
+// one array (blockIdx.y: C_j, dw_before) per CTA, 32 interleaved runs of rows,
+// then their sum.  Launched as a dependent of the gradient kernel.
 __global__ void __launch_bounds__(1024) norm_weight_grads_kernel(BlockNormArgs a, NormShape n, int rows) {
-    __shared__ float part[2][32][33];
+    __shared__ float part[32][33];
     const int c = threadIdx.x, col = blockIdx.x * 32 + c;
-    float s[2] = {0.f, 0.f};
+    const bool before = blockIdx.y != 0;
+    griddep_wait();
+    if (before ? !a.d_w_before : !a.d_w_after && !a.d_channel) return;
+    const float *from = a.partials + (before ? (int64_t)rows * n.width : 0) + col;
+    float s = 0.f;
     if (col < n.width) {
-        for (int r = threadIdx.y; r < rows; r += 32) {
-            if (a.d_w_after || a.d_channel) s[0] += a.partials[(int64_t)r * n.width + col];
-            if (a.d_w_before) s[1] += a.partials[((int64_t)rows + r) * n.width + col];
-        }
+#pragma unroll 8
+        for (int r = threadIdx.y; r < rows; r += 32) s += from[(int64_t)r * n.width];
     }
-    part[0][threadIdx.y][c] = s[0];
-    part[1][threadIdx.y][c] = s[1];
+    part[threadIdx.y][c] = s;
     __syncthreads();
-    if (threadIdx.y < 2) {
-        // lane c of row y sums column c of array y
+    if (threadIdx.y == 0 && col < n.width) {
         float t = 0.f;
-        for (int r = 0; r < 32; ++r) t += part[threadIdx.y][r][c];
-        if (col < n.width) {
-            if (threadIdx.y == 0) {
-                const float w = a.w_after ? a.w_after[col] : 1.f, ch = a.channel ? a.channel[col] : 1.f;
-                if (a.d_w_after) a.d_w_after[col] = n.bs * ch * t;
-                if (a.d_channel) a.d_channel[col] = n.bs * w * t;
-            } else if (a.d_w_before) {
-                a.d_w_before[col] = t;
-            }
+#pragma unroll
+        for (int r = 0; r < 32; ++r) t += part[r][c];
+        if (before) {
+            a.d_w_before[col] = t;
+        } else {
+            const float w = a.w_after ? a.w_after[col] : 1.f, ch = a.channel ? a.channel[col] : 1.f;
+            if (a.d_w_after) a.d_w_after[col] = n.bs * ch * t;
+            if (a.d_channel) a.d_channel[col] = n.bs * w * t;
         }
     }
 }
@@ -744,8 +745,8 @@ cudaError_t launch_block_norm_backward(const sse_norm_config_t &cfg, const Block
     }
     if (a.d_w_after || a.d_channel || a.d_w_before) {
         const int rows = norm_grid(p, a.T) * p.rows;
-        norm_weight_grads_kernel<<<(cfg.width + 31) / 32, dim3(32, 32), 0, stream>>>(a, p.n, rows);
-        return cudaGetLastError();
+        return launch_dependent(norm_weight_grads_kernel, dim3((cfg.width + 31) / 32, 2), dim3(32, 32), 0, stream, a, p.n,
+                                rows);
     }
     return cudaSuccess;
 }
