@@ -20,10 +20,11 @@
 // over a group of columns through shuffles where the group is a power of two of
 // lanes.  Arithmetic is on float32 pairs.  Measured on a GB300, bf16, against
 // the bytes at 6.77 TB/s: per-head norm and gate of 32768 x 2048 67 us (floor
-// 59.5); norm, scale, residual and next norm of 16384 x 2304 54 us (44.6);
-// backward of head norm, gate, residual and next norm of 32768 x 2048 189 us
+// 59.5); norm, scale, residual and next norm of 16384 x 2304 53 us (44.6);
+// backward of head norm, gate, residual and next norm of 32768 x 2048 185 us
 // (158.6).  One word per thread left the same backward at 254 us: the control
-// flow of a row (about 150 of 600 instructions per word) is shared by two words.
+// flow of a row (600 instructions per word then, 510 now) is shared by two words.
+// Bound now by issue at 16 warps per SM (60 % of the slots) as much as by HBM.
 #include "f32x2.cuh"
 #include "sse_internal.cuh"
 

@@ -25,12 +25,13 @@
 //    words, and leave in 16-byte words from the place of the inputs they replace.
 //
 // Measured on a GB300 (72000 tokens x 2048 channels in bf16, one sequence; HBM
-// floor at 6.77 TB/s): forward 131 us, took 175 us with s = 1 and 301 us with
-// s = sqrt(1 - a^2); backward 218 us, took 299 us and 477 us.  One sequence per
-// cluster of 8 waits for the exchange (a step of 1024 rows in 2.5 us); with
-// s = sqrt(1 - a^2) the arithmetic (about 65 instructions per two channels and
-// row, twice through the rows) is the longer part.  An earlier form with the rows
-// in registers and every warp composing for itself took 413 us (s = 1).
+// floor at 6.77 TB/s): forward 131 us, took 174 us with s = 1 and 239 us with
+// s = sqrt(1 - a^2); backward 218 us, took 296 us and 474 us.  What is left is
+// the wait of a cluster for its slowest worker (a step of 1024 rows takes 2.5 us;
+// 20 to 48 % of the warps' time) and, with s = sqrt(1 - a^2), the arithmetic (46
+// instructions per two channels and row forward, 110 backward).  The first form,
+// in which every warp composed for itself between two cluster barriers, took
+// 413 us (s = 1).
 #include <type_traits>
 
 #include <cooperative_groups.h>
