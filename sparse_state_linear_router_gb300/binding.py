@@ -509,7 +509,8 @@ def _rows(what, name, t, rows, width, dtype, device):
     """(pointer, row stride) of a token tensor [rows, width] or [rows, heads, width / heads] whose rows are packed."""
     if t is None:
         return None, width
-    if t.dtype is not dtype or t.device != device or t.numel() != rows * width or t.dim() < 2 or t.shape[0] != rows:
+    if t.dtype is not dtype or t.device != device or t.shape != (rows, width) and (
+            t.dim() < 2 or t.shape[0] != rows or t.numel() != rows * width):
         _refuse_tokens(what, name, t, rows, width, dtype, device)
     if t.is_contiguous():
         return t.data_ptr(), width
@@ -530,7 +531,8 @@ def _packed(what, name, t, rows, width, dtype, device):
     """Pointer of a contiguous token tensor."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.device != device or t.numel() != rows * width or t.dim() < 2 or t.shape[0] != rows:
+    if t.dtype is not dtype or t.device != device or t.shape != (rows, width) and (
+            t.dim() < 2 or t.shape[0] != rows or t.numel() != rows * width):
         _refuse_tokens(what, name, t, rows, width, dtype, device)
     if not t.is_contiguous():
         _refuse(what, f"{name} is not contiguous")
@@ -548,13 +550,14 @@ def _floats(what, name, t, shape, device):
 
 def _on_device(what, device, call, *args):
     """One C call on the tensors' device and its current stream, whichever device is current."""
-    cuda = _torch().cuda
-    index = device.index
-    if index == cuda.current_device():
-        status = call(*args, cuda.current_stream(index).cuda_stream)
+    # The device and the stream as numbers: torch.cuda's own functions put objects around them, 1.2 us of a
+    # 10 us step on the host of a GB300.
+    torch, index = _torch(), device.index
+    if index == torch._C._cuda_getDevice():
+        status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
-        with cuda.device(index):
-            status = call(*args, cuda.current_stream(index).cuda_stream)
+        with torch.cuda.device(index):
+            status = call(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != SSE_OK:
         raise SSEError(status, what)
 
