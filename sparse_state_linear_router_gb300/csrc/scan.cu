@@ -113,6 +113,11 @@ __device__ __forceinline__ float rsqrt_ftz(float x) {
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float sqrt_ftz(float x) {
+    float y;
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
 // a = exp(la) = 2^(la log2 e).  The product's rounding error is |la| 2^-24 of
 // the result: next to the bf16 gates' own steps nothing.  For float32 gates it is
@@ -169,16 +174,20 @@ __device__ __forceinline__ void factors(typename Lane<T>::V la, typename Lane<T>
         if constexpr (NEAR0) {
             const auto c = one_minus_exp_near0<T>(la);
             a = fma2(c, minus, one);
-            s2 = mul2(c, add2(one, a));
+            s2 = fma2(c, a, c);
         } else {
             a = decay<T>(la);
             const auto u = add2(la, la);
             s2 = each(u, one_minus_exp_near0<T>(u), mul2(a, a), [](float x, float near0, float e) { return x > -0.5f ? near0 : 1.f - e; });
         }
         // r = 1 / s; 10^-37 keeps it finite where s is 0: no input enters there, and s r makes its slope 0 too
-        const auto r = each(add2(s2, L::splat(1e-37f)), [](float v) { return rsqrt_ftz(v); });
-        s = mul2(s2, r);
-        if constexpr (GRAD) *slope = mul2(mul2(mul2(a, a), mul2(r, minus)), mul2(s, r));
+        if constexpr (GRAD) {
+            const auto r = each(add2(s2, L::splat(1e-37f)), [](float v) { return rsqrt_ftz(v); });
+            s = mul2(s2, r);
+            *slope = mul2(mul2(mul2(a, a), mul2(r, minus)), mul2(s, r));
+        } else {
+            s = each(s2, [](float v) { return sqrt_ftz(v); });
+        }
     }
 }
 
