@@ -193,8 +193,8 @@ __device__ __forceinline__ void factors(typename Lane<T>::V la, typename Lane<T>
 
 // A word's largest log-gate magnitude so far, as bits: larger bits of a negative
 // number are further from 0.
-__device__ __forceinline__ uint32_t further(uint32_t x, uint32_t y, __nv_bfloat16) { return __vmaxu2(x, y); }
-__device__ __forceinline__ uint32_t further(uint32_t x, uint32_t y, float) { return x > y ? x : y; }
+__device__ __forceinline__ uint32_t further(uint32_t x, uint32_t y, uint32_t z, __nv_bfloat16) { return __vimax3_u16x2(x, y, z); }
+__device__ __forceinline__ uint32_t further(uint32_t x, uint32_t y, uint32_t z, float) { return __vimax3_u32(x, y, z); }
 // Whether all are in [-1/2, 0].
 __device__ __forceinline__ bool near0(uint32_t bits, __nv_bfloat16) {
     return (bits & 0xffffu) <= 0xbf00u && (bits >> 16) <= 0xbf00u;
@@ -533,9 +533,14 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     };
     auto all_near0 = [&](const uint32_t *src) {
         if constexpr (MODE == SSE_INPUT_PLAIN) return false;
+        // 16 bytes at a time: as 4-byte words the compiler keeps them for the rows' factors and spills.
+        const uint4 *words = reinterpret_cast<const uint4 *>(src - lane) + lane;
         uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) bits = further(bits, src[i * 32], T());
+        for (int i = 0; i < kRows / 4; ++i) {
+            const uint4 u = words[i * 32];
+            bits = further(further(bits, u.x, u.y, T()), u.z, u.w, T());
+        }
         return (bool)__all_sync(0xffffffffu, near0(bits, T()));
     };
     // a and s x of row i of a slot
@@ -799,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
         if constexpr (MODE == SSE_INPUT_PLAIN) return false;
         uint32_t bits = 0;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) bits = further(bits, src[i * 32], T());
+        for (int i = 0; i < kRows; i += 2) bits = further(bits, src[i * 32], src[(i + 1) * 32], T());
         return (bool)__all_sync(0xffffffffu, near0(bits, T()));
     };
     // a and s x of row i of a slot
