@@ -278,9 +278,8 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const void *base, int64_
     if (whole) {
         if (col_ok) {
 #pragma unroll
-            for (int k = 0; k < ROWS; k += 4)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 128 + lane * 16), "l"(src + k * stride)
-                             : "memory");
+            for (int k = 0; k < ROWS; k += 4, src += 4 * stride)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 128 + lane * 16), "l"(src) : "memory");
         }
     } else {
 #pragma unroll
@@ -311,15 +310,18 @@ template <int ROWS>
 __device__ __forceinline__ void store_rows(void *base, int64_t stride, int col_byte, const uint32_t *src, int row0, int t0,
                                            int t1, bool whole, bool col_ok, int lane) {
     char *dst = static_cast<char *>(base) + (row0 + (lane >> 3)) * stride + col_byte;
+    const uint4 *from = reinterpret_cast<const uint4 *>(src) + lane;
+    if (whole) {
+        if (col_ok) {
 #pragma unroll
-    for (int k = 0; k < ROWS; k += 4) {
-        bool ok = col_ok;
-        if (!whole) {
-            const int row = row0 + k + (lane >> 3);
-            ok = ok && row >= t0 && row < t1;
+            for (int k = 0; k < ROWS; k += 4, dst += 4 * stride) *reinterpret_cast<uint4 *>(dst) = from[k * 8];
         }
-        const uint4 u = *reinterpret_cast<const uint4 *>(src + k * 32 + lane * 4);
-        if (ok) *reinterpret_cast<uint4 *>(dst + k * stride) = u;
+    } else {
+#pragma unroll
+        for (int k = 0; k < ROWS; k += 4, dst += 4 * stride) {
+            const int row = row0 + k + (lane >> 3);
+            if (col_ok && row >= t0 && row < t1) *reinterpret_cast<uint4 *>(dst) = from[k * 8];
+        }
     }
 }
 
@@ -340,8 +342,12 @@ template <typename V> struct Exchange {
 
 __device__ __forceinline__ void runs_published() { asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
 __device__ __forceinline__ void await_runs() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ void starts_published() { asm volatile("barrier.cta.arrive 2, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ void await_starts() { asm volatile("barrier.cta.sync 2, %0;" ::"n"(kThreads) : "memory"); }
+// A barrier per worker (2 + its number), met by the worker and the conductor: a worker waits for no other worker.
+__device__ __forceinline__ void starts_published() {
+#pragma unroll
+    for (int w = 0; w < kWorkers; ++w) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + w) : "memory");
+}
+__device__ __forceinline__ void await_starts(int warp) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + warp) : "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     };
     auto slot = [&](int at) { return mine + at * (2 * kSlotWords) + lane; };
     auto take_start = [&] {
-        await_starts();
+        await_starts(warp);
         const V h = ex.start[warp][lane];
         cluster_wait();
         return h;
@@ -925,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
                 copies_wait<kStagesBwd - 2>();
                 first_pass(next, run, back, row0, mine + next_slot * (3 * kSlotWords) + lane);
             }
-            await_starts();
+            await_starts(warp);
             const V e = ex.start[warp][lane], state = before[warp][lane];
             cluster_wait();
             if (more) publish(next, run, back);
