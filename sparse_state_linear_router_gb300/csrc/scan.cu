@@ -48,6 +48,7 @@ constexpr int kWorkers = 8;                   // warps that go through rows
 constexpr int kThreads = (kWorkers + 1) * 32;  // and the conductor
 constexpr int kRowsFwd = 16, kRowsBwd = 8;    // rows of a worker in one tile
 constexpr int kMaxCluster = 8;                // the portable cluster size
+constexpr int kSolo = 6, kShare = 5;          // CTAs go alone if the largest part is at most 6/5 of its share
 static_assert(kWorkers * kRowsBwd % kScanCheckpoint == 0 && kScanCheckpoint % kRowsFwd == 0,
               "checkpoints lie at workers' first rows, and the backward's tiles at checkpoints");
 
@@ -333,7 +334,7 @@ __device__ __forceinline__ void store_rows(void *base, int64_t stride, int col_b
 // global memory, so its release has little to wait for; the workers' arrivals
 // carry no data to other CTAs and are relaxed.
 // ---------------------------------------------------------------------------
-template <typename V> struct Exchange {
+template <typename V> struct alignas(16) Exchange {
     Run<V> warp[kWorkers][32];       // the workers' runs
     Run<V> cta[2][kMaxCluster][32];  // the runs of the cluster's CTAs, two steps in turn
     V start[kWorkers][32];           // what each worker's rows start from; read before the worker's next arrival
@@ -397,7 +398,7 @@ template <typename V> struct Outbox {
 // starts; `meanwhile` runs while the cluster gathers.  REVERSE: the last worker
 // comes first.  `state` moves past the cluster's tiles.  Its length is what the
 // cluster waits for, so steps without a reset take the short way.
-template <bool REVERSE, typename V, typename F>
+template <bool REVERSE, bool ONE, typename V, typename F>
 __device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, int buf, int rank, int csize, int lane,
                                         V &state, F meanwhile) {
     const uint32_t resets = reset_bits(ex.warp_reset, kWorkers, lane);
@@ -416,12 +417,24 @@ __device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, i
         for (int k = 1; k < kWorkers; ++k)
             all.q = apply(r[k], all.q, (resets >> (REVERSE ? kWorkers - 1 - k : k)) & 1u);
     }
+    V mine = state;
+    if constexpr (ONE) {
+        meanwhile();
+#pragma unroll
+        for (int k = 0; k < kWorkers; ++k) {
+            const int w = REVERSE ? kWorkers - 1 - k : k;
+            ex.start[w][lane] = mine;
+            mine = apply(r[k], mine, (resets >> w) & 1u);
+        }
+        starts_published();
+        state = mine;
+        return;
+    }
     out.send(buf, csize, lane, all, resets);
     cluster_arrive_release();
     meanwhile();
     cluster_wait();
     const uint32_t cta_resets = reset_bits(ex.cta_reset[buf], csize, lane);
-    V mine = state;
     if (cta_resets == 0) {
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k) {
@@ -451,16 +464,27 @@ __device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, i
     starts_published();
 }
 
-// The tiles of one cluster.
+// The tiles of one team: a cluster, or one CTA of it (`solo`).  Where the
+// cluster's sequences fall evenly into a part for each CTA, each goes through its
+// own and there is nothing to exchange.
 template <int ROWS> struct Span {
     static constexpr int kTile = kWorkers * ROWS;
     int t0, t1, tile0, tiles, steps;
-    __device__ __forceinline__ Span(const ScanArgs &p, int csize) {
-        t0 = range_start(p, blockIdx.y, gridDim.y);
-        t1 = range_start(p, blockIdx.y + 1, gridDim.y);
+    bool solo;
+    __device__ __forceinline__ Span(const ScanArgs &p, int csize, int rank, int lane) {
+        const int at = range_start(p, (int)blockIdx.y * csize + (lane < csize ? lane : csize), (int)gridDim.y * csize);
+        const int len = __shfl_down_sync(0xffffffffu, at, 1) - at;
+        const int most = __reduce_max_sync(0xffffffffu, lane < csize ? len : 0);
+        t0 = __shfl_sync(0xffffffffu, at, 0);
+        t1 = __shfl_sync(0xffffffffu, at, csize);
+        solo = csize == 1 || (int64_t)most * csize * kShare <= (int64_t)(t1 - t0) * kSolo;
+        if (solo) {
+            t0 = __shfl_sync(0xffffffffu, at, rank);
+            t1 = __shfl_sync(0xffffffffu, at, rank + 1);
+        }
         tile0 = t0 / kTile;
         tiles = t1 > t0 ? (t1 + kTile - 1) / kTile - tile0 : 0;
-        steps = (tiles + csize - 1) / csize;
+        steps = solo ? tiles : (tiles + csize - 1) / csize;
     }
 };
 
@@ -487,28 +511,23 @@ constexpr int kStagesFwd = 3, kStagesBwd = 3;  // tiles of a worker's ring
 // s = sqrt(1 - a^2) 301 against 240 us; at 512 channels, where an SM has one CTA
 // at most, 150 against 189 us.
 // ---------------------------------------------------------------------------
-template <typename T, int MODE, bool HOLD>
-__global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
+template <typename T, int MODE, bool HOLD, bool ONE>
+__device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, const Span<kRowsFwd> &sp,
+                                              Exchange<typename Lane<T>::V> &ex, uint4 *ring, int csize, int rank, int col0) {
     using L = Lane<T>;
     using V = typename L::V;
     constexpr int kRows = kRowsFwd, kTile = kWorkers * kRows;
     constexpr int kSlotWords = kRows * 32, kSlotBytes = kSlotWords * 4;  // one tensor's rows of a worker
-    extern __shared__ uint4 ring[];
-    __shared__ Exchange<V> ex;
-    const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
+    const int col = col0 + lane * L::kCols;
     const bool live = col < width;
-    const Span<kRows> sp(p, csize);
-    cluster_arrive_relaxed();  // every CTA has started before the first run is sent
-    cluster_wait();
 
     if (warp == kWorkers) {
         const Outbox<V> out(ex, rank, csize, lane);
         V state = L::splat(0.f);  // the state ahead of the cluster's tiles
         for (int step = 0; step < sp.steps; ++step) {
             await_runs();
-            conduct<false>(out, ex, step & 1, rank, csize, lane, state, [] {});
+            conduct<false, ONE>(out, ex, step & 1, rank, csize, lane, state, [] {});
         }
         return;
     }
@@ -624,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
         ex.warp[warp][lane] = run;
         if (lane == 0) ex.warp_reset[warp] = m.starts;
         runs_published();
-        cluster_arrive_relaxed();
+        if (!ONE) cluster_arrive_relaxed();
     };
     auto states_of = [&](auto near, V h, uint32_t *src) {
 #pragma unroll
@@ -671,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     auto take_start = [&] {
         await_starts(warp);
         const V h = ex.start[warp][lane];
-        cluster_wait();
+        if (!ONE) cluster_wait();
         return h;
     };
     Marks now;
@@ -712,8 +731,26 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
             at = next_at;
         }
     }
-    // empty sequences keep their initial state
-    if (p.final_state && live) {
+}
+
+template <typename T, int MODE, bool HOLD>
+__global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
+    using L = Lane<T>;
+    extern __shared__ uint4 ring[];
+    __shared__ Exchange<typename L::V> ex;
+    const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols;
+    const Span<kRowsFwd> sp(p, csize, rank, lane);
+    if (sp.solo) {
+        forward_tiles<T, MODE, HOLD, true>(p, width, sp, ex, ring, 1, 0, col0);
+    } else {
+        cluster_arrive_relaxed();  // every CTA has started before the first run is sent
+        cluster_wait();
+        forward_tiles<T, MODE, HOLD, false>(p, width, sp, ex, ring, csize, rank, col0);
+    }
+    const int col = col0 + lane * L::kCols;
+    if (p.final_state && col < width && warp < kWorkers) {  // empty sequences keep their initial state
         const int n = gridDim.y * csize * kWorkers;
         for (int s = ((int)blockIdx.y * csize + rank) * kWorkers + warp; s < p.num_seqs; s += n)
             if (__ldg(p.cu_seqlens + s) >= __ldg(p.cu_seqlens + s + 1)) {
@@ -729,25 +766,28 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
 // and goes through the cluster; a tile's states come from its checkpoint and the
 // CTA's own rows, composed by the conductor in the same step.
 // ---------------------------------------------------------------------------
-template <typename T, int MODE>
-__global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, int width) {
+template <typename V> struct BackShared {
+    Exchange<V> ex;                  // adjoint runs
+    Run<V> fwd[kWorkers][32];        // the workers' state runs
+    V before[kWorkers][32];          // the state ahead of each worker's rows
+    uint32_t fwd_reset[kWorkers];
+};
+
+template <typename T, int MODE, bool ONE>
+__device__ __forceinline__ void backward_tiles(const ScanArgs &p, int width, const Span<kRowsBwd> &sp,
+                                               BackShared<typename Lane<T>::V> &sh, uint4 *ring, int csize, int rank, int col0) {
     using L = Lane<T>;
     using V = typename L::V;
     constexpr int kRows = kRowsBwd, kTile = kWorkers * kRows;
     constexpr int kSlotWords = kRows * 32, kSlotBytes = kSlotWords * 4;  // one tensor's rows of a worker
-    extern __shared__ uint4 ring[];
-    __shared__ Exchange<V> ex;                 // adjoint runs
-    __shared__ Run<V> fwd[kWorkers][32];       // the workers' state runs
-    __shared__ V before[kWorkers][32];         // the state ahead of each worker's rows
-    __shared__ uint32_t fwd_reset[kWorkers];
-    const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
+    Exchange<V> &ex = sh.ex;
+    auto &fwd = sh.fwd;
+    auto &before = sh.before;
+    auto &fwd_reset = sh.fwd_reset;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols, col = col0 + lane * L::kCols;
+    const int col = col0 + lane * L::kCols;
     const bool live = col < width;
-    const Span<kRows> sp(p, csize);
     const int last_tile = sp.tile0 + sp.tiles - 1 - rank;  // rank 0 has the last; below tile0 there are no rows
-    cluster_arrive_relaxed();
-    cluster_wait();
 
     if (warp == kWorkers) {
         auto checkpoint = [&](int step) {
@@ -762,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
             V state = check;
             if (step + 1 < sp.steps) check = checkpoint(step + 1);
             await_runs();
-            conduct<true>(out, ex, step & 1, rank, csize, lane, adjoint, [&] {
+            conduct<true, ONE>(out, ex, step & 1, rank, csize, lane, adjoint, [&] {
                 const uint32_t resets = reset_bits(fwd_reset, kWorkers, lane);
 #pragma unroll
                 for (int w = 0; w < kWorkers; ++w) {
@@ -865,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
             ex.warp_reset[warp] = m.ends;
         }
         runs_published();
-        cluster_arrive_relaxed();
+        if (!ONE) cluster_arrive_relaxed();
     };
     // EDGES: sequences begin or end among the rows.
     auto rows_of = [&](auto edges, auto near, const Marks &m, V state, V e, uint32_t *src) {
@@ -933,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
             }
             await_starts(warp);
             const V e = ex.start[warp][lane], state = before[warp][lane];
-            cluster_wait();
+            if (!ONE) cluster_wait();
             if (more) publish(next, run, back);
             second_pass(now, state, e, mine + slot * (3 * kSlotWords) + lane);
             load(step + kStagesBwd);
@@ -941,7 +981,26 @@ __global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, 
             slot = next_slot;
         }
     }
-    if (p.d_init && live) {  // empty sequences hand the final state's gradient through
+}
+
+template <typename T, int MODE>
+__global__ void __launch_bounds__(kThreads, 2) scan_backward_kernel(ScanArgs p, int width) {
+    using L = Lane<T>;
+    extern __shared__ uint4 ring[];
+    __shared__ BackShared<typename L::V> sh;
+    const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols;
+    const Span<kRowsBwd> sp(p, csize, rank, lane);
+    if (sp.solo) {
+        backward_tiles<T, MODE, true>(p, width, sp, sh, ring, 1, 0, col0);
+    } else {
+        cluster_arrive_relaxed();
+        cluster_wait();
+        backward_tiles<T, MODE, false>(p, width, sp, sh, ring, csize, rank, col0);
+    }
+    const int col = col0 + lane * L::kCols;
+    if (p.d_init && col < width && warp < kWorkers) {  // empty sequences hand the final state's gradient through
         const int n = gridDim.y * csize * kWorkers;
         for (int q = ((int)blockIdx.y * csize + rank) * kWorkers + warp; q < p.num_seqs; q += n)
             if (__ldg(p.cu_seqlens + q) >= __ldg(p.cu_seqlens + q + 1)) {
