@@ -334,21 +334,35 @@ __device__ __forceinline__ void store_rows(void *base, int64_t stride, int col_b
 // global memory, so its release has little to wait for; the workers' arrivals
 // carry no data to other CTAs and are relaxed.
 // ---------------------------------------------------------------------------
-template <typename V> struct alignas(16) Exchange {
-    Run<V> warp[kWorkers][32];       // the workers' runs
-    Run<V> cta[2][kMaxCluster][32];  // the runs of the cluster's CTAs, two steps in turn
-    V start[kWorkers][32];           // what each worker's rows start from; read before the worker's next arrival
-    uint32_t warp_reset[kWorkers], cta_reset[2][kMaxCluster];
+// EARLY: a worker publishes the next tile's run before it meets the conductor for
+// this one, so the workers' words and barriers are there twice, for two steps in
+// turn.  72000 tokens x 2048 channels, s = 1, one sequence: forward 162 against
+// 178 us; the backward's runs come late in its step, 303 against 298 us.
+template <typename V, bool EARLY> struct alignas(16) Exchange {
+    Run<V> warp[EARLY ? 2 : 1][kWorkers][32];  // the workers' runs; then, in the place of P, what the rows start from
+    Run<V> cta[2][kMaxCluster][32];            // the runs of the cluster's CTAs, two steps in turn
+    uint32_t warp_reset[EARLY ? 2 : 1][kWorkers], cta_reset[2][kMaxCluster];
+    static __device__ __forceinline__ int turn(int step) { return EARLY ? step & 1 : 0; }
+
+    // Named barriers.  1 and 2: the runs, all workers.  From 3: the starts, the conductor and a worker, or a pair of
+    // them (EARLY: 16 barriers do not go round), so that no worker waits for all the others.
+    static __device__ __forceinline__ void runs_published(int step) {
+        asm volatile("barrier.cta.arrive %0, %1;" ::"r"(1 + turn(step)), "n"(kThreads) : "memory");
+    }
+    static __device__ __forceinline__ void await_runs(int step) {
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + turn(step)), "n"(kThreads) : "memory");
+    }
+    static __device__ __forceinline__ void starts_published(int step) {
+#pragma unroll
+        for (int w = 0; w < kWorkers; w += EARLY ? 2 : 1)
+            asm volatile("barrier.cta.arrive %0, %1;" ::"r"(3 + w + turn(step)), "n"(EARLY ? 96 : 64) : "memory");
+    }
+    static __device__ __forceinline__ void await_starts(int step, int warp) {
+        asm volatile("barrier.cta.sync %0, %1;" ::"r"(3 + (EARLY ? warp & ~1 : warp) + turn(step)), "n"(EARLY ? 96 : 64)
+                     : "memory");
+    }
 };
 
-__device__ __forceinline__ void runs_published() { asm volatile("barrier.cta.arrive 1, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ void await_runs() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-// A barrier per worker (2 + its number), met by the worker and the conductor: a worker waits for no other worker.
-__device__ __forceinline__ void starts_published() {
-#pragma unroll
-    for (int w = 0; w < kWorkers; ++w) asm volatile("barrier.cta.arrive %0, 64;" ::"r"(2 + w) : "memory");
-}
-__device__ __forceinline__ void await_starts(int warp) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(2 + warp) : "memory"); }
 __device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive_release() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -364,9 +378,9 @@ template <typename V> __device__ __forceinline__ V apply(const Run<V> &r, V h, b
 }
 
 // Where this CTA's runs go in the cluster's CTAs (a conductor's registers).
-template <typename V> struct Outbox {
+template <typename V, bool EARLY> struct Outbox {
     uint32_t run[kMaxCluster], reset;
-    __device__ __forceinline__ Outbox(Exchange<V> &ex, int rank, int csize, int lane) {
+    __device__ __forceinline__ Outbox(Exchange<V, EARLY> &ex, int rank, int csize, int lane) {
         const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&ex.cta[0][rank][lane]);
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k)
@@ -375,7 +389,7 @@ template <typename V> struct Outbox {
             : "r"((uint32_t)__cvta_generic_to_shared(&ex.cta_reset[0][rank])), "r"(lane < csize ? lane : 0));
     }
     __device__ __forceinline__ void send(int buf, int csize, int lane, const Run<V> &r, uint32_t resets) const {
-        const uint32_t off = buf * (uint32_t)sizeof(Exchange<V>::cta[0]);
+        const uint32_t off = buf * (uint32_t)sizeof(Exchange<V, EARLY>::cta[0]);
 #pragma unroll
         for (int k = 0; k < kMaxCluster; ++k)
             if (k < csize) {
@@ -389,7 +403,7 @@ template <typename V> struct Outbox {
                 }
             }
         if (lane < csize)
-            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(reset + buf * (uint32_t)sizeof(Exchange<V>::cta_reset[0])),
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(reset + buf * (uint32_t)sizeof(Exchange<V, EARLY>::cta_reset[0])),
                          "r"(resets) : "memory");
     }
 };
@@ -398,13 +412,15 @@ template <typename V> struct Outbox {
 // starts; `meanwhile` runs while the cluster gathers.  REVERSE: the last worker
 // comes first.  `state` moves past the cluster's tiles.  Its length is what the
 // cluster waits for, so steps without a reset take the short way.
-template <bool REVERSE, bool ONE, typename V, typename F>
-__device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, int buf, int rank, int csize, int lane,
+template <bool REVERSE, bool ONE, typename V, bool EARLY, typename F>
+__device__ __forceinline__ void conduct(const Outbox<V, EARLY> &out, Exchange<V, EARLY> &ex, int step, int rank, int csize, int lane,
                                         V &state, F meanwhile) {
-    const uint32_t resets = reset_bits(ex.warp_reset, kWorkers, lane);
+    const int buf = step & 1;
+    auto &warp = ex.warp[ex.turn(step)];
+    const uint32_t resets = reset_bits(ex.warp_reset[ex.turn(step)], kWorkers, lane);
     Run<V> r[kWorkers];
 #pragma unroll
-    for (int k = 0; k < kWorkers; ++k) r[k] = ex.warp[REVERSE ? kWorkers - 1 - k : k][lane];
+    for (int k = 0; k < kWorkers; ++k) r[k] = warp[REVERSE ? kWorkers - 1 - k : k][lane];
     Run<V> all = r[0];
     if (resets == 0) {
 #pragma unroll
@@ -423,10 +439,10 @@ __device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, i
 #pragma unroll
         for (int k = 0; k < kWorkers; ++k) {
             const int w = REVERSE ? kWorkers - 1 - k : k;
-            ex.start[w][lane] = mine;
+            warp[w][lane].P = mine;
             mine = apply(r[k], mine, (resets >> w) & 1u);
         }
-        starts_published();
+        ex.starts_published(step);
         state = mine;
         return;
     }
@@ -446,7 +462,7 @@ __device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, i
         }
 #pragma unroll
         for (int k = 0; k < kWorkers; ++k) {
-            ex.start[REVERSE ? kWorkers - 1 - k : k][lane] = mine;
+            warp[REVERSE ? kWorkers - 1 - k : k][lane].P = mine;
             mine = fma2(r[k].P, mine, r[k].q);
         }
     } else {
@@ -457,11 +473,11 @@ __device__ __forceinline__ void conduct(const Outbox<V> &out, Exchange<V> &ex, i
 #pragma unroll
         for (int k = 0; k < kWorkers; ++k) {
             const int w = REVERSE ? kWorkers - 1 - k : k;
-            ex.start[w][lane] = mine;
+            warp[w][lane].P = mine;
             mine = apply(r[k], mine, (resets >> w) & 1u);
         }
     }
-    starts_published();
+    ex.starts_published(step);
 }
 
 // The tiles of one team: a cluster, or one CTA of it (`solo`).  Where the
@@ -513,7 +529,7 @@ constexpr int kStagesFwd = 3, kStagesBwd = 3;  // tiles of a worker's ring
 // ---------------------------------------------------------------------------
 template <typename T, int MODE, bool HOLD, bool ONE>
 __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, const Span<kRowsFwd> &sp,
-                                              Exchange<typename Lane<T>::V> &ex, uint4 *ring, int csize, int rank, int col0) {
+                                              Exchange<typename Lane<T>::V, true> &ex, uint4 *ring, int csize, int rank, int col0) {
     using L = Lane<T>;
     using V = typename L::V;
     constexpr int kRows = kRowsFwd, kTile = kWorkers * kRows;
@@ -523,11 +539,11 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
     const bool live = col < width;
 
     if (warp == kWorkers) {
-        const Outbox<V> out(ex, rank, csize, lane);
+        const Outbox<V, true> out(ex, rank, csize, lane);
         V state = L::splat(0.f);  // the state ahead of the cluster's tiles
         for (int step = 0; step < sp.steps; ++step) {
-            await_runs();
-            conduct<false, ONE>(out, ex, step & 1, rank, csize, lane, state, [] {});
+            ex.await_runs(step);
+            conduct<false, ONE>(out, ex, step, rank, csize, lane, state, [] {});
         }
         return;
     }
@@ -639,11 +655,10 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
             run.P = L::splat(0.f);
         }
     };
-    auto publish = [&](const Marks &m, const Run<V> &run) {
-        ex.warp[warp][lane] = run;
-        if (lane == 0) ex.warp_reset[warp] = m.starts;
-        runs_published();
-        if (!ONE) cluster_arrive_relaxed();
+    auto publish = [&](const Marks &m, const Run<V> &run, int step) {
+        ex.warp[step & 1][warp][lane] = run;
+        if (lane == 0) ex.warp_reset[step & 1][warp] = m.starts;
+        ex.runs_published(step);
     };
     auto states_of = [&](auto near, V h, uint32_t *src) {
 #pragma unroll
@@ -687,10 +702,15 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
         __syncwarp();  // the slot is free
     };
     auto slot = [&](int at) { return mine + at * (2 * kSlotWords) + lane; };
-    auto take_start = [&] {
-        await_starts(warp);
-        const V h = ex.start[warp][lane];
-        if (!ONE) cluster_wait();
+    // The workers' part in the cluster's barrier carries nothing.
+    if (!ONE && sp.steps > 0) cluster_arrive_relaxed();
+    auto take_start = [&](int step) {
+        ex.await_starts(step, warp);
+        const V h = ex.warp[step & 1][warp][lane].P;
+        if (!ONE) {
+            cluster_wait();
+            if (step + 1 < sp.steps) cluster_arrive_relaxed();
+        }
         return h;
     };
     Marks now;
@@ -702,8 +722,8 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
         for (int step = 0; step < sp.steps; ++step, row0 += stride) {
             copies_wait<kStagesFwd - 1>();
             first_pass(now, entry, run, row0, slot(at));
-            publish(now, run);
-            const V h = take_start();
+            publish(now, run, step);
+            const V h = take_start(step);
             second_pass(now, entry, h, slot(at));
             load(step + kStagesFwd);
             at = at + 1 == kStagesFwd ? 0 : at + 1;
@@ -713,7 +733,7 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
         V next_entry = entry;
         copies_wait<kStagesFwd - 1>();
         first_pass(now, entry, run, first_row, slot(0));
-        publish(now, run);
+        publish(now, run, 0);
         int at = 0;
         for (int step = 0; step < sp.steps; ++step) {
             const bool more = step + 1 < sp.steps;
@@ -721,9 +741,9 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
             if (more) {
                 copies_wait<kStagesFwd - 2>();
                 first_pass(next, next_entry, run, now.row0 + stride, slot(next_at));
+                publish(next, run, step + 1);
             }
-            const V h = take_start();
-            if (more) publish(next, run);
+            const V h = take_start(step);
             second_pass(now, entry, h, slot(at));
             load(step + kStagesFwd);
             now = next;
@@ -737,7 +757,7 @@ template <typename T, int MODE, bool HOLD>
 __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     extern __shared__ uint4 ring[];
-    __shared__ Exchange<typename L::V> ex;
+    __shared__ Exchange<typename L::V, true> ex;
     const int csize = cg::this_cluster().num_blocks(), rank = cg::this_cluster().block_rank();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols;
@@ -767,9 +787,8 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
 // CTA's own rows, composed by the conductor in the same step.
 // ---------------------------------------------------------------------------
 template <typename V> struct BackShared {
-    Exchange<V> ex;                  // adjoint runs
-    Run<V> fwd[kWorkers][32];        // the workers' state runs
-    V before[kWorkers][32];          // the state ahead of each worker's rows
+    Exchange<V, false> ex;        // adjoint runs
+    Run<V> fwd[kWorkers][32];     // the workers' state runs; then, in the place of P, the state ahead of its rows
     uint32_t fwd_reset[kWorkers];
 };
 
@@ -780,9 +799,8 @@ __device__ __forceinline__ void backward_tiles(const ScanArgs &p, int width, con
     using V = typename L::V;
     constexpr int kRows = kRowsBwd, kTile = kWorkers * kRows;
     constexpr int kSlotWords = kRows * 32, kSlotBytes = kSlotWords * 4;  // one tensor's rows of a worker
-    Exchange<V> &ex = sh.ex;
+    Exchange<V, false> &ex = sh.ex;
     auto &fwd = sh.fwd;
-    auto &before = sh.before;
     auto &fwd_reset = sh.fwd_reset;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = col0 + lane * L::kCols;
@@ -795,19 +813,20 @@ __device__ __forceinline__ void backward_tiles(const ScanArgs &p, int width, con
             return live && row > sp.t0 ? L::load_state(p.checkpoints + (int64_t)(row / kScanCheckpoint) * width + col)
                                        : L::splat(0.f);
         };
-        const Outbox<V> out(ex, rank, csize, lane);
+        const Outbox<V, false> out(ex, rank, csize, lane);
         V check = sp.steps > 0 ? checkpoint(0) : L::splat(0.f);
         V adjoint = L::splat(0.f);  // what the tokens behind the cluster's tiles hand back
         for (int step = 0; step < sp.steps; ++step) {
             V state = check;
             if (step + 1 < sp.steps) check = checkpoint(step + 1);
-            await_runs();
-            conduct<true, ONE>(out, ex, step & 1, rank, csize, lane, adjoint, [&] {
+            ex.await_runs(step);
+            conduct<true, ONE>(out, ex, step, rank, csize, lane, adjoint, [&] {
                 const uint32_t resets = reset_bits(fwd_reset, kWorkers, lane);
 #pragma unroll
                 for (int w = 0; w < kWorkers; ++w) {
-                    before[w][lane] = state;
-                    state = apply(fwd[w][lane], state, (resets >> w) & 1u);
+                    const Run<V> r = fwd[w][lane];
+                    fwd[w][lane].P = state;
+                    state = apply(r, state, (resets >> w) & 1u);
                 }
             });
         }
@@ -899,13 +918,12 @@ __device__ __forceinline__ void backward_tiles(const ScanArgs &p, int width, con
     };
     auto publish = [&](const Marks &m, const Run<V> &run, const Run<V> &back) {
         fwd[warp][lane] = run;
-        ex.warp[warp][lane] = back;
+        ex.warp[0][warp][lane] = back;
         if (lane == 0) {
             fwd_reset[warp] = m.starts;
-            ex.warp_reset[warp] = m.ends;
+            ex.warp_reset[0][warp] = m.ends;
         }
-        runs_published();
-        if (!ONE) cluster_arrive_relaxed();
+        ex.runs_published(0);
     };
     // EDGES: sequences begin or end among the rows.
     auto rows_of = [&](auto edges, auto near, const Marks &m, V state, V e, uint32_t *src) {
@@ -963,6 +981,7 @@ __device__ __forceinline__ void backward_tiles(const ScanArgs &p, int width, con
         copies_wait<kStagesBwd - 1>();
         first_pass(now, run, back, row0, mine + lane);
         publish(now, run, back);
+        if (!ONE) cluster_arrive_relaxed();
         for (int step = 0; step < sp.steps; ++step) {
             const bool more = step + 1 < sp.steps;
             const int next_slot = slot + 1 == kStagesBwd ? 0 : slot + 1;
@@ -971,10 +990,13 @@ __device__ __forceinline__ void backward_tiles(const ScanArgs &p, int width, con
                 copies_wait<kStagesBwd - 2>();
                 first_pass(next, run, back, row0, mine + next_slot * (3 * kSlotWords) + lane);
             }
-            await_starts(warp);
-            const V e = ex.start[warp][lane], state = before[warp][lane];
+            ex.await_starts(step, warp);
+            const V e = ex.warp[0][warp][lane].P, state = fwd[warp][lane].P;
             if (!ONE) cluster_wait();
-            if (more) publish(next, run, back);
+            if (more) {
+                publish(next, run, back);
+                if (!ONE) cluster_arrive_relaxed();
+            }
             second_pass(now, state, e, mine + slot * (3 * kSlotWords) + lane);
             load(step + kStagesBwd);
             now = next;
