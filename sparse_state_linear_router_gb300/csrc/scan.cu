@@ -521,12 +521,18 @@ constexpr int kStagesFwd = 3, kStagesBwd = 3;  // tiles of a worker's ring
 //  - HOLD false: the next tile's run is made while this one's is exchanged, and
 //    the second pass makes the decays and inputs again from shared memory;
 //  - HOLD true: they stay in registers between the passes, and only the SM's
-//    other CTA is at work during the exchange.  For input factors that cost more
-//    than the wait, where each SM has two CTAs.
-// 72000 tokens x 2048 channels, one sequence: s = 1 175 against 191 us (HOLD),
-// s = sqrt(1 - a^2) 301 against 240 us; at 512 channels, where an SM has one CTA
-// at most, 150 against 189 us.
+//    other CTA is at work during the exchange.
+// s = 1: 72000 tokens x 2048 channels, one sequence: 161 against 191 us (HOLD).
+// s = sqrt(1 - a^2) in bf16, 20000 tokens, one sequence: clusters of 8 (2048
+// channels) 77 against 69 us (HOLD), of 7 87 and 79, of 6 89 and 89, of 5 (3008
+// channels) 103 and 102, with s = 1 - a 94 and 103, of 4 114 and 125; 72000
+// tokens in 16 ragged sequences, clusters of 4: 226 and 236; CTAs that go alone
+// (8 x 4096 tokens): 97 and 79.  float32 (one channel per lane, half the
+// arithmetic): 170 and 202, alone 142 both.  At 512 channels, where an SM has one
+// CTA at most: 150 and 189.
 // ---------------------------------------------------------------------------
+enum { kRemake, kHoldAlone, kHold };  // HOLD never, where CTAs go alone, always
+
 template <typename T, int MODE, bool HOLD, bool ONE>
 __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, const Span<kRowsFwd> &sp,
                                               Exchange<typename Lane<T>::V, true> &ex, uint4 *ring, int csize, int rank, int col0) {
@@ -753,7 +759,7 @@ __device__ __forceinline__ void forward_tiles(const ScanArgs &p, int width, cons
     }
 }
 
-template <typename T, int MODE, bool HOLD>
+template <typename T, int MODE, int FORM>
 __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, int width) {
     using L = Lane<T>;
     extern __shared__ uint4 ring[];
@@ -763,11 +769,11 @@ __global__ void __launch_bounds__(kThreads, 2) scan_forward_kernel(ScanArgs p, i
     const int col0 = (int)(blockIdx.x / csize) * 32 * L::kCols;
     const Span<kRowsFwd> sp(p, csize, rank, lane);
     if (sp.solo) {
-        forward_tiles<T, MODE, HOLD, true>(p, width, sp, ex, ring, 1, 0, col0);
+        forward_tiles<T, MODE, FORM != kRemake, true>(p, width, sp, ex, ring, 1, 0, col0);
     } else {
         cluster_arrive_relaxed();  // every CTA has started before the first run is sent
         cluster_wait();
-        forward_tiles<T, MODE, HOLD, false>(p, width, sp, ex, ring, csize, rank, col0);
+        forward_tiles<T, MODE, FORM == kHold, false>(p, width, sp, ex, ring, csize, rank, col0);
     }
     const int col = col0 + lane * L::kCols;
     if (p.final_state && col < width && warp < kWorkers) {  // empty sequences keep their initial state
@@ -1103,11 +1109,12 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
     const int64_t tiles = ((int64_t)a.total_tokens + tile - 1) / tile;
     int csize = 1, ranges = 1;
     choose_clusters(columns, tiles, a.num_seqs, csize, ranges);
-    constexpr bool kHeavy = MODE != SSE_INPUT_PLAIN;
+    constexpr bool kHeavy = MODE != SSE_INPUT_PLAIN && sizeof(T) == 2;
     const bool hold = kHeavy && columns * csize * ranges >= 192;  // two CTAs on a quarter of the SMs or more
-    const auto kernel = what == kBackward ? scan_backward_kernel<T, MODE>
-                        : hold            ? scan_forward_kernel<T, MODE, kHeavy>
-                                          : scan_forward_kernel<T, MODE, false>;
+    const auto kernel = what == kBackward    ? scan_backward_kernel<T, MODE>
+                        : hold && csize >= 7 ? scan_forward_kernel<T, MODE, kHeavy ? kHold : kRemake>
+                        : hold               ? scan_forward_kernel<T, MODE, kHeavy ? kHoldAlone : kRemake>
+                                             : scan_forward_kernel<T, MODE, kRemake>;
     const size_t smem = (size_t)tile * 128 * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
