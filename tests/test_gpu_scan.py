@@ -498,3 +498,30 @@ def test_helpers_refuse(dtype="bf16"):
     refused(binding.scan_backward, cfg, x, la, cu, torch.empty(2, 64, device="cuda"), c["d_out"])
     refused(binding.scan_step, cfg, c["init"], x, la)
     refused(binding.scan_step, cfg, None, x, la)
+
+
+EVEN = [
+    ([512] * 8, 0),                                          # every CTA has a sequence of its own
+    ([500, 0, 520, 512, 480, 0, 508, 530, 505, 515, 0], 37),  # nearly so, with empty ones and rows behind
+    ([512] * 4 + [2048], 0),                                 # the first clusters' CTAs alone, the last ones together
+    ([64] * 61 + [130], 0),                                  # many to a CTA, edges inside tiles
+]
+
+
+@pytest.mark.parametrize("mode", MODES)
+@pytest.mark.parametrize("dtype,width", [("bf16", 2048), ("f32", 1024)])
+@pytest.mark.parametrize("lens,tail", EVEN, ids=["even", "nearly", "half", "many"])
+def test_even_sequences_beside_uneven_ones(lens, tail, dtype, width, mode):
+    """Sequences that fall evenly into the parts of a cluster's CTAs (which then exchange nothing), next to some that
+    do not; the final states over the initial ones."""
+    c = make(lens, width, dtype, seed=23, tail=tail)
+    f, b = run(c, mode, dtype)
+    sub, sub_f, sub_b = _pick(c, f, b, [0, 1, 31, 63, 64, 129, 700, width - 1])
+    check(sub, mode, dtype, sub_f, sub_b)
+    from sparse_state_linear_router_gb300 import binding
+    state = c["init"].clone()
+    cfg = binding.make_scan_config(width, mode, dtype)
+    got = binding.scan_forward(cfg, c["x"], c["la"], c["cu"], initial_state=state, final_state=state)
+    torch.cuda.synchronize()
+    n = sum(lens)
+    assert torch.equal(got["out"][:n], f["out"][:n]) and torch.equal(state, f["final_state"])
