@@ -32,6 +32,7 @@
 // instructions per two channels and row forward, 110 backward).  The first form,
 // in which every warp composed for itself between two cluster barriers, took
 // 413 us (s = 1).
+#include <atomic>
 #include <type_traits>
 
 #include <cooperative_groups.h>
@@ -1069,24 +1070,53 @@ __global__ void __launch_bounds__(128) scan_step_kernel(ScanArgs p, int width, i
 
 enum What { kForward, kBackward, kStep };
 
+// Clusters of c CTAs that the current device holds at a time, two CTAs per SM (a
+// property of the device, asked for once: every kernel here has the same two).
+int clusters_held(int c) {
+    static std::atomic<int> known[16][kMaxCluster + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return c == 1 ? 304 : 256 / c;
+    int n = known[dev][c].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    const auto kernel = scan_forward_kernel<__nv_bfloat16, SSE_INPUT_PLAIN, kRemake>;
+    constexpr int kSmem = kWorkers * kRowsFwd * 128 * 2 * kStagesFwd;
+    cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.gridDim = dim3(c);
+    cfg.blockDim = kThreads;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)c, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        return c == 1 ? 304 : 256 / c;
+    }
+    known[dev][c].store(n, std::memory_order_relaxed);
+    return n;
+}
+
 // Cluster size and ranges of the token axis: as many CTAs as the GPU holds at a
-// time, two per SM (a second wave of clusters would double the time: at 2560
-// channels and 20000 tokens, 40 clusters of 7 took 99 us where 40 of 6 take 72).
-// Larger clusters wait longer for each other (72000 x 2048 channels in 16 even
-// sequences: 192, 176, 168, 161 us with 8, 4, 2, 1 CTAs in 1, 2, 4, 8 ranges);
-// more ranges of whole sequences split uneven lengths less evenly (sequences cut
-// at random: the largest of R ranges is R^2 / 4S over its share; counted half).
+// time (a second wave of clusters would double the time: at 2560 channels and
+// 20000 tokens, 40 clusters of 7 took 99 us where 40 of 6 take 72).  A GB300 held
+// 304, 152, 97, 74, 58, 46, 38, 36 clusters of 1 to 8.  Larger clusters wait longer
+// for each other; more ranges of whole sequences split uneven lengths less evenly.
+// The two factors below are fitted to times of forwards and backwards at 2048
+// channels: 72001 tokens in 16 sequences cut at random, s = sqrt(1 - a^2), 249, 224,
+// 197, 240, 238 us with clusters of 8, 4, 3, 2, 1 in 1, 2, 3, 4, 8 ranges; in 5
+// (32768 tokens) 114, 107, 107, 143 with 8, 4, 3, 2.
 void choose_clusters(int columns, int64_t tiles, int num_seqs, int &csize, int &ranges) {
-    // Clusters of 1 to 8 CTAs that an idle GPU held, less a few: 304, 152, 97, 74, 58, 46, 38, 36.
-    static const int held[kMaxCluster + 1] = {0, 304, 148, 93, 71, 55, 44, 36, 34};
     double best = 0;
     for (int c = kMaxCluster; c >= 1; --c) {
-        if ((c > 1 && columns > held[c]) || (c > 1 && c > tiles)) continue;
-        int64_t r = held[c] / columns;
+        const int held = clusters_held(c);
+        if (c > 1 && (columns > held || c > tiles)) continue;
+        int64_t r = held / columns;
         if (r > num_seqs) r = num_seqs;
         if (r > tiles / c) r = tiles / c;
         if (r < 1) r = 1;
-        const double rate = (double)columns * c * r / ((1 + 0.025 * c) * (r > 1 ? 1 + 0.125 * r * r / num_seqs : 1));
+        const double rate = (double)columns * c * r / ((1 + 0.04 * c) * (r > 1 ? 1 + 0.06 * r * r * r / num_seqs : 1));
         if (rate > best) {
             best = rate;
             csize = c;
