@@ -23,15 +23,17 @@
 //    zero: a NaN of one sequence does not reach the next.
 //  - Rows come by asynchronous copies up to three tiles ahead, in 16-byte
 //    words, and leave in 16-byte words from the place of the inputs they replace.
+//  - Where a cluster's sequences fall evenly into a part for each of its CTAs,
+//    each CTA goes through its own part alone.
 //
-// Measured on a GB300 (72000 tokens x 2048 channels in bf16, one sequence; HBM
-// floor at 6.77 TB/s): forward 131 us, took 174 us with s = 1 and 239 us with
-// s = sqrt(1 - a^2); backward 218 us, took 296 us and 474 us.  What is left is
-// the wait of a cluster for its slowest worker (a step of 1024 rows takes 2.5 us;
-// 20 to 48 % of the warps' time) and, with s = sqrt(1 - a^2), the arithmetic (46
-// instructions per two channels and row forward, 110 backward).  The first form,
-// in which every warp composed for itself between two cluster barriers, took
-// 413 us (s = 1).
+// Measured on a GB300 (72000 tokens x 2048 channels in bf16; HBM floor at 6.77
+// TB/s: forward 131 us, backward 218 us).  One sequence: forward 162 us with s = 1
+// and 217 us with s = sqrt(1 - a^2), backward 296 and 407 us.  16 even sequences:
+// 164 and 160, 226 and 333 us.  What is left is a cluster's exchange (the difference
+// between the two) and, with s = sqrt(1 - a^2), the arithmetic.  The first form, in
+// which every warp composed for itself between two cluster barriers, took 413 us
+// forward (s = 1, one sequence).  Exchange by asynchronous remote stores that an
+// mbarrier counts, instead of the cluster's barrier: 196 against 179 us.
 #include <atomic>
 #include <type_traits>
 
@@ -138,11 +140,21 @@ template <typename T> __device__ __forceinline__ typename Lane<T>::V decay(typen
     }
 }
 
-// 1 - exp(u) for -1/2 <= u <= 0: -u times the Chebyshev interpolation of degree
-// 5 of (exp(u) - 1) / u on that interval (1.5e-9 off, 6e-8 with float32
-// roundings).  1 - exp(u) formed from exp(u) would cancel here.
+// 1 - exp(u) for -1/2 <= u <= 0: -u times the Chebyshev interpolation of (exp(u) -
+// 1) / u on that interval, for float32 gates of degree 5 (1.5e-9 off, 5e-8 with
+// float32 roundings), for bf16 ones of degree 4 (8e-8, 1.4e-7 with roundings: next
+// to the gates' own steps of 2^-9 nothing; 3 to 5 % of the time with s = sqrt(1 -
+// a^2)).  1 - exp(u) formed from exp(u) would cancel here.
 template <typename T> __device__ __forceinline__ typename Lane<T>::V one_minus_exp_near0(typename Lane<T>::V u) {
     using L = Lane<T>;
+    if constexpr (sizeof(T) == 2) {
+        auto p = L::splat(-0.00678286f);
+        p = fma2(p, u, L::splat(-0.04101321f));
+        p = fma2(p, u, L::splat(-0.16655193f));
+        p = fma2(p, u, L::splat(-0.49999288f));
+        p = fma2(p, u, L::splat(-0.99999994f));
+        return mul2(p, u);
+    }
     auto p = L::splat(-0.0011234042f);
     p = fma2(p, u, L::splat(-0.008189614f));
     p = fma2(p, u, L::splat(-0.041630074f));
