@@ -32,6 +32,7 @@ namespace sse {
 namespace {
 
 constexpr int kSms = 152;
+constexpr size_t kRoom = 220 * 1024;  // shared memory of an SM that the CTAs of a call may take together
 
 // How the sum of squares of the norm after the block is shared.
 enum { kGroupNone, kGroupRow, kGroupShuffle, kGroupShared };
@@ -681,11 +682,10 @@ NormPlan plan_norm(const sse_norm_config_t &c, const BlockNormArgs &a, bool back
     const size_t fixed = p.coef_bytes + p.sum_bytes + (p.n.mode == kGroupShared ? sizeof(float) * p.rows * p.n.nv : 0);
     // As many CTAs on an SM as its registers and shared memory hold (up to 128 registers per thread with two words, 64
     // and 96 with one), then up to three rows of each.
-    const size_t room = 220 * 1024;
     p.per_sm = most_per_sm(p, backward);
-    while (p.per_sm > 1 && p.per_sm * (p.row_bytes + fixed) > room) --p.per_sm;
+    while (p.per_sm > 1 && p.per_sm * (p.row_bytes + fixed) > kRoom) --p.per_sm;
     p.n.stages = 3;
-    while (p.n.stages > 1 && p.per_sm * (p.n.stages * p.row_bytes + fixed) > room) --p.n.stages;
+    while (p.n.stages > 1 && p.per_sm * (p.n.stages * p.row_bytes + fixed) > kRoom) --p.n.stages;
     p.smem = p.n.stages * p.row_bytes + fixed;
     return p;
 }
@@ -699,7 +699,9 @@ template <typename T, int VPT, int MAXT>
 cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
     const auto kernel = backward ? norm_backward_kernel<T, VPT, MAXT> : norm_forward_kernel<T, VPT, MAXT>;
     if (p.smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+        // The limit belongs to the kernel and not to the call, whose size differs from that of another host thread's:
+        // every call sets the same one.
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
         if (e != cudaSuccess) return e;
     }
     const int64_t width = p.n.width, fwd[5] = {a.o_stride, a.z_stride, a.r_stride, 0, 0},
