@@ -382,7 +382,8 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
  *   d_log_gate_t = dh_t (a_t h_{t-1} + s'(log_gate_t) x_t);
  *   d_initial_state = a_1 dh_1
  * with the states recomputed in float32 from the checkpoints.  With
- * SSE_INPUT_UNIT, s' is unbounded at log_gate = 0 and taken as zero there.
+ * SSE_INPUT_UNIT, s' is unbounded at log_gate = 0 and taken as zero there (where
+ * 1 - a^2 is below the least normal float32; s counts as zero there, too).
  * d_final_state and d_initial_state may be NULL.  Apart from final_state,
  * outputs do not overlap inputs.
  * Tokens at and past cu_seqlens[num_seqs] (a padded batch) belong to no

@@ -194,11 +194,12 @@ __device__ __forceinline__ void factors(typename Lane<T>::V la, typename Lane<T>
             const auto u = add2(la, la);
             s2 = each(u, one_minus_exp_near0<T>(u), mul2(a, a), [](float x, float near0, float e) { return x > -0.5f ? near0 : 1.f - e; });
         }
-        // r = 1 / s; 10^-37 keeps it finite where s is 0: no input enters there, and s r makes its slope 0 too
+        // r = 1 / s, 0 where no input enters (1 - a^2 below the least normal number, as the forward's root takes it):
+        // the slope is 0 there.  A NaN stays.  The slope has one reciprocal root's error, 2^-22.9.
         if constexpr (GRAD) {
-            const auto r = each(add2(s2, L::splat(1e-37f)), [](float v) { return rsqrt_ftz(v); });
+            const auto r = each(s2, [](float v) { return fabsf(v) < 1.17549435e-38f ? 0.f : rsqrt_ftz(v); });
             s = mul2(s2, r);
-            *slope = mul2(mul2(mul2(a, a), mul2(r, minus)), mul2(s, r));
+            *slope = mul2(mul2(a, a), mul2(r, minus));
         } else {
             s = each(s2, [](float v) { return sqrt_ftz(v); });
         }

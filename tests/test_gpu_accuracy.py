@@ -1,0 +1,69 @@
+"""Float32 accuracy of the scan and the block norms against float64 where
+approximate instructions, or the order of a sum, could lose it (marked gpu).
+u = 2^-24 is half a step of float32 next to 1; rsqrt.approx is at most
+2^-22.9 off."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+ROOT = 2.0 ** -22.9
+
+
+@pytest.fixture(scope="module")
+def b():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from sparse_state_linear_router_gb300 import binding
+    binding.load()
+    return binding
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+@pytest.mark.parametrize("each", [False, True], ids=["one", "many"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_slope_of_the_unit_input_factor(b, dtype, each):
+    """s = sqrt(1 - a^2) and its slope -a^2 / s for log-gates between 0 and -2^-32, read off from a token with x = 1
+    and d_out = 1 that no other token reaches: d_log_gate is the slope, dx is s.
+
+    There a and a^2 round to 1 and 1 - a^2 to -2 log_gate without an error, so what is left is one root in the slope
+    (2^-22.9) and in s, which may be formed from the reciprocal root, another product (u).  With a token in every
+    sequence a comes from the exponential: at most 2^-22 + u off (ex2.approx and a product), twice that and u in a^2,
+    and the series for 1 - a^2 at most 1e-7.  2^-30 covers 1 - a^2 against 1 and the second order."""
+    T, W = 96, 4096
+    g = torch.Generator().manual_seed(3)
+    dt = torch.float32 if dtype == "f32" else torch.bfloat16
+    la = -(2.0 ** (torch.rand(T, W, generator=g) * -90 - 32))      # from 2^-122 to 2^-32
+    la = la.to(dt).cuda()
+    if each:
+        cu, at = torch.arange(T + 1), None
+        x = d = torch.ones(T, W)
+    else:
+        cu, at = torch.tensor([0, T]), torch.randint(16, T - 16, (W,), generator=g)   # no first or last rows
+        x = d = torch.zeros(T, W).scatter_(0, at[None], 1.0)
+    cu, x, d = cu.int().cuda(), x.to(dt).cuda(), d.to(dt).cuda()
+    cfg = b.make_scan_config(W, "unit", dtype)
+    f = b.scan_forward(cfg, x, la, cu, want_checkpoints=True)
+    r = b.scan_backward(cfg, x, la, cu, f["checkpoints"], d)
+    torch.cuda.synchronize()
+    l64 = _f64(la)
+    s = np.sqrt(-np.expm1(2 * l64))
+    slope = -np.exp(2 * l64) / s
+    got_slope, got_s = _f64(r["d_log_gate"]), _f64(r["dx"])
+    if not each:
+        pick = at.numpy(), np.arange(W)
+        s, slope, got_slope, got_s = (v[pick] for v in (s, slope, got_slope, got_s))
+    half = 0.0 if dtype == "f32" else torch.finfo(dt).eps / 2
+    slack = 2.0 ** -30 + half
+    gate = 2 * (2.0 ** -22 + U) + U if each else 0.0
+    series = 0.5e-7 if each else 0.0
+    worst = np.abs(got_slope / slope - 1).max()
+    assert worst <= ROOT + gate + series + 2 * U * each + slack, worst
+    worst = np.abs(got_s / s - 1).max()
+    assert worst <= ROOT + U + series + slack, worst
