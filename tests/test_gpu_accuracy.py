@@ -67,3 +67,32 @@ def test_slope_of_the_unit_input_factor(b, dtype, each):
     assert worst <= ROOT + gate + series + 2 * U * each + slack, worst
     worst = np.abs(got_s / s - 1).max()
     assert worst <= ROOT + U + series + slack, worst
+
+
+@pytest.mark.parametrize("gate", ["silu", "sigmoid"])
+def test_float32_gates(b, gate):
+    """act(z) and act'(z) of float32 gates from -86 to 30.
+
+    sigma = 1 / (1 + exp(-z)): exp at most 2 units in the last place off (4 u), the sum rounded (u), the reciprocal
+    one unit off (2 u): 7 u.  act: one product more, and those with the block's output of 1 are exact.  act' = sigma
+    (1 - sigma) or sigma (1 + z (1 - sigma)): 1 - sigma is off by 7 u sigma + u, z times that and its own rounding in
+    the sum, and one more product."""
+    W, T = 1024, 32
+    z = torch.linspace(-86, 30, T * W).reshape(T, W).cuda()
+    one = torch.ones(T, W, device="cuda")
+    cfg = b.make_norm_config(W, gate=gate, dtype="f32")
+    f = b.block_norm(cfg, one, gate=z)["residual_out"]
+    r = b.block_norm_backward(cfg, one, one, gate=z)
+    torch.cuda.synchronize()
+    z = _f64(z)
+    sg = 1 / (1 + np.exp(-z))
+    rest = 1 / (1 + np.exp(z))              # 1 - sigma
+    act = z * sg if gate == "silu" else sg
+    for got in (_f64(f), _f64(r["d_block_out"])):
+        bad = np.abs(got - act) > 8.5 * U * np.abs(act)
+        assert not bad.any(), (bad.sum(), z[bad][0], got[bad][0], act[bad][0])
+    inner = 1 + z * rest if gate == "silu" else rest
+    off = (np.abs(z) if gate == "silu" else 1.0) * (7 * U * sg + U)
+    tol = sg * (off + 9 * U * np.abs(inner) + U)
+    bad = np.abs(_f64(r["d_gate"]) - sg * inner) > 1.01 * tol
+    assert not bad.any(), (bad.sum(), z[bad][0])
