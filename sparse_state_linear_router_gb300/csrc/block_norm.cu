@@ -35,7 +35,7 @@ constexpr int kSms = 152;
 constexpr size_t kRoom = 220 * 1024;  // shared memory of an SM that the CTAs of a call may take together
 
 // How the sum of squares of the norm after the block is shared.
-enum { kGroupNone, kGroupRow, kGroupShuffle, kGroupShared };
+enum { kGroupNone, kGroupRow, kGroupShuffle, kGroupShared, kGroupWide };
 
 // One 16-byte word of a row as float32 pairs.
 template <typename T> struct Row {
@@ -134,7 +134,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 // CTA.  Every thread of the CTA makes the same calls (they synchronize).
 struct Team {
     float *warp_words;  // [2][rows][2][32]: this row's words, two buffers in turn; zero behind the last warp
-    float *vec_words;   // [rows][words of a row]: kGroupShared only
+    float *vec_words;   // [rows][words of a row]: kGroupShared and kGroupWide
     int turn;
     __device__ __forceinline__ Team(uint4 *smem, uint32_t sums_at, uint32_t words_at) {
         warp_words = reinterpret_cast<float *>(reinterpret_cast<char *>(smem) + sums_at);
@@ -171,9 +171,35 @@ struct Team {
 
 // Sums over each group of the row; in: per 16-byte word v (0 for a word past
 // the row), out: the sum of the word's group.  gw: words of a group.
-template <int VPT>
+// WIDE: the kernels for groups of more than 32 words, kGroupWide, and no others
+// (in one kernel with the rest it took registers of those: the norm before alone
+// of 16384 x 2304 bf16 42 against 38 us).
+template <bool WIDE, int VPT>
 __device__ __forceinline__ void group_sum(Team &tm, int mode, int gw, int nv, float (&v)[VPT]) {
-    if (mode == kGroupRow) {
+    if constexpr (WIDE) {
+        // A warp adds up a group, 32 words at a time, into the place of its first word: no sum has more than 32 terms
+        // one after the other.
+        float *w = tm.vec_words + threadIdx.y * nv;
+        __syncthreads();  // the sums of the call before have been read
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = threadIdx.x + i * blockDim.x;
+            if (j < nv) w[j] = v[i];
+        }
+        __syncthreads();
+        for (int j0 = ((int)threadIdx.x >> 5) * gw; j0 < nv; j0 += ((int)blockDim.x >> 5) * gw) {
+            float s = 0.f;
+            for (int k = threadIdx.x & 31; k < gw; k += 32) s += w[j0 + k];
+            s = warp_sum(s);
+            if ((threadIdx.x & 31) == 0) w[j0] = s;  // which only this lane has read
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int j = threadIdx.x + i * blockDim.x;
+            if (j < nv) v[i] = w[j / gw * gw];
+        }
+    } else if (mode == kGroupRow) {
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) s += v[i];
@@ -187,7 +213,7 @@ __device__ __forceinline__ void group_sum(Team &tm, int mode, int gw, int nv, fl
             if (o < gw)
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    } else {
+    } else {  // up to 32 words: each thread adds up its words' groups
         float *w = tm.vec_words + threadIdx.y * nv;
         __syncthreads();  // the sums of the call before have been read
 #pragma unroll
@@ -318,7 +344,7 @@ __device__ __forceinline__ void load_coef(const BlockNormArgs &a, const NormShap
     }
 }
 
-template <typename T, int VPT, int MAXT>
+template <typename T, int VPT, int MAXT, bool WIDE>
 __global__ void __launch_bounds__(MAXT, VPT == 1 ? 8 : 1) norm_forward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int P = Row<T>::kP;
     extern __shared__ uint4 smem[];
@@ -357,7 +383,7 @@ __global__ void __launch_bounds__(MAXT, VPT == 1 ? 8 : 1) norm_forward_kernel(Bl
                 for (int k = 0; k < P; ++k) t = fma2(u[i][k], u[i][k], t);
                 ss[i] = fold(t);
             }
-            group_sum<VPT>(tm, n.mode, n.gw, n.nv, ss);
+            group_sum<WIDE>(tm, n.mode, n.gw, n.nv, ss);
 #pragma unroll
             for (int i = 0; i < VPT; ++i) {
                 const F2 rstd = both(rsqrt_ftz(fmaf(ss[i], n.inv_group, n.eps)));
@@ -460,7 +486,7 @@ template <typename T, bool SMEM> struct Coefs {
     }
 };
 
-template <typename T, int VPT, int MAXT>
+template <typename T, int VPT, int MAXT, bool WIDE>
 __global__ void __launch_bounds__(MAXT, VPT == 1 ? 5 : 1) norm_backward_kernel(BlockNormArgs a, NormShape n) {
     constexpr int E = Row<T>::kE, P = Row<T>::kP;
     extern __shared__ uint4 smem[];
@@ -545,7 +571,7 @@ __global__ void __launch_bounds__(MAXT, VPT == 1 ? 5 : 1) norm_backward_kernel(B
                     for (int k = 0; k < P; ++k) t = fma2(o[k], o[k], t);
                     rstd[i] = fold(t);
                 }
-                group_sum<VPT>(tm, n.mode, n.gw, n.nv, rstd);
+                group_sum<WIDE>(tm, n.mode, n.gw, n.nv, rstd);
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) rstd[i] = rsqrt_ftz(fmaf(rstd[i], n.inv_group, n.eps));
             } else {
@@ -580,7 +606,7 @@ __global__ void __launch_bounds__(MAXT, VPT == 1 ? 5 : 1) norm_backward_kernel(B
                 dot[i] = fold(t);
             }
             if (n.mode != kGroupNone) {
-                group_sum<VPT>(tm, n.mode, n.gw, n.nv, dot);
+                group_sum<WIDE>(tm, n.mode, n.gw, n.nv, dot);
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
                     // d = rstd (d - o_hat mean), o_hat = o rstd
@@ -668,7 +694,7 @@ NormPlan plan_norm(const sse_norm_config_t &c, const BlockNormArgs &a, bool back
     p.n.nv = c.width / E;
     p.n.gw = group / E;
     const bool pow2 = (p.n.gw & (p.n.gw - 1)) == 0;
-    p.n.mode = !after ? kGroupNone : group == c.width ? kGroupRow : pow2 && p.n.gw <= 32 ? kGroupShuffle : kGroupShared;
+    p.n.mode = !after ? kGroupNone : group == c.width ? kGroupRow : p.n.gw > 32 ? kGroupWide : pow2 ? kGroupShuffle : kGroupShared;
     p.n.gate = c.gate;
     p.n.eps = c.eps;
     p.n.rs = c.residual_scale;
@@ -690,7 +716,7 @@ NormPlan plan_norm(const sse_norm_config_t &c, const BlockNormArgs &a, bool back
     for (int t = 0; t < (backward ? 5 : 3); ++t)
         if (!(backward ? bwd : fwd)[t]) p.n.slot[t] = present * p.vpt * p.n.word;
     p.row_bytes = (present + (present < (backward ? 5 : 3))) * p.vpt * p.n.word;
-    const size_t fixed = p.coef_bytes + p.sum_bytes + (p.n.mode == kGroupShared ? sizeof(float) * p.rows * p.n.nv : 0);
+    const size_t fixed = p.coef_bytes + p.sum_bytes + (p.n.mode >= kGroupShared ? sizeof(float) * p.rows * p.n.nv : 0);
     // As many CTAs on an SM as its registers and shared memory hold (up to 128 registers per thread with two words, 64
     // and 96 with one), then up to three rows of each.
     p.per_sm = most_per_sm(p, backward);
@@ -706,9 +732,9 @@ int norm_grid(const NormPlan &p, int64_t T) {
     return (int)(need < most ? need : most);
 }
 
-template <typename T, int VPT, int MAXT>
+template <typename T, int VPT, int MAXT, bool WIDE>
 cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    const auto kernel = backward ? norm_backward_kernel<T, VPT, MAXT> : norm_forward_kernel<T, VPT, MAXT>;
+    const auto kernel = backward ? norm_backward_kernel<T, VPT, MAXT, WIDE> : norm_forward_kernel<T, VPT, MAXT, WIDE>;
     if (p.smem > 48 * 1024) {
         // The limit belongs to the kernel and not to the call, whose size differs from that of another host thread's:
         // every call sets the same one.
@@ -730,9 +756,11 @@ cudaError_t launch_t(NormPlan p, const BlockNormArgs &a, bool backward, cudaStre
 
 template <typename T>
 cudaError_t launch_rows(const NormPlan &p, const BlockNormArgs &a, bool backward, cudaStream_t stream) {
-    if (p.vpt == 1) return launch_t<T, 1, 128>(p, a, backward, stream);
-    if (p.threads <= 512) return launch_t<T, 2, 512>(p, a, backward, stream);
-    return launch_t<T, 2, 1024>(p, a, backward, stream);
+    if (p.vpt == 1) return launch_t<T, 1, 128, false>(p, a, backward, stream);  // 32 words at most
+    const bool wide = p.n.mode == kGroupWide;
+    if (p.threads <= 512)
+        return wide ? launch_t<T, 2, 512, true>(p, a, backward, stream) : launch_t<T, 2, 512, false>(p, a, backward, stream);
+    return wide ? launch_t<T, 2, 1024, true>(p, a, backward, stream) : launch_t<T, 2, 1024, false>(p, a, backward, stream);
 }
 
 }  // namespace

@@ -96,3 +96,29 @@ def test_float32_gates(b, gate):
     tol = sg * (off + 9 * U * np.abs(inner) + U)
     bad = np.abs(_f64(r["d_gate"]) - sg * inner) > 1.01 * tol
     assert not bad.any(), (bad.sum(), z[bad][0])
+
+
+@pytest.mark.parametrize("group", [4096, 2048, 1360])
+def test_sums_of_wide_groups(b, group):
+    """Norms over float32 groups whose first 16-byte word outweighs every other so far that a sum over the words one
+    by one would lose each of them: they are a little under half a step of the first.  The tolerance is that of a
+    mean of at most a few hundred serially added terms, 2^-17, its root (half) and u for each product."""
+    T, W = 3, group * 2
+    o = torch.full((T, W), (0.9 * 2.0 ** -24) ** 0.5)
+    o[:, ::group], o[:, 1::group], o[:, 2::group], o[:, 3::group] = 1.0, 1.0, 1.0, 1.0   # sum 4, half a step 2^-22
+    o = o.cuda()
+    w = torch.ones(W, device="cuda")
+    cfg = b.make_norm_config(W, group=group, eps=1e-12, dtype="f32")
+    f = b.block_norm(cfg, o, w_after=w)["residual_out"]
+    d = torch.ones(T, W, device="cuda")
+    r = b.block_norm_backward(cfg, d, o, w_after=w)
+    torch.cuda.synchronize()
+    v = _f64(o).reshape(T, 2, group)
+    rstd = 1 / np.sqrt((v * v).mean(axis=2, keepdims=True) + 1e-12)
+    hat = v * rstd
+    want = hat.reshape(T, W)
+    assert (np.abs(_f64(f) / want - 1) <= 2.0 ** -18 + ROOT + 4 * U).all()
+    dot = hat.mean(axis=2, keepdims=True)
+    back = (rstd * (1 - hat * dot)).reshape(T, W)
+    size = (rstd * (1 + np.abs(hat * dot))).reshape(T, W)
+    assert (np.abs(_f64(r["d_block_out"]) - back) <= (2.0 ** -16 + 8 * U) * size).all()
