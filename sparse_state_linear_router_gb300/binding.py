@@ -570,8 +570,8 @@ def _first(what, t):
 
 
 def _sequences(what, cu_seqlens, device):
-    if (cu_seqlens.dtype is not _torch().int32 or cu_seqlens.device != device or cu_seqlens.dim() != 1 or
-            cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
+    if (cu_seqlens is None or cu_seqlens.dtype is not _torch().int32 or cu_seqlens.device != device or
+            cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1 or not cu_seqlens.is_contiguous()):
         _refuse(what, f"cu_seqlens is not a contiguous int32 [sequences + 1] on {device}")
     return cu_seqlens.numel() - 1
 
@@ -619,6 +619,8 @@ def scan_backward(cfg, x, log_gate, cu_seqlens, checkpoints, d_out, *, initial_s
     px, sx = _rows(what, "x", x, T, W, dt, dev)
     pg, sg = _rows(what, "log_gate", log_gate, T, W, dt, dev)
     pd = _packed(what, "d_out", d_out, T, W, dt, dev)
+    if log_gate is None:
+        _refuse(what, "log_gate is None")
     if checkpoints is None:
         _refuse(what, "checkpoints is None: scan_forward(..., want_checkpoints=True) returns them")
     pc = _floats(what, "checkpoints", checkpoints, (-(-T // SCAN_CHECKPOINT), W), dev)

@@ -67,3 +67,19 @@ def test_norms_of_several_sizes_from_several_threads(b):
         assert status == [{b.SSE_OK}] * len(pair)
         for a, e in zip(got, want):
             assert torch.equal(a[0], e[0]) and torch.equal(a[1], e[1])
+
+
+def test_missing_tensors_are_refused(b):
+    T, W = 6, 64
+    x = torch.zeros(T, W, dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    check, cfg = torch.zeros(1, W, device="cuda"), b.make_scan_config(W)
+    state = torch.zeros(T, W, device="cuda")
+    for call in (lambda: b.scan_forward(cfg, None, x, cu), lambda: b.scan_forward(cfg, x, None, cu),
+                 lambda: b.scan_forward(cfg, x, x, None), lambda: b.scan_backward(cfg, x, None, cu, check, x),
+                 lambda: b.scan_backward(cfg, x, x, None, check, x), lambda: b.scan_backward(cfg, x, x, cu, check, None),
+                 lambda: b.scan_backward(cfg, x, x, cu, None, x), lambda: b.scan_step(cfg, state, x, None),
+                 lambda: b.scan_step(cfg, None, x, x)):
+        with pytest.raises(b.SSEError) as e:
+            call()
+        assert e.value.status == b.SSE_ERR_INVALID_ARG
