@@ -1140,8 +1140,24 @@ void choose_clusters(int columns, int64_t tiles, int num_seqs, int &csize, int &
     }
 }
 
+struct Choice {
+    int csize, ranges, form;  // form: of the forward's rows
+};
+
+Choice choose(const sse_scan_config_t &cfg, bool forward, int64_t total_tokens, int num_seqs) {
+    const int columns = (cfg.width * (cfg.dtype == SSE_BF16 ? 2 : 4) + 127) / 128;
+    const int tile = kWorkers * (forward ? kRowsFwd : kRowsBwd);
+    Choice c{1, 1, kRemake};
+    choose_clusters(columns, (total_tokens + tile - 1) / tile, num_seqs, c.csize, c.ranges);
+    // held: costly bf16 input factors with two CTAs on a quarter of the SMs or more
+    if (cfg.input_scale != SSE_INPUT_PLAIN && cfg.dtype == SSE_BF16 && columns * c.csize * c.ranges >= 192)
+        c.form = c.csize >= 7 ? kHold : kHoldAlone;
+    return c;
+}
+
 template <typename T, int MODE>
-cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t stream) {
+cudaError_t launch_t(What what, const sse_scan_config_t &scan, const ScanArgs &a, cudaStream_t stream) {
+    const int width = scan.width;
     if (what == kStep) {
         const int words = width * (int)sizeof(T) / 16;
         const int64_t blocks = ((int64_t)a.num_seqs * words + 127) / 128;
@@ -1150,27 +1166,24 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
         return cudaGetLastError();
     }
     const int columns = (width + 32 * Lane<T>::kCols - 1) / (32 * Lane<T>::kCols);
-    const int rows = what == kForward ? kRowsFwd : kRowsBwd, tile = kWorkers * rows;
-    const int64_t tiles = ((int64_t)a.total_tokens + tile - 1) / tile;
-    int csize = 1, ranges = 1;
-    choose_clusters(columns, tiles, a.num_seqs, csize, ranges);
+    const int tile = kWorkers * (what == kForward ? kRowsFwd : kRowsBwd);
+    const Choice c = choose(scan, what == kForward, a.total_tokens, a.num_seqs);
     constexpr bool kHeavy = MODE != SSE_INPUT_PLAIN && sizeof(T) == 2;
-    const bool hold = kHeavy && columns * csize * ranges >= 192;  // two CTAs on a quarter of the SMs or more
-    const auto kernel = what == kBackward    ? scan_backward_kernel<T, MODE>
-                        : hold && csize >= 7 ? scan_forward_kernel<T, MODE, kHeavy ? kHold : kRemake>
-                        : hold               ? scan_forward_kernel<T, MODE, kHeavy ? kHoldAlone : kRemake>
-                                             : scan_forward_kernel<T, MODE, kRemake>;
+    const auto kernel = what == kBackward      ? scan_backward_kernel<T, MODE>
+                        : c.form == kHold      ? scan_forward_kernel<T, MODE, kHeavy ? kHold : kRemake>
+                        : c.form == kHoldAlone ? scan_forward_kernel<T, MODE, kHeavy ? kHoldAlone : kRemake>
+                                               : scan_forward_kernel<T, MODE, kRemake>;
     const size_t smem = (size_t)tile * 128 * (what == kForward ? 2 * kStagesFwd : 3 * kStagesBwd);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.dynamicSmemBytes = smem;
-    cfg.gridDim = dim3(columns * csize, ranges);
+    cfg.gridDim = dim3(columns * c.csize, c.ranges);
     cfg.blockDim = kThreads;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim = {(unsigned)csize, 1, 1};
+    attr[0].val.clusterDim = {(unsigned)c.csize, 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, a, width);
@@ -1179,9 +1192,9 @@ cudaError_t launch_t(What what, const ScanArgs &a, int width, cudaStream_t strea
 template <typename T>
 cudaError_t launch_mode(What what, const sse_scan_config_t &cfg, const ScanArgs &a, cudaStream_t stream) {
     switch (cfg.input_scale) {
-    case SSE_INPUT_PLAIN: return launch_t<T, SSE_INPUT_PLAIN>(what, a, cfg.width, stream);
-    case SSE_INPUT_COMPLEMENT: return launch_t<T, SSE_INPUT_COMPLEMENT>(what, a, cfg.width, stream);
-    default: return launch_t<T, SSE_INPUT_UNIT>(what, a, cfg.width, stream);
+    case SSE_INPUT_PLAIN: return launch_t<T, SSE_INPUT_PLAIN>(what, cfg, a, stream);
+    case SSE_INPUT_COMPLEMENT: return launch_t<T, SSE_INPUT_COMPLEMENT>(what, cfg, a, stream);
+    default: return launch_t<T, SSE_INPUT_UNIT>(what, cfg, a, stream);
     }
 }
 
@@ -1203,3 +1216,12 @@ cudaError_t launch_scan_step(const sse_scan_config_t &cfg, const ScanArgs &a, cu
 }
 
 }  // namespace sse
+
+// What a forward of these sizes takes, for tests: its form, and the clusters.  Not part of the ABI.
+extern "C" int sse_debug_scan_form(const sse_scan_config_t *cfg, int32_t total_tokens, int32_t num_seqs, int32_t *csize,
+                                   int32_t *ranges) {
+    const sse::Choice c = sse::choose(*cfg, true, total_tokens, num_seqs);
+    *csize = c.csize;
+    *ranges = c.ranges;
+    return c.form;
+}
