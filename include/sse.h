@@ -360,8 +360,8 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
  * The config's input_scale chooses s: SSE_INPUT_PLAIN s = 1;
  * SSE_INPUT_COMPLEMENT s = 1 - a; SSE_INPUT_UNIT s = sqrt(1 - a^2) (keeps the
  * variance of the state).  log_gate <= 0 (decays in [0, 1]; the log_gate and v
- * of sse_front_end fit as they are); a log-gate of -infinity empties the
- * state.  Positive log-gates are outside the method and not checked.  A NaN or
+ * of sse_front_end fit as they are); a log-gate of -infinity empties a finite
+ * state (0 times an infinity or a NaN is a NaN).  Positive log-gates are outside the method and not checked.  A NaN or
  * an infinity stays in its own sequence and channel, from its token on.
  *
  *   x, log_gate, d_out   [total_tokens, width] in cfg->dtype.  x and log_gate
@@ -375,8 +375,10 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
  *   checkpoints          float32 [sse_scan_checkpoint_rows(total_tokens),
  *                        width], may be NULL (not written): the state before
  *                        every 64th packed token, which the backward reads
- *                        instead of repeating the forward.  Rows that no
- *                        sequence passes through are left as they were.
+ *                        instead of repeating the forward.  Where that token
+ *                        is the first of its sequence the row's value means
+ *                        nothing (the backward takes initial_state); rows that
+ *                        no sequence passes through are left as they were.
  * Backward, for L = <d_out, out> + <d_final_state, final_state>:
  *   dh_t = d_out_t + a_{t+1} dh_{t+1};  dx_t = s(a_t) dh_t;
  *   d_log_gate_t = dh_t (a_t h_{t-1} + s'(log_gate_t) x_t);

@@ -18,13 +18,20 @@
 // them), so the next rows' loads are in flight while this one is summed.  Sums
 // over the row go through shuffles and one word per warp of shared memory; sums
 // over a group of columns through shuffles where the group is a power of two of
-// lanes.  Arithmetic is on float32 pairs.  Measured on a GB300, bf16, against
-// the bytes at 6.77 TB/s: per-head norm and gate of 32768 x 2048 67 us (floor
-// 59.5); norm, scale, residual and next norm of 16384 x 2304 53 us (44.6);
-// backward of head norm, gate, residual and next norm of 32768 x 2048 185 us
-// (158.6).  One word per thread left the same backward at 254 us: the control
-// flow of a row (600 instructions per word then, 510 now) is shared by two words.
-// Bound now by issue at 16 warps per SM (60 % of the slots) as much as by HBM.
+// lanes, else through shared memory: up to 32 words by every thread for its own,
+// beyond by a warp per group.  Arithmetic is on float32 pairs.  Measured on a
+// GB300, bf16, against the bytes at 6.77 TB/s: per-head norm and gate of 32768 x
+// 2048 67 us (floor 59.5); norm, scale, residual and next norm of 16384 x 2304 53
+// us (44.6); backward of head norm, gate, residual and next norm of 32768 x 2048
+// 182 us (158.6); the norm before alone, 32768 x 2048, 52 us (39.6).  Groups of 96
+// and 192 columns: 16384 x 2304 67 and 71 us (44.6), backward 131 and 138 (66.9);
+// of 512: 16384 x 2048 with a gate 63 (49.6) and 121 (79.3).  float32, 16384 x
+// 2048, norm over the row, gate, residual and next norm: 120 us (99.1) and 165
+// (158.6).  Rows of 16384 columns have 64 registers per thread and spill: 4096 of
+// them 123 us (79.3) and 331 (118.9).  One word per thread left the same backward
+// (every part, 32768 x 2048) at 254 us: the control flow of a row (600 instructions
+// per word then, 510 now) is shared by two words.  Bound now by issue at 16 warps
+// per SM (60 % of the slots) as much as by HBM.
 #include "f32x2.cuh"
 #include "sse_internal.cuh"
 
@@ -114,6 +121,7 @@ template <typename T, bool GRAD, int P> __device__ __forceinline__ void act(int 
     }
 }
 
+// At most 2^-22.9 off, in float32 rows too: once per row or group, next to the 2^-24 of every product behind it.
 __device__ __forceinline__ float rsqrt_ftz(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

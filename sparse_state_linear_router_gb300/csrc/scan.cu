@@ -27,10 +27,15 @@
 //    each CTA goes through its own part alone.
 //
 // Measured on a GB300 (72000 tokens x 2048 channels in bf16; HBM floor at 6.77
-// TB/s: forward 131 us, backward 218 us).  One sequence: forward 162 us with s = 1
-// and 217 us with s = sqrt(1 - a^2), backward 296 and 407 us.  16 even sequences:
-// 164 and 160, 226 and 333 us.  What is left is a cluster's exchange (the difference
-// between the two) and, with s = sqrt(1 - a^2), the arithmetic.  The first form, in
+// TB/s: forward 131 us, backward 218 us).  One sequence: forward 160 us with s = 1,
+// 212 with s = 1 - a and 217 with s = sqrt(1 - a^2), backward 293, 362 and 398 us.
+// 16 even sequences: 164, 157 and 159, 223, 288 and 319 us.  What is left is a
+// cluster's exchange (the difference between the two) and, with a costly input
+// factor, the arithmetic.  Gates below -1/2 take the general form of the factor:
+// with log-gates 16 times as strong 222 and 224, 369 and 414 us, in even sequences
+// 165 and 171, 302 and 336.  A column of one sequence has 8 CTAs at most, so narrow
+// rows are bound by its steps: 512 channels 97 to 126 us forward, 211 to 221
+// backward.  The first form, in
 // which every warp composed for itself between two cluster barriers, took 413 us
 // forward (s = 1, one sequence).  Exchange by asynchronous remote stores that an
 // mbarrier counts, instead of the cluster's barrier: 196 against 179 us.
@@ -112,6 +117,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {  // NaN stays NaN
     return y;
 }
 
+// The root and its reciprocal, for float32 channels too: 2^-23 and 2^-22.9 off at most, once per row and channel, against
+// 1e-7 of the series below them.
 __device__ __forceinline__ float rsqrt_ftz(float x) {
     float y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -497,9 +504,10 @@ __device__ __forceinline__ void conduct(const Outbox<V, EARLY> &out, Exchange<V,
 
 // The tiles of one team: a cluster, or one CTA of it (`solo`).  Where the
 // cluster's sequences fall evenly into a part for each CTA, each goes through its
-// own and there is nothing to exchange.  16 even sequences, 72000 x 2048: s = 1 168
-// us alone and 174 together, backward 224 and 294; s = sqrt(1 - a^2) 175 and 236, 339
-// and 374: a part a fifth over its share is about where they meet.
+// own and there is nothing to exchange.  16 even sequences, 72000 x 2048, when this
+// was added: s = 1 168 us alone and 174 together, backward 224 and 294; s = sqrt(1 -
+// a^2) 175 and 236, 339 and 374: a part a fifth over its share is about where they
+// meet.
 template <int ROWS> struct Span {
     static constexpr int kTile = kWorkers * ROWS;
     int t0, t1, tile0, tiles, steps;
@@ -1122,7 +1130,11 @@ int clusters_held(int c) {
 // The two factors below are fitted to times of forwards and backwards at 2048
 // channels: 72001 tokens in 16 sequences cut at random, s = sqrt(1 - a^2), 249, 224,
 // 197, 240, 238 us with clusters of 8, 4, 3, 2, 1 in 1, 2, 3, 4, 8 ranges; in 5
-// (32768 tokens) 114, 107, 107, 143 with 8, 4, 3, 2.
+// (32768 tokens) 114, 107, 107, 143 with 8, 4, 3, 2.  (Clusters of 1 are rated far
+// below what they took there.)  The host knows how many sequences there are and not
+// how long: a batch in which one has 90 % of 72000 tokens beside 15 short ones gets
+// the clusters of 3 that suit even ones, 231 to 306 us forward and 481 to 531
+// backward, where that sequence alone would get clusters of 8.
 void choose_clusters(int columns, int64_t tiles, int num_seqs, int &csize, int &ranges) {
     double best = 0;
     for (int c = kMaxCluster; c >= 1; --c) {
