@@ -361,8 +361,9 @@ sse_status_t sse_front_end(const sse_config_t *cfg, int32_t hidden, int64_t tota
  * SSE_INPUT_COMPLEMENT s = 1 - a; SSE_INPUT_UNIT s = sqrt(1 - a^2) (keeps the
  * variance of the state).  log_gate <= 0 (decays in [0, 1]; the log_gate and v
  * of sse_front_end fit as they are); a log-gate of -infinity empties a finite
- * state (0 times an infinity or a NaN is a NaN).  Positive log-gates are outside the method and not checked.  A NaN or
- * an infinity stays in its own sequence and channel, from its token on.
+ * state (0 times an infinity or a NaN is a NaN).  Positive log-gates are
+ * outside the method and not checked.  A NaN or an infinity stays in its own
+ * sequence and channel, from its token on.
  *
  *   x, log_gate, d_out   [total_tokens, width] in cfg->dtype.  x and log_gate
  *                        take a row stride in elements (>= width, whole
