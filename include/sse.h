@@ -506,6 +506,201 @@ sse_status_t sse_block_norm_backward(const sse_norm_config_t *cfg, int64_t total
                                      float *d_w_after, float *d_channel_scale, float *d_w_before, void *workspace,
                                      size_t workspace_bytes, sse_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * sse_conv_forward / sse_conv_backward / sse_conv_step -- the short causal
+ * convolution in front of a recurrent mixer, one filter of `taps` weights per
+ * channel, over the same packed varlen batches.  Per sequence and channel:
+ *   u_t = bias + sum_j weight[j] x_{t - (taps - 1) + j},   out_t = act(u_t)
+ * Rows before a sequence's first are those of its initial state.
+ *
+ *   x, d_out             [total_tokens, width] in cfg->dtype; x takes a row
+ *                        stride in elements (>= width, whole 16-byte words);
+ *                        d_out and every output are packed.
+ *   weight               float32 [width, taps]; weight[taps - 1] meets x_t
+ *   bias                 float32 [width], may be NULL (zero)
+ *   initial_state        [num_seqs, taps - 1, width] in cfg->dtype, the newest
+ *                        row last, may be NULL (zero)
+ *   final_state          likewise: the last taps - 1 inputs of each sequence,
+ *                        those of the initial state among them where it is
+ *                        shorter (bit for bit); may be NULL.
+ * Backward, for L = <d_out, out> + <d_final_state, final_state>: dx, d_weight,
+ * d_bias (NULL: not written) and d_initial_state (NULL: not written), with u
+ * formed anew from x.  d_final_state may be NULL (zero).  The weights'
+ * gradients are summed over the tokens in float32 in a fixed order
+ * (deterministic) and are zero when there are none.
+ * Workspace (backward only): sse_conv_backward_workspace_size bytes, 256-byte
+ * aligned, contents undefined on entry and exit.
+ *
+ * sse_conv_step is one token of each of `batch` sequences: state
+ * [batch, taps - 1, width] loses its oldest row and gains x, out [batch, width].
+ *
+ * Outputs do not overlap inputs (the step's state apart); final_state equal to
+ * initial_state is refused.  Tokens at and past cu_seqlens[num_seqs] (a padded
+ * batch) belong to no sequence: their rows are not read and the outputs' rows
+ * stay as they were.  All sums are float32, rounded once to cfg->dtype.  taps is
+ * 2 to 4, act SSE_GATE_NONE or SSE_GATE_SILU, width at most 65536; width and the
+ * row strides are whole 16-byte words of cfg->dtype; total_tokens and num_seqs
+ * are below 2^30.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t width; /* channels: columns of every row */
+    int32_t taps;  /* weights of one channel */
+    int32_t act;   /* sse_gate_t: SSE_GATE_NONE or SSE_GATE_SILU */
+    int32_t dtype; /* sse_dtype_t of the token tensors and the states */
+} sse_conv_config_t;
+
+sse_status_t sse_conv_forward(const sse_conv_config_t *cfg, const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                              const void *initial_state, void *final_state, void *out, sse_stream_t stream);
+
+size_t sse_conv_backward_workspace_size(const sse_conv_config_t *cfg, int64_t total_tokens);
+
+sse_status_t sse_conv_backward(const sse_conv_config_t *cfg, const void *x, int64_t x_stride, const float *weight,
+                               const float *bias, const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                               const void *initial_state, const void *d_out, const void *d_final_state, void *dx,
+                               float *d_weight, float *d_bias, void *d_initial_state, void *workspace,
+                               size_t workspace_bytes, sse_stream_t stream);
+
+sse_status_t sse_conv_step(const sse_conv_config_t *cfg, const void *x, int64_t x_stride, const float *weight,
+                           const float *bias, int32_t batch, void *state, void *out, sse_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * sse_selective_forward / sse_selective_backward / sse_selective_step -- the
+ * selective state space scan: a gated linear recurrence with `state` float32
+ * states per channel, whose decays and inputs the tokens choose, over the same
+ * packed varlen batches.  Per sequence, channel c (of group g(c)) and state n:
+ *   D_t = softplus(delta_t[c] + delta_bias[c])
+ *   h_t[n] = exp(D_t A[c, n]) h_{t-1}[n] + D_t B_t[g, n] x_t[c]
+ *   y_t = sum_n C_t[g, n] h_t[n] + skip[c] x_t[c]
+ *   out_t[c] = y_t silu(gate_t[c])
+ * A <= 0 (decays in [0, 1]; positive A is outside the method and not checked).
+ * Each of the groups' B and C serves width / groups channels in a row.
+ *
+ *   x, delta, gate       [total_tokens, width] in cfg->dtype, each with its own
+ *                        row stride in elements (>= width, whole 16-byte
+ *                        words).  gate may be NULL (none: out = y).
+ *   B, C                 [total_tokens, groups, state] in cfg->dtype, each with
+ *                        its own row stride (>= groups * state, whole words)
+ *   A                    float32 [width, state]
+ *   delta_bias, skip     float32 [width], may be NULL (zero)
+ *   initial_state        float32 [num_seqs, width, state], may be NULL (zero)
+ *   final_state          likewise, may be NULL (not written).  An empty
+ *                        sequence's final state is its initial state.
+ *   checkpoints          float32 [sse_selective_checkpoint_rows(total_tokens),
+ *                        width, state], may be NULL (not written): the state
+ *                        before every 16th packed token, which the backward
+ *                        reads instead of repeating the forward.  Rows whose
+ *                        token is the first of its sequence, or belongs to
+ *                        none, mean nothing.
+ *   out                  [total_tokens, width], packed
+ * Backward: the gradients of L = <d_out, out> + <d_final_state, final_state>,
+ * with the states formed anew in float32 from the checkpoints.  d_gate is given
+ * exactly with gate, d_skip only with skip; d_skip, d_delta_bias, d_final_state
+ * and d_initial_state may be NULL.  dx, d_delta, d_gate, d_B, d_C are packed, in
+ * cfg->dtype; d_A, d_skip, d_delta_bias float32, summed over the tokens, zero
+ * when there are none.
+ * Workspaces: sse_selective_forward_workspace_size and
+ * sse_selective_backward_workspace_size bytes, 256-byte aligned, contents
+ * undefined on entry and exit; NULL where the size is 0.
+ *
+ * sse_selective_step is one token of each of `batch` sequences: state
+ * float32 [batch, width, state] is replaced, out [batch, width].
+ *
+ * Outputs do not overlap inputs (the step's state apart); final_state equal to
+ * initial_state is refused.  Tokens at and past cu_seqlens[num_seqs] (a padded
+ * batch) belong to no sequence: their rows are not read and the outputs' rows
+ * stay as they were.  Sums and states are float32, rounded once to cfg->dtype,
+ * formed in a fixed order (deterministic).  A NaN stays in its own sequence and
+ * channel, in the gradients of B, C and the weights in its own token or channel.
+ * state is 8, 16, 32 or 64; width at most 65536, width / groups and the row
+ * strides whole 16-byte words of cfg->dtype; total_tokens and num_seqs are below
+ * 2^30.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t width;  /* channels */
+    int32_t state;  /* states of a channel */
+    int32_t groups; /* of channels that share B and C; divides width */
+    int32_t dtype;  /* sse_dtype_t of the token tensors */
+} sse_selective_config_t;
+
+/* Rows of the checkpoints of total_tokens packed tokens (0 for bad sizes). */
+int64_t sse_selective_checkpoint_rows(int64_t total_tokens);
+
+size_t sse_selective_forward_workspace_size(const sse_selective_config_t *cfg, int64_t total_tokens,
+                                            int32_t num_seqs);
+
+sse_status_t sse_selective_forward(const sse_selective_config_t *cfg, const void *x, int64_t x_stride,
+                                   const void *delta, int64_t delta_stride, const float *delta_bias, const float *A,
+                                   const void *B, int64_t b_stride, const void *C, int64_t c_stride,
+                                   const float *skip, const void *gate, int64_t gate_stride,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                   const float *initial_state, float *final_state, void *out, float *checkpoints,
+                                   void *workspace, size_t workspace_bytes, sse_stream_t stream);
+
+size_t sse_selective_backward_workspace_size(const sse_selective_config_t *cfg, int64_t total_tokens,
+                                             int32_t num_seqs);
+
+sse_status_t sse_selective_backward(const sse_selective_config_t *cfg, const void *x, int64_t x_stride,
+                                    const void *delta, int64_t delta_stride, const float *delta_bias, const float *A,
+                                    const void *B, int64_t b_stride, const void *C, int64_t c_stride,
+                                    const float *skip, const void *gate, int64_t gate_stride,
+                                    const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                    const float *initial_state, const float *checkpoints, const void *d_out,
+                                    const float *d_final_state, void *dx, void *d_delta, float *d_delta_bias,
+                                    float *d_A, void *d_B, void *d_C, float *d_skip, void *d_gate,
+                                    float *d_initial_state, void *workspace, size_t workspace_bytes,
+                                    sse_stream_t stream);
+
+sse_status_t sse_selective_step(const sse_selective_config_t *cfg, const void *x, int64_t x_stride,
+                                const void *delta, int64_t delta_stride, const float *delta_bias, const float *A,
+                                const void *B, int64_t b_stride, const void *C, int64_t c_stride, const float *skip,
+                                const void *gate, int64_t gate_stride, int32_t batch, float *state, void *out,
+                                sse_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * sse_layer_norm / sse_layer_norm_backward -- the norm before a block with its
+ * mean taken out (sse_block_norm's norms keep it), and the residual stream, in
+ * one pass over each token:
+ *   r' = x + residual
+ *   out = (r' - mean r') / sqrt(mean (r' - mean r')^2 + eps) * weight + bias
+ *   x, residual          [total_tokens, width] in cfg->dtype, each with its own
+ *                        row stride in elements (>= width, whole 16-byte
+ *                        words); residual may be NULL (none)
+ *   weight, bias         float32 [width], each may be NULL (one, zero)
+ *   residual_out         r', packed, may be NULL; may be x or residual itself
+ *                        when that is packed (an in-place residual stream)
+ *   out                  packed.  It is formed from r' before r' is rounded.
+ * Backward: gradients of L = <d_out, out> + <d_residual_out, r'>, taken at the
+ * r' that the forward stored (x itself where there was no residual): dx, which
+ * is also the residual's gradient.  d_residual_out may be NULL (zero).
+ * d_weight and d_bias are float32 [width], may be NULL, and are summed over the
+ * tokens in a fixed order (deterministic), zero when there are none.
+ * Workspace (backward only): sse_layer_norm_backward_workspace_size bytes,
+ * 256-byte aligned, contents undefined on entry and exit.
+ *
+ * Sums are float32 (the mean first, then the squares about it): values whose
+ * squares leave its range are outside.  Apart from residual_out, outputs do not
+ * overlap inputs.  width is at most 16384 for SSE_BF16 and 8192 for SSE_F32;
+ * width and the row strides are whole 16-byte words of cfg->dtype; eps is a
+ * positive normal number; total_tokens is below 2^31.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    int32_t width; /* columns of every row */
+    float eps;     /* added to the variance */
+    int32_t dtype; /* sse_dtype_t of the token tensors */
+} sse_layer_norm_config_t;
+
+sse_status_t sse_layer_norm(const sse_layer_norm_config_t *cfg, int64_t total_tokens, const void *x, int64_t x_stride,
+                            const void *residual, int64_t residual_stride, const float *weight, const float *bias,
+                            void *residual_out, void *out, sse_stream_t stream);
+
+size_t sse_layer_norm_backward_workspace_size(const sse_layer_norm_config_t *cfg, int64_t total_tokens);
+
+sse_status_t sse_layer_norm_backward(const sse_layer_norm_config_t *cfg, int64_t total_tokens, const void *x,
+                                     int64_t x_stride, const float *weight, const void *d_out,
+                                     const void *d_residual_out, void *dx, float *d_weight, float *d_bias,
+                                     void *workspace, size_t workspace_bytes, sse_stream_t stream);
+
 /* Device-side status bits (bit mask), written by the kernels into the first
  * word of the workspace of sse_forward, sse_backward, sse_delta_forward and
  * sse_front_end (each call clears them first).

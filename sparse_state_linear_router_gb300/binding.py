@@ -5,8 +5,8 @@ The functions named like the C entry points (``sse_route``, ``sse_forward``,
 stream handle) and only marshal arguments.  The ``route`` / ``forward`` /
 ``decode_step`` helpers take torch tensors, allocate outputs and the
 workspace with torch (device memory plumbing only) and call the C entry
-points on the current torch stream.  The ``scan_*`` and ``block_norm*`` helpers
-also check the tensors' shapes, types, strides and device (SSEError with
+points on the current torch stream.  The ``scan_*``, ``block_norm*``, ``conv_*``,
+``selective_*`` and ``layer_norm*`` helpers also check the tensors' shapes, types, strides and device (SSEError with
 SSE_ERR_INVALID_ARG) and run on the tensors' device, whichever is current.  Every step of the layer runs in the
 library's CUDA kernels; there is no CPU or PyTorch fallback: if libsse.so is
 missing, loading raises.
@@ -36,13 +36,18 @@ EXPORTED = ("sse_abi_version", "sse_status_string", "sse_route_workspace_size", 
             "sse_get_last_device_error", "sse_backward_workspace_size", "sse_backward",
             "sse_delta_forward_workspace_size", "sse_delta_forward", "sse_delta_decode_step",
             "sse_scan_checkpoint_rows", "sse_scan_forward", "sse_scan_backward", "sse_scan_step",
-            "sse_block_norm", "sse_block_norm_backward_workspace_size", "sse_block_norm_backward")
+            "sse_block_norm", "sse_block_norm_backward_workspace_size", "sse_block_norm_backward",
+            "sse_conv_forward", "sse_conv_backward_workspace_size", "sse_conv_backward", "sse_conv_step",
+            "sse_selective_checkpoint_rows", "sse_selective_forward_workspace_size", "sse_selective_forward",
+            "sse_selective_backward_workspace_size", "sse_selective_backward", "sse_selective_step",
+            "sse_layer_norm", "sse_layer_norm_backward_workspace_size", "sse_layer_norm_backward")
 
 SSE_INPUT_PLAIN, SSE_INPUT_COMPLEMENT, SSE_INPUT_UNIT = 0, 1, 2
 _INPUT_SCALES = {"plain": SSE_INPUT_PLAIN, "complement": SSE_INPUT_COMPLEMENT, "unit": SSE_INPUT_UNIT}
 SSE_GATE_NONE, SSE_GATE_SILU, SSE_GATE_SIGMOID, SSE_GATE_LINEAR = 0, 1, 2, 3
 _GATES = {"none": SSE_GATE_NONE, "silu": SSE_GATE_SILU, "sigmoid": SSE_GATE_SIGMOID, "linear": SSE_GATE_LINEAR}
 SCAN_CHECKPOINT = 64  # packed tokens between two of the scan's stored states
+SELECTIVE_CHECKPOINT = 16  # and of the selective scan's
 
 
 class sse_config_t(ctypes.Structure):
@@ -60,6 +65,19 @@ class sse_norm_config_t(ctypes.Structure):
     _fields_ = [("width", ctypes.c_int32), ("group", ctypes.c_int32), ("gate", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float),
                 ("dtype", ctypes.c_int32)]
+
+
+class sse_conv_config_t(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("taps", ctypes.c_int32), ("act", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class sse_selective_config_t(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("state", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class sse_layer_norm_config_t(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
 class SSEError(RuntimeError):
@@ -136,6 +154,33 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sse_block_norm_backward.restype = ctypes.c_int
     lib.sse_block_norm_backward.argtypes = [normp, i64, P, i64, P, i64, P, i64, P, P, P, P, P, P, P, P, P, P, P, P,
                                             sz, P]
+    convp, selp, lnp = (ctypes.POINTER(c) for c in (sse_conv_config_t, sse_selective_config_t, sse_layer_norm_config_t))
+    lib.sse_conv_forward.restype = ctypes.c_int
+    lib.sse_conv_forward.argtypes = [convp, P, i64, P, P, P, i32, i64, P, P, P, P]
+    lib.sse_conv_backward_workspace_size.restype = sz
+    lib.sse_conv_backward_workspace_size.argtypes = [convp, i64]
+    lib.sse_conv_backward.restype = ctypes.c_int
+    lib.sse_conv_backward.argtypes = [convp, P, i64, P, P, P, i32, i64, P, P, P, P, P, P, P, P, sz, P]
+    lib.sse_conv_step.restype = ctypes.c_int
+    lib.sse_conv_step.argtypes = [convp, P, i64, P, P, i32, P, P, P]
+    inputs = [P, i64, P, i64, P, P, P, i64, P, i64, P, P, i64]  # x, delta, delta_bias, A, B, C, skip, gate
+    lib.sse_selective_checkpoint_rows.restype = i64
+    lib.sse_selective_checkpoint_rows.argtypes = [i64]
+    for size in (lib.sse_selective_forward_workspace_size, lib.sse_selective_backward_workspace_size):
+        size.restype = sz
+        size.argtypes = [selp, i64, i32]
+    lib.sse_selective_forward.restype = ctypes.c_int
+    lib.sse_selective_forward.argtypes = [selp, *inputs, P, i32, i64, P, P, P, P, P, sz, P]
+    lib.sse_selective_backward.restype = ctypes.c_int
+    lib.sse_selective_backward.argtypes = [selp, *inputs, P, i32, i64, P, P, P, P, P, P, P, P, P, P, P, P, P, P, sz, P]
+    lib.sse_selective_step.restype = ctypes.c_int
+    lib.sse_selective_step.argtypes = [selp, *inputs, i32, P, P, P]
+    lib.sse_layer_norm.restype = ctypes.c_int
+    lib.sse_layer_norm.argtypes = [lnp, i64, P, i64, P, i64, P, P, P, P, P]
+    lib.sse_layer_norm_backward_workspace_size.restype = sz
+    lib.sse_layer_norm_backward_workspace_size.argtypes = [lnp, i64]
+    lib.sse_layer_norm_backward.restype = ctypes.c_int
+    lib.sse_layer_norm_backward.argtypes = [lnp, i64, P, i64, P, P, P, P, P, P, P, sz, P]
     _lib = lib
     return lib
 
@@ -268,6 +313,81 @@ def sse_block_norm_backward(cfg, total_tokens, block_out, block_stride, gate, ga
                                           residual_out, residual_stride, w_after, channel_scale, w_before,
                                           d_residual_out, d_next_in, d_block_out, d_gate, d_residual, d_w_after,
                                           d_channel_scale, d_w_before, workspace, workspace_bytes, stream)
+
+
+def sse_conv_forward(cfg, x, x_stride, weight, bias, cu_seqlens, num_seqs, total_tokens, initial_state, final_state,
+                     out, stream) -> int:
+    return load().sse_conv_forward(ctypes.byref(cfg), x, x_stride, weight, bias, cu_seqlens, num_seqs, total_tokens,
+                                   initial_state, final_state, out, stream)
+
+
+def sse_conv_backward_workspace_size(cfg: sse_conv_config_t, total_tokens: int) -> int:
+    return load().sse_conv_backward_workspace_size(ctypes.byref(cfg), total_tokens)
+
+
+def sse_conv_backward(cfg, x, x_stride, weight, bias, cu_seqlens, num_seqs, total_tokens, initial_state, d_out,
+                      d_final_state, dx, d_weight, d_bias, d_initial_state, workspace, workspace_bytes, stream) -> int:
+    return load().sse_conv_backward(ctypes.byref(cfg), x, x_stride, weight, bias, cu_seqlens, num_seqs, total_tokens,
+                                    initial_state, d_out, d_final_state, dx, d_weight, d_bias, d_initial_state,
+                                    workspace, workspace_bytes, stream)
+
+
+def sse_conv_step(cfg, x, x_stride, weight, bias, batch, state, out, stream) -> int:
+    return load().sse_conv_step(ctypes.byref(cfg), x, x_stride, weight, bias, batch, state, out, stream)
+
+
+def sse_selective_checkpoint_rows(total_tokens: int) -> int:
+    return load().sse_selective_checkpoint_rows(total_tokens)
+
+
+def sse_selective_forward_workspace_size(cfg: sse_selective_config_t, total_tokens: int, num_seqs: int) -> int:
+    return load().sse_selective_forward_workspace_size(ctypes.byref(cfg), total_tokens, num_seqs)
+
+
+def sse_selective_forward(cfg, x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride, skip, gate,
+                          gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state, final_state, out,
+                          checkpoints, workspace, workspace_bytes, stream) -> int:
+    return load().sse_selective_forward(ctypes.byref(cfg), x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride,
+                                        C, c_stride, skip, gate, gate_stride, cu_seqlens, num_seqs, total_tokens,
+                                        initial_state, final_state, out, checkpoints, workspace, workspace_bytes,
+                                        stream)
+
+
+def sse_selective_backward_workspace_size(cfg: sse_selective_config_t, total_tokens: int, num_seqs: int) -> int:
+    return load().sse_selective_backward_workspace_size(ctypes.byref(cfg), total_tokens, num_seqs)
+
+
+def sse_selective_backward(cfg, x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride, skip, gate,
+                           gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state, checkpoints, d_out,
+                           d_final_state, dx, d_delta, d_delta_bias, d_A, d_B, d_C, d_skip, d_gate, d_initial_state,
+                           workspace, workspace_bytes, stream) -> int:
+    return load().sse_selective_backward(ctypes.byref(cfg), x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride,
+                                         C, c_stride, skip, gate, gate_stride, cu_seqlens, num_seqs, total_tokens,
+                                         initial_state, checkpoints, d_out, d_final_state, dx, d_delta, d_delta_bias,
+                                         d_A, d_B, d_C, d_skip, d_gate, d_initial_state, workspace, workspace_bytes,
+                                         stream)
+
+
+def sse_selective_step(cfg, x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride, skip, gate,
+                       gate_stride, batch, state, out, stream) -> int:
+    return load().sse_selective_step(ctypes.byref(cfg), x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C,
+                                     c_stride, skip, gate, gate_stride, batch, state, out, stream)
+
+
+def sse_layer_norm(cfg, total_tokens, x, x_stride, residual, residual_stride, weight, bias, residual_out, out,
+                   stream) -> int:
+    return load().sse_layer_norm(ctypes.byref(cfg), total_tokens, x, x_stride, residual, residual_stride, weight, bias,
+                                 residual_out, out, stream)
+
+
+def sse_layer_norm_backward_workspace_size(cfg: sse_layer_norm_config_t, total_tokens: int) -> int:
+    return load().sse_layer_norm_backward_workspace_size(ctypes.byref(cfg), total_tokens)
+
+
+def sse_layer_norm_backward(cfg, total_tokens, x, x_stride, weight, d_out, d_residual_out, dx, d_weight, d_bias,
+                            workspace, workspace_bytes, stream) -> int:
+    return load().sse_layer_norm_backward(ctypes.byref(cfg), total_tokens, x, x_stride, weight, d_out, d_residual_out,
+                                          dx, d_weight, d_bias, workspace, workspace_bytes, stream)
 
 
 # ---------------------------------------------------------------------------
@@ -709,6 +829,247 @@ def block_norm_backward(cfg, d_residual_out, block_out=None, *, gate=None, w_aft
         _refuse(what, f"workspace is not a contiguous uint8 tensor on {dev}")
     _on_device(what, dev, load().sse_block_norm_backward, ctypes.byref(cfg), T, po, so, pz, sz, pr, sr, wa, wc, wb, pd,
                pn, *map(_ptr, g.values()), workspace.data_ptr(), workspace.numel())
+    return g
+
+
+# ---------------------------------------------------------------------------
+# Selective state space block: short convolution, selective scan, layer norm
+# ---------------------------------------------------------------------------
+def _dtype_of(dtype):
+    return {"bf16": SSE_BF16, "f32": SSE_F32}[dtype] if isinstance(dtype, str) else dtype
+
+
+def make_conv_config(width, taps=4, act="silu", dtype="bf16") -> sse_conv_config_t:
+    return sse_conv_config_t(width, taps, _GATES[act] if isinstance(act, str) else int(act), _dtype_of(dtype))
+
+
+def make_selective_config(width, state=16, groups=1, dtype="bf16") -> sse_selective_config_t:
+    return sse_selective_config_t(width, state, groups, _dtype_of(dtype))
+
+
+def make_layer_norm_config(width, eps=1e-5, dtype="bf16") -> sse_layer_norm_config_t:
+    return sse_layer_norm_config_t(width, float(eps), _dtype_of(dtype))
+
+
+def _state(what, name, t, shape, dtype, device):
+    """Pointer of a contiguous state tensor."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        _refuse(what, f"{name} is not a contiguous {dtype} {list(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _room(what, workspace, need, device):
+    """The workspace of a call that needs `need` bytes: the caller's, or one of its own."""
+    if workspace is None:
+        return _torch().empty(need, dtype=_torch().uint8, device=device) if need else None
+    if workspace.dtype is not _torch().uint8 or workspace.device != device or not workspace.is_contiguous():
+        _refuse(what, f"workspace is not a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def _present(what, **tensors):
+    for name, t in tensors.items():
+        if t is None:
+            _refuse(what, f"{name} is None")
+
+
+def conv_forward(cfg, x, weight, cu_seqlens, *, bias=None, initial_state=None, want_final_state=True, out=None,
+                 final_state=None):
+    """The short causal convolution (sse_conv_forward) over packed sequences;
+    x [T, width], weight [width, taps], states [S, taps - 1, width] of x's
+    type.  Returns dict(out, final_state)."""
+    torch, what = _torch(), "sse_conv_forward"
+    T, dev = _first(what, x)
+    S, W, K, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.taps, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    _present(what, weight=weight)
+    pi = _state(what, "initial_state", initial_state, (S, K - 1, W), dt, dev)
+    po, pf = _packed(what, "out", out, T, W, dt, dev), _state(what, "final_state", final_state, (S, K - 1, W), dt, dev)
+    pw, pb = _floats(what, "weight", weight, (W, K), dev), _floats(what, "bias", bias, (W,), dev)
+    if out is None:
+        out = _like(x)
+        po = out.data_ptr()
+    if final_state is None and want_final_state:
+        final_state = torch.empty((S, K - 1, W), dtype=dt, device=dev)
+        pf = final_state.data_ptr()
+    _on_device(what, dev, load().sse_conv_forward, ctypes.byref(cfg), px, sx, pw, pb, cu_seqlens.data_ptr(), S, T, pi, pf,
+               po)
+    return {"out": out, "final_state": final_state}
+
+
+def conv_backward(cfg, x, weight, cu_seqlens, d_out, *, bias=None, initial_state=None, d_final_state=None,
+                  want_d_initial_state=True, workspace=None):
+    """Gradients of <d_out, out> + <d_final_state, final_state> of conv_forward
+    (sse_conv_backward); returns dict(dx, d_weight, d_bias, d_initial_state),
+    d_bias None without a bias."""
+    torch, what = _torch(), "sse_conv_backward"
+    T, dev = _first(what, x)
+    S, W, K, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.taps, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    _present(what, weight=weight, d_out=d_out)
+    pw, pb = _floats(what, "weight", weight, (W, K), dev), _floats(what, "bias", bias, (W,), dev)
+    pd = _packed(what, "d_out", d_out, T, W, dt, dev)
+    pi = _state(what, "initial_state", initial_state, (S, K - 1, W), dt, dev)
+    pf = _state(what, "d_final_state", d_final_state, (S, K - 1, W), dt, dev)
+    workspace = _room(what, workspace, load().sse_conv_backward_workspace_size(ctypes.byref(cfg), T), dev)
+    g = {"dx": _like(x), "d_weight": torch.empty((W, K), dtype=torch.float32, device=dev),
+         "d_bias": None if bias is None else torch.empty((W,), dtype=torch.float32, device=dev),
+         "d_initial_state": torch.empty((S, K - 1, W), dtype=dt, device=dev) if want_d_initial_state else None}
+    _on_device(what, dev, load().sse_conv_backward, ctypes.byref(cfg), px, sx, pw, pb, cu_seqlens.data_ptr(), S, T, pi, pd,
+               pf, *map(_ptr, g.values()), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return g
+
+
+def conv_step(cfg, state, x, weight, *, bias=None, out=None):
+    """One token of each sequence (sse_conv_step): x [B, width]; ``state``
+    [B, taps - 1, width] is updated in place.  Returns dict(out)."""
+    what = "sse_conv_step"
+    B, dev = _first(what, x)
+    W, K, dt = cfg.width, cfg.taps, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, B, W, dt, dev)
+    _present(what, state=state, weight=weight)
+    ps = _state(what, "state", state, (B, K - 1, W), dt, dev)
+    pw, pb = _floats(what, "weight", weight, (W, K), dev), _floats(what, "bias", bias, (W,), dev)
+    if out is None:
+        out = _like(x)
+        po = out.data_ptr()
+    else:
+        po = _packed(what, "out", out, B, W, dt, dev)
+    _on_device(what, dev, load().sse_conv_step, ctypes.byref(cfg), px, sx, pw, pb, B, ps, po)
+    return {"out": out}
+
+
+def _selective_inputs(what, cfg, T, dev, x, delta, A, B, C, delta_bias, skip, gate):
+    """The arguments from x to gate_stride of the three entry points."""
+    W, N, G, dt = cfg.width, cfg.state, cfg.groups, _token_dtype(cfg)
+    _present(what, delta=delta, A=A, B=B, C=C)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    pd, sd = _rows(what, "delta", delta, T, W, dt, dev)
+    pb, sb = _rows(what, "B", B, T, G * N, dt, dev)
+    pc, sc = _rows(what, "C", C, T, G * N, dt, dev)
+    pz, sz = _rows(what, "gate", gate, T, W, dt, dev)
+    return (px, sx, pd, sd, _floats(what, "delta_bias", delta_bias, (W,), dev), _floats(what, "A", A, (W, N), dev), pb, sb,
+            pc, sc, _floats(what, "skip", skip, (W,), dev), pz, sz)
+
+
+def selective_forward(cfg, x, delta, A, B, C, cu_seqlens, *, delta_bias=None, skip=None, gate=None, initial_state=None,
+                      want_final_state=True, want_checkpoints=False, out=None, final_state=None, checkpoints=None,
+                      workspace=None):
+    """The selective state space scan (sse_selective_forward) over packed
+    sequences; x, delta, gate [T, width], A [width, state], B, C
+    [T, groups, state] (or [T, groups * state]), states [S, width, state].
+    Returns dict(out, final_state, checkpoints); checkpoints are what
+    selective_backward reads."""
+    torch, what = _torch(), "sse_selective_forward"
+    T, dev = _first(what, x)
+    S, W, N, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.state, _token_dtype(cfg)
+    args = _selective_inputs(what, cfg, T, dev, x, delta, A, B, C, delta_bias, skip, gate)
+    rows = -(-T // SELECTIVE_CHECKPOINT)
+    pi = _floats(what, "initial_state", initial_state, (S, W, N), dev)
+    po, pf, pc = (_packed(what, "out", out, T, W, dt, dev), _floats(what, "final_state", final_state, (S, W, N), dev),
+                  _floats(what, "checkpoints", checkpoints, (rows, W, N), dev))
+    workspace = _room(what, workspace, load().sse_selective_forward_workspace_size(ctypes.byref(cfg), T, S), dev)
+    if out is None:
+        out = _like(x)
+        po = out.data_ptr()
+    if final_state is None and want_final_state:
+        final_state = torch.empty((S, W, N), dtype=torch.float32, device=dev)
+        pf = final_state.data_ptr()
+    if checkpoints is None and want_checkpoints:
+        checkpoints = torch.empty((rows, W, N), dtype=torch.float32, device=dev)
+        pc = checkpoints.data_ptr()
+    _on_device(what, dev, load().sse_selective_forward, ctypes.byref(cfg), *args, cu_seqlens.data_ptr(), S, T, pi, pf, po,
+               pc, _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return {"out": out, "final_state": final_state, "checkpoints": checkpoints}
+
+
+def selective_backward(cfg, x, delta, A, B, C, cu_seqlens, checkpoints, d_out, *, delta_bias=None, skip=None, gate=None,
+                       initial_state=None, d_final_state=None, want_d_initial_state=True, workspace=None):
+    """Gradients of <d_out, out> + <d_final_state, final_state> of
+    selective_forward (sse_selective_backward); returns dict(dx, d_delta,
+    d_delta_bias, d_A, d_B, d_C, d_skip, d_gate, d_initial_state), None where
+    the part is absent."""
+    torch, what = _torch(), "sse_selective_backward"
+    T, dev = _first(what, x)
+    S, W, N, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.state, _token_dtype(cfg)
+    args = _selective_inputs(what, cfg, T, dev, x, delta, A, B, C, delta_bias, skip, gate)
+    _present(what, d_out=d_out)
+    if checkpoints is None:
+        _refuse(what, "checkpoints is None: selective_forward(..., want_checkpoints=True) returns them")
+    pc = _floats(what, "checkpoints", checkpoints, (-(-T // SELECTIVE_CHECKPOINT), W, N), dev)
+    pi = _floats(what, "initial_state", initial_state, (S, W, N), dev)
+    pd = _packed(what, "d_out", d_out, T, W, dt, dev)
+    pf = _floats(what, "d_final_state", d_final_state, (S, W, N), dev)
+    workspace = _room(what, workspace, load().sse_selective_backward_workspace_size(ctypes.byref(cfg), T, S), dev)
+    floats = lambda *shape: torch.empty(shape, dtype=torch.float32, device=dev)  # noqa: E731
+    g = {"dx": _like(x), "d_delta": _like(delta), "d_delta_bias": None if delta_bias is None else floats(W),
+         "d_A": floats(W, N), "d_B": _like(B), "d_C": _like(C), "d_skip": None if skip is None else floats(W),
+         "d_gate": None if gate is None else _like(gate),
+         "d_initial_state": floats(S, W, N) if want_d_initial_state else None}
+    _on_device(what, dev, load().sse_selective_backward, ctypes.byref(cfg), *args, cu_seqlens.data_ptr(), S, T, pi, pc, pd,
+               pf, *map(_ptr, g.values()), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return g
+
+
+def selective_step(cfg, state, x, delta, A, B, C, *, delta_bias=None, skip=None, gate=None, out=None):
+    """One token of each sequence (sse_selective_step): x, delta, gate
+    [batch, width], B, C [batch, groups, state]; ``state`` [batch, width,
+    state] float32 is updated in place.  Returns dict(out)."""
+    what = "sse_selective_step"
+    rows, dev = _first(what, x)
+    args = _selective_inputs(what, cfg, rows, dev, x, delta, A, B, C, delta_bias, skip, gate)
+    _present(what, state=state)
+    ps = _floats(what, "state", state, (rows, cfg.width, cfg.state), dev)
+    if out is None:
+        out = _like(x)
+        po = out.data_ptr()
+    else:
+        po = _packed(what, "out", out, rows, cfg.width, _token_dtype(cfg), dev)
+    _on_device(what, dev, load().sse_selective_step, ctypes.byref(cfg), *args, rows, ps, po)
+    return {"out": out}
+
+
+def layer_norm(cfg, x, weight=None, bias=None, *, residual=None, residual_out=None, out=None, want_residual_out=True):
+    """The layer norm with the residual stream (sse_layer_norm); x, residual
+    [T, width].  Returns dict(out, residual_out); residual_out is None without
+    a residual (it would be x)."""
+    what = "sse_layer_norm"
+    T, dev = _first(what, x)
+    W, dt = cfg.width, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    pr, sr = _rows(what, "residual", residual, T, W, dt, dev)
+    pw, pb = _floats(what, "weight", weight, (W,), dev), _floats(what, "bias", bias, (W,), dev)
+    pt, po = _packed(what, "residual_out", residual_out, T, W, dt, dev), _packed(what, "out", out, T, W, dt, dev)
+    if out is None:
+        out = _like(x)
+        po = out.data_ptr()
+    if residual_out is None and residual is not None and want_residual_out:
+        residual_out = _like(x)
+        pt = residual_out.data_ptr()
+    _on_device(what, dev, load().sse_layer_norm, ctypes.byref(cfg), T, px, sx, pr, sr, pw, pb, pt, po)
+    return {"out": out, "residual_out": residual_out}
+
+
+def layer_norm_backward(cfg, x, weight, d_out, *, d_residual_out=None, want_d_weight=True, want_d_bias=True,
+                        workspace=None):
+    """Gradients of <d_out, out> + <d_residual_out, residual_out> of layer_norm
+    (sse_layer_norm_backward); x is the forward's residual_out.  Returns
+    dict(dx, d_weight, d_bias); dx is the residual's gradient too."""
+    torch, what = _torch(), "sse_layer_norm_backward"
+    T, dev = _first(what, x)
+    W, dt = cfg.width, _token_dtype(cfg)
+    px, sx = _rows(what, "x", x, T, W, dt, dev)
+    _present(what, d_out=d_out)
+    pw = _floats(what, "weight", weight, (W,), dev)
+    pd = _packed(what, "d_out", d_out, T, W, dt, dev)
+    pr = _packed(what, "d_residual_out", d_residual_out, T, W, dt, dev)
+    workspace = _room(what, workspace, load().sse_layer_norm_backward_workspace_size(ctypes.byref(cfg), T), dev)
+    g = {"dx": _like(x), "d_weight": torch.empty((W,), dtype=torch.float32, device=dev) if want_d_weight else None,
+         "d_bias": torch.empty((W,), dtype=torch.float32, device=dev) if want_d_bias else None}
+    _on_device(what, dev, load().sse_layer_norm_backward, ctypes.byref(cfg), T, px, sx, pw, pd, pr, *map(_ptr, g.values()),
+               _ptr(workspace), 0 if workspace is None else workspace.numel())
     return g
 
 

@@ -1,0 +1,434 @@
+// conv.cu -- the short causal convolution, one filter of K taps per channel:
+//   u_t = bias + sum_j w[j] x_{t - (K - 1) + j},  out_t = act(u_t)
+// with the rows before a sequence from its state.  Gradients, with g_t =
+// d_out_t act'(u_t), zero outside the sequence:
+//   dx_p = sum_j w[j] g_{p + K - 1 - j}  (+ d_final of the last K - 1 rows; rows p
+//   before the sequence are the initial state's),  dw[j] = sum_t g_t x_{t-(K-1)+j},
+//   db = sum_t g_t
+//
+// Bound by HBM: 2 K + 6 operations per element against 4 to 8 bytes (backward 6 K
+// + 20 against 6 to 12).  A thread has four columns and a run of tokens, whose last
+// K - 1 rows (and, in the backward, K - 1 gradients g) stay in registers, so a row
+// is read once but for the K - 1 rows in front of a run (backward: and behind it).
+// The packed token axis is one axis: runs are cut without regard to sequences, and
+// a sequence's first row takes the state's rows into the window.
+#include "f32x2.cuh"
+#include "sse_internal.cuh"
+
+namespace sse {
+namespace {
+
+constexpr int kWarps = 4;  // runs of a CTA
+
+// Four columns of one row.
+template <typename T> struct Quad;
+template <> struct Quad<__nv_bfloat16> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(Raw u, F2 (&f)[2]) {
+        f[0] = f2_bits(u.x << 16, u.x & 0xffff0000u);
+        f[1] = f2_bits(u.y << 16, u.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t two(F2 v) {
+        const float2 f = f2_get(v);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static __device__ __forceinline__ Raw pack(const F2 (&f)[2]) { return make_uint2(two(f[0]), two(f[1])); }
+    static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
+};
+template <> struct Quad<float> {
+    using Raw = uint4;
+    static __device__ __forceinline__ void unpack(Raw u, F2 (&f)[2]) {
+        f[0] = f2_bits(u.x, u.y);
+        f[1] = f2_bits(u.z, u.w);
+    }
+    static __device__ __forceinline__ Raw pack(const F2 (&f)[2]) {
+        const float2 a = f2_get(f[0]), b = f2_get(f[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+};
+
+__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+
+// 1 / (1 + exp(-u)).  For bf16 rows from the approximate exponential and reciprocal: the product's rounding is |u| 2^-24 of
+// exp(-u), next to the rows' own steps of 2^-8 nothing.  In float32 exp is expf.  The reciprocal is one unit in the last
+// place off.
+template <typename T> __device__ __forceinline__ F2 sigmoid2(F2 u) {
+    float ex, ey, x, y;
+    if constexpr (sizeof(T) == 4) {
+        const float2 v = f2_get(u);
+        ex = expf(-v.x);
+        ey = expf(-v.y);
+    } else {
+        const float2 t = f2_get(mul2(u, both(-1.44269504f)));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(t.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(t.y));
+    }
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(1.f + ex));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ey));
+    return f2(x, y);
+}
+
+__device__ __forceinline__ int clamp_token(int t, int T) { return t < 0 ? 0 : t > T ? T : t; }
+
+// Largest s in [0, S) with cu[s] <= t (0 if none): the sequence of token t.
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int S, int t) {
+    int lo = 0, hi = S;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(cu + mid) <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// What a thread has of the filter.
+template <int K> struct Filter {
+    F2 w[K][2], b[2];
+    __device__ __forceinline__ Filter(const ConvArgs &a, int col) {
+        float v[4 * K];
+        const float4 *at = reinterpret_cast<const float4 *>(a.weight + (int64_t)col * K);
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+            const float4 f = __ldg(at + i);
+            v[4 * i] = f.x, v[4 * i + 1] = f.y, v[4 * i + 2] = f.z, v[4 * i + 3] = f.w;
+        }
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            w[j][0] = f2(v[j], v[K + j]);
+            w[j][1] = f2(v[2 * K + j], v[3 * K + j]);
+        }
+        float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (a.bias) f = __ldg(reinterpret_cast<const float4 *>(a.bias + col));
+        b[0] = f2(f.x, f.y);
+        b[1] = f2(f.z, f.w);
+    }
+};
+
+// The last K rows, the newest last, as they were stored.
+template <typename T, int K> struct Window {
+    using Raw = typename Quad<T>::Raw;
+    Raw row[K];
+    __device__ __forceinline__ void push(Raw u) {
+#pragma unroll
+        for (int i = 0; i + 1 < K; ++i) row[i] = row[i + 1];
+        row[K - 1] = u;
+    }
+    static __device__ __forceinline__ Raw of(const ConvArgs &a, int t, int col) {
+        return *reinterpret_cast<const Raw *>(static_cast<const T *>(a.x) + (int64_t)t * a.x_stride + col);
+    }
+    // State row i of sequence q.
+    static __device__ __forceinline__ int64_t state_at(int q, int i, int width, int col) {
+        return ((int64_t)q * (K - 1) + i) * width + col;
+    }
+    // The rows before token t of sequence q, which begins at `start`: rows 1 to K - 1.
+    __device__ __forceinline__ void before(const ConvArgs &a, int t, int q, int start, int width, int col) {
+#pragma unroll
+        for (int i = 0; i < K - 1; ++i) {
+            const int r = t - (K - 1) + i;
+            row[i + 1] = r >= start ? of(a, r, col)
+                         : a.init   ? *reinterpret_cast<const Raw *>(static_cast<const T *>(a.init) +
+                                                                   state_at(q, r - start + K - 1, width, col))
+                                    : Quad<T>::zero();
+        }
+    }
+    // u of the newest row.
+    __device__ __forceinline__ void sum(const Filter<K> &f, F2 (&u)[2]) const {
+        u[0] = f.b[0], u[1] = f.b[1];
+#pragma unroll
+        for (int j = 0; j < K; ++j) {
+            F2 x[2];
+            Quad<T>::unpack(row[j], x);
+            u[0] = fma2(f.w[j][0], x[0], u[0]);
+            u[1] = fma2(f.w[j][1], x[1], u[1]);
+        }
+    }
+};
+
+// Runs: gridDim.y CTAs of kWarps warps, `run` tokens each.
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(32 * kWarps) conv_forward_kernel(ConvArgs a, int width, int run) {
+    using Raw = typename Quad<T>::Raw;
+    const int lane = threadIdx.x & 31;
+    const int col = (blockIdx.x * 32 + lane) * 4;
+    if (col >= width) return;
+    const int id = blockIdx.y * kWarps + (threadIdx.x >> 5), runs = gridDim.y * kWarps;
+    const int end_of_all = clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens);
+    int t = id * run;
+    const int t1 = min(t + run, end_of_all);
+    const Filter<K> f(a, col);
+    if (t < t1) {
+        int q = sequence_of(a.cu_seqlens, a.num_seqs, t);
+        int start = __ldg(a.cu_seqlens + q), end = __ldg(a.cu_seqlens + q + 1);
+        Window<T, K> win;
+        win.before(a, t, q, start, width, col);
+        for (; t < t1; ++t) {
+            if (t == end) {  // the next sequence that has tokens
+                while (end <= t && q + 1 < a.num_seqs) {
+                    ++q;
+                    start = end;
+                    end = __ldg(a.cu_seqlens + q + 1);
+                }
+                win.before(a, t, q, start, width, col);
+            }
+            win.push(Window<T, K>::of(a, t, col));
+            F2 u[2];
+            win.sum(f, u);
+            if constexpr (SILU) {
+                u[0] = mul2(u[0], sigmoid2<T>(u[0]));
+                u[1] = mul2(u[1], sigmoid2<T>(u[1]));
+            }
+            *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + (int64_t)t * width + col) = Quad<T>::pack(u);
+            if (t + 1 == end && a.final_state)
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i)
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.final_state) + Window<T, K>::state_at(q, i, width, col)) =
+                        win.row[i + 1];
+        }
+    }
+    if (a.final_state)  // empty sequences keep their state
+        for (int q = id; q < a.num_seqs; q += runs)
+            if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1))
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i) {
+                    const int64_t at = Window<T, K>::state_at(q, i, width, col);
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.final_state) + at) =
+                        a.init ? *reinterpret_cast<const Raw *>(static_cast<const T *>(a.init) + at) : Quad<T>::zero();
+                }
+}
+
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(32 * kWarps) conv_backward_kernel(ConvArgs a, int width, int run) {
+    using Raw = typename Quad<T>::Raw;
+    __shared__ float4 part[kWarps][K + 1][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = (blockIdx.x * 32 + lane) * 4;
+    const bool live = col < width;
+    const int id = blockIdx.y * kWarps + warp, runs = gridDim.y * kWarps;
+    const int end_of_all = clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens);
+    const int t0 = id * run, t1 = min(t0 + run, end_of_all);
+    F2 dw[K][2], db[2];
+#pragma unroll
+    for (int j = 0; j < K; ++j) dw[j][0] = dw[j][1] = both(0.f);
+    db[0] = db[1] = both(0.f);
+    if (live && t0 < t1) {
+        const Filter<K> f(a, col);
+        int q = sequence_of(a.cu_seqlens, a.num_seqs, t0);
+        // The run's part of one sequence after the other: rows [s0, s1) of the gradient, and the rows of the initial
+        // state where the sequence begins in the run.  Row p is complete with g_{p + K - 1}.
+        for (int s0 = t0; s0 < t1 && q < a.num_seqs; ++q) {
+            const int start = __ldg(a.cu_seqlens + q), end = __ldg(a.cu_seqlens + q + 1);
+            if (end <= s0) continue;
+            const int s1 = min(end, t1);
+            Window<T, K> win;
+            win.before(a, s0, q, start, width, col);
+            F2 g[K][2];
+#pragma unroll
+            for (int j = 0; j < K; ++j) g[j][0] = g[j][1] = both(0.f);
+            for (int t = s0; t < s1 + K - 1; ++t) {
+#pragma unroll
+                for (int j = 0; j + 1 < K; ++j) g[j][0] = g[j + 1][0], g[j][1] = g[j + 1][1];
+                g[K - 1][0] = g[K - 1][1] = both(0.f);
+                if (t < end) {
+                    win.push(Window<T, K>::of(a, t, col));
+                    Quad<T>::unpack(*reinterpret_cast<const Raw *>(static_cast<const T *>(a.d_out) + (int64_t)t * width + col),
+                                    g[K - 1]);
+                    if constexpr (SILU) {
+                        F2 u[2];
+                        win.sum(f, u);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {  // silu' = s (1 + u (1 - s))
+                            const F2 s = sigmoid2<T>(u[i]);
+                            g[K - 1][i] = mul2(g[K - 1][i], mul2(s, fma2(u[i], fma2(s, both(-1.f), both(1.f)), both(1.f))));
+                        }
+                    }
+                    if (t < s1) {
+#pragma unroll
+                        for (int j = 0; j < K; ++j) {
+                            F2 x[2];
+                            Quad<T>::unpack(win.row[j], x);
+                            dw[j][0] = fma2(g[K - 1][0], x[0], dw[j][0]);
+                            dw[j][1] = fma2(g[K - 1][1], x[1], dw[j][1]);
+                        }
+                        db[0] = add2(db[0], g[K - 1][0]);
+                        db[1] = add2(db[1], g[K - 1][1]);
+                    }
+                }
+                const int p = t - (K - 1);
+                if (p < s0 && (s0 != start || !a.d_init)) continue;  // another run's row, or nobody's
+                F2 d[2] = {both(0.f), both(0.f)};
+#pragma unroll
+                for (int j = 0; j < K; ++j) {
+                    d[0] = fma2(f.w[j][0], g[K - 1 - j][0], d[0]);
+                    d[1] = fma2(f.w[j][1], g[K - 1 - j][1], d[1]);
+                }
+                if (a.d_final && p >= end - (K - 1)) {
+                    F2 e[2];
+                    Quad<T>::unpack(*reinterpret_cast<const Raw *>(static_cast<const T *>(a.d_final) +
+                                                                 Window<T, K>::state_at(q, p - end + K - 1, width, col)),
+                                    e);
+                    d[0] = add2(d[0], e[0]);
+                    d[1] = add2(d[1], e[1]);
+                }
+                T *to = p >= start ? static_cast<T *>(a.dx) + (int64_t)p * width + col
+                                   : static_cast<T *>(a.d_init) + Window<T, K>::state_at(q, p - start + K - 1, width, col);
+                *reinterpret_cast<Raw *>(to) = Quad<T>::pack(d);
+            }
+            s0 = s1;
+        }
+    }
+    if (live && a.d_init)  // empty sequences hand the final state's gradient through
+        for (int q = id; q < a.num_seqs; q += runs)
+            if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1))
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i) {
+                    const int64_t at = Window<T, K>::state_at(q, i, width, col);
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.d_init) + at) =
+                        a.d_final ? *reinterpret_cast<const Raw *>(static_cast<const T *>(a.d_final) + at) : Quad<T>::zero();
+                }
+    griddep_launch_dependents();
+#pragma unroll
+    for (int j = 0; j <= K; ++j) {
+        const float2 lo = f2_get(j < K ? dw[j < K ? j : 0][0] : db[0]), hi = f2_get(j < K ? dw[j < K ? j : 0][1] : db[1]);
+        part[warp][j][lane] = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    __syncthreads();
+    if (!live) return;
+    for (int j = warp; j <= K; j += kWarps) {
+        float4 s = part[0][j][lane];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) {
+            const float4 v = part[w][j][lane];
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        *reinterpret_cast<float4 *>(a.partials + ((int64_t)blockIdx.y * (K + 1) + j) * width + col) = s;
+    }
+}
+
+// The weights' gradients from the CTAs' partial rows, in a fixed order: 32 columns of one tap (blockIdx.y; the bias
+// last) per CTA, 32 interleaved runs of rows, then their sum.  Launched as a dependent of the gradient kernel.
+__global__ void __launch_bounds__(1024) conv_weights_kernel(ConvArgs a, int width, int taps, int rows) {
+    __shared__ float sums[32][33];
+    const int c = threadIdx.x, col = blockIdx.x * 32 + c, j = blockIdx.y;
+    griddep_wait();
+    if (j == taps && !a.d_bias) return;
+    const float *from = a.partials + (int64_t)j * width + col;
+    float s = 0.f;
+    if (col < width) {
+#pragma unroll 8
+        for (int r = threadIdx.y; r < rows; r += 32) s += from[(int64_t)r * (taps + 1) * width];
+    }
+    sums[threadIdx.y][c] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && col < width) {
+        float t = 0.f;
+#pragma unroll
+        for (int r = 0; r < 32; ++r) t += sums[r][c];
+        if (j == taps)
+            a.d_bias[col] = t;
+        else
+            a.d_weight[(int64_t)col * taps + j] = t;
+    }
+}
+
+// One token of each sequence.
+template <typename T, int K, bool SILU>
+__global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs a, int width) {
+    using Raw = typename Quad<T>::Raw;
+    const int quads = width / 4;
+    const int64_t i = (int64_t)blockIdx.x * 128 + threadIdx.x;
+    const int64_t b = i / quads;
+    if (b >= a.num_seqs) return;
+    const int col = (int)(i - b * quads) * 4;
+    const Filter<K> f(a, col);
+    Window<T, K> win;
+    T *state = static_cast<T *>(a.final_state);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k)
+        win.row[k] = *reinterpret_cast<const Raw *>(state + Window<T, K>::state_at((int)b, k, width, col));
+    win.row[K - 1] = Window<T, K>::of(a, (int)b, col);
+    F2 u[2];
+    win.sum(f, u);
+    if constexpr (SILU) {
+        u[0] = mul2(u[0], sigmoid2<T>(u[0]));
+        u[1] = mul2(u[1], sigmoid2<T>(u[1]));
+    }
+    *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + b * width + col) = Quad<T>::pack(u);
+#pragma unroll
+    for (int k = 0; k < K - 1; ++k)
+        *reinterpret_cast<Raw *>(state + Window<T, K>::state_at((int)b, k, width, col)) = win.row[k + 1];
+}
+
+enum What { kForward, kBackward, kStep };
+
+constexpr int kSms = 152;
+
+// Tokens of a warp's run, and CTAs along the tokens.
+void cut(int width, int64_t T, bool backward, int &run, int &ctas) {
+    const int64_t columns = (width + 127) / 128, warps = (int64_t)kSms * 16;
+    int64_t r = (T * columns + warps - 1) / warps;
+    const int least = 8, most = backward ? 64 : 32;
+    run = (int)(r < least ? least : r > most ? most : r);
+    const int64_t n = (T + (int64_t)run * kWarps - 1) / ((int64_t)run * kWarps);
+    ctas = n < 1 ? 1 : (int)n;
+    while (ctas > 65535) {  // the grid's limit
+        run *= 2;
+        ctas = (int)((T + (int64_t)run * kWarps - 1) / ((int64_t)run * kWarps));
+    }
+}
+
+template <typename T, int K, bool SILU>
+cudaError_t launch_t(What what, const sse_conv_config_t &c, const ConvArgs &a, cudaStream_t s) {
+    if (what == kStep) {
+        const int64_t blocks = ((int64_t)a.num_seqs * (c.width / 4) + 127) / 128;
+        if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
+        conv_step_kernel<T, K, SILU><<<(unsigned)blocks, 128, 0, s>>>(a, c.width);
+        return cudaGetLastError();
+    }
+    int run, ctas;
+    cut(c.width, a.total_tokens, what == kBackward, run, ctas);
+    const dim3 grid((c.width + 127) / 128, ctas);
+    if (what == kForward) {
+        conv_forward_kernel<T, K, SILU><<<grid, 32 * kWarps, 0, s>>>(a, c.width, run);
+        return cudaGetLastError();
+    }
+    conv_backward_kernel<T, K, SILU><<<grid, 32 * kWarps, 0, s>>>(a, c.width, run);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(conv_weights_kernel, dim3((c.width + 31) / 32, K + 1), dim3(32, 32), 0, s, a, c.width, K, ctas);
+}
+
+template <typename T> cudaError_t launch_taps(What what, const sse_conv_config_t &c, const ConvArgs &a, cudaStream_t s) {
+    const bool silu = c.act == SSE_GATE_SILU;
+    switch (c.taps) {
+    case 2: return silu ? launch_t<T, 2, true>(what, c, a, s) : launch_t<T, 2, false>(what, c, a, s);
+    case 3: return silu ? launch_t<T, 3, true>(what, c, a, s) : launch_t<T, 3, false>(what, c, a, s);
+    default: return silu ? launch_t<T, 4, true>(what, c, a, s) : launch_t<T, 4, false>(what, c, a, s);
+    }
+}
+
+cudaError_t launch(What what, const sse_conv_config_t &c, const ConvArgs &a, cudaStream_t s) {
+    return c.dtype == SSE_BF16 ? launch_taps<__nv_bfloat16>(what, c, a, s) : launch_taps<float>(what, c, a, s);
+}
+
+}  // namespace
+
+int64_t conv_partial_rows(const sse_conv_config_t &cfg, int64_t T) {
+    int run, ctas;
+    cut(cfg.width, T, true, run, ctas);
+    return ctas;
+}
+cudaError_t launch_conv_forward(const sse_conv_config_t &cfg, const ConvArgs &a, cudaStream_t stream) {
+    return launch(kForward, cfg, a, stream);
+}
+cudaError_t launch_conv_backward(const sse_conv_config_t &cfg, const ConvArgs &a, cudaStream_t stream) {
+    return launch(kBackward, cfg, a, stream);
+}
+cudaError_t launch_conv_step(const sse_conv_config_t &cfg, const ConvArgs &a, cudaStream_t stream) {
+    return launch(kStep, cfg, a, stream);
+}
+
+}  // namespace sse

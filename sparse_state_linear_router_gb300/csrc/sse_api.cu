@@ -834,6 +834,326 @@ sse_status_t sse_block_norm_backward(const sse_norm_config_t *cfg, int64_t total
                : SSE_ERR_CUDA;
 }
 
+namespace {
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+
+bool workspace_ok(const void *workspace, size_t bytes, size_t need) {
+    return need == 0 || (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u) == 0 && bytes >= need);
+}
+
+bool all_aligned16(std::initializer_list<const void *> pointers) {
+    for (const void *p : pointers)
+        if (!aligned16(p)) return false;
+    return true;
+}
+
+sse_status_t status_of(cudaError_t e) { return e == cudaSuccess ? SSE_OK : SSE_ERR_CUDA; }
+
+sse_status_t check_conv(const sse_conv_config_t *cfg, int64_t total_tokens, int32_t num_seqs) {
+    if (!cfg) return SSE_ERR_INVALID_ARG;
+    const sse_conv_config_t &c = *cfg;
+    if (c.width < 1 || c.taps < 1 || (c.dtype != SSE_F32 && c.dtype != SSE_BF16)) return SSE_ERR_INVALID_ARG;
+    if (c.act < SSE_GATE_NONE || c.act > SSE_GATE_LINEAR) return SSE_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_tokens < 0 || (num_seqs == 0 && total_tokens != 0)) return SSE_ERR_INVALID_ARG;
+    if (c.act > SSE_GATE_SILU || c.taps < 2 || c.taps > 4) return SSE_ERR_UNSUPPORTED;
+    if (c.width > sse::kScanMaxWidth || c.width % (c.dtype == SSE_BF16 ? 8 : 4)) return SSE_ERR_UNSUPPORTED;
+    if (total_tokens >= (int64_t(1) << 30) || num_seqs >= (1 << 30)) return SSE_ERR_UNSUPPORTED;
+    return SSE_OK;
+}
+
+sse::ConvArgs conv_args(const void *x, int64_t x_stride, const float *weight, const float *bias,
+                        const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens, const void *init) {
+    sse::ConvArgs a{};
+    a.x = x;
+    a.x_stride = x_stride;
+    a.weight = weight;
+    a.bias = bias;
+    a.cu_seqlens = cu_seqlens;
+    a.num_seqs = num_seqs;
+    a.total_tokens = (int32_t)total_tokens;
+    a.init = init;
+    return a;
+}
+}  // namespace
+
+sse_status_t sse_conv_forward(const sse_conv_config_t *cfg, const void *x, int64_t x_stride, const float *weight,
+                              const float *bias, const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                              const void *initial_state, void *final_state, void *out, sse_stream_t stream) {
+    SSE_RANGE("sse_conv_forward");
+    const sse_status_t st = check_conv(cfg, total_tokens, num_seqs);
+    if (st != SSE_OK) return st;
+    if (!cu_seqlens || (total_tokens > 0 && (!x || !weight || !out))) return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, cfg->width, cfg->dtype == SSE_BF16 ? 2 : 4)) return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, initial_state, final_state, out})) return SSE_ERR_INVALID_ARG;
+    if (final_state && final_state == initial_state) return SSE_ERR_INVALID_ARG;
+    if (num_seqs == 0) return SSE_OK;
+    sse::ConvArgs a = conv_args(x, x_stride, weight, bias, cu_seqlens, num_seqs, total_tokens, initial_state);
+    a.final_state = final_state;
+    a.out = out;
+    return status_of(sse::launch_conv_forward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t sse_conv_backward_workspace_size(const sse_conv_config_t *cfg, int64_t total_tokens) {
+    if (check_conv(cfg, total_tokens, 1) != SSE_OK) return 0;
+    return round256(sizeof(float) * (size_t)sse::conv_partial_rows(*cfg, total_tokens) * (cfg->taps + 1) * cfg->width);
+}
+
+sse_status_t sse_conv_backward(const sse_conv_config_t *cfg, const void *x, int64_t x_stride, const float *weight,
+                               const float *bias, const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                               const void *initial_state, const void *d_out, const void *d_final_state, void *dx,
+                               float *d_weight, float *d_bias, void *d_initial_state, void *workspace,
+                               size_t workspace_bytes, sse_stream_t stream) {
+    SSE_RANGE("sse_conv_backward");
+    const sse_status_t st = check_conv(cfg, total_tokens, num_seqs);
+    if (st != SSE_OK) return st;
+    if (!cu_seqlens || !d_weight || (total_tokens > 0 && (!x || !weight || !d_out || !dx))) return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, cfg->width, cfg->dtype == SSE_BF16 ? 2 : 4)) return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, initial_state, d_out, d_final_state, dx, d_weight, d_bias, d_initial_state}))
+        return SSE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, sse_conv_backward_workspace_size(cfg, total_tokens)))
+        return SSE_ERR_WORKSPACE;
+    sse::ConvArgs a = conv_args(x, x_stride, weight, bias, cu_seqlens, num_seqs, total_tokens, initial_state);
+    a.d_out = d_out;
+    a.d_final = d_final_state;
+    a.dx = dx;
+    a.d_weight = d_weight;
+    a.d_bias = d_bias;
+    a.d_init = d_initial_state;
+    a.partials = static_cast<float *>(workspace);
+    return status_of(sse::launch_conv_backward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sse_status_t sse_conv_step(const sse_conv_config_t *cfg, const void *x, int64_t x_stride, const float *weight,
+                           const float *bias, int32_t batch, void *state, void *out, sse_stream_t stream) {
+    SSE_RANGE("sse_conv_step");
+    const sse_status_t st = check_conv(cfg, 0, batch);
+    if (st != SSE_OK) return st;
+    if (batch > 0 && (!x || !weight || !state || !out)) return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(x_stride, cfg->width, cfg->dtype == SSE_BF16 ? 2 : 4)) return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, bias, state, out})) return SSE_ERR_INVALID_ARG;
+    if (batch == 0) return SSE_OK;
+    sse::ConvArgs a = conv_args(x, x_stride, weight, bias, nullptr, batch, batch, nullptr);
+    a.final_state = state;
+    a.out = out;
+    return status_of(sse::launch_conv_step(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+sse_status_t check_selective(const sse_selective_config_t *cfg, int64_t total_tokens, int32_t num_seqs) {
+    if (!cfg) return SSE_ERR_INVALID_ARG;
+    const sse_selective_config_t &c = *cfg;
+    if (c.width < 1 || c.state < 1 || c.groups < 1 || (c.dtype != SSE_F32 && c.dtype != SSE_BF16))
+        return SSE_ERR_INVALID_ARG;
+    if (c.width % c.groups) return SSE_ERR_INVALID_ARG;
+    if (num_seqs < 0 || total_tokens < 0 || (num_seqs == 0 && total_tokens != 0)) return SSE_ERR_INVALID_ARG;
+    if (c.state != 8 && c.state != 16 && c.state != 32 && c.state != 64) return SSE_ERR_UNSUPPORTED;
+    if (c.width > sse::kScanMaxWidth || c.width / c.groups % (c.dtype == SSE_BF16 ? 8 : 4)) return SSE_ERR_UNSUPPORTED;
+    if (total_tokens >= (int64_t(1) << 30) || num_seqs >= (1 << 30)) return SSE_ERR_UNSUPPORTED;
+    return SSE_OK;
+}
+
+sse::SelectiveArgs selective_args(const void *x, int64_t x_stride, const void *delta, int64_t delta_stride,
+                                  const float *delta_bias, const float *A, const void *B, int64_t b_stride,
+                                  const void *C, int64_t c_stride, const float *skip, const void *gate,
+                                  int64_t gate_stride, const int32_t *cu_seqlens, int32_t num_seqs,
+                                  int64_t total_tokens, const float *init) {
+    sse::SelectiveArgs a{};
+    a.x = x; a.x_stride = x_stride;
+    a.delta = delta; a.delta_stride = delta_stride;
+    a.delta_bias = delta_bias;
+    a.A = A;
+    a.B = B; a.b_stride = b_stride;
+    a.C = C; a.c_stride = c_stride;
+    a.skip = skip;
+    a.gate = gate; a.gate_stride = gate_stride;
+    a.cu_seqlens = cu_seqlens;
+    a.num_seqs = num_seqs;
+    a.total_tokens = (int32_t)total_tokens;
+    a.init = init;
+    return a;
+}
+
+// What the three entry points ask of their inputs; `rows` tokens.
+sse_status_t check_selective_inputs(const sse_selective_config_t &c, const sse::SelectiveArgs &a, int64_t rows) {
+    const int esz = c.dtype == SSE_BF16 ? 2 : 4;
+    if (rows > 0 && (!a.x || !a.delta || !a.A || !a.B || !a.C)) return SSE_ERR_INVALID_ARG;
+    if (!stride_ok(a.x_stride, c.width, esz) || !stride_ok(a.delta_stride, c.width, esz) ||
+        !stride_ok(a.b_stride, c.groups * c.state, esz) || !stride_ok(a.c_stride, c.groups * c.state, esz) ||
+        (a.gate && !stride_ok(a.gate_stride, c.width, esz)))
+        return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({a.x, a.delta, a.delta_bias, a.A, a.B, a.C, a.skip, a.gate, a.init})) return SSE_ERR_INVALID_ARG;
+    return SSE_OK;
+}
+}  // namespace
+
+int64_t sse_selective_checkpoint_rows(int64_t total_tokens) {
+    if (total_tokens < 0 || total_tokens >= (int64_t(1) << 30)) return 0;
+    return (total_tokens + sse::kSelectiveCheckpoint - 1) / sse::kSelectiveCheckpoint;
+}
+
+size_t sse_selective_forward_workspace_size(const sse_selective_config_t *cfg, int64_t total_tokens,
+                                            int32_t num_seqs) {
+    if (check_selective(cfg, total_tokens, num_seqs) != SSE_OK) return 0;
+    return round256(sse::selective_forward_workspace(*cfg, total_tokens, num_seqs));
+}
+
+sse_status_t sse_selective_forward(const sse_selective_config_t *cfg, const void *x, int64_t x_stride,
+                                   const void *delta, int64_t delta_stride, const float *delta_bias, const float *A,
+                                   const void *B, int64_t b_stride, const void *C, int64_t c_stride,
+                                   const float *skip, const void *gate, int64_t gate_stride,
+                                   const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                   const float *initial_state, float *final_state, void *out, float *checkpoints,
+                                   void *workspace, size_t workspace_bytes, sse_stream_t stream) {
+    SSE_RANGE("sse_selective_forward");
+    sse_status_t st = check_selective(cfg, total_tokens, num_seqs);
+    if (st != SSE_OK) return st;
+    sse::SelectiveArgs a = selective_args(x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride,
+                                          skip, gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state);
+    if ((st = check_selective_inputs(*cfg, a, total_tokens)) != SSE_OK) return st;
+    if (!cu_seqlens || (total_tokens > 0 && !out)) return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({final_state, out, checkpoints})) return SSE_ERR_INVALID_ARG;
+    if (final_state && final_state == initial_state) return SSE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, sse_selective_forward_workspace_size(cfg, total_tokens, num_seqs)))
+        return SSE_ERR_WORKSPACE;
+    if (num_seqs == 0) return SSE_OK;
+    a.final_state = final_state;
+    a.out = out;
+    a.checkpoints = checkpoints;
+    a.workspace = static_cast<char *>(workspace);
+    return status_of(sse::launch_selective_forward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t sse_selective_backward_workspace_size(const sse_selective_config_t *cfg, int64_t total_tokens,
+                                             int32_t num_seqs) {
+    if (check_selective(cfg, total_tokens, num_seqs) != SSE_OK) return 0;
+    return round256(sse::selective_backward_workspace(*cfg, total_tokens, num_seqs));
+}
+
+sse_status_t sse_selective_backward(const sse_selective_config_t *cfg, const void *x, int64_t x_stride,
+                                    const void *delta, int64_t delta_stride, const float *delta_bias, const float *A,
+                                    const void *B, int64_t b_stride, const void *C, int64_t c_stride,
+                                    const float *skip, const void *gate, int64_t gate_stride,
+                                    const int32_t *cu_seqlens, int32_t num_seqs, int64_t total_tokens,
+                                    const float *initial_state, const float *checkpoints, const void *d_out,
+                                    const float *d_final_state, void *dx, void *d_delta, float *d_delta_bias,
+                                    float *d_A, void *d_B, void *d_C, float *d_skip, void *d_gate,
+                                    float *d_initial_state, void *workspace, size_t workspace_bytes,
+                                    sse_stream_t stream) {
+    SSE_RANGE("sse_selective_backward");
+    sse_status_t st = check_selective(cfg, total_tokens, num_seqs);
+    if (st != SSE_OK) return st;
+    sse::SelectiveArgs a = selective_args(x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride,
+                                          skip, gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state);
+    if ((st = check_selective_inputs(*cfg, a, total_tokens)) != SSE_OK) return st;
+    if (!cu_seqlens || !d_A || (d_skip && !skip)) return SSE_ERR_INVALID_ARG;
+    if (total_tokens > 0 && (!checkpoints || !d_out || !dx || !d_delta || !d_B || !d_C ||
+                             (gate != nullptr) != (d_gate != nullptr)))
+        return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({checkpoints, d_out, d_final_state, dx, d_delta, d_delta_bias, d_A, d_B, d_C, d_skip, d_gate,
+                        d_initial_state}))
+        return SSE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, sse_selective_backward_workspace_size(cfg, total_tokens, num_seqs)))
+        return SSE_ERR_WORKSPACE;
+    a.checkpoints = const_cast<float *>(checkpoints);
+    a.d_out = d_out;
+    a.d_final = d_final_state;
+    a.dx = dx;
+    a.d_delta = d_delta;
+    a.d_delta_bias = d_delta_bias;
+    a.d_A = d_A;
+    a.d_B = d_B;
+    a.d_C = d_C;
+    a.d_skip = d_skip;
+    a.d_gate = d_gate;
+    a.d_init = d_initial_state;
+    a.workspace = static_cast<char *>(workspace);
+    return status_of(sse::launch_selective_backward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+sse_status_t sse_selective_step(const sse_selective_config_t *cfg, const void *x, int64_t x_stride,
+                                const void *delta, int64_t delta_stride, const float *delta_bias, const float *A,
+                                const void *B, int64_t b_stride, const void *C, int64_t c_stride, const float *skip,
+                                const void *gate, int64_t gate_stride, int32_t batch, float *state, void *out,
+                                sse_stream_t stream) {
+    SSE_RANGE("sse_selective_step");
+    sse_status_t st = check_selective(cfg, 0, batch);
+    if (st != SSE_OK) return st;
+    sse::SelectiveArgs a = selective_args(x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride,
+                                          skip, gate, gate_stride, nullptr, batch, batch, nullptr);
+    if ((st = check_selective_inputs(*cfg, a, batch)) != SSE_OK) return st;
+    if (batch > 0 && (!state || !out)) return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({state, out})) return SSE_ERR_INVALID_ARG;
+    if (batch == 0) return SSE_OK;
+    a.final_state = state;
+    a.out = out;
+    return status_of(sse::launch_selective_step(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+sse_status_t check_layer_norm(const sse_layer_norm_config_t *cfg, int64_t total_tokens) {
+    if (!cfg) return SSE_ERR_INVALID_ARG;
+    const sse_layer_norm_config_t &c = *cfg;
+    if (c.width < 1 || (c.dtype != SSE_F32 && c.dtype != SSE_BF16) || total_tokens < 0) return SSE_ERR_INVALID_ARG;
+    if (!(c.eps >= std::numeric_limits<float>::min()) || !std::isfinite(c.eps)) return SSE_ERR_INVALID_ARG;
+    if (c.width % (c.dtype == SSE_BF16 ? 8 : 4) || c.width > sse::block_norm_max_width(c.dtype))
+        return SSE_ERR_UNSUPPORTED;
+    if (total_tokens >= (int64_t(1) << 31)) return SSE_ERR_UNSUPPORTED;
+    return SSE_OK;
+}
+}  // namespace
+
+sse_status_t sse_layer_norm(const sse_layer_norm_config_t *cfg, int64_t total_tokens, const void *x, int64_t x_stride,
+                            const void *residual, int64_t residual_stride, const float *weight, const float *bias,
+                            void *residual_out, void *out, sse_stream_t stream) {
+    SSE_RANGE("sse_layer_norm");
+    const sse_status_t st = check_layer_norm(cfg, total_tokens);
+    if (st != SSE_OK) return st;
+    if (total_tokens == 0) return SSE_OK;
+    const int esz = cfg->dtype == SSE_BF16 ? 2 : 4;
+    if (!x || !out || !stride_ok(x_stride, cfg->width, esz) || (residual && !stride_ok(residual_stride, cfg->width, esz)))
+        return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, residual, weight, bias, residual_out, out})) return SSE_ERR_INVALID_ARG;
+    // in place only element for element
+    if (residual_out && ((residual_out == x && x_stride != cfg->width) ||
+                         (residual_out == residual && residual_stride != cfg->width)))
+        return SSE_ERR_INVALID_ARG;
+    sse::LayerNormArgs a{};
+    a.T = total_tokens;
+    a.x = x; a.x_stride = x_stride;
+    a.r = residual; a.r_stride = residual_stride;
+    a.weight = weight; a.bias = bias;
+    a.r_out = residual_out; a.out = out;
+    return status_of(sse::launch_layer_norm(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t sse_layer_norm_backward_workspace_size(const sse_layer_norm_config_t *cfg, int64_t total_tokens) {
+    if (check_layer_norm(cfg, total_tokens) != SSE_OK) return 0;
+    return round256(sizeof(float) * 2 * (size_t)sse::layer_norm_partial_rows(*cfg, total_tokens) * cfg->width);
+}
+
+sse_status_t sse_layer_norm_backward(const sse_layer_norm_config_t *cfg, int64_t total_tokens, const void *x,
+                                     int64_t x_stride, const float *weight, const void *d_out,
+                                     const void *d_residual_out, void *dx, float *d_weight, float *d_bias,
+                                     void *workspace, size_t workspace_bytes, sse_stream_t stream) {
+    SSE_RANGE("sse_layer_norm_backward");
+    const sse_status_t st = check_layer_norm(cfg, total_tokens);
+    if (st != SSE_OK) return st;
+    if (total_tokens > 0 && (!x || !d_out || !dx || !stride_ok(x_stride, cfg->width, cfg->dtype == SSE_BF16 ? 2 : 4)))
+        return SSE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, weight, d_out, d_residual_out, dx, d_weight, d_bias})) return SSE_ERR_INVALID_ARG;
+    if (!workspace_ok(workspace, workspace_bytes, sse_layer_norm_backward_workspace_size(cfg, total_tokens)))
+        return SSE_ERR_WORKSPACE;
+    sse::LayerNormArgs a{};
+    a.T = total_tokens;
+    a.x = x; a.x_stride = x_stride;
+    a.weight = weight;
+    a.d_out = d_out; a.d_r_out = d_residual_out;
+    a.dx = dx;
+    a.d_weight = d_weight; a.d_bias = d_bias;
+    a.partials = static_cast<float *>(workspace);
+    return status_of(sse::launch_layer_norm_backward(*cfg, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 sse_status_t sse_read_device_status(void *workspace, int32_t *flags, sse_stream_t stream) {
     if (!workspace || !flags || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return SSE_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -443,4 +443,71 @@ int64_t block_norm_partial_rows(const sse_norm_config_t &cfg, int64_t T);
 cudaError_t launch_block_norm(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream);
 cudaError_t launch_block_norm_backward(const sse_norm_config_t &cfg, const BlockNormArgs &a, cudaStream_t stream);
 
+// Short causal convolution (conv.cu); pointers as in sse_conv_forward /
+// sse_conv_backward / sse_conv_step.
+struct ConvArgs {
+    const void *x;
+    int64_t x_stride;  // elements between rows
+    const float *weight, *bias;
+    const int32_t *cu_seqlens;
+    int32_t num_seqs, total_tokens;
+    const void *init;
+    void *final_state, *out;
+    // backward only
+    const void *d_out, *d_final;
+    void *dx, *d_init;
+    float *d_weight, *d_bias;
+    float *partials;  // [conv_partial_rows, taps + 1, width]: sums over each part of the tokens
+};
+int64_t conv_partial_rows(const sse_conv_config_t &cfg, int64_t T);
+cudaError_t launch_conv_forward(const sse_conv_config_t &cfg, const ConvArgs &a, cudaStream_t stream);
+cudaError_t launch_conv_backward(const sse_conv_config_t &cfg, const ConvArgs &a, cudaStream_t stream);
+// One token per sequence: a.num_seqs rows, a.final_state the states, in place.
+cudaError_t launch_conv_step(const sse_conv_config_t &cfg, const ConvArgs &a, cudaStream_t stream);
+
+// Selective state space scan (selective.cu); pointers as in
+// sse_selective_forward / sse_selective_backward / sse_selective_step.
+constexpr int kSelectiveCheckpoint = 16;  // packed tokens between two stored states
+struct SelectiveArgs {
+    const void *x, *delta, *B, *C, *gate;
+    int64_t x_stride, delta_stride, b_stride, c_stride, gate_stride;  // elements between rows
+    const float *delta_bias, *A, *skip;
+    const int32_t *cu_seqlens;
+    int32_t num_seqs, total_tokens;
+    const float *init;
+    float *final_state;
+    void *out;
+    float *checkpoints;  // written by the forward, read by the backward
+    // backward only
+    const void *d_out;
+    const float *d_final;
+    void *dx, *d_delta, *d_B, *d_C, *d_gate;
+    float *d_delta_bias, *d_A, *d_skip, *d_init;
+    char *workspace;
+};
+size_t selective_forward_workspace(const sse_selective_config_t &cfg, int64_t T, int32_t S);
+size_t selective_backward_workspace(const sse_selective_config_t &cfg, int64_t T, int32_t S);
+cudaError_t launch_selective_forward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream);
+cudaError_t launch_selective_backward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream);
+// One token per sequence: a.num_seqs rows, a.final_state the states, in place.
+cudaError_t launch_selective_step(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream);
+
+// Layer norm (layer_norm.cu); pointers as in sse_layer_norm and
+// sse_layer_norm_backward.
+struct LayerNormArgs {
+    int64_t T;
+    const void *x, *r;
+    int64_t x_stride, r_stride;
+    const float *weight, *bias;
+    void *r_out, *out;
+    // backward only
+    const void *d_out, *d_r_out;
+    void *dx;
+    float *d_weight, *d_bias;
+    float *partials;  // [2, partial rows, width]: column sums of each CTA
+};
+int64_t layer_norm_partial_rows(const sse_layer_norm_config_t &cfg, int64_t T);
+cudaError_t launch_layer_norm(const sse_layer_norm_config_t &cfg, const LayerNormArgs &a, cudaStream_t stream);
+cudaError_t launch_layer_norm_backward(const sse_layer_norm_config_t &cfg, const LayerNormArgs &a, cudaStream_t stream);
+
 }  // namespace sse
