@@ -12,78 +12,12 @@
 // is read once but for the K - 1 rows in front of a run (backward: and behind it).
 // The packed token axis is one axis: runs are cut without regard to sequences, and
 // a sequence's first row takes the state's rows into the window.
-#include "f32x2.cuh"
-#include "sse_internal.cuh"
+#include "quad.cuh"
 
 namespace sse {
 namespace {
 
 constexpr int kWarps = 4;  // runs of a CTA
-
-// Four columns of one row.
-template <typename T> struct Quad;
-template <> struct Quad<__nv_bfloat16> {
-    using Raw = uint2;
-    static __device__ __forceinline__ void unpack(Raw u, F2 (&f)[2]) {
-        f[0] = f2_bits(u.x << 16, u.x & 0xffff0000u);
-        f[1] = f2_bits(u.y << 16, u.y & 0xffff0000u);
-    }
-    static __device__ __forceinline__ uint32_t two(F2 v) {
-        const float2 f = f2_get(v);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
-        return *reinterpret_cast<const uint32_t *>(&b);
-    }
-    static __device__ __forceinline__ Raw pack(const F2 (&f)[2]) { return make_uint2(two(f[0]), two(f[1])); }
-    static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
-};
-template <> struct Quad<float> {
-    using Raw = uint4;
-    static __device__ __forceinline__ void unpack(Raw u, F2 (&f)[2]) {
-        f[0] = f2_bits(u.x, u.y);
-        f[1] = f2_bits(u.z, u.w);
-    }
-    static __device__ __forceinline__ Raw pack(const F2 (&f)[2]) {
-        const float2 a = f2_get(f[0]), b = f2_get(f[1]);
-        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
-    }
-    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
-};
-
-__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
-
-// 1 / (1 + exp(-u)).  For bf16 rows from the approximate exponential and reciprocal: the product's rounding is |u| 2^-24 of
-// exp(-u), next to the rows' own steps of 2^-8 nothing.  In float32 exp is expf.  The reciprocal is one unit in the last
-// place off.
-template <typename T> __device__ __forceinline__ F2 sigmoid2(F2 u) {
-    float ex, ey, x, y;
-    if constexpr (sizeof(T) == 4) {
-        const float2 v = f2_get(u);
-        ex = expf(-v.x);
-        ey = expf(-v.y);
-    } else {
-        const float2 t = f2_get(mul2(u, both(-1.44269504f)));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ex) : "f"(t.x));
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(ey) : "f"(t.y));
-    }
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(1.f + ex));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ey));
-    return f2(x, y);
-}
-
-__device__ __forceinline__ int clamp_token(int t, int T) { return t < 0 ? 0 : t > T ? T : t; }
-
-// Largest s in [0, S) with cu[s] <= t (0 if none): the sequence of token t.
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int S, int t) {
-    int lo = 0, hi = S;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(cu + mid) <= t)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
 
 // What a thread has of the filter.
 template <int K> struct Filter {

@@ -1,0 +1,84 @@
+// quad.cuh -- four columns of one row in the two storage types, and the
+// activations of the convolution and the selective scan, on float32 pairs.
+#pragma once
+
+#include "f32x2.cuh"
+#include "sse_internal.cuh"
+
+namespace sse {
+
+template <typename T> struct Quad;
+template <> struct Quad<__nv_bfloat16> {
+    using Raw = uint2;
+    static __device__ __forceinline__ void unpack(Raw u, F2 (&f)[2]) {
+        f[0] = f2_bits(u.x << 16, u.x & 0xffff0000u);
+        f[1] = f2_bits(u.y << 16, u.y & 0xffff0000u);
+    }
+    static __device__ __forceinline__ uint32_t two(F2 v) {
+        const float2 f = f2_get(v);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f.x, f.y);
+        return *reinterpret_cast<const uint32_t *>(&b);
+    }
+    static __device__ __forceinline__ Raw pack(const F2 (&f)[2]) { return make_uint2(two(f[0]), two(f[1])); }
+    static __device__ __forceinline__ Raw zero() { return make_uint2(0, 0); }
+};
+template <> struct Quad<float> {
+    using Raw = uint4;
+    static __device__ __forceinline__ void unpack(Raw u, F2 (&f)[2]) {
+        f[0] = f2_bits(u.x, u.y);
+        f[1] = f2_bits(u.z, u.w);
+    }
+    static __device__ __forceinline__ Raw pack(const F2 (&f)[2]) {
+        const float2 a = f2_get(f[0]), b = f2_get(f[1]);
+        return make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    }
+    static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
+};
+
+__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+__device__ __forceinline__ float ex2_ftz(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp_ftz(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ F2 ex2_ftz(F2 x) {
+    const float2 v = f2_get(x);
+    return f2(ex2_ftz(v.x), ex2_ftz(v.y));
+}
+__device__ __forceinline__ F2 rcp_ftz(F2 x) {
+    const float2 v = f2_get(x);
+    return f2(rcp_ftz(v.x), rcp_ftz(v.y));
+}
+
+// 1 / (1 + exp(-u)).  For bf16 rows from the approximate exponential: the product's rounding is |u| 2^-24 of exp(-u), next to
+// the rows' own steps of 2^-8 nothing.  In float32 exp is expf.  The reciprocal is one unit in the last place off.
+template <typename T> __device__ __forceinline__ F2 sigmoid2(F2 u) {
+    if constexpr (sizeof(T) == 4) {
+        const float2 v = f2_get(u);
+        return rcp_ftz(f2(1.f + expf(-v.x), 1.f + expf(-v.y)));
+    } else {
+        return rcp_ftz(add2(ex2_ftz(mul2(u, both(-1.44269504f))), both(1.f)));
+    }
+}
+
+__device__ __forceinline__ int clamp_token(int t, int T) { return t < 0 ? 0 : t > T ? T : t; }
+
+// Largest s in [0, S) with cu[s] <= t (0 if none): the sequence of token t, and for a token past the last one the last sequence.
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int S, int t) {
+    int lo = 0, hi = S;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(cu + mid) <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace sse

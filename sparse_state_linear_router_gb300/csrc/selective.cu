@@ -7,10 +7,14 @@
 //   dD = x sum_n B g + sum_n A g a h_{t-1},  d_delta = dD softplus'
 //   dB[n] = sum_c g D x,  dC[n] = sum_c dy h  (over the channels of the group)
 //   dA = sum_t D g a h_{t-1},  d_skip = sum_t dy x,  d_delta_bias = sum_t d_delta
-#include "sse_internal.cuh"
+#include "selective.cuh"
 
 namespace sse {
 namespace {
+
+// Lanes of a pair of channels, and at most so many states each.
+constexpr int kL = 4, kNT = 4;
+
 
 template <typename T> __device__ __forceinline__ float load(const void *p, int64_t i) {
     if constexpr (sizeof(T) == 2)
@@ -28,36 +32,11 @@ template <typename T> __device__ __forceinline__ void store(void *p, int64_t i, 
 __device__ __forceinline__ float sigmoid(float u) { return 1.f / (1.f + expf(-u)); }
 __device__ __forceinline__ float softplus(float u) { return fmaxf(u, 0.f) + log1pf(expf(-fabsf(u))); }
 
-__device__ __forceinline__ int clamp_token(int t, int T) { return t < 0 ? 0 : t > T ? T : t; }
-
 template <int L> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
 }
-template <int L> __device__ __forceinline__ float channels_sum(float v) {  // over the channels of a warp
-#pragma unroll
-    for (int o = 16; o >= L; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-// L lanes of a channel, four states each.  A warp has 32 / L channels of one group (`per` channels a group, `warps`
-// warps a group), the lanes behind a group's end nothing.
-struct Place {
-    int c, g;  // channel and group
-    bool live;
-};
-template <int L> __device__ __forceinline__ Place place(int width, int groups, int lane) {
-    const int per = width / groups, warps = (per + 32 / L - 1) / (32 / L);
-    const int w = blockIdx.x;
-    Place p;
-    p.g = w / warps;
-    const int i = (w - p.g * warps) * (32 / L) + lane / L;
-    p.live = i < per;
-    p.c = p.g * per + (p.live ? i : per - 1);
-    return p;
-}
-
 struct Token {  // of a channel
     float x, d, raw, B[4], C[4];
 };
@@ -75,161 +54,309 @@ __device__ __forceinline__ Token token(const SelectiveArgs &a, int64_t t, int c,
     return k;
 }
 
-template <typename T, int L>
-__global__ void __launch_bounds__(32) selective_forward_kernel(SelectiveArgs a, sse_selective_config_t cfg) {
-    const int lane = threadIdx.x, N = 4 * L;
-    const Place p = place<L>(cfg.width, cfg.groups, lane);
-    const int n0 = lane % L * 4, at = p.g * N + n0;
-    const float bias = a.delta_bias ? a.delta_bias[p.c] : 0.f, skip = a.skip ? a.skip[p.c] : 0.f;
-    float A[4], h[4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) A[n] = a.A[(int64_t)p.c * N + n0 + n];
-    for (int q = blockIdx.y; q < a.num_seqs; q += gridDim.y) {
-        const int t0 = clamp_token(a.cu_seqlens[q], a.total_tokens), t1 = clamp_token(a.cu_seqlens[q + 1], a.total_tokens);
-        const int64_t state = ((int64_t)q * cfg.width + p.c) * N + n0;
-#pragma unroll
-        for (int n = 0; n < 4; ++n) h[n] = a.init ? a.init[state + n] : 0.f;
-        for (int t = t0; t < t1; ++t) {
-            if (a.checkpoints && t % kSelectiveCheckpoint == 0 && p.live)
-                for (int n = 0; n < 4; ++n)
-                    a.checkpoints[((int64_t)(t / kSelectiveCheckpoint) * cfg.width + p.c) * N + n0 + n] = h[n];
-            const Token k = token<T>(a, t, p.c, at, bias);
-            float y = 0.f;
-#pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                h[n] = fmaf(expf(k.d * A[n]), h[n], k.d * k.x * k.B[n]);
-                y = fmaf(k.C[n], h[n], y);
-            }
-            y = fmaf(skip, k.x, lanes_sum<L>(y));
-            if (a.gate) {
-                const float z = load<T>(a.gate, (int64_t)t * a.gate_stride + p.c);
-                y *= z * sigmoid(z);
-            }
-            if (p.live && n0 == 0) store<T>(a.out, (int64_t)t * cfg.width + p.c, y);
-        }
-        if (a.final_state && p.live)
-#pragma unroll
-            for (int n = 0; n < 4; ++n) a.final_state[state + n] = h[n];
-    }
-}
+// ---------------------------------------------------------------------------
+// Forward.  A warp is a CTA; it has 16 channels of a group and one range of
+// tokens, which it goes through in tiles of 16.  L = 4 lanes share a pair of
+// channels, NT states each (lane = j * 8 + pair); SL slices of 4 NT states.
+// Per tile:
+//   1. steps D and D x, B and C in float32 to shared memory (16 bytes per pair
+//      of channels: D0, D1, D x0, D x1), lanes over (token, four channels);
+//   2. token by token, h = 2^(D A log2 e) h + (D x) B and this thread's part of
+//      sum C h, its states in registers;
+//   3. the parts' sum, skip and gate, lanes over (token, four channels) again.
+// FULL: the whole forward.  Otherwise only what a later range starts from: the
+// state at the range's end from nothing (or from the sequence that begins in
+// it), and the sum of its steps, exp(A sum D) being the decay over the range.
+// ---------------------------------------------------------------------------
+template <typename T, int N, int L, bool FULL> struct Layout {
+    static constexpr int kCols = 64 / L;
+    static constexpr int kRow = kCols * sizeof(T), kBRow = N * sizeof(T);
+    static constexpr int kTensors = FULL ? 3 : 2, kMats = FULL ? 2 : 1;
+    static constexpr int kStage = kTile * (kTensors * kRow + kMats * kBRow);
+    static constexpr int kStep = 2 * kStage;                      // float4 [16][kCols / 2]
+    static constexpr int kB = kStep + kTile * kCols / 2 * 16;     // float [16][N], then C
+    static constexpr int kY = kB + kMats * kTile * N * 4;         // float [16][kYRow]
+    static constexpr int kYRow = 64 + (kCols < 32 ? kCols : 0);   // floats: [L][kCols], padded for the banks
+    static constexpr int kH = kY + (FULL ? kTile * kYRow * 4 : 0);  // slices: float4 [SL][2][32]
+    static constexpr int kBytes = kH + (N > 16 ? N * 64 : 0);
+};
 
-// Partial sums: of B's and C's gradients [warps of a group][T][groups][2][N], of A's and the two vectors' [S][width][N + 2].
-template <typename T, int L>
-__global__ void __launch_bounds__(32) selective_backward_kernel(SelectiveArgs a, sse_selective_config_t cfg, float *token_sums,
-                                                                float *weight_sums) {
-    constexpr int kRows = kSelectiveCheckpoint;
-    const int lane = threadIdx.x, N = 4 * L;
-    const Place p = place<L>(cfg.width, cfg.groups, lane);
-    const int n0 = lane % L * 4, at = p.g * N + n0;
-    const int part = blockIdx.x % (gridDim.x / cfg.groups);
-    const float bias = a.delta_bias ? a.delta_bias[p.c] : 0.f, skip = a.skip ? a.skip[p.c] : 0.f;
-    float A[4];
+struct ForwardWork {  // what ranges hand on
+    float *q, *steps;  // [ranges][width][N], [ranges][width]
+};
+
+template <typename T, int NT, int L, int SL, bool FULL>
+__global__ void __launch_bounds__(32) selective_forward_kernel(SelectiveArgs a, SelectiveShape sh, ForwardWork wk) {
+    constexpr int N = L * NT * SL, P = NT / 2;
+    using Lay = Layout<T, N, L, FULL>;
+    constexpr int kCols = Lay::kCols, kQuads = kCols / 4;
+    using Raw = typename Quad<T>::Raw;
+    extern __shared__ __align__(16) char smem[];
+    const int lane = threadIdx.x, j = lane / (32 / L), cl = lane % (32 / L), r = blockIdx.y;
+    const Columns cols(sh, blockIdx.x, kCols);
+    const Ranges rg(a, sh.ranges);
+    int t0 = rg.start(r);
+    const int t1 = rg.start(r + 1);
+    const int pair = cols.c0 + 2 * cl;
+    const bool live = 2 * cl < cols.left;
+    const int64_t states = (int64_t)pair * N + j * NT;  // this thread's first state of its first channel, slice 0
+    if constexpr (FULL) {
+        if (a.final_state)  // empty sequences keep their state
+            for (int q = r; q < a.num_seqs; q += sh.ranges)
+                if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1) && live)
+                    for (int i = j; i < 2 * N; i += L) {
+                        const int64_t at = ((int64_t)q * sh.width + pair) * N + i;
+                        a.final_state[at] = a.init ? a.init[at] : 0.f;
+                    }
+    } else {
+        const int from = rg.origin(t1);
+        if (t1 >= rg.end || from == t1) return;  // the next range begins a sequence
+        if (from > t0) t0 = from;
+    }
+    if (t0 >= t1) return;
+    const int origin = rg.origin(t0);
+
+    F2 hs[2][P], As[2][P];  // the states at hand, and A log2 e
+    auto load_A = [&](int s) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) A[n] = a.A[(int64_t)p.c * N + n0 + n];
-    for (int q = blockIdx.y; q < a.num_seqs; q += gridDim.y) {
-        const int t0 = clamp_token(a.cu_seqlens[q], a.total_tokens), t1 = clamp_token(a.cu_seqlens[q + 1], a.total_tokens);
-        const int64_t state = ((int64_t)q * cfg.width + p.c) * N + n0;
-        float e[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, d_skip = 0.f, d_bias = 0.f;  // e = a_{t+1} g_{t+1}
+        for (int c = 0; c < 2; ++c) {
+            no_pairs(As[c]);
+            if (live) read_pairs(a.A + states + (int64_t)c * N + s * L * NT, As[c]);
 #pragma unroll
-        for (int n = 0; n < 4; ++n) e[n] = a.d_final ? a.d_final[state + n] : 0.f;
-        for (int lo = t1 > t0 ? (t1 - 1) / kRows * kRows : t0 - 1; lo + kRows > t0 && t1 > t0; lo -= kRows) {
-            const int s0 = max(lo, t0), s1 = min(lo + kRows, t1);
-            float before[kRows][4], h[4];
+            for (int k = 0; k < P; ++k) As[c][k] = mul2(As[c][k], both(kLog2e));
+        }
+    };
+    // this thread's states in an array of [.., width, N] at row i
+    auto get = [&](const float *p, int64_t i, int s) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                h[n] = s0 > t0 ? a.checkpoints[((int64_t)(s0 / kRows) * cfg.width + p.c) * N + n0 + n]
-                       : a.init ? a.init[state + n] : 0.f;
-            for (int t = s0; t < s1; ++t) {
-                const Token k = token<T>(a, t, p.c, at, bias);
+        for (int c = 0; c < 2; ++c) {
+            no_pairs(hs[c]);
+            if (p && live) read_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * L * NT, hs[c]);
+        }
+    };
+    auto put = [&](float *p, int64_t i, int s) {
+        if (live)
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    before[t - s0][n] = h[n];
-                    h[n] = fmaf(expf(k.d * A[n]), h[n], k.d * k.x * k.B[n]);
-                }
+            for (int c = 0; c < 2; ++c) write_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * L * NT, hs[c]);
+    };
+    // a slice's states between tiles: registers with one slice, else shared memory (4 NT bytes of a thread, then the next's)
+    float *kept = reinterpret_cast<float *>(smem + Lay::kH) + lane * 4;
+    auto keep = [&](int s) {
+        if constexpr (SL > 1) {
+            static_assert(NT == 4, "a word per channel");
+#pragma unroll
+            for (int c = 0; c < 2; ++c) write_pairs(kept + (s * 2 + c) * 128, hs[c]);
+        }
+    };
+    auto recall = [&](int s) {
+        if constexpr (SL > 1) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) read_pairs(kept + (s * 2 + c) * 128, hs[c]);
+            load_A(s);
+        }
+    };
+
+    // the states that the range starts from
+    if constexpr (FULL) {
+        if (origin < t0) {
+            int r0 = r - 1;  // the range that the sequence begins in
+            for (int i = r - 1; i > 0; i -= 32) {
+                const uint32_t m = __ballot_sync(0xffffffffu, i - lane > 0 && rg.start(i - lane) > origin);
+                r0 -= __popc(m);
+                if (m != 0xffffffffu) break;
             }
-            for (int t = s1 - 1; t >= s0; --t) {
-                const Token k = token<T>(a, t, p.c, at, bias);
-                const float d_out = load<T>(a.d_out, (int64_t)t * cfg.width + p.c);
-                float dy = d_out, z = 0.f, s = 0.f;
-                if (a.gate) {
-                    z = load<T>(a.gate, (int64_t)t * a.gate_stride + p.c);
-                    s = sigmoid(z);
-                    dy *= z * s;
-                }
-                float y = 0.f, Bg = 0.f, Aw = 0.f;
-                float *sums = token_sums + (((int64_t)part * a.total_tokens + t) * cfg.groups + p.g) * 2 * N + n0;
+            for (int s = 0; s < SL; ++s) {
+                load_A(s);
+                get(wk.q, r0, s);
+                for (int i = r0 + 1; i < r; ++i) {
+                    F2 now[2][P];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float dec = expf(k.d * A[n]), u = dec * before[t - s0][n], b = k.d * k.x;
-                    const float now = fmaf(b, k.B[n], u);
-                    y = fmaf(k.C[n], now, y);
-                    const float g = fmaf(k.C[n], dy, e[n]);
-                    e[n] = dec * g;
-                    const float w = g * u;
-                    Bg = fmaf(k.B[n], g, Bg);
-                    Aw = fmaf(A[n], w, Aw);
-                    dA[n] = fmaf(k.d, w, dA[n]);
-                    const float dB = channels_sum<L>(p.live ? g * b : 0.f), dC = channels_sum<L>(p.live ? dy * now : 0.f);
-                    if (lane < L) {
-                        sums[n] = dB;
-                        sums[N + n] = dC;
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < P; ++k) now[c][k] = hs[c][k];
+                    get(wk.q, i, s);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const F2 d = both(live ? wk.steps[(int64_t)i * sh.width + pair + c] : 0.f);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) hs[c][k] = fma2(ex2_ftz(mul2(d, As[c][k])), now[c][k], hs[c][k]);
                     }
                 }
-                y = fmaf(skip, k.x, lanes_sum<L>(y));
-                Bg = lanes_sum<L>(Bg);
-                Aw = lanes_sum<L>(Aw);
-                const float dd = fmaf(k.x, Bg, Aw) * sigmoid(k.raw);
-                d_skip = fmaf(dy, k.x, d_skip);
-                d_bias += dd;
-                if (p.live && n0 == 0) {
-                    const int64_t i = (int64_t)t * cfg.width + p.c;
-                    store<T>(a.dx, i, fmaf(skip, dy, k.d * Bg));
-                    store<T>(a.d_delta, i, dd);
-                    if (a.gate) store<T>(a.d_gate, i, d_out * y * s * (1.f + z * (1.f - s)));
+                keep(s);
+            }
+        } else {
+            get(nullptr, 0, 0);
+            for (int s = 0; s < SL; ++s) keep(s);
+        }
+    } else {
+        get(nullptr, 0, 0);
+        for (int s = 0; s < SL; ++s) keep(s);
+    }
+    if constexpr (SL == 1) load_A(0);
+
+    const int row_first = t0 & ~(kTile - 1);
+    const int esz = (int)sizeof(T), live_bytes = cols.left * esz;
+    const uint32_t smem_at = (uint32_t)__cvta_generic_to_shared(smem);
+    auto fetch = [&](int row0, int stage) {
+        if (row0 < t1) {
+            const uint32_t at = smem_at + stage * Lay::kStage;
+            const int64_t c = (int64_t)cols.c0 * esz, n = (int64_t)cols.g * N * esz;
+            copy_rows<Lay::kRow>(at, static_cast<const char *>(a.x) + c, a.x_stride * esz, live_bytes, row0, t0, t1, a.x, lane);
+            copy_rows<Lay::kRow>(at + kTile * Lay::kRow, static_cast<const char *>(a.delta) + c, a.delta_stride * esz, live_bytes,
+                                 row0, t0, t1, a.x, lane);
+            const uint32_t mats = at + kTile * Lay::kTensors * Lay::kRow;
+            copy_rows<Lay::kBRow>(mats, static_cast<const char *>(a.B) + n, a.b_stride * esz, Lay::kBRow, row0, t0, t1, a.x, lane);
+            if constexpr (FULL) {
+                if (a.gate)
+                    copy_rows<Lay::kRow>(at + 2 * kTile * Lay::kRow, static_cast<const char *>(a.gate) + c, a.gate_stride * esz,
+                                         live_bytes, row0, t0, t1, a.x, lane);
+                copy_rows<Lay::kBRow>(mats + kTile * Lay::kBRow, static_cast<const char *>(a.C) + n, a.c_stride * esz,
+                                      Lay::kBRow, row0, t0, t1, a.x, lane);
+            }
+        }
+        copies_commit();
+    };
+
+    // parts 1 and 3: lane has four channels of every fourth token
+    const int qd = lane % kQuads, tq = lane / kQuads;
+    const bool quad_live = qd * 4 < cols.left;
+    F2 bias[2], skip[2];
+    load_quad(a.delta_bias, cols.c0 + qd * 4, quad_live, bias);
+    load_quad(FULL ? a.skip : nullptr, cols.c0 + qd * 4, quad_live, skip);
+    F2 steps = both(0.f);  // sums of this thread's channels' steps
+    float4 *step = reinterpret_cast<float4 *>(smem + Lay::kStep);
+    float *bs = reinterpret_cast<float *>(smem + Lay::kB), *cs = bs + kTile * N;
+    float *ys = reinterpret_cast<float *>(smem + Lay::kY);
+    Edges ed;
+    fetch(row_first, 0);
+    int stage = 0;
+    for (int row0 = row_first; row0 < t1; row0 += kTile, stage ^= 1) {
+        fetch(row0 + kTile, stage ^ 1);
+        ed.find(rg, row0, t0, t1, lane);
+        copies_wait<1>();
+        const char *at = smem + stage * Lay::kStage;
+#pragma unroll
+        for (int k = 0; k < kTile; k += 32 / kQuads) {
+            const int i = k + tq, t = row0 + i;
+            F2 x[2], d[2];
+            Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + i * Lay::kRow + qd * 4 * esz), x);
+            Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + (kTile + i) * Lay::kRow + qd * 4 * esz), d);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                d[p] = softplus2(add2(d[p], bias[p]));
+                if (t < t0 || t >= t1) d[p] = both(0.f);  // neither decay nor input
+                x[p] = mul2(x[p], d[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // banks: every other four lanes the other pair first
+                const bool other = (p ^ (lane >> 2)) & 1;
+                const float2 u = f2_get(other ? d[1] : d[0]), v = f2_get(other ? x[1] : x[0]);
+                step[i * (kCols / 2) + qd * 2 + other] = make_float4(u.x, u.y, v.x, v.y);
+            }
+        }
+        {
+            const char *mats = at + kTile * Lay::kTensors * Lay::kRow;
+#pragma unroll
+            for (int k = lane; k < Lay::kMats * kTile * N / 4; k += 32) {
+                F2 f[2];
+                Quad<T>::unpack(*reinterpret_cast<const Raw *>(mats + k * 4 * esz), f);
+                const float2 u = f2_get(f[0]), v = f2_get(f[1]);
+                *reinterpret_cast<float4 *>(bs + k * 4) = make_float4(u.x, u.y, v.x, v.y);
+            }
+        }
+        __syncwarp();
+        for (int s = 0; s < SL; ++s) {
+            recall(s);
+            if constexpr (FULL)
+                if (a.checkpoints && row0 >= t0) put(a.checkpoints, row0 / kTile, s);
+            auto token = [&](int i) {  // returns this thread's part of y
+                const float4 d = step[i * (kCols / 2) + cl];
+                const float *bt = bs + i * N + s * L * NT + j * NT, *ct = cs + i * N + s * L * NT + j * NT;
+                F2 B[P], y[2] = {both(0.f), both(0.f)};
+                read_pairs(bt, B);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const F2 dc = both(c ? d.y : d.x), xc = both(c ? d.w : d.z);
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+                        hs[c][k] = fma2(ex2_ftz(mul2(dc, As[c][k])), hs[c][k], mul2(xc, B[k]));
+                }
+                if constexpr (FULL) {
+                    F2 C[P];
+                    read_pairs(ct, C);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < P; ++k) y[c] = fma2(hs[c][k], C[k], y[c]);
+                } else if (s == 0) {
+                    steps = add2(steps, f2(d.x, d.y));
+                }
+                const float2 u = f2_get(y[0]), v = f2_get(y[1]);
+                return make_float2(u.x + u.y, v.x + v.y);
+            };
+            auto leave = [&](int i, float2 part) {
+                if constexpr (FULL) {
+                    float2 *to = reinterpret_cast<float2 *>(ys + i * Lay::kYRow + j * kCols + cl * 2);
+                    if (SL > 1 && s) part.x += to->x, part.y += to->y;
+                    *to = part;
+                }
+            };
+            if ((ed.starts | ed.ends) == 0) {
+                // four tokens' loads before their stores
+#pragma unroll 1
+                for (int i = 0; i < kTile; i += 4) {
+                    float2 part[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) part[u] = token(i + u);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) leave(i + u, part[u]);
+                }
+            } else {
+                for (int i = 0; i < kTile; ++i) {
+                    if ((ed.starts >> i) & 1u) get(a.init, __shfl_sync(0xffffffffu, ed.seq, i), s);
+                    leave(i, token(i));
+                    if constexpr (FULL) {
+                        const int q = __shfl_sync(0xffffffffu, ed.seq, i);
+                        if (((ed.ends >> i) & 1u) && a.final_state) put(a.final_state, q, s);
+                    }
                 }
             }
+            keep(s);
         }
-        if (p.live) {
-            float *w = weight_sums + ((int64_t)q * cfg.width + p.c) * (N + 2);
+        __syncwarp();
+        if constexpr (FULL) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                if (a.d_init) a.d_init[state + n] = e[n];
-                w[n0 + n] = dA[n];
+            for (int k = 0; k < kTile; k += 32 / kQuads) {
+                const int i = k + tq, t = row0 + i;
+                F2 y[2] = {both(0.f), both(0.f)}, x[2];
+#pragma unroll
+                for (int l = 0; l < L; ++l) {
+                    const float4 u = *reinterpret_cast<const float4 *>(ys + i * Lay::kYRow + l * kCols + qd * 4);
+                    y[0] = add2(y[0], f2(u.x, u.y));
+                    y[1] = add2(y[1], f2(u.z, u.w));
+                }
+                Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + i * Lay::kRow + qd * 4 * esz), x);
+                y[0] = fma2(skip[0], x[0], y[0]);
+                y[1] = fma2(skip[1], x[1], y[1]);
+                if (a.gate) {
+                    F2 z[2];
+                    Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + (2 * kTile + i) * Lay::kRow + qd * 4 * esz), z);
+                    y[0] = mul2(y[0], mul2(z[0], sigmoid2<T>(z[0])));
+                    y[1] = mul2(y[1], mul2(z[1], sigmoid2<T>(z[1])));
+                }
+                if (t >= t0 && t < t1 && quad_live)
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + (int64_t)t * sh.width + cols.c0 + qd * 4) = Quad<T>::pack(y);
             }
-            if (n0 == 0) {
-                w[N] = d_skip;
-                w[N + 1] = d_bias;
-            }
+            __syncwarp();  // the stage is free
         }
     }
-}
-
-template <typename T>
-__global__ void selective_tokens_kernel(SelectiveArgs a, sse_selective_config_t cfg, const float *sums, int parts) {
-    const int64_t row = (int64_t)cfg.groups * cfg.state, i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, t = i / row;
-    if (t >= clamp_token(a.cu_seqlens[a.num_seqs], a.total_tokens)) return;
-    const int g = (int)(i - t * row) / cfg.state, n = (int)(i % cfg.state);
-    float dB = 0.f, dC = 0.f;
-    for (int p = 0; p < parts; ++p) {
-        const float *s = sums + (((int64_t)p * a.total_tokens + t) * cfg.groups + g) * 2 * cfg.state + n;
-        dB += s[0];
-        dC += s[cfg.state];
+    if constexpr (!FULL) {
+        for (int s = 0; s < SL; ++s) {
+            recall(s);
+            put(wk.q, r, s);
+        }
+        if (j == 0 && live) *reinterpret_cast<float2 *>(wk.steps + (int64_t)r * sh.width + pair) = f2_get(steps);
     }
-    store<T>(a.d_B, i, dB);
-    store<T>(a.d_C, i, dC);
-}
-
-__global__ void selective_weights_kernel(SelectiveArgs a, sse_selective_config_t cfg, const float *sums) {
-    const int N = cfg.state, i = blockIdx.x * blockDim.x + threadIdx.x, c = i / (N + 2), n = i % (N + 2);
-    if (c >= cfg.width) return;
-    float s = 0.f;
-    for (int q = 0; q < a.num_seqs; ++q) s += sums[(int64_t)q * cfg.width * (N + 2) + i];
-    if (n < N)
-        a.d_A[(int64_t)c * N + n] = s;
-    else if (n == N && a.d_skip)
-        a.d_skip[c] = s;
-    else if (n == N + 1 && a.d_delta_bias)
-        a.d_delta_bias[c] = s;
 }
 
 template <typename T, int L>
@@ -263,12 +390,26 @@ __global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, ss
     store<T>(a.out, t * cfg.width + c, y);
 }
 
-int warps_of_group(const sse_selective_config_t &c) {
-    const int per = c.width / c.groups, channels = 128 / c.state;
-    return (per + channels - 1) / channels;
-}
+enum What { kForward, kStep };
 
-enum What { kForward, kBackward, kStep };
+template <typename T, int N> cudaError_t launch_forward(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
+    constexpr int L = kL, NT = N / L < kNT ? N / L : kNT, SL = N / (L * NT);
+    const SelectiveShape sh = selective_shape(c, 64 / kL, a.total_tokens);
+    ForwardWork wk;
+    wk.q = reinterpret_cast<float *>(a.workspace);
+    wk.steps = wk.q + (int64_t)sh.ranges * c.width * N;
+    const dim3 grid(sh.tiles * c.groups, sh.ranges);
+    const auto states = selective_forward_kernel<T, NT, L, SL, false>, full = selective_forward_kernel<T, NT, L, SL, true>;
+    constexpr int kStates = Layout<T, N, L, false>::kBytes, kFull = Layout<T, N, L, true>::kBytes;
+    if constexpr (kFull > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
+        if (e != cudaSuccess) return e;
+    }
+    static_assert(kStates <= 48 * 1024, "the default limit");
+    if (sh.ranges > 1) states<<<grid, 32, kStates, s>>>(a, sh, wk);
+    full<<<grid, 32, kFull, s>>>(a, sh, wk);
+    return cudaGetLastError();
+}
 
 template <typename T, int L>
 cudaError_t launch_t(What what, const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
@@ -278,19 +419,7 @@ cudaError_t launch_t(What what, const sse_selective_config_t &c, const Selective
         selective_step_kernel<T, L><<<(unsigned)blocks, 256, 0, s>>>(a, c);
         return cudaGetLastError();
     }
-    const int warps = warps_of_group(c);
-    const dim3 grid(warps * c.groups, a.num_seqs < 1 ? 1 : a.num_seqs < 65535 ? a.num_seqs : 65535);
-    if (what == kForward) {
-        selective_forward_kernel<T, L><<<grid, 32, 0, s>>>(a, c);
-        return cudaGetLastError();
-    }
-    float *token_sums = reinterpret_cast<float *>(a.workspace);
-    float *weight_sums = token_sums + (int64_t)warps * a.total_tokens * c.groups * 2 * c.state;
-    if (a.num_seqs > 0) selective_backward_kernel<T, L><<<grid, 32, 0, s>>>(a, c, token_sums, weight_sums);
-    const int64_t n = (int64_t)a.total_tokens * c.groups * c.state;
-    if (n > 0) selective_tokens_kernel<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a, c, token_sums, warps);
-    selective_weights_kernel<<<(c.width * (c.state + 2) + 255) / 256, 256, 0, s>>>(a, c, weight_sums);
-    return cudaGetLastError();
+    return launch_forward<T, 4 * L>(c, a, s);
 }
 
 template <typename T> cudaError_t launch_state(What what, const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
@@ -308,15 +437,12 @@ cudaError_t launch(What what, const sse_selective_config_t &c, const SelectiveAr
 
 }  // namespace
 
-size_t selective_forward_workspace(const sse_selective_config_t &, int64_t, int32_t) { return 0; }
-size_t selective_backward_workspace(const sse_selective_config_t &c, int64_t T, int32_t S) {
-    return sizeof(float) * ((size_t)warps_of_group(c) * T * c.groups * 2 * c.state + (size_t)S * c.width * (c.state + 2));
+size_t selective_forward_workspace(const sse_selective_config_t &c, int64_t T, int32_t) {
+    const SelectiveShape s = selective_shape(c, 64 / kL, T);
+    return s.ranges > 1 ? sizeof(float) * (size_t)s.ranges * c.width * (c.state + 1) : 0;
 }
 cudaError_t launch_selective_forward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {
     return launch(kForward, cfg, a, stream);
-}
-cudaError_t launch_selective_backward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {
-    return launch(kBackward, cfg, a, stream);
 }
 cudaError_t launch_selective_step(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {
     return launch(kStep, cfg, a, stream);

@@ -1,0 +1,184 @@
+// selective.cuh -- what the forward and the backward of the selective scan share:
+// ranges of the packed token axis, tiles of 16 tokens by 32 channels, and their
+// staging.
+#pragma once
+
+#include "quad.cuh"
+
+namespace sse {
+
+constexpr int kTile = 16;        // tokens of a tile, aligned in the packed token axis
+constexpr int kMaxRanges = 128;  // of the token axis
+static_assert(kTile == kSelectiveCheckpoint, "a checkpoint is the state before a tile");
+
+struct SelectiveShape {
+    int width, groups, per, tiles;  // channels; groups; channels and tiles of a group
+    int ranges;
+};
+
+// Warps of a call, `cols` channels each, and ranges of the token axis: at least six warps for each SM.  (A range that
+// begins inside a sequence costs a pass of its own over the range before it.)
+inline SelectiveShape selective_shape(const sse_selective_config_t &c, int cols, int64_t T) {
+    SelectiveShape s{c.width, c.groups, c.width / c.groups, 0, 1};
+    s.tiles = (s.per + cols - 1) / cols;
+    const int64_t tiles = (int64_t)s.tiles * c.groups;
+    int64_t r = (152 * 6 + tiles - 1) / tiles;
+    if (r > T / (4 * kTile)) r = T / (4 * kTile);
+    s.ranges = (int)(r < 1 ? 1 : r > kMaxRanges ? kMaxRanges : r);
+    return s;
+}
+
+// log2 e and what float32 leaves of it.
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596303e-8f;
+
+// softplus(v) = max(v, 0) + log1p(exp(-|v|)), log1p(u) = 2 atanh(u / (2 + u)): the odd series of atanh on [0, 1/3] as a
+// polynomial of degree 4 in the square (relative error 8e-9 by its coefficients).  The exponent's rounding is put back to
+// first order: small steps are proportional to exp(v), and a step's relative error goes into a state's whole memory.
+__device__ __forceinline__ F2 softplus2(F2 v) {
+    const float2 f = f2_get(v);
+    const F2 m = f2(-fabsf(f.x), -fabsf(f.y));
+    const F2 t = mul2(m, both(kLog2e));
+    const F2 r = fma2(m, both(kLog2eRest), fma2(m, both(kLog2e), mul2(t, both(-1.f))));
+    F2 u = ex2_ftz(t);
+    u = fma2(u, mul2(r, both(0.693147181f)), u);
+    const F2 s = mul2(u, rcp_ftz(add2(u, both(2.f)))), z = mul2(s, s);
+    F2 p = both(0.28178346f);
+    p = fma2(p, z, both(0.2796061f));
+    p = fma2(p, z, both(0.4002491f));
+    p = fma2(p, z, both(0.66666317f));
+    p = fma2(p, z, both(2.f));
+    // a NaN stays one: exp(-|v|) has it
+    return fma2(s, p, f2(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
+}
+
+// ---------------------------------------------------------------------------
+// Ranges of the token axis.  A range begins at a multiple of 16, or at the start
+// of a sequence that is no further than a quarter of a range from there; one that
+// begins inside a sequence takes the state that the ranges before it hand on.
+// ---------------------------------------------------------------------------
+struct Ranges {
+    const int32_t *cu;
+    int S, end, n;  // sequences, their last token's successor, ranges with tokens
+    __device__ __forceinline__ Ranges(const SelectiveArgs &a, int ranges) : cu(a.cu_seqlens), S(a.num_seqs) {
+        end = clamp_token(__ldg(cu + S), a.total_tokens);
+        n = max(1, min(ranges, end / (4 * kTile)));  // of 64 tokens and more: starts are in order
+    }
+    __device__ __forceinline__ int start(int r) const {
+        if (r <= 0) return 0;
+        if (r >= n) return end;
+        const int t = (int)((int64_t)end * r / n) & ~(kTile - 1), near = end / (4 * n);
+        const int s = sequence_of(cu, S, t), lo = clamp_token(__ldg(cu + s), end), hi = clamp_token(__ldg(cu + s + 1), end);
+        if (t - lo <= hi - t) return t - lo <= near ? lo : t;
+        return hi - t <= near ? hi : t;
+    }
+    // The first token of the sequence that token t continues; t itself where t begins one, or is the end.
+    __device__ __forceinline__ int origin(int t) const {
+        return t >= end ? t : clamp_token(__ldg(cu + sequence_of(cu, S, t)), t);
+    }
+};
+
+// Where sequences begin and end among the 16 tokens of a tile; tokens outside [t0, t1) have no bits.
+struct Edges {
+    uint32_t starts, ends;  // bit i: token i is the first / last of its sequence
+    int seq;                // lane i: the sequence of token i
+    int lo, hi;             // tokens of the last sequence looked up
+    __device__ __forceinline__ Edges() : starts(0), ends(0), seq(0), lo(1), hi(0) {}
+    __device__ __forceinline__ void find(const Ranges &rg, int row0, int t0, int t1, int lane) {
+        if (row0 > lo && row0 + kTile < hi) {  // inside the sequence of the tile before
+            starts = ends = 0;
+            return;
+        }
+        const int t = row0 + (lane < kTile ? lane : kTile - 1);
+        int b = 0, e = 0;
+        seq = -1;
+        if (t >= t0 && t < t1) {
+            seq = sequence_of(rg.cu, rg.S, t);
+            b = __ldg(rg.cu + seq);
+            e = __ldg(rg.cu + seq + 1);
+        }
+        const bool mine = lane < kTile && seq >= 0;
+        starts = __ballot_sync(0xffffffffu, mine && b == t);
+        ends = __ballot_sync(0xffffffffu, mine && e == t + 1);
+        lo = __shfl_sync(0xffffffffu, b, kTile - 1);
+        hi = __shfl_sync(0xffffffffu, e, kTile - 1);
+    }
+};
+
+// A warp's channels: COLS of one group, or what is left of it.
+struct Columns {
+    int g, c0, left;  // group, first channel, channels
+    __device__ __forceinline__ Columns(const SelectiveShape &s, int tile, int cols) {
+        g = tile / s.tiles;
+        const int i = (tile - g * s.tiles) * cols;
+        c0 = g * s.per + i;
+        left = min(cols, s.per - i);
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Staging: rows of a tile to shared memory by asynchronous copies of 16 bytes.
+// Rows outside [t0, t1) and channels past the group's end are filled with zeros.
+// ---------------------------------------------------------------------------
+// `bytes` of each of the 16 rows, of which `live` exist (whole words).
+template <int BYTES>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const char *src, int64_t stride, int live, int row0, int t0, int t1,
+                                          const void *safe, int lane) {
+    constexpr int W = BYTES / 16;
+#pragma unroll
+    for (int k = 0; k < kTile * W; k += 32) {
+        const int id = k + lane, row = id / W, w = id % W;
+        if (kTile * W < 32 && id >= kTile * W) break;
+        const int t = row0 + row;
+        const bool ok = t >= t0 && t < t1 && w * 16 < live;
+        const void *from = ok ? static_cast<const void *>(src + (int64_t)t * stride + w * 16) : safe;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + id * 16), "l"(from), "r"(ok ? 16 : 0)
+                     : "memory");
+    }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Waits until at most N of this thread's groups are in flight; then the whole warp's words are there.
+template <int N> __device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    __syncwarp();
+}
+
+// Four channels' float32 parameters; zeros where there are none.
+__device__ __forceinline__ void load_quad(const float *p, int c, bool live, F2 (&f)[2]) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p && live) v = __ldg(reinterpret_cast<const float4 *>(p + c));
+    f[0] = f2(v.x, v.y);
+    f[1] = f2(v.z, v.w);
+}
+
+// 2 P floats in a row as P pairs, by 16-byte words where there are whole ones (P = 1: one of 8 bytes).
+template <int P> __device__ __forceinline__ void read_pairs(const float *p, F2 (&f)[P]) {
+    if constexpr (P == 1) {
+        const float2 v = *reinterpret_cast<const float2 *>(p);
+        f[0] = f2(v.x, v.y);
+    } else {
+        static_assert(P % 2 == 0, "whole 16-byte words");
+#pragma unroll
+        for (int k = 0; k < P; k += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + 2 * k);
+            f[k] = f2(v.x, v.y);
+            f[k + 1] = f2(v.z, v.w);
+        }
+    }
+}
+template <int P> __device__ __forceinline__ void write_pairs(float *p, const F2 (&f)[P]) {
+    if constexpr (P == 1) {
+        *reinterpret_cast<float2 *>(p) = f2_get(f[0]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < P; k += 2) {
+            const float2 u = f2_get(f[k]), v = f2_get(f[k + 1]);
+            *reinterpret_cast<float4 *>(p + 2 * k) = make_float4(u.x, u.y, v.x, v.y);
+        }
+    }
+}
+template <int P> __device__ __forceinline__ void no_pairs(F2 (&f)[P]) {
+#pragma unroll
+    for (int k = 0; k < P; ++k) f[k] = both(0.f);
+}
+
+}  // namespace sse

@@ -1,0 +1,623 @@
+// selective_backward.cu -- the gradients of the selective scan (formulas at the
+// head of selective.cu).
+//
+// A warp has 16 channels of a group and one range of tokens, which it goes
+// through backwards in tiles of 16.  Four lanes share a pair of channels, NT
+// states each (lane = j * 8 + pair); SL slices of 4 NT states.  Per tile:
+//   1. steps D and D x, dy, B and C in float32 to shared memory, lanes over
+//      (token, four channels);
+//   2. in halves of 8 tokens, the later one first: forwards from the checkpoint,
+//      the states before the half's tokens in registers; then backwards: g = C dy + e, e = a g, and this thread's parts of the
+//      sums over states (y, sum B g, sum A g a h) and over channels (dB, dC);
+//   3. the sums over states, lanes over (token, four channels), and with them
+//      dx, d_delta, d_gate.
+// The sums over channels go over the eight pairs of a warp by shuffles, over the
+// four warps of a CTA through shared memory, and over the CTAs of a group in a
+// second kernel: a float32 row of 2 N for each token and 64 channels.  Every sum
+// has a fixed order.
+#include <type_traits>
+
+#include "selective.cuh"
+
+namespace sse {
+namespace {
+
+constexpr int kL = 4, kCols = 16;
+constexpr int kSpan = 8;  // tokens whose states are held in registers, and of an epilogue
+
+template <typename T, int N, bool FULL> struct Layout {
+    static constexpr int NT = N == 8 ? 2 : 4, SL = N / (kL * NT);
+    static constexpr int kWarps = FULL ? 4 : 1;
+    static constexpr int kRow = kCols * sizeof(T), kBRow = N * sizeof(T);
+    static constexpr int kTensors = FULL ? 4 : 2, kMats = FULL ? 2 : 1;  // delta, d_out, gate, x (without FULL: delta, dy); C, B
+    // of a warp
+    static constexpr int kCheck = kTile * (FULL ? 4 : 3) * kRow;
+    static constexpr int kStage = kCheck + (FULL ? kCols * N * 4 : 0);
+    static constexpr int kStep = 2 * kStage;                    // float4 [16][8]: D0, D1, D x0, D x1
+    static constexpr int kDy = kStep + kTile * kCols / 2 * 16;  // float [16][16]
+    static constexpr int kPart = kDy + kTile * kCols * 4;       // float [3][8][4][16]: y, sum B g, sum A g a h
+    static constexpr int kKept = kPart + (FULL ? 3 * kSpan * kL * kCols * 4 : 0);  // slices: e and dA, float4 [SL][2][2][32]
+    static constexpr int kWarpBytes = kKept + (SL > 1 ? SL * 4 * 32 * 16 : 0);
+    // of the CTA
+    static constexpr int kMat = kTile * kBRow * kMats;
+    static constexpr int kRaw = kWarps * kWarpBytes;            // C and B as stored, two stages
+    static constexpr int kC = kRaw + 2 * kMat;                  // float [16][N]: C, then B
+    static constexpr int kSums = kC + kMats * kTile * N * 4;    // float [2][kWarps][8][32]
+    static constexpr int kBytes = kSums + (FULL ? 2 * kWarps * kSpan * 32 * 4 : 0);
+};
+
+struct BackwardWork {
+    float *q, *steps;   // what ranges hand on: [ranges][width][N], [ranges][width]
+    float *tokens;      // [parts][T][groups][2 N]: dB and dC of 64 channels
+    float *weights;     // [ranges][width][N + 2]: dA, d_skip, d_delta_bias
+    int parts;          // CTAs of a group
+};
+
+// FULL: the gradients.  Otherwise what an earlier range starts from: e at the range's first token from nothing behind it
+// (or from the sequence that ends in it), and the sum of its steps.
+template <typename T, int N, bool FULL>
+__global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1) selective_backward_kernel(SelectiveArgs a, SelectiveShape sh,
+                                                                                    BackwardWork wk) {
+    using Lay = Layout<T, N, FULL>;
+    using Raw = typename Quad<T>::Raw;
+    constexpr int NT = Lay::NT, SL = Lay::SL, P = NT / 2, kQuads = kCols / 4, kWarps = Lay::kWarps;
+    extern __shared__ __align__(16) char all_smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane >> 3, cl = lane & 7, r = blockIdx.y;
+    char *smem = all_smem + (FULL ? warp * Lay::kWarpBytes : 0);
+    const int g = blockIdx.x / (FULL ? wk.parts : sh.tiles), part = blockIdx.x - g * (FULL ? wk.parts : sh.tiles);
+    const int first = (FULL ? part * kWarps + warp : part) * kCols;
+    const int left = max(0, min(kCols, sh.per - first)), c0 = g * sh.per + (left ? first : 0);
+    const Ranges rg(a, sh.ranges);
+    const int t0 = rg.start(r);
+    int t1 = rg.start(r + 1);
+    const int pair = c0 + 2 * cl;
+    const bool live = 2 * cl < left;
+    const int64_t states = (int64_t)pair * N + j * NT;
+    if constexpr (FULL) {
+        if (a.d_init)  // empty sequences hand the final state's gradient through
+            for (int q = r; q < a.num_seqs; q += sh.ranges)
+                if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1) && live)
+                    for (int i = j; i < 2 * N; i += kL) {
+                        const int64_t at = ((int64_t)q * sh.width + pair) * N + i;
+                        a.d_init[at] = a.d_final ? a.d_final[at] : 0.f;
+                    }
+    } else {
+        if (t0 >= t1 || rg.origin(t0) == t0) return;  // the range begins a sequence
+        t1 = min(t1, clamp_token(__ldg(a.cu_seqlens + sequence_of(rg.cu, rg.S, t0) + 1), rg.end));
+    }
+
+    F2 e[2][P], A[2][P], dA[2][P], h[2][P];  // A: A log2 e
+    auto load_A = [&](int s) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            no_pairs(A[c]);
+            if (live) read_pairs(a.A + states + (int64_t)c * N + s * kL * NT, A[c]);
+#pragma unroll
+            for (int k = 0; k < P; ++k) A[c][k] = mul2(A[c][k], both(kLog2e));
+        }
+    };
+    // this thread's states in an array of [.., width, N] at row i
+    auto get = [&](const float *p, int64_t i, int s, F2 (&to)[2][P]) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            no_pairs(to[c]);
+            if (p && live) read_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * kL * NT, to[c]);
+        }
+    };
+    auto put = [&](float *p, int64_t i, int s, const F2 (&from)[2][P]) {
+        if (live)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) write_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * kL * NT, from[c]);
+    };
+    // a slice's e and dA between tiles: registers with one slice, else shared memory
+    float *kept = reinterpret_cast<float *>(smem + Lay::kKept) + lane * 4;
+    auto keep = [&](int s) {
+        if constexpr (SL > 1) {
+            static_assert(NT == 4, "a word per channel");
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                write_pairs(kept + (s * 4 + c) * 128, e[c]);
+                write_pairs(kept + (s * 4 + 2 + c) * 128, dA[c]);
+            }
+        }
+    };
+    auto recall = [&](int s) {
+        if constexpr (SL > 1) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                read_pairs(kept + (s * 4 + c) * 128, e[c]);
+                read_pairs(kept + (s * 4 + 2 + c) * 128, dA[c]);
+            }
+            load_A(s);
+        }
+    };
+    // decays of a step, per state
+    auto decays = [&](F2 d, int c, F2 (&to)[P]) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) to[k] = ex2_ftz(mul2(d, A[c][k]));
+    };
+
+    // what the range takes over from those behind it
+    int r_last = r;
+    if (FULL && t0 < t1 && t1 < rg.end && rg.origin(t1) < t1) {
+        const int stop = clamp_token(__ldg(a.cu_seqlens + sequence_of(rg.cu, rg.S, t1) + 1), rg.end);
+        r_last = r + 1;
+        for (int i = r + 2; i < rg.n; i += 32) {  // ranges that begin in front of the sequence's end
+            const uint32_t m = __ballot_sync(0xffffffffu, i + lane < rg.n && rg.start(i + lane) < stop);
+            r_last += __popc(m);
+            if (m != 0xffffffffu) break;
+        }
+    }
+    for (int s = 0; s < SL; ++s) {
+        load_A(s);
+        get(r_last > r ? wk.q : nullptr, r_last, s, e);
+        for (int i = r_last - 1; i > r; --i) {
+            F2 q[2][P];
+            get(wk.q, i, s, q);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                F2 d[P];
+                decays(both(live ? wk.steps[(int64_t)i * sh.width + pair + c] : 0.f), c, d);
+#pragma unroll
+                for (int k = 0; k < P; ++k) e[c][k] = fma2(d[k], e[c][k], q[c][k]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int k = 0; k < P; ++k) dA[c][k] = both(0.f);
+        keep(s);
+    }
+
+    const int esz = (int)sizeof(T), live_bytes = left * esz;
+    const uint32_t smem_at = (uint32_t)__cvta_generic_to_shared(smem), cta_at = (uint32_t)__cvta_generic_to_shared(all_smem);
+    constexpr int kR = kTile * Lay::kRow, kWords = kTile * Lay::kBRow / 16;  // 16-byte words of B or C in a tile
+    auto fetch = [&](int row0, int stage) {
+        if (row0 + kTile > t0 && row0 < t1 && row0 >= 0) {
+            const uint32_t at = smem_at + stage * Lay::kStage;
+            const int64_t c = (int64_t)c0 * esz, packed = (int64_t)sh.width * esz;
+            copy_rows<Lay::kRow>(at, static_cast<const char *>(a.delta) + c, a.delta_stride * esz, live_bytes, row0, t0, t1,
+                                 a.x, lane);
+            copy_rows<Lay::kRow>(at + kR, static_cast<const char *>(a.d_out) + c, packed, live_bytes, row0, t0, t1, a.x, lane);
+            if (a.gate)
+                copy_rows<Lay::kRow>(at + 2 * kR, static_cast<const char *>(a.gate) + c, a.gate_stride * esz, live_bytes, row0,
+                                     t0, t1, a.x, lane);
+            if constexpr (FULL) {
+                copy_rows<Lay::kRow>(at + 3 * kR, static_cast<const char *>(a.x) + c, a.x_stride * esz, live_bytes, row0, t0,
+                                     t1, a.x, lane);
+                const char *from = reinterpret_cast<const char *>(a.checkpoints + ((int64_t)(row0 / kTile) * sh.width + c0) * N);
+#pragma unroll
+                for (int k = lane; k < kCols * N / 4; k += 32) {
+                    const bool ok = row0 >= t0 && k * 4 < left * N;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + Lay::kCheck + k * 16),
+                                 "l"(ok ? static_cast<const void *>(from + k * 16) : a.x), "r"(ok ? 16 : 0) : "memory");
+                }
+            }
+            for (int k = tid; k < Lay::kMats * kWords; k += 32 * kWarps) {  // each word by the thread that converts it
+                const int m = k / kWords, i = (k % kWords) / (Lay::kBRow / 16), w = k % (Lay::kBRow / 16), t = row0 + i;
+                const bool ok = t >= t0 && t < t1;
+                const char *from = static_cast<const char *>(m ? a.B : a.C) +
+                                   ((int64_t)t * (m ? a.b_stride : a.c_stride) + (int64_t)g * N) * esz + w * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(cta_at + Lay::kRaw + stage * Lay::kMat + k * 16),
+                             "l"(ok ? static_cast<const void *>(from) : a.x), "r"(ok ? 16 : 0) : "memory");
+            }
+        }
+        copies_commit();
+    };
+
+    const int qd = lane % kQuads, tq = lane / kQuads;
+    const bool quad_live = qd * 4 < left;
+    F2 bias[2], skip[2], d_skip[2] = {both(0.f), both(0.f)}, d_bias[2] = {both(0.f), both(0.f)};
+    load_quad(a.delta_bias, c0 + qd * 4, quad_live, bias);
+    load_quad(FULL ? a.skip : nullptr, c0 + qd * 4, quad_live, skip);
+    F2 steps = both(0.f);
+    float4 *step = reinterpret_cast<float4 *>(smem + Lay::kStep);
+    float *dys = reinterpret_cast<float *>(smem + Lay::kDy);
+    float *cs = reinterpret_cast<float *>(all_smem + Lay::kC), *bs = cs + kTile * N;
+    float *parts = reinterpret_cast<float *>(smem + Lay::kPart);
+    float *sums = reinterpret_cast<float *>(all_smem + Lay::kSums);
+    Edges ed;
+    int stage = 0, turn = 0;
+    const int row_last = (t1 - 1) & ~(kTile - 1);
+    if (t0 < t1) fetch(row_last, 0);
+    for (int row0 = row_last; t0 < t1 && row0 + kTile > t0; row0 -= kTile, stage ^= 1) {
+        fetch(row0 - kTile, stage ^ 1);
+        ed.find(rg, row0, t0, t1, lane);
+        copies_wait<1>();
+        const char *at = smem + stage * Lay::kStage;
+        auto raw = [&](int tensor, int i, F2 (&to)[2]) {
+            Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + (tensor * kTile + i) * Lay::kRow + qd * 4 * esz), to);
+        };
+#pragma unroll
+        for (int k = 0; k < kTile; k += 32 / kQuads) {
+            const int i = k + tq, t = row0 + i;
+            F2 x[2] = {both(0.f), both(0.f)}, d[2], dy[2];
+            raw(0, i, d);
+            raw(1, i, dy);
+            if constexpr (FULL) raw(3, i, x);
+            if (a.gate) {
+                F2 z[2];
+                raw(2, i, z);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) dy[p] = mul2(dy[p], mul2(z[p], sigmoid2<T>(z[p])));
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                d[p] = softplus2(add2(d[p], bias[p]));
+                if (t < t0 || t >= t1) d[p] = both(0.f);  // neither decay nor input; dy is 0 there
+                x[p] = mul2(x[p], d[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // banks: every other four lanes the other pair first
+                const bool other = (p ^ (lane >> 2)) & 1;
+                const float2 u = f2_get(other ? d[1] : d[0]), v = f2_get(other ? x[1] : x[0]);
+                step[i * (kCols / 2) + qd * 2 + other] = make_float4(u.x, u.y, v.x, v.y);
+            }
+            const float2 u = f2_get(dy[0]), v = f2_get(dy[1]);
+            *reinterpret_cast<float4 *>(dys + i * kCols + qd * 4) = make_float4(u.x, u.y, v.x, v.y);
+        }
+        for (int k = tid; k < Lay::kMats * kWords; k += 32 * kWarps) {
+            const char *from = all_smem + Lay::kRaw + stage * Lay::kMat + k * 16;
+            float4 *to = reinterpret_cast<float4 *>(cs + k * (16 / esz));
+#pragma unroll
+            for (int q = 0; q < 4 / esz; ++q) {
+                F2 f[2];
+                Quad<T>::unpack(reinterpret_cast<const Raw *>(from)[q], f);
+                const float2 u = f2_get(f[0]), v = f2_get(f[1]);
+                to[q] = make_float4(u.x, u.y, v.x, v.y);
+            }
+        }
+        __syncthreads();  // B and C; they are written again behind the last barrier of this tile
+        auto row_of = [&](const float *m, int i, int s, F2 (&to)[P]) {  // this thread's states of B or C
+            read_pairs(m + i * N + s * kL * NT + j * NT, to);
+        };
+        if constexpr (!FULL) {
+            for (int s = 0; s < SL; ++s) {
+                recall(s);
+                auto token = [&](int i) {
+                    const float4 d = step[i * (kCols / 2) + cl];
+                    const float2 dy = *reinterpret_cast<const float2 *>(dys + i * kCols + 2 * cl);
+                    F2 C[P];
+                    row_of(cs, i, s, C);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        F2 dec[P];
+                        decays(both(c ? d.y : d.x), c, dec);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) e[c][k] = mul2(dec[k], fma2(C[k], both(c ? dy.y : dy.x), e[c][k]));
+                    }
+                    if (s == 0) steps = add2(steps, f2(d.x, d.y));
+                };
+                if (ed.ends == 0) {
+#pragma unroll 4
+                    for (int i = kTile - 1; i >= 0; --i) token(i);
+                } else {
+                    for (int i = kTile - 1; i >= 0; --i) {
+                        if ((ed.ends >> i) & 1u) get(a.d_final, __shfl_sync(0xffffffffu, ed.seq, i), s, e);
+                        token(i);
+                    }
+                }
+                keep(s);
+            }
+            __syncthreads();
+        } else {
+            // sums over states of the half's tokens, and what follows from them
+            auto epilogue = [&](int from) {
+                __syncwarp();
+                const int i = from + tq, t = row0 + i;
+                F2 sum[3][2];
+#pragma unroll
+                for (int m = 0; m < 3; ++m) {
+                    sum[m][0] = sum[m][1] = both(0.f);
+#pragma unroll
+                    for (int l = 0; l < kL; ++l) {  // banks: see where they are left
+                        const float4 u = *reinterpret_cast<const float4 *>(parts + ((m * kSpan + tq) * kL + (l ^ (tq & 1))) * kCols +
+                                                                         qd * 4);
+                        sum[m][0] = add2(sum[m][0], f2(u.x, u.y));
+                        sum[m][1] = add2(sum[m][1], f2(u.z, u.w));
+                    }
+                }
+                F2 x[2], v[2], d_out[2], dx[2], dd[2], dz[2];
+                raw(0, i, v);
+                raw(1, i, d_out);
+                raw(3, i, x);
+                const float4 dyv = *reinterpret_cast<const float4 *>(dys + i * kCols + qd * 4);
+                const F2 dy[2] = {f2(dyv.x, dyv.y), f2(dyv.z, dyv.w)};
+                const float4 s0 = step[i * (kCols / 2) + qd * 2], s1 = step[i * (kCols / 2) + qd * 2 + 1];
+                const F2 d[2] = {f2(s0.x, s0.y), f2(s1.x, s1.y)};
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    dx[p] = fma2(skip[p], dy[p], mul2(d[p], sum[1][p]));
+                    // sum A g a h came with A log2 e; softplus' = 1 / (1 + exp(-v))
+                    dd[p] = mul2(fma2(x[p], sum[1][p], mul2(sum[2][p], both(0.693147181f))),
+                                 sigmoid2<float>(add2(v[p], bias[p])));
+                    sum[0][p] = fma2(skip[p], x[p], sum[0][p]);
+                }
+                const bool in = t >= t0 && t < t1 && quad_live;
+                const int64_t to = (int64_t)t * sh.width + c0 + qd * 4;
+                if (a.gate) {
+                    F2 z[2];
+                    raw(2, i, z);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {  // silu' = s (1 + z (1 - s))
+                        const F2 s = sigmoid2<T>(z[p]);
+                        dz[p] = mul2(mul2(d_out[p], sum[0][p]), mul2(s, fma2(z[p], fma2(s, both(-1.f), both(1.f)), both(1.f))));
+                    }
+                    if (in) *reinterpret_cast<Raw *>(static_cast<T *>(a.d_gate) + to) = Quad<T>::pack(dz);
+                }
+                if (in) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        d_skip[p] = fma2(dy[p], x[p], d_skip[p]);
+                        d_bias[p] = add2(d_bias[p], dd[p]);
+                    }
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.dx) + to) = Quad<T>::pack(dx);
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.d_delta) + to) = Quad<T>::pack(dd);
+                }
+                __syncwarp();
+            };
+            // The four warps' sums over channels of a half: each warp adds up a quarter of its tokens.
+            auto reduce = [&](int from, int s) {
+                __syncthreads();
+                constexpr int kValues = 2 * kL * NT;
+                const float *src = sums + turn * kWarps * kSpan * 32;
+#pragma unroll
+                for (int k = 0; k < kSpan / kWarps; ++k) {
+                    const int i = warp * (kSpan / kWarps) + k, t = row0 + from + i;
+                    float v = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) v += src[(w * kSpan + i) * 32 + lane];
+                    // lane: dB (the first half of the values), then dC
+                    if (lane < kValues && t >= t0 && t < t1)
+                        wk.tokens[(((int64_t)part * a.total_tokens + t) * sh.groups + g) * 2 * N + lane / (kValues / 2) * N +
+                                  s * kL * NT + lane % (kValues / 2)] = v;
+                }
+                turn ^= 1;
+            };
+            auto half = [&](auto edges, int from, int s) {
+                constexpr bool EDGES = decltype(edges)::value;
+                recall(s);
+                const float *ck = reinterpret_cast<const float *>(at + Lay::kCheck);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) read_pairs(ck + (2 * cl + c) * N + s * kL * NT + j * NT, h[c]);
+                auto forward = [&](int i) {
+                    const float4 d = step[i * (kCols / 2) + cl];
+                    F2 B[P];
+                    row_of(bs, i, s, B);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        F2 dec[P];
+                        decays(both(c ? d.y : d.x), c, dec);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) h[c][k] = fma2(dec[k], h[c][k], mul2(both(c ? d.w : d.z), B[k]));
+                    }
+                };
+                if (from) {  // to the middle of the tile
+#pragma unroll 4
+                    for (int i = 0; i < kSpan; ++i) {
+                        if (EDGES && ((ed.starts >> i) & 1u)) get(a.init, __shfl_sync(0xffffffffu, ed.seq, i), s, h);
+                        forward(i);
+                    }
+                }
+                F2 before[kSpan][2][P];
+#pragma unroll
+                for (int b = 0; b < kSpan; ++b) {
+                    const int i = from + b;
+                    if (EDGES && ((ed.starts >> i) & 1u)) get(a.init, __shfl_sync(0xffffffffu, ed.seq, i), s, h);
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                        for (int k = 0; k < P; ++k) before[b][c][k] = h[c][k];
+                    if (b + 1 < kSpan) forward(i);
+                }
+#pragma unroll
+                for (int b = kSpan - 1; b >= 0; --b) {
+                    const int i = from + b;
+                    if (EDGES && ((ed.ends >> i) & 1u)) get(a.d_final, __shfl_sync(0xffffffffu, ed.seq, i), s, e);
+                    const float4 d = step[i * (kCols / 2) + cl];
+                    const float2 dy = *reinterpret_cast<const float2 *>(dys + i * kCols + 2 * cl);
+                    F2 B[P], C[P], dB[P], dC[P];
+                    row_of(bs, i, s, B);
+                    row_of(cs, i, s, C);
+                    float2 part3[3];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const F2 dc = both(c ? d.y : d.x), xc = both(c ? d.w : d.z), yc = both(c ? dy.y : dy.x);
+                        F2 dec[P], y = both(0.f), Bg = both(0.f), Aw = both(0.f);
+                        decays(dc, c, dec);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) {
+                            const F2 u = mul2(dec[k], before[b][c][k]);
+                            const F2 now = fma2(xc, B[k], u);
+                            y = fma2(C[k], now, y);
+                            const F2 gr = fma2(C[k], yc, e[c][k]);
+                            e[c][k] = mul2(dec[k], gr);
+                            const F2 w = mul2(gr, u);
+                            Bg = fma2(B[k], gr, Bg);
+                            Aw = fma2(A[c][k], w, Aw);
+                            dA[c][k] = fma2(dc, w, dA[c][k]);
+                            dB[k] = c ? fma2(gr, xc, dB[k]) : mul2(gr, xc);
+                            dC[k] = c ? fma2(yc, now, dC[k]) : mul2(yc, now);
+                        }
+                        const float2 f0 = f2_get(y), f1 = f2_get(Bg), f2v = f2_get(Aw);
+                        (c ? part3[0].y : part3[0].x) = f0.x + f0.y;
+                        (c ? part3[1].y : part3[1].x) = f1.x + f1.y;
+                        (c ? part3[2].y : part3[2].x) = f2v.x + f2v.y;
+                    }
+#pragma unroll
+                    for (int m = 0; m < 3; ++m) {
+                        // banks: an epilogue's eight lanes read two tokens, so odd tokens have neighbouring lanes' parts swapped
+                        float2 *to = reinterpret_cast<float2 *>(parts + ((m * kSpan + b) * kL + (j ^ (b & 1))) * kCols + 2 * cl);
+                        if (SL > 1 && s) part3[m].x += to->x, part3[m].y += to->y;
+                        *to = part3[m];
+                    }
+                    // over the eight pairs: lane keeps dB or dC (bit 2) of one of its NT states (bits 1 and 0)
+                    float v[NT];
+                    const bool k2 = lane & 4, k1 = lane & 2, k0 = lane & 1;
+#pragma unroll
+                    for (int k = 0; k < P; ++k) {
+                        const float2 fb = f2_get(dB[k]), fc = f2_get(dC[k]);
+                        v[2 * k] = (k2 ? fc.x : fb.x) + __shfl_xor_sync(0xffffffffu, k2 ? fb.x : fc.x, 4);
+                        v[2 * k + 1] = (k2 ? fc.y : fb.y) + __shfl_xor_sync(0xffffffffu, k2 ? fb.y : fc.y, 4);
+                    }
+                    float one;
+                    int at_value;
+                    if constexpr (NT == 4) {
+                        const float lo = (k1 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, k1 ? v[0] : v[2], 2);
+                        const float hi = (k1 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, k1 ? v[1] : v[3], 2);
+                        one = (k0 ? hi : lo) + __shfl_xor_sync(0xffffffffu, k0 ? lo : hi, 1);
+                        at_value = (lane >> 2 & 1) * kL * NT + j * NT + (lane & 3);
+                    } else {
+                        one = (k1 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, k1 ? v[0] : v[1], 2);
+                        one += __shfl_xor_sync(0xffffffffu, one, 1);
+                        at_value = (lane >> 2 & 1) * kL * NT + j * NT + (lane >> 1 & 1);
+                    }
+                    sums[((turn * kWarps + warp) * kSpan + b) * 32 + at_value] = one;
+                    if (EDGES && ((ed.starts >> i) & 1u)) {
+                        const int q = __shfl_sync(0xffffffffu, ed.seq, i);
+                        if (a.d_init) put(a.d_init, q, s, e);
+                    }
+                }
+                keep(s);
+            };
+#pragma unroll 1
+            for (int from = kTile - kSpan; from >= 0; from -= kSpan) {
+                for (int s = 0; s < SL; ++s) {
+                    if ((ed.starts | ed.ends) == 0)
+                        half(std::false_type{}, from, s);
+                    else
+                        half(std::true_type{}, from, s);
+                    if (SL > 1 && s + 1 < SL) reduce(from, s);
+                }
+                epilogue(from);
+                reduce(from, SL - 1);
+            }
+        }
+    }
+    if constexpr (FULL) {
+        float *w = wk.weights + (int64_t)r * sh.width * (N + 2);
+        for (int s = 0; s < SL; ++s) {
+            recall(s);
+            if (live)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int k = 0; k < P; ++k)
+                        *reinterpret_cast<float2 *>(w + (int64_t)(pair + c) * (N + 2) + s * kL * NT + j * NT + 2 * k) = f2_get(dA[c][k]);
+        }
+        // the vectors' sums over the tokens of the eight lanes of a quad
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float2 u = f2_get(d_skip[p]), v = f2_get(d_bias[p]);
+#pragma unroll
+            for (int o = kQuads; o < 32; o <<= 1) {
+                u.x += __shfl_xor_sync(0xffffffffu, u.x, o), u.y += __shfl_xor_sync(0xffffffffu, u.y, o);
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
+            if (tq == 0 && quad_live) {
+                float *to = w + (int64_t)(c0 + qd * 4 + 2 * p) * (N + 2) + N;
+                to[0] = u.x, to[1] = v.x, to[N + 2] = u.y, to[N + 3] = v.y;
+            }
+        }
+    } else {
+        for (int s = 0; s < SL; ++s) {
+            recall(s);
+            put(wk.q, r, s, e);
+        }
+        if (j == 0 && live) *reinterpret_cast<float2 *>(wk.steps + (int64_t)r * sh.width + pair) = f2_get(steps);
+    }
+}
+
+// dB and dC from the CTAs' rows, four states per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) selective_tokens_kernel(SelectiveArgs a, int groups, int N, const float *sums, int parts) {
+    const int row = groups * N / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / row;
+    if (t >= clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens)) return;
+    const int at = (int)(i - t * row) * 4, g = at / N, n = at % N;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int p = 0; p < parts; ++p) {
+            const float4 v = *reinterpret_cast<const float4 *>(sums + (((int64_t)p * a.total_tokens + t) * groups + g) * 2 * N + m * N + n);
+            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+        }
+        const F2 f[2] = {f2(s.x, s.y), f2(s.z, s.w)};
+        *reinterpret_cast<typename Quad<T>::Raw *>(static_cast<T *>(m ? a.d_C : a.d_B) + t * groups * N + at) = Quad<T>::pack(f);
+    }
+}
+
+// The weights' gradients from the ranges' sums.
+__global__ void __launch_bounds__(128) selective_weights_kernel(SelectiveArgs a, int width, int N, const float *sums, int ranges) {
+    const int i = blockIdx.x * 128 + threadIdx.x, c = i / (N + 2), n = i % (N + 2);
+    if (c >= width) return;
+    float s = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < ranges; ++r) s += sums[(int64_t)r * width * (N + 2) + i];
+    if (n < N)
+        a.d_A[(int64_t)c * N + n] = s;
+    else if (n == N && a.d_skip)
+        a.d_skip[c] = s;
+    else if (n == N + 1 && a.d_delta_bias)
+        a.d_delta_bias[c] = s;
+}
+
+// The workspace: what ranges hand on, the tokens' rows, the ranges' weights.
+size_t carve(const sse_selective_config_t &c, const SelectiveShape &s, int64_t T, char *base, BackwardWork &wk) {
+    const size_t N = c.state;
+    size_t at = 0;
+    auto take = [&](size_t floats) {
+        float *p = reinterpret_cast<float *>(base + at);
+        at += (floats * sizeof(float) + 255) & ~size_t(255);
+        return p;
+    };
+    wk.parts = (s.tiles + 3) / 4;  // four warps a CTA
+    wk.weights = take((size_t)s.ranges * c.width * (N + 2));
+    wk.tokens = take((size_t)wk.parts * T * c.groups * 2 * N);
+    wk.q = wk.steps = nullptr;
+    if (s.ranges > 1) {
+        wk.q = take((size_t)s.ranges * c.width * N);
+        wk.steps = take((size_t)s.ranges * c.width);
+    }
+    return at;
+}
+
+template <typename T, int N> cudaError_t launch_t(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
+    const SelectiveShape sh = selective_shape(c, kCols, a.total_tokens);
+    BackwardWork wk;
+    carve(c, sh, a.total_tokens, a.workspace, wk);
+    const auto states = selective_backward_kernel<T, N, false>, full = selective_backward_kernel<T, N, true>;
+    constexpr int kStates = Layout<T, N, false>::kBytes, kFull = Layout<T, N, true>::kBytes;
+    static_assert(Layout<T, N, true>::kWarps == 4 && kStates <= 48 * 1024 && kFull <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
+    if (e != cudaSuccess) return e;
+    if (sh.ranges > 1) states<<<dim3(sh.tiles * c.groups, sh.ranges), 32, kStates, s>>>(a, sh, wk);
+    full<<<dim3(wk.parts * c.groups, sh.ranges), 32 * Layout<T, N, true>::kWarps, kFull, s>>>(a, sh, wk);
+    const int64_t rows = (int64_t)a.total_tokens * c.groups * N / 4;
+    if (rows > 0)
+        selective_tokens_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a, c.groups, N, wk.tokens, wk.parts);
+    selective_weights_kernel<<<(c.width * (N + 2) + 127) / 128, 128, 0, s>>>(a, c.width, N, wk.weights, sh.ranges);
+    return cudaGetLastError();
+}
+
+template <typename T> cudaError_t launch_state(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
+    switch (c.state) {
+    case 8: return launch_t<T, 8>(c, a, s);
+    case 16: return launch_t<T, 16>(c, a, s);
+    case 32: return launch_t<T, 32>(c, a, s);
+    default: return launch_t<T, 64>(c, a, s);
+    }
+}
+
+}  // namespace
+
+size_t selective_backward_workspace(const sse_selective_config_t &c, int64_t T, int32_t) {
+    BackwardWork wk;
+    return carve(c, selective_shape(c, kCols, T), T, nullptr, wk);
+}
+cudaError_t launch_selective_backward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {
+    return cfg.dtype == SSE_BF16 ? launch_state<__nv_bfloat16>(cfg, a, stream) : launch_state<float>(cfg, a, stream);
+}
+
+}  // namespace sse
