@@ -35,7 +35,32 @@ template <> struct Quad<float> {
     static __device__ __forceinline__ Raw zero() { return make_uint4(0, 0, 0, 0); }
 };
 
+// One column of two rows, as a pair over the rows.
+template <typename T> struct Two;
+template <> struct Two<__nv_bfloat16> {
+    using Raw = uint16_t;
+    static __device__ __forceinline__ F2 unpack(Raw a, Raw b) { return f2_bits((uint32_t)a << 16, (uint32_t)b << 16); }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *a, __nv_bfloat16 *b, F2 v, bool first, bool second) {
+        const uint32_t w = Quad<__nv_bfloat16>::two(v);
+        if (first) *reinterpret_cast<uint16_t *>(a) = (uint16_t)w;
+        if (second) *reinterpret_cast<uint16_t *>(b) = (uint16_t)(w >> 16);
+    }
+};
+template <> struct Two<float> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ F2 unpack(Raw a, Raw b) { return f2_bits(a, b); }
+    static __device__ __forceinline__ void store(float *a, float *b, F2 v, bool first, bool second) {
+        const float2 f = f2_get(v);
+        if (first) *a = f.x;
+        if (second) *b = f.y;
+    }
+};
+
 __device__ __forceinline__ F2 both(float x) { return f2(x, x); }
+__device__ __forceinline__ float fold(F2 v) {
+    const float2 f = f2_get(v);
+    return f.x + f.y;
+}
 __device__ __forceinline__ float ex2_ftz(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

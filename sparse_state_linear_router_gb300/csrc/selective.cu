@@ -7,13 +7,13 @@
 //   dD = x sum_n B g + sum_n A g a h_{t-1},  d_delta = dD softplus'
 //   dB[n] = sum_c g D x,  dC[n] = sum_c dy h  (over the channels of the group)
 //   dA = sum_t D g a h_{t-1},  d_skip = sum_t dy x,  d_delta_bias = sum_t d_delta
+#include <type_traits>
+
 #include "selective.cuh"
 
 namespace sse {
 namespace {
 
-// Lanes of a pair of channels, and at most so many states each.
-constexpr int kL = 4, kNT = 4;
 
 
 template <typename T> __device__ __forceinline__ float load(const void *p, int64_t i) {
@@ -55,58 +55,62 @@ __device__ __forceinline__ Token token(const SelectiveArgs &a, int64_t t, int c,
 }
 
 // ---------------------------------------------------------------------------
-// Forward.  A warp is a CTA; it has 16 channels of a group and one range of
-// tokens, which it goes through in tiles of 16.  L = 4 lanes share a pair of
-// channels, NT states each (lane = j * 8 + pair); SL slices of 4 NT states.
-// Per tile:
-//   1. steps D and D x, B and C in float32 to shared memory (16 bytes per pair
-//      of channels: D0, D1, D x0, D x1), lanes over (token, four channels);
-//   2. token by token, h = 2^(D A log2 e) h + (D x) B and this thread's part of
-//      sum C h, its states in registers;
-//   3. the parts' sum, skip and gate, lanes over (token, four channels) again.
-// FULL: the whole forward.  Otherwise only what a later range starts from: the
-// state at the range's end from nothing (or from the sequence that begins in
+// Forward.  A warp is a CTA; it has 32 channels of a group, one to a lane with
+// its states in registers (two slices of 32 where there are 64), and one range of
+// tokens, which it goes through four tokens at a time.  Rows come to shared memory
+// by asynchronous copies two tiles of 16 tokens ahead; B and C are turned to
+// float32 there, and every lane reads the same 16 bytes.  The next four tokens'
+// steps (pairs over the tokens) are made beside these four's states (pairs over
+// the states), in one stretch of code without branches.
+// kStates makes only what a later range starts from: the state at the range's end from nothing (or from the sequence that begins in
 // it), and the sum of its steps, exp(A sum D) being the decay over the range.
 // ---------------------------------------------------------------------------
-template <typename T, int N, int L, bool FULL> struct Layout {
-    static constexpr int kCols = 64 / L;
+constexpr int kCols = 32;  // channels of a warp
+constexpr int kAlone = 2000;  // warps that sequences make by themselves, for a range each
+constexpr int kBlock = 4;  // tokens at a time
+
+// What a kernel does: the states that later ranges start from, the forward without and with a gate.
+enum { kStates, kPlain, kGated };
+
+template <typename T, int N, int MODE> struct Layout {
+    static constexpr int NT = N < 32 ? N : 32, SL = N / NT;
     static constexpr int kRow = kCols * sizeof(T), kBRow = N * sizeof(T);
-    static constexpr int kTensors = FULL ? 3 : 2, kMats = FULL ? 2 : 1;
-    static constexpr int kStage = kTile * (kTensors * kRow + kMats * kBRow);
-    static constexpr int kStep = 2 * kStage;                      // float4 [16][kCols / 2]
-    static constexpr int kB = kStep + kTile * kCols / 2 * 16;     // float [16][N], then C
-    static constexpr int kY = kB + kMats * kTile * N * 4;         // float [16][kYRow]
-    static constexpr int kYRow = 64 + (kCols < 32 ? kCols : 0);   // floats: [L][kCols], padded for the banks
-    static constexpr int kH = kY + (FULL ? kTile * kYRow * 4 : 0);  // slices: float4 [SL][2][32]
-    static constexpr int kBytes = kH + (N > 16 ? N * 64 : 0);
+    static constexpr int kTensors = MODE == kGated ? 3 : 2, kMats = MODE == kStates ? 1 : 2;
+    static constexpr int kX = 0, kD = kTile * kRow, kZ = 2 * kD;  // a stage: x, delta, gate; B and C
+    static constexpr int kMat = kTensors * kD;
+    static constexpr int kStage = kMat + kMats * kTile * kBRow;
+    static constexpr int kB = 3 * kStage;                     // float [16][N]: B, then C
+    static constexpr int kKept = kB + kMats * kTile * N * 4;  // slices: states and A log2 e, float4 [SL][2][NT / 4][32]
+    static constexpr int kBytes = kKept + (SL > 1 ? SL * 2 * NT * 128 : 0);
 };
 
 struct ForwardWork {  // what ranges hand on
     float *q, *steps;  // [ranges][width][N], [ranges][width]
 };
 
-template <typename T, int NT, int L, int SL, bool FULL>
-__global__ void __launch_bounds__(32) selective_forward_kernel(SelectiveArgs a, SelectiveShape sh, ForwardWork wk) {
-    constexpr int N = L * NT * SL, P = NT / 2;
-    using Lay = Layout<T, N, L, FULL>;
-    constexpr int kCols = Lay::kCols, kQuads = kCols / 4;
-    using Raw = typename Quad<T>::Raw;
+template <typename T, int N, int MODE>
+__global__ void __launch_bounds__(32, 1) selective_forward_kernel(SelectiveArgs a, SelectiveShape sh, ForwardWork wk) {
+    using Lay = Layout<T, N, MODE>;
+    using Raw = typename Two<T>::Raw;
+    constexpr bool FULL = MODE != kStates;
+    constexpr int NT = Lay::NT, SL = Lay::SL, P = NT / 2;
     extern __shared__ __align__(16) char smem[];
-    const int lane = threadIdx.x, j = lane / (32 / L), cl = lane % (32 / L), r = blockIdx.y;
+    const int lane = threadIdx.x, r = blockIdx.y;
     const Columns cols(sh, blockIdx.x, kCols);
     const Ranges rg(a, sh.ranges);
     int t0 = rg.start(r);
     const int t1 = rg.start(r + 1);
-    const int pair = cols.c0 + 2 * cl;
-    const bool live = 2 * cl < cols.left;
-    const int64_t states = (int64_t)pair * N + j * NT;  // this thread's first state of its first channel, slice 0
+    const bool live = lane < cols.left;
+    const int ch = cols.c0 + (live ? lane : 0);
+    const int64_t states = (int64_t)ch * N;  // this thread's first state
     if constexpr (FULL) {
         if (a.final_state)  // empty sequences keep their state
             for (int q = r; q < a.num_seqs; q += sh.ranges)
                 if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1) && live)
-                    for (int i = j; i < 2 * N; i += L) {
-                        const int64_t at = ((int64_t)q * sh.width + pair) * N + i;
-                        a.final_state[at] = a.init ? a.init[at] : 0.f;
+                    for (int i = 0; i < N; i += 4) {
+                        const int64_t at = (int64_t)q * sh.width * N + states + i;
+                        *reinterpret_cast<float4 *>(a.final_state + at) =
+                            a.init ? *reinterpret_cast<const float4 *>(a.init + at) : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
     } else {
         const int from = rg.origin(t1);
@@ -116,246 +120,217 @@ __global__ void __launch_bounds__(32) selective_forward_kernel(SelectiveArgs a, 
     if (t0 >= t1) return;
     const int origin = rg.origin(t0);
 
-    F2 hs[2][P], As[2][P];  // the states at hand, and A log2 e
+    F2 h[P], A[P];  // of the slice at hand; A log2 e
     auto load_A = [&](int s) {
+        read_pairs(a.A + states + s * NT, A);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            no_pairs(As[c]);
-            if (live) read_pairs(a.A + states + (int64_t)c * N + s * L * NT, As[c]);
-#pragma unroll
-            for (int k = 0; k < P; ++k) As[c][k] = mul2(As[c][k], both(kLog2e));
-        }
+        for (int k = 0; k < P; ++k) A[k] = mul2(A[k], both(live ? kLog2e : 0.f));
     };
     // this thread's states in an array of [.., width, N] at row i
     auto get = [&](const float *p, int64_t i, int s) {
+        if (p) {
+            read_pairs(p + i * sh.width * N + states + s * NT, h);
+        } else {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            no_pairs(hs[c]);
-            if (p && live) read_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * L * NT, hs[c]);
+            for (int k = 0; k < P; ++k) h[k] = both(0.f);
         }
     };
     auto put = [&](float *p, int64_t i, int s) {
-        if (live)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) write_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * L * NT, hs[c]);
+        if (live) write_pairs(p + i * sh.width * N + states + s * NT, h);
     };
-    // a slice's states between tiles: registers with one slice, else shared memory (4 NT bytes of a thread, then the next's)
-    float *kept = reinterpret_cast<float *>(smem + Lay::kH) + lane * 4;
-    auto keep = [&](int s) {
-        if constexpr (SL > 1) {
-            static_assert(NT == 4, "a word per channel");
+    // a slice between blocks: registers with one slice, else shared memory
+    float *kept = reinterpret_cast<float *>(smem + Lay::kKept) + lane * 4;
+    auto keep = [&](int s, int which, const F2 (&f)[P]) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) write_pairs(kept + (s * 2 + c) * 128, hs[c]);
+        for (int k = 0; k < P; k += 2) {
+            const F2 two[2] = {f[k], f[k + 1]};
+            write_quad(kept + ((s * 2 + which) * (NT / 4) + k / 2) * 128, two);
         }
     };
-    auto recall = [&](int s) {
-        if constexpr (SL > 1) {
+    auto recall = [&](int s, int which, F2 (&f)[P]) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) read_pairs(kept + (s * 2 + c) * 128, hs[c]);
-            load_A(s);
+        for (int k = 0; k < P; k += 2) {
+            F2 two[2];
+            read_quad(kept + ((s * 2 + which) * (NT / 4) + k / 2) * 128, two);
+            f[k] = two[0], f[k + 1] = two[1];
         }
     };
 
     // the states that the range starts from
-    if constexpr (FULL) {
-        if (origin < t0) {
-            int r0 = r - 1;  // the range that the sequence begins in
-            for (int i = r - 1; i > 0; i -= 32) {
-                const uint32_t m = __ballot_sync(0xffffffffu, i - lane > 0 && rg.start(i - lane) > origin);
-                r0 -= __popc(m);
-                if (m != 0xffffffffu) break;
-            }
-            for (int s = 0; s < SL; ++s) {
-                load_A(s);
-                get(wk.q, r0, s);
-                for (int i = r0 + 1; i < r; ++i) {
-                    F2 now[2][P];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int k = 0; k < P; ++k) now[c][k] = hs[c][k];
-                    get(wk.q, i, s);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const F2 d = both(live ? wk.steps[(int64_t)i * sh.width + pair + c] : 0.f);
-#pragma unroll
-                        for (int k = 0; k < P; ++k) hs[c][k] = fma2(ex2_ftz(mul2(d, As[c][k])), now[c][k], hs[c][k]);
-                    }
-                }
-                keep(s);
-            }
-        } else {
-            get(nullptr, 0, 0);
-            for (int s = 0; s < SL; ++s) keep(s);
+    int r0 = r;  // the range that the sequence at its start begins in
+    if (FULL && origin < t0) {
+        r0 = r - 1;
+        for (int i = r - 1; i > 0; i -= 32) {
+            const uint32_t m = __ballot_sync(0xffffffffu, i - lane > 0 && rg.start(i - lane) > origin);
+            r0 -= __popc(m);
+            if (m != 0xffffffffu) break;
         }
-    } else {
-        get(nullptr, 0, 0);
-        for (int s = 0; s < SL; ++s) keep(s);
     }
-    if constexpr (SL == 1) load_A(0);
+    for (int s = 0; s < SL; ++s) {
+        load_A(s);
+        get(r0 < r ? wk.q : nullptr, r0, s);
+        for (int i = r0 + 1; i < r; ++i) {
+            F2 now[P];
+            const F2 d = both(wk.steps[(int64_t)i * sh.width + ch]);
+#pragma unroll
+            for (int k = 0; k < P; ++k) now[k] = h[k];
+            get(wk.q, i, s);
+#pragma unroll
+            for (int k = 0; k < P; ++k) h[k] = fma2(ex2_ftz(mul2(d, A[k])), now[k], h[k]);
+        }
+        if constexpr (SL > 1) {
+            keep(s, 0, h);
+            keep(s, 1, A);
+        }
+    }
 
-    const int row_first = t0 & ~(kTile - 1);
+    // A tile's rows, two tiles ahead.  Rows outside the range and channels past the group's end are zeros.
     const int esz = (int)sizeof(T), live_bytes = cols.left * esz;
     const uint32_t smem_at = (uint32_t)__cvta_generic_to_shared(smem);
+    float *bs = reinterpret_cast<float *>(smem + Lay::kB), *cs = bs + kTile * N;
     auto fetch = [&](int row0, int stage) {
         if (row0 < t1) {
             const uint32_t at = smem_at + stage * Lay::kStage;
             const int64_t c = (int64_t)cols.c0 * esz, n = (int64_t)cols.g * N * esz;
-            copy_rows<Lay::kRow>(at, static_cast<const char *>(a.x) + c, a.x_stride * esz, live_bytes, row0, t0, t1, a.x, lane);
-            copy_rows<Lay::kRow>(at + kTile * Lay::kRow, static_cast<const char *>(a.delta) + c, a.delta_stride * esz, live_bytes,
-                                 row0, t0, t1, a.x, lane);
-            const uint32_t mats = at + kTile * Lay::kTensors * Lay::kRow;
-            copy_rows<Lay::kBRow>(mats, static_cast<const char *>(a.B) + n, a.b_stride * esz, Lay::kBRow, row0, t0, t1, a.x, lane);
-            if constexpr (FULL) {
-                if (a.gate)
-                    copy_rows<Lay::kRow>(at + 2 * kTile * Lay::kRow, static_cast<const char *>(a.gate) + c, a.gate_stride * esz,
-                                         live_bytes, row0, t0, t1, a.x, lane);
-                copy_rows<Lay::kBRow>(mats + kTile * Lay::kBRow, static_cast<const char *>(a.C) + n, a.c_stride * esz,
-                                      Lay::kBRow, row0, t0, t1, a.x, lane);
-            }
+            copy_rows<Lay::kRow>(at + Lay::kX, static_cast<const char *>(a.x) + c, a.x_stride * esz, live_bytes, row0, t0, t1,
+                                 a.x, lane);
+            copy_rows<Lay::kRow>(at + Lay::kD, static_cast<const char *>(a.delta) + c, a.delta_stride * esz, live_bytes, row0,
+                                 t0, t1, a.x, lane);
+            if constexpr (MODE == kGated)
+                copy_rows<Lay::kRow>(at + Lay::kZ, static_cast<const char *>(a.gate) + c, a.gate_stride * esz, live_bytes, row0,
+                                     t0, t1, a.x, lane);
+            copy_rows<Lay::kBRow>(at + Lay::kMat, static_cast<const char *>(a.B) + n, a.b_stride * esz, Lay::kBRow, row0, t0,
+                                  t1, a.x, lane);
+            if constexpr (FULL)
+                copy_rows<Lay::kBRow>(at + Lay::kMat + kTile * Lay::kBRow, static_cast<const char *>(a.C) + n,
+                                      a.c_stride * esz, Lay::kBRow, row0, t0, t1, a.x, lane);
         }
         copies_commit();
     };
-
-    // parts 1 and 3: lane has four channels of every fourth token
-    const int qd = lane % kQuads, tq = lane / kQuads;
-    const bool quad_live = qd * 4 < cols.left;
-    F2 bias[2], skip[2];
-    load_quad(a.delta_bias, cols.c0 + qd * 4, quad_live, bias);
-    load_quad(FULL ? a.skip : nullptr, cols.c0 + qd * 4, quad_live, skip);
-    F2 steps = both(0.f);  // sums of this thread's channels' steps
-    float4 *step = reinterpret_cast<float4 *>(smem + Lay::kStep);
-    float *bs = reinterpret_cast<float *>(smem + Lay::kB), *cs = bs + kTile * N;
-    float *ys = reinterpret_cast<float *>(smem + Lay::kY);
-    Edges ed;
-    fetch(row_first, 0);
-    int stage = 0;
-    for (int row0 = row_first; row0 < t1; row0 += kTile, stage ^= 1) {
-        fetch(row0 + kTile, stage ^ 1);
-        ed.find(rg, row0, t0, t1, lane);
-        copies_wait<1>();
-        const char *at = smem + stage * Lay::kStage;
+    const float bias = a.delta_bias ? a.delta_bias[ch] : 0.f, skip = FULL && a.skip ? a.skip[ch] : 0.f;
+    // This channel's values of tokens i and i + 1 of a tile, as a pair.
+    auto two = [&](const char *stage, int tensor, int i) {
+        const Raw *at = reinterpret_cast<const Raw *>(stage + tensor) + lane;
+        return Two<T>::unpack(at[i * kCols], at[(i + 1) * kCols]);
+    };
+    struct Steps {
+        F2 d[kBlock / 2], dx[kBlock / 2];  // D and D x, pairs over the tokens
+    };
+    auto steps_of = [&](const char *stage, int i, int row, bool whole) {
+        Steps s;
+        F2 none;
 #pragma unroll
-        for (int k = 0; k < kTile; k += 32 / kQuads) {
-            const int i = k + tq, t = row0 + i;
-            F2 x[2], d[2];
-            Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + i * Lay::kRow + qd * 4 * esz), x);
-            Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + (kTile + i) * Lay::kRow + qd * 4 * esz), d);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                d[p] = softplus2(add2(d[p], bias[p]));
-                if (t < t0 || t >= t1) d[p] = both(0.f);  // neither decay nor input
-                x[p] = mul2(x[p], d[p]);
+        for (int u = 0; u < kBlock; u += 2) {
+            F2 d = softplus2<false>(add2(two(stage, Lay::kD, i + u), both(bias)), none);
+            if (!whole) {  // rows outside: neither decay nor input (their x is 0)
+                const float2 f = f2_get(d);
+                d = f2(row + u >= t0 && row + u < t1 ? f.x : 0.f, row + u + 1 >= t0 && row + u + 1 < t1 ? f.y : 0.f);
             }
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {  // banks: every other four lanes the other pair first
-                const bool other = (p ^ (lane >> 2)) & 1;
-                const float2 u = f2_get(other ? d[1] : d[0]), v = f2_get(other ? x[1] : x[0]);
-                step[i * (kCols / 2) + qd * 2 + other] = make_float4(u.x, u.y, v.x, v.y);
-            }
+            s.d[u / 2] = d;
+            s.dx[u / 2] = mul2(d, two(stage, Lay::kX, i + u));
         }
-        {
-            const char *mats = at + kTile * Lay::kTensors * Lay::kRow;
+        return s;
+    };
+
+    F2 steps = both(0.f);  // sums of this channel's steps
+    Edges ed;
+    const int first = t0 & ~(kBlock - 1), tile_first = first & ~(kTile - 1);
+    fetch(tile_first, 0);
+    fetch(tile_first + kTile, 1);
+    copies_wait<1>();
+    const char *here = smem, *ahead = smem + Lay::kStage;  // this tile's stage and the next one's
+    int free_stage = 2;
+    Steps st = steps_of(here, first - tile_first, first, false);
+    for (int tile = tile_first; tile < t1; tile += kTile) {
+        ed.find(rg, tile, t0, t1, lane);
+        fetch(tile + 2 * kTile, free_stage);
+        copies_wait<1>();  // the next tile is there, and the tile before has been read
+        const typename Quad<T>::Raw *mats = reinterpret_cast<const typename Quad<T>::Raw *>(here + Lay::kMat);
 #pragma unroll
-            for (int k = lane; k < Lay::kMats * kTile * N / 4; k += 32) {
-                F2 f[2];
-                Quad<T>::unpack(*reinterpret_cast<const Raw *>(mats + k * 4 * esz), f);
-                const float2 u = f2_get(f[0]), v = f2_get(f[1]);
-                *reinterpret_cast<float4 *>(bs + k * 4) = make_float4(u.x, u.y, v.x, v.y);
-            }
+        for (int k = lane; k < Lay::kMats * kTile * N / 4; k += 32) {
+            F2 f[2];
+            Quad<T>::unpack(mats[k], f);
+            write_quad(bs + k * 4, f);
         }
         __syncwarp();
-        for (int s = 0; s < SL; ++s) {
-            recall(s);
-            if constexpr (FULL)
-                if (a.checkpoints && row0 >= t0) put(a.checkpoints, row0 / kTile, s);
-            auto token = [&](int i) {  // returns this thread's part of y
-                const float4 d = step[i * (kCols / 2) + cl];
-                const float *bt = bs + i * N + s * L * NT + j * NT, *ct = cs + i * N + s * L * NT + j * NT;
-                F2 B[P], y[2] = {both(0.f), both(0.f)};
-                read_pairs(bt, B);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const F2 dc = both(c ? d.y : d.x), xc = both(c ? d.w : d.z);
-#pragma unroll
-                    for (int k = 0; k < P; ++k)
-                        hs[c][k] = fma2(ex2_ftz(mul2(dc, As[c][k])), hs[c][k], mul2(xc, B[k]));
+        if constexpr (FULL)
+            if (a.checkpoints && tile >= t0)
+                for (int s = 0; s < SL; ++s) {
+                    if constexpr (SL > 1) recall(s, 0, h);
+                    put(a.checkpoints, tile / kTile, s);
                 }
-                if constexpr (FULL) {
-                    F2 C[P];
-                    read_pairs(ct, C);
+        // PLAIN: no sequence begins or ends in the tile, and it and the next block are within the range
+        auto block = [&](auto plain, int i0) {
+            constexpr bool PLAIN = decltype(plain)::value;
+            const int row = tile + i0, i1 = (i0 + kBlock) % kTile;
+            const Steps st_next = steps_of(i1 ? here : ahead, i1, row + kBlock, PLAIN);
+            F2 y[kBlock];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
+            for (int u = 0; u < kBlock; ++u) y[u] = both(0.f);
 #pragma unroll
-                        for (int k = 0; k < P; ++k) y[c] = fma2(hs[c][k], C[k], y[c]);
-                } else if (s == 0) {
-                    steps = add2(steps, f2(d.x, d.y));
+            for (int s = 0; s < SL; ++s) {
+                if constexpr (SL > 1) {
+                    recall(s, 0, h);
+                    recall(s, 1, A);
                 }
-                const float2 u = f2_get(y[0]), v = f2_get(y[1]);
-                return make_float2(u.x + u.y, v.x + v.y);
-            };
-            auto leave = [&](int i, float2 part) {
-                if constexpr (FULL) {
-                    float2 *to = reinterpret_cast<float2 *>(ys + i * Lay::kYRow + j * kCols + cl * 2);
-                    if (SL > 1 && s) part.x += to->x, part.y += to->y;
-                    *to = part;
-                }
-            };
-            if ((ed.starts | ed.ends) == 0) {
-                // four tokens' loads before their stores
-#pragma unroll 1
-                for (int i = 0; i < kTile; i += 4) {
-                    float2 part[4];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) part[u] = token(i + u);
+                for (int u = 0; u < kBlock; ++u) {
+                    const int i = i0 + u;
+                    const int q = PLAIN ? 0 : __shfl_sync(0xffffffffu, ed.seq, i);
+                    if (!PLAIN && ((ed.starts >> i) & 1u)) get(a.init, q, s);
+                    const float2 d = f2_get(st.d[u / 2]), dx = f2_get(st.dx[u / 2]);
+                    const F2 dc = both(u & 1 ? d.y : d.x), xc = both(u & 1 ? dx.y : dx.x);
+                    F2 B[P];
+                    read_pairs(bs + i * N + s * NT, B);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) leave(i + u, part[u]);
-                }
-            } else {
-                for (int i = 0; i < kTile; ++i) {
-                    if ((ed.starts >> i) & 1u) get(a.init, __shfl_sync(0xffffffffu, ed.seq, i), s);
-                    leave(i, token(i));
+                    for (int k = 0; k < P; ++k) h[k] = fma2(ex2_ftz(mul2(dc, A[k])), h[k], mul2(xc, B[k]));
                     if constexpr (FULL) {
-                        const int q = __shfl_sync(0xffffffffu, ed.seq, i);
-                        if (((ed.ends >> i) & 1u) && a.final_state) put(a.final_state, q, s);
+                        F2 C[P];
+                        read_pairs(cs + i * N + s * NT, C);
+#pragma unroll
+                        for (int k = 0; k < P; ++k) y[u] = fma2(h[k], C[k], y[u]);
+                        if constexpr (!PLAIN)
+                            if (((ed.ends >> i) & 1u) && a.final_state) put(a.final_state, q, s);
                     }
                 }
+                if constexpr (SL > 1) keep(s, 0, h);
             }
-            keep(s);
+            if constexpr (FULL) {
+#pragma unroll
+                for (int u = 0; u < kBlock; u += 2) {
+                    F2 o = fma2(both(skip), two(here, Lay::kX, i0 + u), f2(fold(y[u]), fold(y[u + 1])));
+                    if constexpr (MODE == kGated) {
+                        const F2 z = two(here, Lay::kZ, i0 + u);
+                        o = mul2(o, mul2(z, sigmoid2<T>(z)));
+                    }
+                    T *to = static_cast<T *>(a.out) + (int64_t)(row + u) * sh.width + ch;
+                    Two<T>::store(to, to + sh.width, o, live && (PLAIN || (row + u >= t0 && row + u < t1)),
+                                  live && (PLAIN || (row + u + 1 >= t0 && row + u + 1 < t1)));
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kBlock / 2; ++u) steps = add2(steps, st.d[u]);
+            }
+            st = st_next;
+        };
+        if ((ed.starts | ed.ends) == 0 && tile >= t0 && tile + kTile + kBlock <= t1) {
+#pragma unroll 1
+            for (int i = 0; i < kTile; i += kBlock) block(std::true_type{}, i);
+        } else {
+#pragma unroll 1
+            for (int i = max(first - tile, 0); i < kTile && tile + i < t1; i += kBlock) block(std::false_type{}, i);
         }
         __syncwarp();
-        if constexpr (FULL) {
-#pragma unroll
-            for (int k = 0; k < kTile; k += 32 / kQuads) {
-                const int i = k + tq, t = row0 + i;
-                F2 y[2] = {both(0.f), both(0.f)}, x[2];
-#pragma unroll
-                for (int l = 0; l < L; ++l) {
-                    const float4 u = *reinterpret_cast<const float4 *>(ys + i * Lay::kYRow + l * kCols + qd * 4);
-                    y[0] = add2(y[0], f2(u.x, u.y));
-                    y[1] = add2(y[1], f2(u.z, u.w));
-                }
-                Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + i * Lay::kRow + qd * 4 * esz), x);
-                y[0] = fma2(skip[0], x[0], y[0]);
-                y[1] = fma2(skip[1], x[1], y[1]);
-                if (a.gate) {
-                    F2 z[2];
-                    Quad<T>::unpack(*reinterpret_cast<const Raw *>(at + (2 * kTile + i) * Lay::kRow + qd * 4 * esz), z);
-                    y[0] = mul2(y[0], mul2(z[0], sigmoid2<T>(z[0])));
-                    y[1] = mul2(y[1], mul2(z[1], sigmoid2<T>(z[1])));
-                }
-                if (t >= t0 && t < t1 && quad_live)
-                    *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + (int64_t)t * sh.width + cols.c0 + qd * 4) = Quad<T>::pack(y);
-            }
-            __syncwarp();  // the stage is free
-        }
+        free_stage = free_stage == 2 ? 0 : free_stage + 1;
+        here = ahead;
+        ahead = smem + (free_stage == 0 ? 2 : free_stage - 1) * Lay::kStage;
     }
     if constexpr (!FULL) {
         for (int s = 0; s < SL; ++s) {
-            recall(s);
+            if constexpr (SL > 1) recall(s, 0, h);
             put(wk.q, r, s);
         }
-        if (j == 0 && live) *reinterpret_cast<float2 *>(wk.steps + (int64_t)r * sh.width + pair) = f2_get(steps);
+        if (live) wk.steps[(int64_t)r * sh.width + ch] = fold(steps);
     }
 }
 
@@ -393,21 +368,21 @@ __global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, ss
 enum What { kForward, kStep };
 
 template <typename T, int N> cudaError_t launch_forward(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
-    constexpr int L = kL, NT = N / L < kNT ? N / L : kNT, SL = N / (L * NT);
-    const SelectiveShape sh = selective_shape(c, 64 / kL, a.total_tokens);
+    const SelectiveShape sh = selective_shape(c, kCols, kAlone, a.total_tokens, a.num_seqs);
     ForwardWork wk;
     wk.q = reinterpret_cast<float *>(a.workspace);
     wk.steps = wk.q + (int64_t)sh.ranges * c.width * N;
     const dim3 grid(sh.tiles * c.groups, sh.ranges);
-    const auto states = selective_forward_kernel<T, NT, L, SL, false>, full = selective_forward_kernel<T, NT, L, SL, true>;
-    constexpr int kStates = Layout<T, N, L, false>::kBytes, kFull = Layout<T, N, L, true>::kBytes;
-    if constexpr (kFull > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
+    const auto states = selective_forward_kernel<T, N, kStates>;
+    const auto full = a.gate ? selective_forward_kernel<T, N, kGated> : selective_forward_kernel<T, N, kPlain>;
+    constexpr int kGatedBytes = Layout<T, N, kGated>::kBytes;
+    static_assert(Layout<T, N, kStates>::kBytes <= 48 * 1024 && Layout<T, N, kPlain>::kBytes <= kGatedBytes, "shared memory");
+    if constexpr (kGatedBytes > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, kGatedBytes);
         if (e != cudaSuccess) return e;
     }
-    static_assert(kStates <= 48 * 1024, "the default limit");
-    if (sh.ranges > 1) states<<<grid, 32, kStates, s>>>(a, sh, wk);
-    full<<<grid, 32, kFull, s>>>(a, sh, wk);
+    if (sh.ranges > 1) states<<<grid, 32, Layout<T, N, kStates>::kBytes, s>>>(a, sh, wk);
+    full<<<grid, 32, a.gate ? kGatedBytes : Layout<T, N, kPlain>::kBytes, s>>>(a, sh, wk);
     return cudaGetLastError();
 }
 
@@ -437,8 +412,8 @@ cudaError_t launch(What what, const sse_selective_config_t &c, const SelectiveAr
 
 }  // namespace
 
-size_t selective_forward_workspace(const sse_selective_config_t &c, int64_t T, int32_t) {
-    const SelectiveShape s = selective_shape(c, 64 / kL, T);
+size_t selective_forward_workspace(const sse_selective_config_t &c, int64_t T, int32_t S) {
+    const SelectiveShape s = selective_shape(c, kCols, kAlone, T, S);
     return s.ranges > 1 ? sizeof(float) * (size_t)s.ranges * c.width * (c.state + 1) : 0;
 }
 cudaError_t launch_selective_forward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {

@@ -13,18 +13,25 @@ static_assert(kTile == kSelectiveCheckpoint, "a checkpoint is the state before a
 
 struct SelectiveShape {
     int width, groups, per, tiles;  // channels; groups; channels and tiles of a group
-    int ranges;
+    int ranges;                     // of the token axis
 };
 
-// Warps of a call, `cols` channels each, and ranges of the token axis: at least six warps for each SM.  (A range that
-// begins inside a sequence costs a pass of its own over the range before it.)
-inline SelectiveShape selective_shape(const sse_selective_config_t &c, int cols, int64_t T) {
+// Warps of a call, `cols` channels each, and ranges of the token axis.  A range that begins inside a sequence costs a
+// pass of its own over the range before it, so there are no more than fill the GPU: about 1024 warps for short calls
+// (8192 tokens x 512 in one sequence: forward 59 us with 64 ranges, 109 with 16 and 84 with 128), about 4096 where ranges
+// have 512 tokens at least (32768 x 2048: 531 us with 64 ranges, 615 with 16).  Sequences that make `alone` warps by
+// themselves have a range each, which even lengths need no such pass for (32 x 1024 x 2048: forward 374 us with 32 ranges,
+// 470 with 64; the backward of 8 x 4096 x 2048: 1543 with 8, 1640 with 32), although uneven ones lose by it (24001 x
+// 2048 in 16: forward 467 with 16 and 388 with 64, backward 1385 and 1234 with 32).
+inline SelectiveShape selective_shape(const sse_selective_config_t &c, int cols, int alone, int64_t T, int32_t S) {
     SelectiveShape s{c.width, c.groups, c.width / c.groups, 0, 1};
     s.tiles = (s.per + cols - 1) / cols;
     const int64_t tiles = (int64_t)s.tiles * c.groups;
-    int64_t r = (152 * 6 + tiles - 1) / tiles;
-    if (r > T / (4 * kTile)) r = T / (4 * kTile);
-    s.ranges = (int)(r < 1 ? 1 : r > kMaxRanges ? kMaxRanges : r);
+    auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
+    const int64_t few = least((1023 + tiles) / tiles, T / (4 * kTile)), many = least((4095 + tiles) / tiles, T / 512);
+    s.ranges = (int)least(most(most(few, many), 1), kMaxRanges);
+    if (S < s.ranges && S * tiles >= alone) s.ranges = S < 1 ? 1 : S;
     return s;
 }
 
@@ -34,7 +41,8 @@ constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596303e-8f;
 // softplus(v) = max(v, 0) + log1p(exp(-|v|)), log1p(u) = 2 atanh(u / (2 + u)): the odd series of atanh on [0, 1/3] as a
 // polynomial of degree 4 in the square (relative error 8e-9 by its coefficients).  The exponent's rounding is put back to
 // first order: small steps are proportional to exp(v), and a step's relative error goes into a state's whole memory.
-__device__ __forceinline__ F2 softplus2(F2 v) {
+// With SLOPE its derivative 1 / (1 + exp(-v)) from the same exponential.
+template <bool SLOPE> __device__ __forceinline__ F2 softplus2(F2 v, F2 &slope) {
     const float2 f = f2_get(v);
     const F2 m = f2(-fabsf(f.x), -fabsf(f.y));
     const F2 t = mul2(m, both(kLog2e));
@@ -47,6 +55,11 @@ __device__ __forceinline__ F2 softplus2(F2 v) {
     p = fma2(p, z, both(0.4002491f));
     p = fma2(p, z, both(0.66666317f));
     p = fma2(p, z, both(2.f));
+    if constexpr (SLOPE) {
+        const F2 q = rcp_ftz(add2(u, both(1.f)));
+        const float2 hi = f2_get(q), lo = f2_get(mul2(u, q));
+        slope = f2(f.x < 0.f ? lo.x : hi.x, f.y < 0.f ? lo.y : hi.y);
+    }
     // a NaN stays one: exp(-|v|) has it
     return fma2(s, p, f2(fmaxf(f.x, 0.f), fmaxf(f.y, 0.f)));
 }
@@ -150,35 +163,75 @@ __device__ __forceinline__ void load_quad(const float *p, int c, bool live, F2 (
     f[1] = f2(v.z, v.w);
 }
 
-// 2 P floats in a row as P pairs, by 16-byte words where there are whole ones (P = 1: one of 8 bytes).
+// Four channels' values in shared memory.
+__device__ __forceinline__ void write_quad(float *to, const F2 (&f)[2]) {
+    const float2 u = f2_get(f[0]), v = f2_get(f[1]);
+    *reinterpret_cast<float4 *>(to) = make_float4(u.x, u.y, v.x, v.y);
+}
+__device__ __forceinline__ void read_quad(const float *from, F2 (&f)[2]) {
+    const float4 v = *reinterpret_cast<const float4 *>(from);
+    f[0] = f2(v.x, v.y);
+    f[1] = f2(v.z, v.w);
+}
+
+// 2 P floats in a row as P pairs.
 template <int P> __device__ __forceinline__ void read_pairs(const float *p, F2 (&f)[P]) {
-    if constexpr (P == 1) {
-        const float2 v = *reinterpret_cast<const float2 *>(p);
-        f[0] = f2(v.x, v.y);
-    } else {
-        static_assert(P % 2 == 0, "whole 16-byte words");
+    static_assert(P % 2 == 0, "whole 16-byte words");
 #pragma unroll
-        for (int k = 0; k < P; k += 2) {
-            const float4 v = *reinterpret_cast<const float4 *>(p + 2 * k);
-            f[k] = f2(v.x, v.y);
-            f[k + 1] = f2(v.z, v.w);
-        }
+    for (int k = 0; k < P; k += 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * k);
+        f[k] = f2(v.x, v.y);
+        f[k + 1] = f2(v.z, v.w);
     }
 }
 template <int P> __device__ __forceinline__ void write_pairs(float *p, const F2 (&f)[P]) {
-    if constexpr (P == 1) {
-        *reinterpret_cast<float2 *>(p) = f2_get(f[0]);
-    } else {
 #pragma unroll
-        for (int k = 0; k < P; k += 2) {
-            const float2 u = f2_get(f[k]), v = f2_get(f[k + 1]);
-            *reinterpret_cast<float4 *>(p + 2 * k) = make_float4(u.x, u.y, v.x, v.y);
-        }
+    for (int k = 0; k < P; k += 2) {
+        const float2 u = f2_get(f[k]), v = f2_get(f[k + 1]);
+        *reinterpret_cast<float4 *>(p + 2 * k) = make_float4(u.x, u.y, v.x, v.y);
     }
 }
-template <int P> __device__ __forceinline__ void no_pairs(F2 (&f)[P]) {
+
+// States of a pair of channels, as pairs over the channels: NT in a row in each of two rows `stride` apart.  swap: the
+// second two come first.
+template <int NT> __device__ __forceinline__ void read_states(const float *p, int64_t stride, int swap, F2 (&f)[NT]) {
 #pragma unroll
-    for (int k = 0; k < P; ++k) f[k] = both(0.f);
+    for (int k = 0; k < NT; k += 2) {
+        const int at = k ^ (swap << 1);
+        const float2 u = *reinterpret_cast<const float2 *>(p + at), v = *reinterpret_cast<const float2 *>(p + stride + at);
+        f[k] = f2(u.x, v.x);
+        f[k + 1] = f2(u.y, v.y);
+    }
+}
+template <int NT> __device__ __forceinline__ void write_states(float *p, int64_t stride, int swap, const F2 (&f)[NT]) {
+#pragma unroll
+    for (int k = 0; k < NT; k += 2) {
+        const int at = k ^ (swap << 1);
+        const float2 u = f2_get(f[k]), v = f2_get(f[k + 1]);
+        *reinterpret_cast<float2 *>(p + at) = make_float2(u.x, v.x);
+        *reinterpret_cast<float2 *>(p + stride + at) = make_float2(u.y, v.y);
+    }
+}
+template <int NT> __device__ __forceinline__ void no_states(F2 (&f)[NT]) {
+#pragma unroll
+    for (int k = 0; k < NT; ++k) f[k] = both(0.f);
+}
+// Four values of B or C to shared memory, each twice: a pair of channels takes one as it is.
+template <typename T> __device__ __forceinline__ void leave_twice(float4 *to, typename Quad<T>::Raw from) {
+    F2 f[2];
+    Quad<T>::unpack(from, f);
+    const float2 u = f2_get(f[0]), v = f2_get(f[1]);
+    to[0] = make_float4(u.x, u.x, u.y, u.y);
+    to[1] = make_float4(v.x, v.x, v.y, v.y);
+}
+// NT values of a token, each twice, at `p`; swap as above.
+template <int NT> __device__ __forceinline__ void read_twice(const float *p, int swap, F2 (&f)[NT]) {
+#pragma unroll
+    for (int k = 0; k < NT; k += 2) {
+        const float4 v = *reinterpret_cast<const float4 *>(p + 2 * (k ^ (swap << 1)));
+        f[k] = f2(v.x, v.y);
+        f[k + 1] = f2(v.z, v.w);
+    }
 }
 
 }  // namespace sse

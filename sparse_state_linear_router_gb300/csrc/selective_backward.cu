@@ -23,26 +23,28 @@ namespace sse {
 namespace {
 
 constexpr int kL = 4, kCols = 16;
+constexpr int kAlone = 1000;  // warps that sequences make by themselves, for a range each
 constexpr int kSpan = 8;  // tokens whose states are held in registers, and of an epilogue
 
 template <typename T, int N, bool FULL> struct Layout {
     static constexpr int NT = N == 8 ? 2 : 4, SL = N / (kL * NT);
     static constexpr int kWarps = FULL ? 4 : 1;
     static constexpr int kRow = kCols * sizeof(T), kBRow = N * sizeof(T);
-    static constexpr int kTensors = FULL ? 4 : 2, kMats = FULL ? 2 : 1;  // delta, d_out, gate, x (without FULL: delta, dy); C, B
+    static constexpr int kMats = FULL ? 2 : 1;  // C, B
     // of a warp
-    static constexpr int kCheck = kTile * (FULL ? 4 : 3) * kRow;
+    static constexpr int kCheck = kTile * (FULL ? 4 : 3) * kRow;  // delta, d_out, gate, x
     static constexpr int kStage = kCheck + (FULL ? kCols * N * 4 : 0);
     static constexpr int kStep = 2 * kStage;                    // float4 [16][8]: D0, D1, D x0, D x1
     static constexpr int kDy = kStep + kTile * kCols / 2 * 16;  // float [16][16]
-    static constexpr int kPart = kDy + kTile * kCols * 4;       // float [3][8][4][16]: y, sum B g, sum A g a h
+    static constexpr int kSlope = kDy + kTile * kCols * 4;      // float [2][16][16]: softplus', d_out silu'(gate)
+    static constexpr int kPart = kSlope + (FULL ? 2 * kTile * kCols * 4 : 0);  // float [3][8][4][16]: y, sum B g, sum A g a h
     static constexpr int kKept = kPart + (FULL ? 3 * kSpan * kL * kCols * 4 : 0);  // slices: e and dA, float4 [SL][2][2][32]
     static constexpr int kWarpBytes = kKept + (SL > 1 ? SL * 4 * 32 * 16 : 0);
     // of the CTA
     static constexpr int kMat = kTile * kBRow * kMats;
     static constexpr int kRaw = kWarps * kWarpBytes;            // C and B as stored, two stages
-    static constexpr int kC = kRaw + 2 * kMat;                  // float [16][N]: C, then B
-    static constexpr int kSums = kC + kMats * kTile * N * 4;    // float [2][kWarps][8][32]
+    static constexpr int kC = kRaw + 2 * kMat;                  // float [16][N][2]: C, then B, each value twice
+    static constexpr int kSums = kC + kMats * kTile * N * 8;    // float [2][kWarps][8][32]
     static constexpr int kBytes = kSums + (FULL ? 2 * kWarps * kSpan * 32 * 4 : 0);
 };
 
@@ -60,7 +62,7 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                                                                                     BackwardWork wk) {
     using Lay = Layout<T, N, FULL>;
     using Raw = typename Quad<T>::Raw;
-    constexpr int NT = Lay::NT, SL = Lay::SL, P = NT / 2, kQuads = kCols / 4, kWarps = Lay::kWarps;
+    constexpr int NT = Lay::NT, SL = Lay::SL, kQuads = kCols / 4, kWarps = Lay::kWarps;
     extern __shared__ __align__(16) char all_smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane >> 3, cl = lane & 7, r = blockIdx.y;
     char *smem = all_smem + (FULL ? warp * Lay::kWarpBytes : 0);
@@ -86,55 +88,42 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
         t1 = min(t1, clamp_token(__ldg(a.cu_seqlens + sequence_of(rg.cu, rg.S, t0) + 1), rg.end));
     }
 
-    F2 e[2][P], A[2][P], dA[2][P], h[2][P];  // A: A log2 e
+    // Of the slice at hand, pairs over the channels; A log2 e.  Every other two pairs of channels have the second two of
+    // their states first, for the sums over channels.
+    F2 e[NT], A[NT], dA[NT], h[NT];
+    const int swap = NT == 4 ? lane >> 1 & 1 : 0;
     auto load_A = [&](int s) {
+        no_states(A);
+        if (live) read_states(a.A + states + s * kL * NT, N, swap, A);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            no_pairs(A[c]);
-            if (live) read_pairs(a.A + states + (int64_t)c * N + s * kL * NT, A[c]);
-#pragma unroll
-            for (int k = 0; k < P; ++k) A[c][k] = mul2(A[c][k], both(kLog2e));
-        }
+        for (int k = 0; k < NT; ++k) A[k] = mul2(A[k], both(kLog2e));
     };
     // this thread's states in an array of [.., width, N] at row i
-    auto get = [&](const float *p, int64_t i, int s, F2 (&to)[2][P]) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            no_pairs(to[c]);
-            if (p && live) read_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * kL * NT, to[c]);
-        }
+    auto get = [&](const float *p, int64_t i, int s, F2 (&to)[NT]) {
+        no_states(to);
+        if (p && live) read_states(p + i * sh.width * N + states + s * kL * NT, N, swap, to);
     };
-    auto put = [&](float *p, int64_t i, int s, const F2 (&from)[2][P]) {
-        if (live)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) write_pairs(p + i * sh.width * N + states + (int64_t)c * N + s * kL * NT, from[c]);
+    auto put = [&](float *p, int64_t i, int s, const F2 (&from)[NT]) {
+        if (live) write_states(p + i * sh.width * N + states + s * kL * NT, N, swap, from);
     };
     // a slice's e and dA between tiles: registers with one slice, else shared memory
     float *kept = reinterpret_cast<float *>(smem + Lay::kKept) + lane * 4;
     auto keep = [&](int s) {
         if constexpr (SL > 1) {
-            static_assert(NT == 4, "a word per channel");
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                write_pairs(kept + (s * 4 + c) * 128, e[c]);
-                write_pairs(kept + (s * 4 + 2 + c) * 128, dA[c]);
-            }
+            write_states(kept + s * 512, 128, 0, e);
+            write_states(kept + s * 512 + 256, 128, 0, dA);
         }
     };
     auto recall = [&](int s) {
         if constexpr (SL > 1) {
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                read_pairs(kept + (s * 4 + c) * 128, e[c]);
-                read_pairs(kept + (s * 4 + 2 + c) * 128, dA[c]);
-            }
+            read_states(kept + s * 512, 128, 0, e);
+            read_states(kept + s * 512 + 256, 128, 0, dA);
             load_A(s);
         }
     };
-    // decays of a step, per state
-    auto decays = [&](F2 d, int c, F2 (&to)[P]) {
+    auto decays = [&](F2 d, F2 (&to)[NT]) {
 #pragma unroll
-        for (int k = 0; k < P; ++k) to[k] = ex2_ftz(mul2(d, A[c][k]));
+        for (int k = 0; k < NT; ++k) to[k] = ex2_ftz(mul2(d, A[k]));
     };
 
     // what the range takes over from those behind it
@@ -152,20 +141,15 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
         load_A(s);
         get(r_last > r ? wk.q : nullptr, r_last, s, e);
         for (int i = r_last - 1; i > r; --i) {
-            F2 q[2][P];
+            F2 q[NT], dec[NT];
+            float2 d = make_float2(0.f, 0.f);
+            if (live) d = *reinterpret_cast<const float2 *>(wk.steps + (int64_t)i * sh.width + pair);
             get(wk.q, i, s, q);
+            decays(f2(d.x, d.y), dec);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                F2 d[P];
-                decays(both(live ? wk.steps[(int64_t)i * sh.width + pair + c] : 0.f), c, d);
-#pragma unroll
-                for (int k = 0; k < P; ++k) e[c][k] = fma2(d[k], e[c][k], q[c][k]);
-            }
+            for (int k = 0; k < NT; ++k) e[k] = fma2(dec[k], e[k], q[k]);
         }
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int k = 0; k < P; ++k) dA[c][k] = both(0.f);
+        no_states(dA);
         keep(s);
     }
 
@@ -213,7 +197,8 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
     F2 steps = both(0.f);
     float4 *step = reinterpret_cast<float4 *>(smem + Lay::kStep);
     float *dys = reinterpret_cast<float *>(smem + Lay::kDy);
-    float *cs = reinterpret_cast<float *>(all_smem + Lay::kC), *bs = cs + kTile * N;
+    float *cs = reinterpret_cast<float *>(all_smem + Lay::kC), *bs = cs + kTile * N * 2;
+    float *slopes = reinterpret_cast<float *>(smem + Lay::kSlope);
     float *parts = reinterpret_cast<float *>(smem + Lay::kPart);
     float *sums = reinterpret_cast<float *>(all_smem + Lay::kSums);
     Edges ed;
@@ -231,7 +216,7 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
 #pragma unroll
         for (int k = 0; k < kTile; k += 32 / kQuads) {
             const int i = k + tq, t = row0 + i;
-            F2 x[2] = {both(0.f), both(0.f)}, d[2], dy[2];
+            F2 x[2] = {both(0.f), both(0.f)}, d[2], dy[2], slope[2];
             raw(0, i, d);
             raw(1, i, dy);
             if constexpr (FULL) raw(3, i, x);
@@ -239,37 +224,38 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                 F2 z[2];
                 raw(2, i, z);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) dy[p] = mul2(dy[p], mul2(z[p], sigmoid2<T>(z[p])));
+                for (int p = 0; p < 2; ++p) {  // silu' = s (1 + z (1 - s))
+                    const F2 s = sigmoid2<T>(z[p]);
+                    if constexpr (FULL)
+                        slope[p] = mul2(dy[p], mul2(s, fma2(z[p], fma2(s, both(-1.f), both(1.f)), both(1.f))));
+                    dy[p] = mul2(dy[p], mul2(z[p], s));
+                }
+                if constexpr (FULL) write_quad(slopes + (kTile + i) * kCols + qd * 4, slope);
             }
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                d[p] = softplus2(add2(d[p], bias[p]));
+                d[p] = softplus2<FULL>(add2(d[p], bias[p]), slope[p]);
                 if (t < t0 || t >= t1) d[p] = both(0.f);  // neither decay nor input; dy is 0 there
                 x[p] = mul2(x[p], d[p]);
             }
+            if constexpr (FULL) write_quad(slopes + i * kCols + qd * 4, slope);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {  // banks: every other four lanes the other pair first
                 const bool other = (p ^ (lane >> 2)) & 1;
                 const float2 u = f2_get(other ? d[1] : d[0]), v = f2_get(other ? x[1] : x[0]);
                 step[i * (kCols / 2) + qd * 2 + other] = make_float4(u.x, u.y, v.x, v.y);
             }
-            const float2 u = f2_get(dy[0]), v = f2_get(dy[1]);
-            *reinterpret_cast<float4 *>(dys + i * kCols + qd * 4) = make_float4(u.x, u.y, v.x, v.y);
+            write_quad(dys + i * kCols + qd * 4, dy);
         }
         for (int k = tid; k < Lay::kMats * kWords; k += 32 * kWarps) {
             const char *from = all_smem + Lay::kRaw + stage * Lay::kMat + k * 16;
-            float4 *to = reinterpret_cast<float4 *>(cs + k * (16 / esz));
+            float4 *to = reinterpret_cast<float4 *>(cs + k * (16 / esz) * 2);
 #pragma unroll
-            for (int q = 0; q < 4 / esz; ++q) {
-                F2 f[2];
-                Quad<T>::unpack(reinterpret_cast<const Raw *>(from)[q], f);
-                const float2 u = f2_get(f[0]), v = f2_get(f[1]);
-                to[q] = make_float4(u.x, u.y, v.x, v.y);
-            }
+            for (int q = 0; q < 4 / esz; ++q) leave_twice<T>(to + 2 * q, reinterpret_cast<const Raw *>(from)[q]);
         }
         __syncthreads();  // B and C; they are written again behind the last barrier of this tile
-        auto row_of = [&](const float *m, int i, int s, F2 (&to)[P]) {  // this thread's states of B or C
-            read_pairs(m + i * N + s * kL * NT + j * NT, to);
+        auto row_of = [&](const float *m, int i, int s, F2 (&to)[NT]) {  // this thread's states of B or C
+            read_twice(m + (i * N + s * kL * NT + j * NT) * 2, swap, to);
         };
         if constexpr (!FULL) {
             for (int s = 0; s < SL; ++s) {
@@ -277,15 +263,11 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                 auto token = [&](int i) {
                     const float4 d = step[i * (kCols / 2) + cl];
                     const float2 dy = *reinterpret_cast<const float2 *>(dys + i * kCols + 2 * cl);
-                    F2 C[P];
+                    F2 C[NT], dec[NT];
                     row_of(cs, i, s, C);
+                    decays(f2(d.x, d.y), dec);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        F2 dec[P];
-                        decays(both(c ? d.y : d.x), c, dec);
-#pragma unroll
-                        for (int k = 0; k < P; ++k) e[c][k] = mul2(dec[k], fma2(C[k], both(c ? dy.y : dy.x), e[c][k]));
-                    }
+                    for (int k = 0; k < NT; ++k) e[k] = mul2(dec[k], fma2(C[k], f2(dy.x, dy.y), e[k]));
                     if (s == 0) steps = add2(steps, f2(d.x, d.y));
                 };
                 if (ed.ends == 0) {
@@ -317,34 +299,22 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                         sum[m][1] = add2(sum[m][1], f2(u.z, u.w));
                     }
                 }
-                F2 x[2], v[2], d_out[2], dx[2], dd[2], dz[2];
-                raw(0, i, v);
-                raw(1, i, d_out);
+                F2 x[2], dx[2], dd[2], dz[2], dy[2], slope[2], gate[2];
                 raw(3, i, x);
-                const float4 dyv = *reinterpret_cast<const float4 *>(dys + i * kCols + qd * 4);
-                const F2 dy[2] = {f2(dyv.x, dyv.y), f2(dyv.z, dyv.w)};
-                const float4 s0 = step[i * (kCols / 2) + qd * 2], s1 = step[i * (kCols / 2) + qd * 2 + 1];
-                const F2 d[2] = {f2(s0.x, s0.y), f2(s1.x, s1.y)};
+                read_quad(dys + i * kCols + qd * 4, dy);
+                read_quad(slopes + i * kCols + qd * 4, slope);
+                read_quad(slopes + (kTile + i) * kCols + qd * 4, gate);
+                const float2 d[2] = {*reinterpret_cast<const float2 *>(step + i * (kCols / 2) + qd * 2),
+                                     *reinterpret_cast<const float2 *>(step + i * (kCols / 2) + qd * 2 + 1)};
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    dx[p] = fma2(skip[p], dy[p], mul2(d[p], sum[1][p]));
-                    // sum A g a h came with A log2 e; softplus' = 1 / (1 + exp(-v))
-                    dd[p] = mul2(fma2(x[p], sum[1][p], mul2(sum[2][p], both(0.693147181f))),
-                                 sigmoid2<float>(add2(v[p], bias[p])));
-                    sum[0][p] = fma2(skip[p], x[p], sum[0][p]);
+                    dx[p] = fma2(skip[p], dy[p], mul2(f2(d[p].x, d[p].y), sum[1][p]));
+                    dd[p] = mul2(fma2(x[p], sum[1][p], mul2(sum[2][p], both(0.693147181f))), slope[p]);  // the sum has A log2 e
+                    dz[p] = mul2(gate[p], fma2(skip[p], x[p], sum[0][p]));
                 }
                 const bool in = t >= t0 && t < t1 && quad_live;
                 const int64_t to = (int64_t)t * sh.width + c0 + qd * 4;
-                if (a.gate) {
-                    F2 z[2];
-                    raw(2, i, z);
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {  // silu' = s (1 + z (1 - s))
-                        const F2 s = sigmoid2<T>(z[p]);
-                        dz[p] = mul2(mul2(d_out[p], sum[0][p]), mul2(s, fma2(z[p], fma2(s, both(-1.f), both(1.f)), both(1.f))));
-                    }
-                    if (in) *reinterpret_cast<Raw *>(static_cast<T *>(a.d_gate) + to) = Quad<T>::pack(dz);
-                }
+                if (a.gate && in) *reinterpret_cast<Raw *>(static_cast<T *>(a.d_gate) + to) = Quad<T>::pack(dz);
                 if (in) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
@@ -377,101 +347,94 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
             auto half = [&](auto edges, int from, int s) {
                 constexpr bool EDGES = decltype(edges)::value;
                 recall(s);
-                const float *ck = reinterpret_cast<const float *>(at + Lay::kCheck);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) read_pairs(ck + (2 * cl + c) * N + s * kL * NT + j * NT, h[c]);
-                auto forward = [&](int i) {
+                read_states(reinterpret_cast<const float *>(at + Lay::kCheck) + 2 * cl * N + s * kL * NT + j * NT, N, swap, h);
+                auto forward = [&](int i, F2 (&dec)[NT]) {
                     const float4 d = step[i * (kCols / 2) + cl];
-                    F2 B[P];
+                    F2 B[NT];
                     row_of(bs, i, s, B);
+                    decays(f2(d.x, d.y), dec);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        F2 dec[P];
-                        decays(both(c ? d.y : d.x), c, dec);
-#pragma unroll
-                        for (int k = 0; k < P; ++k) h[c][k] = fma2(dec[k], h[c][k], mul2(both(c ? d.w : d.z), B[k]));
-                    }
+                    for (int k = 0; k < NT; ++k) h[k] = fma2(dec[k], h[k], mul2(f2(d.z, d.w), B[k]));
                 };
                 if (from) {  // to the middle of the tile
 #pragma unroll 4
                     for (int i = 0; i < kSpan; ++i) {
+                        F2 dec[NT];
                         if (EDGES && ((ed.starts >> i) & 1u)) get(a.init, __shfl_sync(0xffffffffu, ed.seq, i), s, h);
-                        forward(i);
+                        forward(i, dec);
                     }
                 }
-                F2 before[kSpan][2][P];
+                F2 before[kSpan][NT], dec[kSpan][NT];
 #pragma unroll
                 for (int b = 0; b < kSpan; ++b) {
                     const int i = from + b;
                     if (EDGES && ((ed.starts >> i) & 1u)) get(a.init, __shfl_sync(0xffffffffu, ed.seq, i), s, h);
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-#pragma unroll
-                        for (int k = 0; k < P; ++k) before[b][c][k] = h[c][k];
-                    if (b + 1 < kSpan) forward(i);
+                    for (int k = 0; k < NT; ++k) before[b][k] = h[k];
+                    forward(i, dec[b]);
                 }
+                // what a token takes from shared memory, loaded before the token behind it leaves its sums
+                struct Operands {
+                    float4 d;
+                    float2 dy;
+                    F2 B[NT], C[NT];
+                };
+                auto operands = [&](int i) {
+                    Operands o;
+                    o.d = step[i * (kCols / 2) + cl];
+                    o.dy = *reinterpret_cast<const float2 *>(dys + i * kCols + 2 * cl);
+                    row_of(bs, i, s, o.B);
+                    row_of(cs, i, s, o.C);
+                    return o;
+                };
+                Operands next = operands(from + kSpan - 1);
 #pragma unroll
                 for (int b = kSpan - 1; b >= 0; --b) {
                     const int i = from + b;
+                    const Operands o = next;
+                    if (b) next = operands(i - 1);
                     if (EDGES && ((ed.ends >> i) & 1u)) get(a.d_final, __shfl_sync(0xffffffffu, ed.seq, i), s, e);
-                    const float4 d = step[i * (kCols / 2) + cl];
-                    const float2 dy = *reinterpret_cast<const float2 *>(dys + i * kCols + 2 * cl);
-                    F2 B[P], C[P], dB[P], dC[P];
-                    row_of(bs, i, s, B);
-                    row_of(cs, i, s, C);
-                    float2 part3[3];
+                    const F2 d = f2(o.d.x, o.d.y), x = f2(o.d.z, o.d.w), dy = f2(o.dy.x, o.dy.y);
+                    F2 sum[3] = {both(0.f), both(0.f), both(0.f)};
+                    float vB[NT], vC[NT];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const F2 dc = both(c ? d.y : d.x), xc = both(c ? d.w : d.z), yc = both(c ? dy.y : dy.x);
-                        F2 dec[P], y = both(0.f), Bg = both(0.f), Aw = both(0.f);
-                        decays(dc, c, dec);
-#pragma unroll
-                        for (int k = 0; k < P; ++k) {
-                            const F2 u = mul2(dec[k], before[b][c][k]);
-                            const F2 now = fma2(xc, B[k], u);
-                            y = fma2(C[k], now, y);
-                            const F2 gr = fma2(C[k], yc, e[c][k]);
-                            e[c][k] = mul2(dec[k], gr);
-                            const F2 w = mul2(gr, u);
-                            Bg = fma2(B[k], gr, Bg);
-                            Aw = fma2(A[c][k], w, Aw);
-                            dA[c][k] = fma2(dc, w, dA[c][k]);
-                            dB[k] = c ? fma2(gr, xc, dB[k]) : mul2(gr, xc);
-                            dC[k] = c ? fma2(yc, now, dC[k]) : mul2(yc, now);
-                        }
-                        const float2 f0 = f2_get(y), f1 = f2_get(Bg), f2v = f2_get(Aw);
-                        (c ? part3[0].y : part3[0].x) = f0.x + f0.y;
-                        (c ? part3[1].y : part3[1].x) = f1.x + f1.y;
-                        (c ? part3[2].y : part3[2].x) = f2v.x + f2v.y;
+                    for (int k = 0; k < NT; ++k) {
+                        const F2 u = mul2(dec[b][k], before[b][k]);
+                        const F2 now = b + 1 == kSpan ? h[k] : EDGES ? fma2(x, o.B[k], u) : before[(b + 1) % kSpan][k];
+                        const F2 gr = fma2(o.C[k], dy, e[k]);
+                        e[k] = mul2(dec[b][k], gr);
+                        const F2 w = mul2(gr, u);
+                        sum[0] = fma2(o.C[k], now, sum[0]);
+                        sum[1] = fma2(o.B[k], gr, sum[1]);
+                        sum[2] = fma2(A[k], w, sum[2]);
+                        dA[k] = fma2(d, w, dA[k]);
+                        const float2 fB = f2_get(mul2(gr, x)), fC = f2_get(mul2(dy, now));
+                        vB[k] = fB.x + fB.y;
+                        vC[k] = fC.x + fC.y;
                     }
 #pragma unroll
                     for (int m = 0; m < 3; ++m) {
                         // banks: an epilogue's eight lanes read two tokens, so odd tokens have neighbouring lanes' parts swapped
                         float2 *to = reinterpret_cast<float2 *>(parts + ((m * kSpan + b) * kL + (j ^ (b & 1))) * kCols + 2 * cl);
-                        if (SL > 1 && s) part3[m].x += to->x, part3[m].y += to->y;
-                        *to = part3[m];
+                        float2 v = f2_get(sum[m]);
+                        if (SL > 1 && s) v.x += to->x, v.y += to->y;
+                        *to = v;
                     }
-                    // over the eight pairs: lane keeps dB or dC (bit 2) of one of its NT states (bits 1 and 0)
-                    float v[NT];
-                    const bool k2 = lane & 4, k1 = lane & 2, k0 = lane & 1;
-#pragma unroll
-                    for (int k = 0; k < P; ++k) {
-                        const float2 fb = f2_get(dB[k]), fc = f2_get(dC[k]);
-                        v[2 * k] = (k2 ? fc.x : fb.x) + __shfl_xor_sync(0xffffffffu, k2 ? fb.x : fc.x, 4);
-                        v[2 * k + 1] = (k2 ? fc.y : fb.y) + __shfl_xor_sync(0xffffffffu, k2 ? fb.y : fc.y, 4);
-                    }
-                    float one;
-                    int at_value;
+                    // Over the eight pairs of channels: by bit 1 of the lane the first or second two states, which `swap` has
+                    // put first; by bit 2 dB or dC; by bit 0 one of the two states.
                     if constexpr (NT == 4) {
-                        const float lo = (k1 ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, k1 ? v[0] : v[2], 2);
-                        const float hi = (k1 ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, k1 ? v[1] : v[3], 2);
-                        one = (k0 ? hi : lo) + __shfl_xor_sync(0xffffffffu, k0 ? lo : hi, 1);
-                        at_value = (lane >> 2 & 1) * kL * NT + j * NT + (lane & 3);
-                    } else {
-                        one = (k1 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, k1 ? v[0] : v[1], 2);
-                        one += __shfl_xor_sync(0xffffffffu, one, 1);
-                        at_value = (lane >> 2 & 1) * kL * NT + j * NT + (lane >> 1 & 1);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            vB[k] += __shfl_xor_sync(0xffffffffu, vB[k + 2], 2);
+                            vC[k] += __shfl_xor_sync(0xffffffffu, vC[k + 2], 2);
+                        }
                     }
+                    const bool k2 = lane & 4, k0 = lane & 1;
+                    const float v0 = (k2 ? vC[0] : vB[0]) + __shfl_xor_sync(0xffffffffu, k2 ? vB[0] : vC[0], 4);
+                    const float v1 = (k2 ? vC[1] : vB[1]) + __shfl_xor_sync(0xffffffffu, k2 ? vB[1] : vC[1], 4);
+                    float one = (k0 ? v1 : v0) + __shfl_xor_sync(0xffffffffu, k0 ? v0 : v1, 1);
+                    if constexpr (NT == 2) one += __shfl_xor_sync(0xffffffffu, one, 2);
+                    const int at_value = (lane >> 2 & 1) * kL * NT + j * NT + (swap << 1) + (lane & 1);
                     sums[((turn * kWarps + warp) * kSpan + b) * 32 + at_value] = one;
                     if (EDGES && ((ed.starts >> i) & 1u)) {
                         const int q = __shfl_sync(0xffffffffu, ed.seq, i);
@@ -498,12 +461,7 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
         float *w = wk.weights + (int64_t)r * sh.width * (N + 2);
         for (int s = 0; s < SL; ++s) {
             recall(s);
-            if (live)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int k = 0; k < P; ++k)
-                        *reinterpret_cast<float2 *>(w + (int64_t)(pair + c) * (N + 2) + s * kL * NT + j * NT + 2 * k) = f2_get(dA[c][k]);
+            if (live) write_states(w + (int64_t)pair * (N + 2) + s * kL * NT + j * NT, N + 2, swap, dA);
         }
         // the vectors' sums over the tokens of the eight lanes of a quad
 #pragma unroll
@@ -584,7 +542,7 @@ size_t carve(const sse_selective_config_t &c, const SelectiveShape &s, int64_t T
 }
 
 template <typename T, int N> cudaError_t launch_t(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
-    const SelectiveShape sh = selective_shape(c, kCols, a.total_tokens);
+    const SelectiveShape sh = selective_shape(c, kCols, kAlone, a.total_tokens, a.num_seqs);
     BackwardWork wk;
     carve(c, sh, a.total_tokens, a.workspace, wk);
     const auto states = selective_backward_kernel<T, N, false>, full = selective_backward_kernel<T, N, true>;
@@ -612,9 +570,9 @@ template <typename T> cudaError_t launch_state(const sse_selective_config_t &c, 
 
 }  // namespace
 
-size_t selective_backward_workspace(const sse_selective_config_t &c, int64_t T, int32_t) {
+size_t selective_backward_workspace(const sse_selective_config_t &c, int64_t T, int32_t S) {
     BackwardWork wk;
-    return carve(c, selective_shape(c, kCols, T), T, nullptr, wk);
+    return carve(c, selective_shape(c, kCols, kAlone, T, S), T, nullptr, wk);
 }
 cudaError_t launch_selective_backward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {
     return cfg.dtype == SSE_BF16 ? launch_state<__nv_bfloat16>(cfg, a, stream) : launch_state<float>(cfg, a, stream);
