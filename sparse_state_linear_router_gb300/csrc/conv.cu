@@ -11,13 +11,40 @@
 // K - 1 rows (and, in the backward, K - 1 gradients g) stay in registers, so a row
 // is read once but for the K - 1 rows in front of a run (backward: and behind it).
 // The packed token axis is one axis: runs are cut without regard to sequences, and
-// a sequence's first row takes the state's rows into the window.
+// a sequence's first row takes the state's rows into the window.  Rows inside a
+// sequence come in batches of four by asynchronous copies, two or three batches
+// ahead.
+//
+// Measured on a GB300, K = 4 with SiLU, 32768 x 2048 in bf16: forward 50 us (HBM
+// floor at 6.77 TB/s: 40), backward 94 (59), of which the activation is 18.  One row
+// after another took 290 us together, batches loaded to registers 52 and 116.
+// float32, 16384 x 2048: 53 and 82 (40, 59); a fourth batch in the backward's ring
+// leaves it two CTAs less on an SM, and 103 us.
 #include "quad.cuh"
 
 namespace sse {
 namespace {
 
 constexpr int kWarps = 4;  // runs of a CTA
+constexpr int kBatch = 4;   // rows copied and summed at a time
+
+// A thread's ring of rows in shared memory: its own quads of one tensor (four batches) or two (three).  The thread that
+// copies a quad is the one that reads it, so there is no barrier.
+template <typename T, int TENSORS> struct Ring {
+    using Raw = typename Quad<T>::Raw;
+    static constexpr int kGroups = TENSORS == 1 ? 4 : 3;
+    static constexpr int kBytes = kGroups * kBatch * TENSORS * 32 * kWarps * (int)sizeof(Raw);
+    static __device__ __forceinline__ char *slot(char *smem, int group, int row, int tensor) {
+        return smem + (((group * kBatch + row) * TENSORS + tensor) * 32 * kWarps + threadIdx.x) * sizeof(Raw);
+    }
+    static __device__ __forceinline__ void copy(char *to, const T *from) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from),
+                     "n"(sizeof(Raw)) : "memory");
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // Until the oldest of kGroups batches is there.
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory"); }
+};
 
 // What a thread has of the filter.
 template <int K> struct Filter {
@@ -84,22 +111,24 @@ template <typename T, int K> struct Window {
 
 // Runs: gridDim.y CTAs of kWarps warps, `run` tokens each.
 template <typename T, int K, bool SILU>
-__global__ void __launch_bounds__(32 * kWarps) conv_forward_kernel(ConvArgs a, int width, int run) {
+__global__ void __launch_bounds__(32 * kWarps, 6) conv_forward_kernel(ConvArgs a, int width, int run) {
     using Raw = typename Quad<T>::Raw;
+    using Rows = Ring<T, 1>;
     const int lane = threadIdx.x & 31;
     const int col = (blockIdx.x * 32 + lane) * 4;
     if (col >= width) return;
     const int id = blockIdx.y * kWarps + (threadIdx.x >> 5), runs = gridDim.y * kWarps;
     const int end_of_all = clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens);
-    int t = id * run;
+    int t = id * run, t0 = t;
     const int t1 = min(t + run, end_of_all);
+    extern __shared__ __align__(16) char smem[];
     const Filter<K> f(a, col);
     if (t < t1) {
         int q = sequence_of(a.cu_seqlens, a.num_seqs, t);
         int start = __ldg(a.cu_seqlens + q), end = __ldg(a.cu_seqlens + q + 1);
         Window<T, K> win;
         win.before(a, t, q, start, width, col);
-        for (; t < t1; ++t) {
+        while (t < t1) {
             if (t == end) {  // the next sequence that has tokens
                 while (end <= t && q + 1 < a.num_seqs) {
                     ++q;
@@ -108,15 +137,58 @@ __global__ void __launch_bounds__(32 * kWarps) conv_forward_kernel(ConvArgs a, i
                 }
                 win.before(a, t, q, start, width, col);
             }
-            win.push(Window<T, K>::of(a, t, col));
-            F2 u[2];
-            win.sum(f, u);
-            if constexpr (SILU) {
-                u[0] = mul2(u[0], sigmoid2<T>(u[0]));
-                u[1] = mul2(u[1], sigmoid2<T>(u[1]));
+            // whole batches of one sequence
+            const int batches = (min(t1, end) - t) / kBatch;
+            auto copy = [&](int k) {
+                if (k < batches)
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i)
+                        Rows::copy(Rows::slot(smem, k % Rows::kGroups, i, 0),
+                                         static_cast<const T *>(a.x) + (int64_t)(t0 + k * kBatch + i) * a.x_stride + col);
+                Rows::commit();
+            };
+            if (batches > 0) {
+                t0 = t;
+                for (int k = 0; k + 1 < Rows::kGroups; ++k) copy(k);
             }
-            *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + (int64_t)t * width + col) = Quad<T>::pack(u);
-            if (t + 1 == end && a.final_state)
+            for (int k = 0; k < batches; ++k) {
+                copy(k + Rows::kGroups - 1);
+                Rows::wait();
+                F2 x[K - 1 + kBatch][2];
+#pragma unroll
+                for (int i = 0; i < K - 1; ++i) Quad<T>::unpack(win.row[i + 1], x[i]);
+                Raw r[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    r[i] = *reinterpret_cast<const Raw *>(Rows::slot(smem, k % Rows::kGroups, i, 0));
+                    Quad<T>::unpack(r[i], x[K - 1 + i]);
+                    F2 u[2] = {f.b[0], f.b[1]};
+#pragma unroll
+                    for (int j = 0; j < K; ++j) {
+                        u[0] = fma2(f.w[j][0], x[i + j][0], u[0]);
+                        u[1] = fma2(f.w[j][1], x[i + j][1], u[1]);
+                    }
+                    if constexpr (SILU) {
+                        u[0] = mul2(u[0], sigmoid2<T>(u[0]));
+                        u[1] = mul2(u[1], sigmoid2<T>(u[1]));
+                    }
+                    *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + (int64_t)(t + i) * width + col) = Quad<T>::pack(u);
+                }
+#pragma unroll
+                for (int i = 1; i < K; ++i) win.row[i] = r[kBatch - K + i];
+                t += kBatch;
+            }
+            for (const int stop = min(t1, min(end, t + kBatch)); t < stop; ++t) {
+                win.push(Window<T, K>::of(a, t, col));
+                F2 u[2];
+                win.sum(f, u);
+                if constexpr (SILU) {
+                    u[0] = mul2(u[0], sigmoid2<T>(u[0]));
+                    u[1] = mul2(u[1], sigmoid2<T>(u[1]));
+                }
+                *reinterpret_cast<Raw *>(static_cast<T *>(a.out) + (int64_t)t * width + col) = Quad<T>::pack(u);
+            }
+            if (t == end && a.final_state)
 #pragma unroll
                 for (int i = 0; i < K - 1; ++i)
                     *reinterpret_cast<Raw *>(static_cast<T *>(a.final_state) + Window<T, K>::state_at(q, i, width, col)) =
@@ -135,9 +207,11 @@ __global__ void __launch_bounds__(32 * kWarps) conv_forward_kernel(ConvArgs a, i
 }
 
 template <typename T, int K, bool SILU>
-__global__ void __launch_bounds__(32 * kWarps) conv_backward_kernel(ConvArgs a, int width, int run) {
+__global__ void __launch_bounds__(32 * kWarps, 4) conv_backward_kernel(ConvArgs a, int width, int run) {
     using Raw = typename Quad<T>::Raw;
+    using Rows = Ring<T, 2>;
     __shared__ float4 part[kWarps][K + 1][32];
+    extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int col = (blockIdx.x * 32 + lane) * 4;
     const bool live = col < width;
@@ -162,7 +236,64 @@ __global__ void __launch_bounds__(32 * kWarps) conv_backward_kernel(ConvArgs a, 
             F2 g[K][2];
 #pragma unroll
             for (int j = 0; j < K; ++j) g[j][0] = g[j][1] = both(0.f);
-            for (int t = s0; t < s1 + K - 1; ++t) {
+            for (int t = s0; t < s1 + K - 1;) {
+                // Whole batches whose gradients need nothing but rows of this run and sequence.  Behind each: K - 1 rows of the
+                // window and of g.
+                const int batches = t == s0 + K - 1 ? (s1 - t) / kBatch : 0, from = t;
+                auto copy = [&](int k) {
+                    if (k < batches)
+#pragma unroll
+                        for (int i = 0; i < kBatch; ++i) {
+                            const int64_t row = from + k * kBatch + i;
+                            Rows::copy(Rows::slot(smem, k % Rows::kGroups, i, 0), static_cast<const T *>(a.x) + row * a.x_stride + col);
+                            Rows::copy(Rows::slot(smem, k % Rows::kGroups, i, 1), static_cast<const T *>(a.d_out) + row * width + col);
+                        }
+                    Rows::commit();
+                };
+                if (batches > 0)
+                    for (int k = 0; k + 1 < Rows::kGroups; ++k) copy(k);
+                for (int k = 0; k < batches; ++k) {
+                    copy(k + Rows::kGroups - 1);
+                    Rows::wait();
+                    F2 x[K - 1 + kBatch][2], gs[K - 1 + kBatch][2];
+#pragma unroll
+                    for (int i = 0; i < K - 1; ++i) {
+                        Quad<T>::unpack(win.row[i + 1], x[i]);
+                        gs[i][0] = g[i + 1][0], gs[i][1] = g[i + 1][1];
+                    }
+                    Raw rx[kBatch];
+#pragma unroll
+                    for (int i = 0; i < kBatch; ++i) {
+                        rx[i] = *reinterpret_cast<const Raw *>(Rows::slot(smem, k % Rows::kGroups, i, 0));
+                        Quad<T>::unpack(rx[i], x[K - 1 + i]);
+                        Quad<T>::unpack(*reinterpret_cast<const Raw *>(Rows::slot(smem, k % Rows::kGroups, i, 1)), gs[K - 1 + i]);
+                        F2 dx[2] = {both(0.f), both(0.f)};
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            if constexpr (SILU) {  // silu' = s (1 + u (1 - s))
+                                F2 u = f.b[c];
+#pragma unroll
+                                for (int j = 0; j < K; ++j) u = fma2(f.w[j][c], x[i + j][c], u);
+                                const F2 s = sigmoid2<T>(u);
+                                gs[K - 1 + i][c] = mul2(gs[K - 1 + i][c], mul2(s, fma2(u, fma2(s, both(-1.f), both(1.f)), both(1.f))));
+                            }
+                            const F2 gr = gs[K - 1 + i][c];
+#pragma unroll
+                            for (int j = 0; j < K; ++j) {
+                                dw[j][c] = fma2(gr, x[i + j][c], dw[j][c]);
+                                dx[c] = fma2(f.w[j][c], gs[K - 1 + i - j][c], dx[c]);
+                            }
+                            db[c] = add2(db[c], gr);
+                        }
+                        *reinterpret_cast<Raw *>(static_cast<T *>(a.dx) + (int64_t)(t + i - (K - 1)) * width + col) = Quad<T>::pack(dx);
+                    }
+#pragma unroll
+                    for (int i = 1; i < K; ++i) {
+                        win.row[i] = rx[kBatch - K + i];
+                        g[i][0] = gs[kBatch - 1 + i][0], g[i][1] = gs[kBatch - 1 + i][1];
+                    }
+                    t += kBatch;
+                }
 #pragma unroll
                 for (int j = 0; j + 1 < K; ++j) g[j][0] = g[j + 1][0], g[j][1] = g[j + 1][1];
                 g[K - 1][0] = g[K - 1][1] = both(0.f);
@@ -191,7 +322,7 @@ __global__ void __launch_bounds__(32 * kWarps) conv_backward_kernel(ConvArgs a, 
                         db[1] = add2(db[1], g[K - 1][1]);
                     }
                 }
-                const int p = t - (K - 1);
+                const int p = t++ - (K - 1);
                 if (p < s0 && (s0 != start || !a.d_init)) continue;  // another run's row, or nobody's
                 F2 d[2] = {both(0.f), both(0.f)};
 #pragma unroll
@@ -304,7 +435,7 @@ constexpr int kSms = 152;
 void cut(int width, int64_t T, bool backward, int &run, int &ctas) {
     const int64_t columns = (width + 127) / 128, warps = (int64_t)kSms * 16;
     int64_t r = (T * columns + warps - 1) / warps;
-    const int least = 8, most = backward ? 64 : 32;
+    const int least = 8, most = backward ? 128 : 64;
     run = (int)(r < least ? least : r > most ? most : r);
     const int64_t n = (T + (int64_t)run * kWarps - 1) / ((int64_t)run * kWarps);
     ctas = n < 1 ? 1 : (int)n;
@@ -326,11 +457,14 @@ cudaError_t launch_t(What what, const sse_conv_config_t &c, const ConvArgs &a, c
     cut(c.width, a.total_tokens, what == kBackward, run, ctas);
     const dim3 grid((c.width + 127) / 128, ctas);
     if (what == kForward) {
-        conv_forward_kernel<T, K, SILU><<<grid, 32 * kWarps, 0, s>>>(a, c.width, run);
+        conv_forward_kernel<T, K, SILU><<<grid, 32 * kWarps, Ring<T, 1>::kBytes, s>>>(a, c.width, run);
         return cudaGetLastError();
     }
-    conv_backward_kernel<T, K, SILU><<<grid, 32 * kWarps, 0, s>>>(a, c.width, run);
-    const cudaError_t e = cudaGetLastError();
+    constexpr int kRing = Ring<T, 2>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(conv_backward_kernel<T, K, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing);
+    if (e != cudaSuccess) return e;
+    conv_backward_kernel<T, K, SILU><<<grid, 32 * kWarps, kRing, s>>>(a, c.width, run);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_dependent(conv_weights_kernel, dim3((c.width + 31) / 32, K + 1), dim3(32, 32), 0, s, a, c.width, K, ctas);
 }

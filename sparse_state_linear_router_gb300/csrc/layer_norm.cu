@@ -12,8 +12,7 @@
 // row takes one barrier and no sum of squares about a distant zero.  The
 // backward's sums p and p (x - m) go with them: sum p (x - mean) is the sum of
 // [p (x - m)] + (m - mean) [p] over the warps.  Rows of one warp take no barrier.
-#include "f32x2.cuh"
-#include "sse_internal.cuh"
+#include "quad.cuh"
 
 namespace sse {
 namespace {
@@ -49,11 +48,6 @@ template <typename T> struct Word {
     }
 };
 
-__device__ __forceinline__ F2 both(float x) { return f2(x, x); }
-__device__ __forceinline__ float fold(F2 v) {
-    const float2 f = f2_get(v);
-    return f.x + f.y;
-}
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -101,35 +95,58 @@ __device__ __forceinline__ void join(const LnShape &n, float4 &v, int vpt, int e
     v = t;
 }
 
-// Words of a row: warp w, word i, lane l has word (w * VPT + i) * 32 + l.
-template <typename T, int VPT>
-__global__ void __launch_bounds__(VPT == 4 ? 512 : 256) layer_norm_kernel(LayerNormArgs a, LnShape n) {
+// A thread's words of a row: warp w, word i, lane l has word (w * VPT + i) * 32 + l.
+template <typename T, int VPT> struct Words {
+    uint4 u[VPT];
+    __device__ __forceinline__ void load(const LnShape &n, const void *p, int64_t stride, int64_t row, int first, bool ok) {
+        const T *at = static_cast<const T *>(p) + row * stride + first * Word<T>::kE;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+            u[i] = ok && first + i * 32 < n.nv ? *reinterpret_cast<const uint4 *>(at + i * 32 * Word<T>::kE) : make_uint4(0, 0, 0, 0);
+    }
+};
+// Word j of a float32 vector.
+template <typename T> __device__ __forceinline__ void vector_word(const float *p, int j, F2 (&f)[Word<T>::kP]) {
+#pragma unroll
+    for (int k = 0; k < Word<T>::kP; k += 2) {
+        const float4 v = __ldg(reinterpret_cast<const float4 *>(p + j * Word<T>::kE + 2 * k));
+        f[k] = f2(v.x, v.y);
+        f[k + 1] = f2(v.z, v.w);
+    }
+}
+
+// Threads of a row up to which the backward has its column sums in registers: 168 a thread (float32, whose words are half as
+// many elements, 128).
+template <typename T> constexpr int most_in_registers() { return sizeof(T) == 2 ? 384 : 512; }
+
+// The next row's words are loaded while this one's are at work.
+template <typename T, int VPT, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1) layer_norm_kernel(LayerNormArgs a, LnShape n) {
     constexpr int E = Word<T>::kE, P = Word<T>::kP;
     __shared__ float4 words[64];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int warp = n.warps == 1 ? 0 : wid;
+    const int warp = n.warps == 1 ? 0 : wid, j0 = warp * VPT * 32 + lane;
     const int64_t rows_on = n.warps == 1 ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
     const int64_t first = n.warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + wid : blockIdx.x;
     const float mine = (float)warp_elements(n, warp, VPT, E), inv_mine = 1.f / mine;
     int turn = 0;
+    Words<T, VPT> x, r;
+    x.load(n, a.x, a.x_stride, first, j0, first < a.T);
+    r.load(n, a.r, a.r_stride, first, j0, a.r && first < a.T);
     for (int64_t row = first; row < a.T; row += rows_on) {
         F2 v[VPT][P];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = (warp * VPT + i) * 32 + lane;
-            uint4 u = make_uint4(0, 0, 0, 0), s = u;
-            if (j < n.nv) {
-                u = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.x_stride + j * E);
-                if (a.r) s = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.r) + row * a.r_stride + j * E);
-            }
-            Word<T>::unpack(u, v[i]);
+            Word<T>::unpack(x.u[i], v[i]);
             if (a.r) {
                 F2 w[P];
-                Word<T>::unpack(s, w);
+                Word<T>::unpack(r.u[i], w);
 #pragma unroll
                 for (int k = 0; k < P; ++k) v[i][k] = add2(v[i][k], w[k]);
             }
         }
+        x.load(n, a.x, a.x_stride, row + rows_on, j0, row + rows_on < a.T);
+        if (a.r) r.load(n, a.r, a.r_stride, row + rows_on, j0, row + rows_on < a.T);
         F2 t = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -139,7 +156,7 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 256) layer_norm_kernel(LayerN
         t = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
-            if ((warp * VPT + i) * 32 + lane < n.nv)
+            if (j0 + i * 32 < n.nv)
 #pragma unroll
                 for (int k = 0; k < P; ++k) {
                     const F2 d = add2(v[i][k], both(-m.x));
@@ -151,56 +168,64 @@ __global__ void __launch_bounds__(VPT == 4 ? 512 : 256) layer_norm_kernel(LayerN
         const float rstd = rsqrt_ftz(fmaf(m.y, n.inv_width, n.eps));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = (warp * VPT + i) * 32 + lane;
+            const int j = j0 + i * 32;
             if (j >= n.nv) continue;
             const int64_t at = row * n.width + j * E;
             if (a.r_out) *reinterpret_cast<uint4 *>(static_cast<T *>(a.r_out) + at) = Word<T>::pack(v[i]);
-            F2 y[P];
+            F2 w[P], b[P];
+            if (a.weight) vector_word<T>(a.weight, j, w);
+            if (a.bias) vector_word<T>(a.bias, j, b);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                y[k] = mul2(add2(v[i][k], both(-m.x)), both(rstd));
-                float2 b = make_float2(0.f, 0.f);
-                if (a.bias) b = __ldg(reinterpret_cast<const float2 *>(a.bias + j * E + 2 * k));
-                if (a.weight) {
-                    const float2 w = __ldg(reinterpret_cast<const float2 *>(a.weight + j * E + 2 * k));
-                    y[k] = fma2(y[k], f2(w.x, w.y), f2(b.x, b.y));
-                } else {
-                    y[k] = add2(y[k], f2(b.x, b.y));
-                }
+                v[i][k] = mul2(add2(v[i][k], both(-m.x)), both(rstd));
+                if (a.weight) v[i][k] = mul2(v[i][k], w[k]);
+                if (a.bias) v[i][k] = add2(v[i][k], b[k]);
             }
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at) = Word<T>::pack(y);
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at) = Word<T>::pack(v[i]);
         }
     }
 }
 
 template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(LayerNormArgs a, LnShape n) {
+__global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4) layer_norm_backward_kernel(LayerNormArgs a, LnShape n) {
     constexpr int E = Word<T>::kE, P = Word<T>::kP;
     __shared__ float4 words[64];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int warp = n.warps == 1 ? 0 : wid;
+    const int warp = n.warps == 1 ? 0 : wid, j0 = warp * VPT * 32 + lane;
     const int64_t rows_on = n.warps == 1 ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
     const int64_t first = n.warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + wid : blockIdx.x;
     const float inv_mine = 1.f / (float)warp_elements(n, warp, VPT, E);
-    F2 sum_w[VPT][P], sum_b[VPT][P];
+    // column sums: in registers, or where there are too few, in words of shared memory of the thread's own
+    constexpr bool SHARED = MAXT > most_in_registers<T>();
+    extern __shared__ __align__(16) float sums[];
+    F2 sum_w[SHARED ? 1 : VPT][P], sum_b[SHARED ? 1 : VPT][P];
+    auto mine = [&](int which, int i, int k) { return sums + (((which * VPT + i) * (P / 2) + k / 2) * blockDim.x + threadIdx.x) * 4; };
 #pragma unroll
     for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int k = 0; k < P; ++k) sum_w[i][k] = sum_b[i][k] = both(0.f);
+        for (int k = 0; k < P; k += 2) {
+            const F2 none[2] = {both(0.f), both(0.f)};
+            if constexpr (SHARED) {
+                write_quad(mine(0, i, k), none);
+                write_quad(mine(1, i, k), none);
+            } else {
+                sum_w[i][k] = sum_w[i][k + 1] = sum_b[i][k] = sum_b[i][k + 1] = both(0.f);
+            }
+        }
     int turn = 0;
+    Words<T, VPT> x, dy, dr;
+    x.load(n, a.x, a.x_stride, first, j0, first < a.T);
+    dy.load(n, a.d_out, n.width, first, j0, first < a.T);
     for (int64_t row = first; row < a.T; row += rows_on) {
         F2 v[VPT][P], d[VPT][P];
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = (warp * VPT + i) * 32 + lane;
-            uint4 u = make_uint4(0, 0, 0, 0), s = u;
-            if (j < n.nv) {
-                u = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.x) + row * a.x_stride + j * E);
-                s = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.d_out) + row * n.width + j * E);
-            }
-            Word<T>::unpack(u, v[i]);
-            Word<T>::unpack(s, d[i]);
+            Word<T>::unpack(x.u[i], v[i]);
+            Word<T>::unpack(dy.u[i], d[i]);
         }
+        if (a.d_r_out) dr.load(n, a.d_r_out, n.width, row, j0, true);
+        x.load(n, a.x, a.x_stride, row + rows_on, j0, row + rows_on < a.T);
+        dy.load(n, a.d_out, n.width, row + rows_on, j0, row + rows_on < a.T);
         F2 t = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -211,16 +236,14 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(LayerNormArgs
         F2 sq = both(0.f), sp = both(0.f), sx = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = (warp * VPT + i) * 32 + lane;
+            const int j = j0 + i * 32;
             if (j >= n.nv) continue;
+            F2 w[P];
+            if (a.weight) vector_word<T>(a.weight, j, w);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
                 const F2 c = add2(v[i][k], both(-m.x));
-                F2 p = d[i][k];
-                if (a.weight) {
-                    const float2 w = __ldg(reinterpret_cast<const float2 *>(a.weight + j * E + 2 * k));
-                    p = mul2(p, f2(w.x, w.y));
-                }
+                const F2 p = a.weight ? mul2(d[i][k], w[k]) : d[i][k];
                 sq = fma2(c, c, sq);
                 sp = add2(sp, p);
                 sx = fma2(p, c, sx);
@@ -235,26 +258,40 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(LayerNormArgs
         const float mean_p = m.z * n.inv_width, slope = m.w * n.inv_width * rstd * rstd;  // mean(p x_hat) rstd
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = (warp * VPT + i) * 32 + lane;
+            const int j = j0 + i * 32;
             if (j >= n.nv) continue;
-            const int64_t at = row * n.width + j * E;
-            F2 e[P];
-            if (a.d_r_out)
-                Word<T>::unpack(*reinterpret_cast<const uint4 *>(static_cast<const T *>(a.d_r_out) + at), e);
+            F2 e[P], w[P];
+            if (a.d_r_out) Word<T>::unpack(dr.u[i], e);
+            if (a.weight) vector_word<T>(a.weight, j, w);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
                 const F2 c = add2(v[i][k], both(-m.x));
-                sum_w[i][k] = fma2(d[i][k], mul2(c, both(rstd)), sum_w[i][k]);
-                sum_b[i][k] = add2(sum_b[i][k], d[i][k]);
-                F2 p = d[i][k];
-                if (a.weight) {
-                    const float2 w = __ldg(reinterpret_cast<const float2 *>(a.weight + j * E + 2 * k));
-                    p = mul2(p, f2(w.x, w.y));
+                if constexpr (SHARED) {
+                    v[i][k] = mul2(c, both(rstd));  // x_hat, for the sums below
+                } else {
+                    sum_w[i][k] = fma2(d[i][k], mul2(c, both(rstd)), sum_w[i][k]);
+                    sum_b[i][k] = add2(sum_b[i][k], d[i][k]);
                 }
+                F2 p = a.weight ? mul2(d[i][k], w[k]) : d[i][k];
                 p = mul2(fma2(c, both(-slope), add2(p, both(-mean_p))), both(rstd));
                 e[k] = a.d_r_out ? add2(p, e[k]) : p;
             }
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + at) = Word<T>::pack(e);
+            *reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * n.width + j * E) = Word<T>::pack(e);
+            if constexpr (SHARED) {
+#pragma unroll
+                for (int k = 0; k < P; k += 2) {
+                    F2 w[2], b[2];
+                    read_quad(mine(0, i, k), w);
+                    read_quad(mine(1, i, k), b);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        w[q] = fma2(d[i][k + q], v[i][k + q], w[q]);
+                        b[q] = add2(b[q], d[i][k + q]);
+                    }
+                    write_quad(mine(0, i, k), w);
+                    write_quad(mine(1, i, k), b);
+                }
+            }
         }
     }
     griddep_launch_dependents();
@@ -262,14 +299,19 @@ __global__ void __launch_bounds__(MAXT) layer_norm_backward_kernel(LayerNormArgs
     if (first < rows_on)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = (warp * VPT + i) * 32 + lane;
+            const int j = j0 + i * 32;
             if (j >= n.nv) continue;
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                if (a.d_weight)
-                    *reinterpret_cast<float2 *>(a.partials + first * n.width + j * E + 2 * k) = f2_get(sum_w[i][k]);
-                if (a.d_bias)
-                    *reinterpret_cast<float2 *>(a.partials + (rows_on + first) * n.width + j * E + 2 * k) = f2_get(sum_b[i][k]);
+            for (int k = 0; k < P; k += 2) {
+                F2 w[2], b[2];
+                if constexpr (SHARED) {
+                    read_quad(mine(0, i, k), w);
+                    read_quad(mine(1, i, k), b);
+                } else {
+                    w[0] = sum_w[i][k], w[1] = sum_w[i][k + 1], b[0] = sum_b[i][k], b[1] = sum_b[i][k + 1];
+                }
+                if (a.d_weight) write_quad(a.partials + first * n.width + j * E + 2 * k, w);
+                if (a.d_bias) write_quad(a.partials + (rows_on + first) * n.width + j * E + 2 * k, b);
             }
         }
 }
@@ -318,8 +360,8 @@ LnPlan plan(const sse_layer_norm_config_t &c, int64_t T, bool backward) {
     p.n.warps = (p.n.nv + 32 * p.vpt - 1) / (32 * p.vpt);
     p.teams = p.n.warps == 1 ? 4 : 1;
     p.threads = 32 * p.n.warps * p.teams;
-    // as many as an SM holds: 64 registers a thread forward, 128 backward (64 where a row has more than 512 threads)
-    int per_sm = (backward ? p.threads > 512 ? 1024 : 512 : 1024) / p.threads;
+    // as many as an SM holds: 128 registers a thread; backward 168 for bf16 up to 384 threads, 64 with more than 512
+    int per_sm = (backward && p.threads <= 384 && c.dtype == SSE_BF16 ? 384 : p.threads <= 512 ? 512 : 1024) / p.threads;
     if (per_sm < 1) per_sm = 1;
     const int64_t need = (T + p.teams - 1) / p.teams, hold = (int64_t)kSms * per_sm;
     p.grid = (int)(need < hold ? need : hold);
@@ -327,22 +369,27 @@ LnPlan plan(const sse_layer_norm_config_t &c, int64_t T, bool backward) {
 }
 
 template <typename T> cudaError_t launch_forward(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
-    switch (p.vpt) {
-    case 1: layer_norm_kernel<T, 1><<<p.grid, p.threads, 0, s>>>(a, p.n); break;
-    case 2: layer_norm_kernel<T, 2><<<p.grid, p.threads, 0, s>>>(a, p.n); break;
-    case 3: layer_norm_kernel<T, 3><<<p.grid, p.threads, 0, s>>>(a, p.n); break;
-    default: layer_norm_kernel<T, 4><<<p.grid, p.threads, 0, s>>>(a, p.n);
-    }
+    const auto kernel = p.threads > 128 ? layer_norm_kernel<T, 4, 512>  // more than 512 words: four a thread
+                        : p.vpt == 1    ? layer_norm_kernel<T, 1, 128>
+                        : p.vpt == 2    ? layer_norm_kernel<T, 2, 128>
+                        : p.vpt == 3    ? layer_norm_kernel<T, 3, 128>
+                                        : layer_norm_kernel<T, 4, 128>;
+    kernel<<<p.grid, p.threads, 0, s>>>(a, p.n);
     return cudaGetLastError();
 }
 
 template <typename T> cudaError_t launch_backward(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
-    if (p.vpt == 1)
-        layer_norm_backward_kernel<T, 1, 512><<<p.grid, p.threads, 0, s>>>(a, p.n);
-    else if (p.threads <= 512)
-        layer_norm_backward_kernel<T, 2, 512><<<p.grid, p.threads, 0, s>>>(a, p.n);
-    else
-        layer_norm_backward_kernel<T, 2, 1024><<<p.grid, p.threads, 0, s>>>(a, p.n);
+    const auto kernel = p.vpt == 1         ? layer_norm_backward_kernel<T, 1, 128>
+                        : p.threads <= 128 ? layer_norm_backward_kernel<T, 2, 128>
+                        : p.threads <= most_in_registers<T>() ? layer_norm_backward_kernel<T, 2, most_in_registers<T>()>
+                        : p.threads <= 512 ? layer_norm_backward_kernel<T, 2, 512>
+                                           : layer_norm_backward_kernel<T, 2, 1024>;
+    const int shared = p.threads > most_in_registers<T>() ? 2 * 2 * 16 / (int)sizeof(T) * 4 * p.threads : 0;  // the sums of two words
+    if (shared) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<p.grid, p.threads, shared, s>>>(a, p.n);
     return cudaGetLastError();
 }
 

@@ -61,6 +61,16 @@ __device__ __forceinline__ float fold(F2 v) {
     const float2 f = f2_get(v);
     return f.x + f.y;
 }
+// Two pairs as one 16-byte word.
+__device__ __forceinline__ void write_quad(float *to, const F2 (&f)[2]) {
+    const float2 u = f2_get(f[0]), v = f2_get(f[1]);
+    *reinterpret_cast<float4 *>(to) = make_float4(u.x, u.y, v.x, v.y);
+}
+__device__ __forceinline__ void read_quad(const float *from, F2 (&f)[2]) {
+    const float4 v = *reinterpret_cast<const float4 *>(from);
+    f[0] = f2(v.x, v.y);
+    f[1] = f2(v.z, v.w);
+}
 __device__ __forceinline__ float ex2_ftz(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

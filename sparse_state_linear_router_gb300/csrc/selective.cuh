@@ -163,17 +163,6 @@ __device__ __forceinline__ void load_quad(const float *p, int c, bool live, F2 (
     f[1] = f2(v.z, v.w);
 }
 
-// Four channels' values in shared memory.
-__device__ __forceinline__ void write_quad(float *to, const F2 (&f)[2]) {
-    const float2 u = f2_get(f[0]), v = f2_get(f[1]);
-    *reinterpret_cast<float4 *>(to) = make_float4(u.x, u.y, v.x, v.y);
-}
-__device__ __forceinline__ void read_quad(const float *from, F2 (&f)[2]) {
-    const float4 v = *reinterpret_cast<const float4 *>(from);
-    f[0] = f2(v.x, v.y);
-    f[1] = f2(v.z, v.w);
-}
-
 // 2 P floats in a row as P pairs.
 template <int P> __device__ __forceinline__ void read_pairs(const float *p, F2 (&f)[P]) {
     static_assert(P % 2 == 0, "whole 16-byte words");
