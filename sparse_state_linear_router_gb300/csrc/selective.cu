@@ -16,42 +16,10 @@ namespace {
 
 
 
-template <typename T> __device__ __forceinline__ float load(const void *p, int64_t i) {
-    if constexpr (sizeof(T) == 2)
-        return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    else
-        return static_cast<const float *>(p)[i];
-}
-template <typename T> __device__ __forceinline__ void store(void *p, int64_t i, float v) {
-    if constexpr (sizeof(T) == 2)
-        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<float *>(p)[i] = v;
-}
-
-__device__ __forceinline__ float sigmoid(float u) { return 1.f / (1.f + expf(-u)); }
-__device__ __forceinline__ float softplus(float u) { return fmaxf(u, 0.f) + log1pf(expf(-fabsf(u))); }
-
 template <int L> __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
-}
-struct Token {  // of a channel
-    float x, d, raw, B[4], C[4];
-};
-template <typename T>
-__device__ __forceinline__ Token token(const SelectiveArgs &a, int64_t t, int c, int at, float bias) {
-    Token k;
-    k.x = load<T>(a.x, t * a.x_stride + c);
-    k.raw = load<T>(a.delta, t * a.delta_stride + c) + bias;
-    k.d = softplus(k.raw);
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        k.B[n] = load<T>(a.B, t * a.b_stride + at + n);
-        k.C[n] = load<T>(a.C, t * a.c_stride + at + n);
-    }
-    return k;
 }
 
 // ---------------------------------------------------------------------------
@@ -334,35 +302,56 @@ __global__ void __launch_bounds__(32, 1) selective_forward_kernel(SelectiveArgs 
     }
 }
 
+// One token of each sequence: L lanes for a pair of channels, four states of both each.  Bound by HBM (the states in and
+// out): 256 x 2048 with 16 states 16.6 us (floor 10.5); one channel and library functions per thread took 25.
 template <typename T, int L>
 __global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, sse_selective_config_t cfg) {
     constexpr int N = 4 * L;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, channel = i / L;
-    const int64_t b = channel / cfg.width;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, pair = i / L;
+    const int pairs = cfg.width / 2, n0 = (int)(i % L) * 4;
+    int64_t b = pair / pairs;
     const bool live = b < a.num_seqs;
     if (!__any_sync(0xffffffffu, live)) return;
-    const int64_t t = live ? b : a.num_seqs - 1;
-    const int c = live ? (int)(channel - b * cfg.width) : cfg.width - 1, n0 = (int)(i % L) * 4;
-    const int g = c / (cfg.width / cfg.groups);
-    const Token k = token<T>(a, t, c, g * N + n0, a.delta_bias ? a.delta_bias[c] : 0.f);
-    float *state = a.final_state + (t * cfg.width + c) * N + n0;
-    float4 h = *reinterpret_cast<const float4 *>(state);
-    const float4 A = *reinterpret_cast<const float4 *>(a.A + (int64_t)c * N + n0);
-    const float u = k.d * k.x;
-    h.x = fmaf(expf(k.d * A.x), h.x, u * k.B[0]);
-    h.y = fmaf(expf(k.d * A.y), h.y, u * k.B[1]);
-    h.z = fmaf(expf(k.d * A.z), h.z, u * k.B[2]);
-    h.w = fmaf(expf(k.d * A.w), h.w, u * k.B[3]);
-    float y = lanes_sum<L>(fmaf(k.C[0], h.x, fmaf(k.C[1], h.y, fmaf(k.C[2], h.z, k.C[3] * h.w))));
-    if (!live) return;
-    *reinterpret_cast<float4 *>(state) = h;
-    if (n0) return;
-    if (a.skip) y = fmaf(a.skip[c], k.x, y);
-    if (a.gate) {
-        const float z = load<T>(a.gate, t * a.gate_stride + c);
-        y *= z * sigmoid(z);
+    if (!live) b = a.num_seqs - 1;
+    const int c = (int)(live ? pair - b * pairs : 0) * 2, at = c / (cfg.width / cfg.groups) * N + n0;
+    float *state = a.final_state + (b * cfg.width + c) * N + n0;
+    F2 h[2][2], A[2][2], B[2], C[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        read_quad(state + k * N, h[k]);
+        read_quad(a.A + (int64_t)(c + k) * N + n0, A[k]);
     }
-    store<T>(a.out, t * cfg.width + c, y);
+    Quad<T>::unpack(*reinterpret_cast<const typename Quad<T>::Raw *>(static_cast<const T *>(a.B) + b * a.b_stride + at), B);
+    Quad<T>::unpack(*reinterpret_cast<const typename Quad<T>::Raw *>(static_cast<const T *>(a.C) + b * a.c_stride + at), C);
+    auto two = [](const void *p, int64_t at) {  // neighbouring channels
+        const typename Two<T>::Raw *v = static_cast<const typename Two<T>::Raw *>(p) + at;
+        return Two<T>::unpack(v[0], v[1]);
+    };
+    auto vector = [&](const float *p) {
+        const float2 v = p ? *reinterpret_cast<const float2 *>(p + c) : make_float2(0.f, 0.f);
+        return f2(v.x, v.y);
+    };
+    F2 none;
+    const F2 x = two(a.x, b * a.x_stride + c);
+    const F2 d = softplus2<false>(add2(two(a.delta, b * a.delta_stride + c), vector(a.delta_bias)), none), in = mul2(d, x);
+    const float2 dv = f2_get(d), iv = f2_get(in);
+    float y[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const F2 dk = both((k ? dv.y : dv.x) * kLog2e), ik = both(k ? iv.y : iv.x);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) h[k][m] = fma2(ex2_ftz(mul2(dk, A[k][m])), h[k][m], mul2(ik, B[m]));
+        y[k] = lanes_sum<L>(fold(fma2(h[k][0], C[0], mul2(h[k][1], C[1]))));
+        if (live) write_quad(state + k * N, h[k]);
+    }
+    if (!live || n0) return;
+    F2 o = fma2(vector(a.skip), x, f2(y[0], y[1]));
+    if (a.gate) {
+        const F2 z = two(a.gate, b * a.gate_stride + c);
+        o = mul2(o, mul2(z, sigmoid2<T>(z)));
+    }
+    T *to = static_cast<T *>(a.out) + b * cfg.width + c;
+    Two<T>::store(to, to + 1, o, true, true);
 }
 
 enum What { kForward, kStep };
@@ -389,7 +378,7 @@ template <typename T, int N> cudaError_t launch_forward(const sse_selective_conf
 template <typename T, int L>
 cudaError_t launch_t(What what, const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
     if (what == kStep) {
-        const int64_t blocks = ((int64_t)a.num_seqs * c.width * L + 255) / 256;
+        const int64_t blocks = ((int64_t)a.num_seqs * (c.width / 2) * L + 255) / 256;
         if (blocks >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
         selective_step_kernel<T, L><<<(unsigned)blocks, 256, 0, s>>>(a, c);
         return cudaGetLastError();
