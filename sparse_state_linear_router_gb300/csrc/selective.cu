@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(32, 1) selective_forward_kernel(SelectiveArgs 
                     F2 B[P];
                     read_pairs(bs + i * N + s * NT, B);
 #pragma unroll
-                    for (int k = 0; k < P; ++k) h[k] = fma2(ex2_ftz(mul2(dc, A[k])), h[k], mul2(xc, B[k]));
+                    for (int k = 0; k < P; ++k) h[k] = fma2(decay2(dc, A[k]), h[k], mul2(xc, B[k]));
                     if constexpr (FULL) {
                         F2 C[P];
                         read_pairs(cs + i * N + s * NT, C);
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, ss
     for (int k = 0; k < 2; ++k) {
         const F2 dk = both((k ? dv.y : dv.x) * kLog2e), ik = both(k ? iv.y : iv.x);
 #pragma unroll
-        for (int m = 0; m < 2; ++m) h[k][m] = fma2(ex2_ftz(mul2(dk, A[k][m])), h[k][m], mul2(ik, B[m]));
+        for (int m = 0; m < 2; ++m) h[k][m] = fma2(decay2(dk, A[k][m]), h[k][m], mul2(ik, B[m]));
         y[k] = lanes_sum<L>(fold(fma2(h[k][0], C[0], mul2(h[k][1], C[1]))));
         if (live) write_quad(state + k * N, h[k]);
     }

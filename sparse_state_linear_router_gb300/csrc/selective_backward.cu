@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
     };
     auto decays = [&](F2 d, F2 (&to)[NT]) {
 #pragma unroll
-        for (int k = 0; k < NT; ++k) to[k] = ex2_ftz(mul2(d, A[k]));
+        for (int k = 0; k < NT; ++k) to[k] = decay2(d, A[k]);
     };
 
     // what the range takes over from those behind it
@@ -388,6 +388,8 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                     return o;
                 };
                 Operands next = operands(from + kSpan - 1);
+                F2 dA_half[NT];  // a sum of its own: 4096 terms one after the other would lose four bits
+                no_states(dA_half);
 #pragma unroll
                 for (int b = kSpan - 1; b >= 0; --b) {
                     const int i = from + b;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                         sum[0] = fma2(o.C[k], now, sum[0]);
                         sum[1] = fma2(o.B[k], gr, sum[1]);
                         sum[2] = fma2(A[k], w, sum[2]);
-                        dA[k] = fma2(d, w, dA[k]);
+                        dA_half[k] = fma2(d, w, dA_half[k]);
                         const float2 fB = f2_get(mul2(gr, x)), fC = f2_get(mul2(dy, now));
                         vB[k] = fB.x + fB.y;
                         vC[k] = fC.x + fC.y;
@@ -441,6 +443,8 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
                         if (a.d_init) put(a.d_init, q, s, e);
                     }
                 }
+#pragma unroll
+                for (int k = 0; k < NT; ++k) dA[k] = add2(dA[k], dA_half[k]);
                 keep(s);
             };
 #pragma unroll 1
