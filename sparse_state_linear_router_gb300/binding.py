@@ -635,6 +635,8 @@ def _rows(what, name, t, rows, width, dtype, device):
     if t.is_contiguous():
         return t.data_ptr(), width
     stride = t.stride()
+    if len(stride) == 2 and stride[1] == 1 and rows > 1 and stride[0] >= width:  # a slice of wider rows, most often
+        return t.data_ptr(), stride[0]
     inner = 1
     for n, s in zip(t.shape[:0:-1], stride[:0:-1]):
         if n != 1 and s != inner:
@@ -869,12 +871,6 @@ def _room(what, workspace, need, device):
     return workspace
 
 
-def _present(what, **tensors):
-    for name, t in tensors.items():
-        if t is None:
-            _refuse(what, f"{name} is None")
-
-
 def conv_forward(cfg, x, weight, cu_seqlens, *, bias=None, initial_state=None, want_final_state=True, out=None,
                  final_state=None):
     """The short causal convolution (sse_conv_forward) over packed sequences;
@@ -884,7 +880,8 @@ def conv_forward(cfg, x, weight, cu_seqlens, *, bias=None, initial_state=None, w
     T, dev = _first(what, x)
     S, W, K, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.taps, _token_dtype(cfg)
     px, sx = _rows(what, "x", x, T, W, dt, dev)
-    _present(what, weight=weight)
+    if weight is None:
+        _refuse(what, "weight is None")
     pi = _state(what, "initial_state", initial_state, (S, K - 1, W), dt, dev)
     po, pf = _packed(what, "out", out, T, W, dt, dev), _state(what, "final_state", final_state, (S, K - 1, W), dt, dev)
     pw, pb = _floats(what, "weight", weight, (W, K), dev), _floats(what, "bias", bias, (W,), dev)
@@ -908,7 +905,8 @@ def conv_backward(cfg, x, weight, cu_seqlens, d_out, *, bias=None, initial_state
     T, dev = _first(what, x)
     S, W, K, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.taps, _token_dtype(cfg)
     px, sx = _rows(what, "x", x, T, W, dt, dev)
-    _present(what, weight=weight, d_out=d_out)
+    if weight is None or d_out is None:
+        _refuse(what, "weight or d_out is None")
     pw, pb = _floats(what, "weight", weight, (W, K), dev), _floats(what, "bias", bias, (W,), dev)
     pd = _packed(what, "d_out", d_out, T, W, dt, dev)
     pi = _state(what, "initial_state", initial_state, (S, K - 1, W), dt, dev)
@@ -929,7 +927,8 @@ def conv_step(cfg, state, x, weight, *, bias=None, out=None):
     B, dev = _first(what, x)
     W, K, dt = cfg.width, cfg.taps, _token_dtype(cfg)
     px, sx = _rows(what, "x", x, B, W, dt, dev)
-    _present(what, state=state, weight=weight)
+    if state is None or weight is None:
+        _refuse(what, "state or weight is None")
     ps = _state(what, "state", state, (B, K - 1, W), dt, dev)
     pw, pb = _floats(what, "weight", weight, (W, K), dev), _floats(what, "bias", bias, (W,), dev)
     if out is None:
@@ -944,7 +943,8 @@ def conv_step(cfg, state, x, weight, *, bias=None, out=None):
 def _selective_inputs(what, cfg, T, dev, x, delta, A, B, C, delta_bias, skip, gate):
     """The arguments from x to gate_stride of the three entry points."""
     W, N, G, dt = cfg.width, cfg.state, cfg.groups, _token_dtype(cfg)
-    _present(what, delta=delta, A=A, B=B, C=C)
+    if delta is None or A is None or B is None or C is None:
+        _refuse(what, "delta, A, B or C is None")
     px, sx = _rows(what, "x", x, T, W, dt, dev)
     pd, sd = _rows(what, "delta", delta, T, W, dt, dev)
     pb, sb = _rows(what, "B", B, T, G * N, dt, dev)
@@ -995,7 +995,8 @@ def selective_backward(cfg, x, delta, A, B, C, cu_seqlens, checkpoints, d_out, *
     T, dev = _first(what, x)
     S, W, N, dt = _sequences(what, cu_seqlens, dev), cfg.width, cfg.state, _token_dtype(cfg)
     args = _selective_inputs(what, cfg, T, dev, x, delta, A, B, C, delta_bias, skip, gate)
-    _present(what, d_out=d_out)
+    if d_out is None:
+        _refuse(what, "d_out is None")
     if checkpoints is None:
         _refuse(what, "checkpoints is None: selective_forward(..., want_checkpoints=True) returns them")
     pc = _floats(what, "checkpoints", checkpoints, (-(-T // SELECTIVE_CHECKPOINT), W, N), dev)
@@ -1020,7 +1021,8 @@ def selective_step(cfg, state, x, delta, A, B, C, *, delta_bias=None, skip=None,
     what = "sse_selective_step"
     rows, dev = _first(what, x)
     args = _selective_inputs(what, cfg, rows, dev, x, delta, A, B, C, delta_bias, skip, gate)
-    _present(what, state=state)
+    if state is None:
+        _refuse(what, "state is None")
     ps = _floats(what, "state", state, (rows, cfg.width, cfg.state), dev)
     if out is None:
         out = _like(x)
@@ -1061,7 +1063,8 @@ def layer_norm_backward(cfg, x, weight, d_out, *, d_residual_out=None, want_d_we
     T, dev = _first(what, x)
     W, dt = cfg.width, _token_dtype(cfg)
     px, sx = _rows(what, "x", x, T, W, dt, dev)
-    _present(what, d_out=d_out)
+    if d_out is None:
+        _refuse(what, "d_out is None")
     pw = _floats(what, "weight", weight, (W,), dev)
     pd = _packed(what, "d_out", d_out, T, W, dt, dev)
     pr = _packed(what, "d_residual_out", d_residual_out, T, W, dt, dev)

@@ -44,13 +44,20 @@ constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596303e-8f;
 // exponents beyond -0.3.)
 __device__ __forceinline__ F2 decay2(F2 d, F2 A) { return ex2_ftz(fma2(d, A, both(2.1e-8f))); }
 
+// -150 at least (exp of it is 0), so that an infinity makes no NaN; a NaN stays one.
+__device__ __forceinline__ float above(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-150.f));
+    return y;
+}
+
 // softplus(v) = max(v, 0) + log1p(exp(-|v|)), log1p(u) = 2 atanh(u / (2 + u)): the odd series of atanh on [0, 1/3] as a
 // polynomial of degree 4 in the square (relative error 8e-9 by its coefficients).  The exponent's rounding is put back to
 // first order: small steps are proportional to exp(v), and a step's relative error goes into a state's whole memory.
 // With SLOPE its derivative 1 / (1 + exp(-v)) from the same exponential.
 template <bool SLOPE> __device__ __forceinline__ F2 softplus2(F2 v, F2 &slope) {
     const float2 f = f2_get(v);
-    const F2 m = f2(-fabsf(f.x), -fabsf(f.y));
+    const F2 m = f2(above(-fabsf(f.x)), above(-fabsf(f.y)));
     const F2 t = mul2(m, both(kLog2e));
     const F2 r = fma2(m, both(kLog2eRest), fma2(m, both(kLog2e), mul2(t, both(-1.f))));
     F2 u = ex2_ftz(t);

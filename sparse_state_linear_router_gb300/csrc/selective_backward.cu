@@ -490,24 +490,23 @@ __global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
     }
 }
 
-// dB and dC from the CTAs' rows, four states per thread.
+// dB and dC from the CTAs' rows, four values per thread.
 template <typename T>
 __global__ void __launch_bounds__(256) selective_tokens_kernel(SelectiveArgs a, int groups, int N, const float *sums, int parts) {
-    const int row = groups * N / 4;
+    const int row = groups * N / 2;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / row;
     if (t >= clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens)) return;
-    const int at = (int)(i - t * row) * 4, g = at / N, n = at % N;
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int p = 0; p < parts; ++p) {
-            const float4 v = *reinterpret_cast<const float4 *>(sums + (((int64_t)p * a.total_tokens + t) * groups + g) * 2 * N + m * N + n);
-            s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        const F2 f[2] = {f2(s.x, s.y), f2(s.z, s.w)};
-        *reinterpret_cast<typename Quad<T>::Raw *>(static_cast<T *>(m ? a.d_C : a.d_B) + t * groups * N + at) = Quad<T>::pack(f);
+    const int at = (int)(i - t * row) * 4, g = at / (2 * N), n = at % (2 * N);
+    const int64_t part = (int64_t)a.total_tokens * groups * 2 * N;
+    const float *from = sums + (t * groups + g) * 2 * N + n;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 16
+    for (int p = 0; p < parts; ++p) {
+        const float4 v = *reinterpret_cast<const float4 *>(from + p * part);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
+    const F2 f[2] = {f2(s.x, s.y), f2(s.z, s.w)};
+    *reinterpret_cast<typename Quad<T>::Raw *>(static_cast<T *>(n < N ? a.d_B : a.d_C) + (t * groups + g) * N + n % N) = Quad<T>::pack(f);
 }
 
 // The weights' gradients from the ranges' sums.
@@ -556,7 +555,7 @@ template <typename T, int N> cudaError_t launch_t(const sse_selective_config_t &
     if (e != cudaSuccess) return e;
     if (sh.ranges > 1) states<<<dim3(sh.tiles * c.groups, sh.ranges), 32, kStates, s>>>(a, sh, wk);
     full<<<dim3(wk.parts * c.groups, sh.ranges), 32 * Layout<T, N, true>::kWarps, kFull, s>>>(a, sh, wk);
-    const int64_t rows = (int64_t)a.total_tokens * c.groups * N / 4;
+    const int64_t rows = (int64_t)a.total_tokens * c.groups * N / 2;
     if (rows > 0)
         selective_tokens_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a, c.groups, N, wk.tokens, wk.parts);
     selective_weights_kernel<<<(c.width * (N + 2) + 127) / 128, 128, 0, s>>>(a, c.width, N, wk.weights, sh.ranges);
