@@ -12,6 +12,13 @@
 // row takes one barrier and no sum of squares about a distant zero.  The
 // backward's sums p and p (x - m) go with them: sum p (x - mean) is the sum of
 // [p (x - m)] + (m - mean) [p] over the warps.  Rows of one warp take no barrier.
+//
+// Measured on a GB300, bf16 (floors at 6.77 TB/s): forward with residual 16384 x 2304
+// 53 us (44.6), 16384 x 2048 48 (39.7), 32768 x 1024 46, 4096 x 8192 47; backward with
+// the residual's gradient 16384 x 2048 66 (39.7), 4096 x 8192 95, 8192 x 2048 in float32
+// 53.  Rows loaded when their turn came took 66, 95 and 88 us for the first, the
+// backward and the widest.  The backward is held by the row's chain (load, two rounds of
+// shuffles, barrier) with 12 warps on an SM at 168 registers: DRAM 51 %, issue 44 %.
 #include "quad.cuh"
 
 namespace sse {

@@ -1,6 +1,6 @@
 // selective.cuh -- what the forward and the backward of the selective scan share:
-// ranges of the packed token axis, tiles of 16 tokens by 32 channels, and their
-// staging.
+// ranges of the packed token axis, the steps and their decays, tiles of 16 tokens and
+// their staging.
 #pragma once
 
 #include "quad.cuh"

@@ -7,14 +7,26 @@
 //   1. steps D and D x, dy, B and C in float32 to shared memory, lanes over
 //      (token, four channels);
 //   2. in halves of 8 tokens, the later one first: forwards from the checkpoint,
-//      the states before the half's tokens in registers; then backwards: g = C dy + e, e = a g, and this thread's parts of the
-//      sums over states (y, sum B g, sum A g a h) and over channels (dB, dC);
+//      the decays and the states before the half's tokens in registers; then
+//      backwards: g = C dy + e, e = a g, and this thread's parts of the sums over
+//      states (y, sum B g, sum A g a h) and over channels (dB, dC);
 //   3. the sums over states, lanes over (token, four channels), and with them
 //      dx, d_delta, d_gate.
 // The sums over channels go over the eight pairs of a warp by shuffles, over the
 // four warps of a CTA through shared memory, and over the CTAs of a group in a
 // second kernel: a float32 row of 2 N for each token and 64 channels.  Every sum
-// has a fixed order.
+// has a fixed order.  B and C are in shared memory twice over, so that a pair over
+// the channels takes a value as it is.
+//
+// Bound by instructions: about 48 of a warp for 64 (token, channel, state), 19 of them
+// arithmetic of pairs and 9 the sums over channels, against 14 bytes and 16
+// exponentials for a token and channel (159 us of HBM, 115 of exponentials for 8 x 4096
+// x 2048 with 16 states).  Measured on a GB300, bf16: 1510 us there, 1632 as one
+// sequence of 32768, 24001 x 2048 in 16 ragged sequences 1363, 64 x 512 x 512 414;
+// issue 46 %, shared memory's pipe 57 %, FMA 41 %.  255 registers leave eight warps to
+// an SM.  Spans of 4 tokens, whose 168 registers let twelve in, took 2623 us (1.75
+// passes forwards instead of 1.5, and what did not fit in registers went to L2, shared
+// memory having taken the L1); every step of a tile through shared memory 1655.
 #include <type_traits>
 
 #include "selective.cuh"
@@ -24,7 +36,7 @@ namespace {
 
 constexpr int kL = 4, kCols = 16;
 constexpr int kAlone = 1000;  // warps that sequences make by themselves, for a range each
-constexpr int kSpan = 8;  // tokens whose states are held in registers, and of an epilogue
+constexpr int kSpan = 8;      // tokens whose states are held in registers, and of an epilogue
 
 template <typename T, int N, bool FULL> struct Layout {
     static constexpr int NT = N == 8 ? 2 : 4, SL = N / (kL * NT);
@@ -58,8 +70,8 @@ struct BackwardWork {
 // FULL: the gradients.  Otherwise what an earlier range starts from: e at the range's first token from nothing behind it
 // (or from the sequence that ends in it), and the sum of its steps.
 template <typename T, int N, bool FULL>
-__global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1) selective_backward_kernel(SelectiveArgs a, SelectiveShape sh,
-                                                                                    BackwardWork wk) {
+__global__ void __launch_bounds__(32 * Layout<T, N, FULL>::kWarps, FULL ? 2 : 1)
+selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     using Lay = Layout<T, N, FULL>;
     using Raw = typename Quad<T>::Raw;
     constexpr int NT = Lay::NT, SL = Lay::SL, kQuads = kCols / 4, kWarps = Lay::kWarps;
