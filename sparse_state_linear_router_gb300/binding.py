@@ -635,7 +635,8 @@ def _rows(what, name, t, rows, width, dtype, device):
     if t.is_contiguous():
         return t.data_ptr(), width
     stride = t.stride()
-    if len(stride) == 2 and stride[1] == 1 and rows > 1 and stride[0] >= width:  # a slice of wider rows, most often
+    if rows > 1 and stride[0] >= width and stride[-1] == 1 and (
+            len(stride) == 2 or len(stride) == 3 and stride[1] == t.shape[2]):  # a slice of wider rows, most often
         return t.data_ptr(), stride[0]
     inner = 1
     for n, s in zip(t.shape[:0:-1], stride[:0:-1]):
