@@ -14,11 +14,12 @@
 // [p (x - m)] + (m - mean) [p] over the warps.  Rows of one warp take no barrier.
 //
 // Measured on a GB300, bf16 (floors at 6.77 TB/s): forward with residual 16384 x 2304
-// 53 us (44.6), 16384 x 2048 48 (39.7), 32768 x 1024 46, 4096 x 8192 47; backward with
-// the residual's gradient 16384 x 2048 66 (39.7), 4096 x 8192 95, 8192 x 2048 in float32
-// 53.  Rows loaded when their turn came took 66, 95 and 88 us for the first, the
-// backward and the widest.  The backward is held by the row's chain (load, two rounds of
-// shuffles, barrier) with 12 warps on an SM at 168 registers: DRAM 51 %, issue 44 %.
+// 53 us (44.6), 16384 x 2048 48 (39.7), 32768 x 1024 47, 4096 x 8192 48; backward with
+// the residual's gradient 16384 x 2048 57 (39.7), 32768 x 1024 56, 4096 x 8192 74, 8192 x
+// 2048 in float32 51.  Rows loaded when their turn came took 66 us for the first and 95
+// for the backward.  The backward's rows wait in shared memory, so that what a row keeps
+// over its sums is there and not in registers, and the columns' weights are in registers:
+// 16 warps on an SM instead of 12 and no loads of weights, 66 -> 57 us (either alone 68).
 #include "quad.cuh"
 
 namespace sse {
@@ -80,25 +81,46 @@ __device__ __forceinline__ int warp_elements(const LnShape &n, int w, int vpt, i
 }
 
 // Joins the warps' words {mean, M2, sum p, sum p (x - mean)} of a row; all threads of the team call it.  `turn` alternates
-// between the rows, so that one barrier a row is enough.
-template <int N>
-__device__ __forceinline__ void join(const LnShape &n, float4 &v, int vpt, int e, int warp, int lane, int turn, float4 *words) {
+// between the rows, so that one barrier a row is enough.  Every warp but the last has `whole` elements.
+template <int N, int VPT, int E, int MAXW>
+__device__ __forceinline__ void join(const LnShape &n, float4 &v, int warp, int lane, int turn, float4 *words) {
     if (n.warps == 1) return;
+    constexpr float whole = 32 * VPT * E;
+    const float last = (float)warp_elements(n, n.warps - 1, VPT, E);
     if (lane == 0) words[turn * 32 + warp] = v;
     __syncthreads();
     float mean = 0.f;
-    for (int w = 0; w < n.warps; ++w) mean = fmaf((float)warp_elements(n, w, vpt, e), words[turn * 32 + w].x, mean);
-    mean *= n.inv_width;
-    float4 t = make_float4(mean, 0.f, 0.f, 0.f);
-    for (int w = 0; w < n.warps; ++w) {
-        const float4 u = words[turn * 32 + w];
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int w, const float4 &u) {
         const float d = u.x - mean;
-        t.y += fmaf((float)warp_elements(n, w, vpt, e) * d, d, u.y);
+        t.y += fmaf((w + 1 == n.warps ? last : whole) * d, d, u.y);
         if constexpr (N == 4) {
             t.z += u.z;
             t.w += fmaf(d, u.z, u.w);
         }
+    };
+    if constexpr (N == 4 && MAXW <= 4) {
+        float4 u[MAXW];
+#pragma unroll
+        for (int w = 0; w < MAXW; ++w) {
+            if (w >= n.warps) break;
+            u[w] = words[turn * 32 + w];
+            mean = fmaf(w + 1 == n.warps ? last : whole, u[w].x, mean);
+        }
+        mean *= n.inv_width;
+#pragma unroll
+        for (int w = 0; w < MAXW; ++w) {
+            if (w >= n.warps) break;
+            add(w, u[w]);
+        }
+    } else {
+#pragma unroll 4
+        for (int w = 0; w < n.warps; ++w) mean = fmaf(w + 1 == n.warps ? last : whole, words[turn * 32 + w].x, mean);
+        mean *= n.inv_width;
+#pragma unroll 4
+        for (int w = 0; w < n.warps; ++w) add(w, words[turn * 32 + w]);
     }
+    t.x = mean;
     v = t;
 }
 
@@ -112,6 +134,35 @@ template <typename T, int VPT> struct Words {
             u[i] = ok && first + i * 32 < n.nv ? *reinterpret_cast<const uint4 *>(at + i * 32 * Word<T>::kE) : make_uint4(0, 0, 0, 0);
     }
 };
+// The words of the next DEPTH rows of TENSORS tensors in shared memory, each copied by the thread that reads it: no barrier.
+template <typename T, int VPT, int TENSORS, int DEPTH> struct Ahead {
+    static constexpr int kBytes = DEPTH * TENSORS * VPT * 16;  // of a thread
+    uint32_t at;
+    __device__ __forceinline__ Ahead(const void *ring) : at((uint32_t)__cvta_generic_to_shared(ring) + threadIdx.x * 16) {}
+    __device__ __forceinline__ uint32_t word(int slot, int tensor, int i) const {
+        return at + ((slot * TENSORS + tensor) * VPT + i) * blockDim.x * 16;
+    }
+    // Zeros where there is no word.
+    __device__ __forceinline__ void copy(const LnShape &n, int slot, int tensor, const void *p, int64_t stride, int64_t row, int first,
+                                         bool ok) const {
+        const T *from = static_cast<const T *>(p) + (ok ? row * stride + first * Word<T>::kE : 0);
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const bool live = ok && first + i * 32 < n.nv;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(word(slot, tensor, i)),
+                         "l"(live ? static_cast<const void *>(from + i * 32 * Word<T>::kE) : p), "r"(live ? 16 : 0) : "memory");
+        }
+    }
+    static __device__ __forceinline__ void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // Until the oldest row is there.
+    static __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+    __device__ __forceinline__ uint4 read(int slot, int tensor, int i) const {
+        uint4 u;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
+                     : "r"(word(slot, tensor, i)) : "memory");
+        return u;
+    }
+};
 // Word j of a float32 vector.
 template <typename T> __device__ __forceinline__ void vector_word(const float *p, int j, F2 (&f)[Word<T>::kP]) {
 #pragma unroll
@@ -122,9 +173,11 @@ template <typename T> __device__ __forceinline__ void vector_word(const float *p
     }
 }
 
-// Threads of a row up to which the backward has its column sums in registers: 168 a thread (float32, whose words are half as
-// many elements, 128).
-template <typename T> constexpr int most_in_registers() { return sizeof(T) == 2 ? 384 : 512; }
+// Threads of a row up to which the backward has its column sums in registers: 128 a thread.
+constexpr int kInRegisters = 512;
+
+// Rows that the backward has on their way: two, or one where shared memory has the column sums.
+constexpr int rows_ahead(int threads) { return threads > kInRegisters ? 1 : 2; }
 
 // The next row's words are loaded while this one's are at work.
 template <typename T, int VPT, int MAXT>
@@ -170,7 +223,7 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1) layer_norm_kernel(L
                     t = fma2(d, d, t);
                 }
         m.y = warp_sum(fold(t));
-        join<2>(n, m, VPT, E, warp, lane, turn, words);
+        join<2, VPT, E, MAXT / 32>(n, m, warp, lane, turn, words);
         turn ^= 1;
         const float rstd = rsqrt_ftz(fmaf(m.y, n.inv_width, n.eps));
 #pragma unroll
@@ -194,7 +247,8 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1) layer_norm_kernel(L
 }
 
 template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4) layer_norm_backward_kernel(LayerNormArgs a, LnShape n) {
+__global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : VPT == 1 || sizeof(T) == 4 ? 5 : 4)
+layer_norm_backward_kernel(LayerNormArgs a, LnShape n) {
     constexpr int E = Word<T>::kE, P = Word<T>::kP;
     __shared__ float4 words[64];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
@@ -203,8 +257,10 @@ __global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4)
     const int64_t first = n.warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + wid : blockIdx.x;
     const float inv_mine = 1.f / (float)warp_elements(n, warp, VPT, E);
     // column sums: in registers, or where there are too few, in words of shared memory of the thread's own
-    constexpr bool SHARED = MAXT > most_in_registers<T>();
+    constexpr bool SHARED = MAXT > kInRegisters;
     extern __shared__ __align__(16) float sums[];
+    using Rows = Ahead<T, VPT, 3, rows_ahead(MAXT)>;
+    const Rows ahead(sums + (SHARED ? VPT * P * 4 * blockDim.x : 0));
     F2 sum_w[SHARED ? 1 : VPT][P], sum_b[SHARED ? 1 : VPT][P];
     auto mine = [&](int which, int i, int k) { return sums + (((which * VPT + i) * (P / 2) + k / 2) * blockDim.x + threadIdx.x) * 4; };
 #pragma unroll
@@ -220,19 +276,32 @@ __global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4)
             }
         }
     int turn = 0;
-    Words<T, VPT> x, dy, dr;
-    x.load(n, a.x, a.x_stride, first, j0, first < a.T);
-    dy.load(n, a.d_out, n.width, first, j0, first < a.T);
-    for (int64_t row = first; row < a.T; row += rows_on) {
-        F2 v[VPT][P], d[VPT][P];
+    auto copy = [&](int slot, int64_t row) {
+        ahead.copy(n, slot, 0, a.x, a.x_stride, row, j0, row < a.T);
+        ahead.copy(n, slot, 1, a.d_out, n.width, row, j0, row < a.T);
+        if (a.d_r_out) ahead.copy(n, slot, 2, a.d_r_out, n.width, row, j0, row < a.T);
+        Rows::commit();
+    };
+    constexpr int kDepth = rows_ahead(MAXT);
+    // the columns' weights, from L1 row by row where the column sums are not in registers either
+    F2 w[SHARED ? 1 : VPT][P];
+    auto weights = [&](int i, int j) {
+        if (SHARED && a.weight) vector_word<T>(a.weight, j, w[0]);
+    };
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            Word<T>::unpack(x.u[i], v[i]);
-            Word<T>::unpack(dy.u[i], d[i]);
-        }
-        if (a.d_r_out) dr.load(n, a.d_r_out, n.width, row, j0, true);
-        x.load(n, a.x, a.x_stride, row + rows_on, j0, row + rows_on < a.T);
-        dy.load(n, a.d_out, n.width, row + rows_on, j0, row + rows_on < a.T);
+    for (int i = 0; i < (SHARED ? 1 : VPT); ++i) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) w[i][k] = both(1.f);
+        if (!SHARED && a.weight && j0 + i * 32 < n.nv) vector_word<T>(a.weight, j0 + i * 32, w[i]);
+    }
+#pragma unroll
+    for (int k = 0; k < kDepth; ++k) copy(k, first + k * rows_on);
+    int slot = 0;
+    for (int64_t row = first; row < a.T; row += rows_on) {
+        F2 v[VPT][P];
+        Rows::wait();
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) Word<T>::unpack(ahead.read(slot, 0, i), v[i]);
         F2 t = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -245,12 +314,13 @@ __global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4)
         for (int i = 0; i < VPT; ++i) {
             const int j = j0 + i * 32;
             if (j >= n.nv) continue;
-            F2 w[P];
-            if (a.weight) vector_word<T>(a.weight, j, w);
+            F2 d[P];
+            weights(i, j);
+            Word<T>::unpack(ahead.read(slot, 1, i), d);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
                 const F2 c = add2(v[i][k], both(-m.x));
-                const F2 p = a.weight ? mul2(d[i][k], w[k]) : d[i][k];
+                const F2 p = mul2(d[k], w[SHARED ? 0 : i][k]);
                 sq = fma2(c, c, sq);
                 sp = add2(sp, p);
                 sx = fma2(p, c, sx);
@@ -259,7 +329,7 @@ __global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4)
         m.y = warp_sum(fold(sq));
         m.z = warp_sum(fold(sp));
         m.w = warp_sum(fold(sx));
-        join<4>(n, m, VPT, E, warp, lane, turn, words);
+        join<4, VPT, E, MAXT / 32>(n, m, warp, lane, turn, words);
         turn ^= 1;
         const float rstd = rsqrt_ftz(fmaf(m.y, n.inv_width, n.eps));
         const float mean_p = m.z * n.inv_width, slope = m.w * n.inv_width * rstd * rstd;  // mean(p x_hat) rstd
@@ -267,19 +337,20 @@ __global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4)
         for (int i = 0; i < VPT; ++i) {
             const int j = j0 + i * 32;
             if (j >= n.nv) continue;
-            F2 e[P], w[P];
-            if (a.d_r_out) Word<T>::unpack(dr.u[i], e);
-            if (a.weight) vector_word<T>(a.weight, j, w);
+            F2 v[P], d[P], e[P];
+            weights(i, j);
+            Word<T>::unpack(ahead.read(slot, 0, i), v);
+            Word<T>::unpack(ahead.read(slot, 1, i), d);
+            if (a.d_r_out) Word<T>::unpack(ahead.read(slot, 2, i), e);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                const F2 c = add2(v[i][k], both(-m.x));
-                if constexpr (SHARED) {
-                    v[i][k] = mul2(c, both(rstd));  // x_hat, for the sums below
-                } else {
-                    sum_w[i][k] = fma2(d[i][k], mul2(c, both(rstd)), sum_w[i][k]);
-                    sum_b[i][k] = add2(sum_b[i][k], d[i][k]);
+                const F2 c = add2(v[k], both(-m.x));
+                v[k] = mul2(c, both(rstd));  // x_hat
+                if constexpr (!SHARED) {
+                    sum_w[i][k] = fma2(d[k], v[k], sum_w[i][k]);
+                    sum_b[i][k] = add2(sum_b[i][k], d[k]);
                 }
-                F2 p = a.weight ? mul2(d[i][k], w[k]) : d[i][k];
+                F2 p = mul2(d[k], w[SHARED ? 0 : i][k]);
                 p = mul2(fma2(c, both(-slope), add2(p, both(-mean_p))), both(rstd));
                 e[k] = a.d_r_out ? add2(p, e[k]) : p;
             }
@@ -292,14 +363,16 @@ __global__ void __launch_bounds__(MAXT, MAXT > 128 ? 1 : sizeof(T) == 2 ? 3 : 4)
                     read_quad(mine(1, i, k), b);
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        w[q] = fma2(d[i][k + q], v[i][k + q], w[q]);
-                        b[q] = add2(b[q], d[i][k + q]);
+                        w[q] = fma2(d[k + q], v[k + q], w[q]);
+                        b[q] = add2(b[q], d[k + q]);
                     }
                     write_quad(mine(0, i, k), w);
                     write_quad(mine(1, i, k), b);
                 }
             }
         }
+        copy(slot, row + kDepth * rows_on);
+        slot = slot + 1 == kDepth ? 0 : slot + 1;
     }
     griddep_launch_dependents();
     // this team's column sums: one partial row of each
@@ -367,8 +440,9 @@ LnPlan plan(const sse_layer_norm_config_t &c, int64_t T, bool backward) {
     p.n.warps = (p.n.nv + 32 * p.vpt - 1) / (32 * p.vpt);
     p.teams = p.n.warps == 1 ? 4 : 1;
     p.threads = 32 * p.n.warps * p.teams;
-    // as many as an SM holds: 128 registers a thread; backward 168 for bf16 up to 384 threads, 64 with more than 512
-    int per_sm = (backward && p.threads <= 384 && c.dtype == SSE_BF16 ? 384 : p.threads <= 512 ? 512 : 1024) / p.threads;
+    // as many as an SM holds: 128 registers a thread; backward 96 for rows of few words, 64 with more than 512 threads
+    const bool small = backward && p.threads <= 128 && (p.vpt == 1 || c.dtype == SSE_F32);
+    int per_sm = (small ? 640 : p.threads <= 512 ? 512 : 1024) / p.threads;
     if (per_sm < 1) per_sm = 1;
     const int64_t need = (T + p.teams - 1) / p.teams, hold = (int64_t)kSms * per_sm;
     p.grid = (int)(need < hold ? need : hold);
@@ -385,19 +459,23 @@ template <typename T> cudaError_t launch_forward(const LnPlan &p, const LayerNor
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t launch_backward(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
-    const auto kernel = p.vpt == 1         ? layer_norm_backward_kernel<T, 1, 128>
-                        : p.threads <= 128 ? layer_norm_backward_kernel<T, 2, 128>
-                        : p.threads <= most_in_registers<T>() ? layer_norm_backward_kernel<T, 2, most_in_registers<T>()>
-                        : p.threads <= 512 ? layer_norm_backward_kernel<T, 2, 512>
-                                           : layer_norm_backward_kernel<T, 2, 1024>;
-    const int shared = p.threads > most_in_registers<T>() ? 2 * 2 * 16 / (int)sizeof(T) * 4 * p.threads : 0;  // the sums of two words
-    if (shared) {
-        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+template <typename T, int VPT, int MAXT> cudaError_t launch_backward_t(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
+    const auto kernel = layer_norm_backward_kernel<T, VPT, MAXT>;
+    constexpr int kSums = MAXT > kInRegisters ? VPT * 16 / (int)sizeof(T) / 2 * 16 : 0;
+    constexpr int kBytes = kSums + Ahead<T, VPT, 3, rows_ahead(MAXT)>::kBytes;  // of a thread
+    static_assert(kBytes * MAXT + 1024 <= 227 * 1024, "shared memory");
+    if constexpr (kBytes * MAXT > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes * MAXT);
         if (e != cudaSuccess) return e;
     }
-    kernel<<<p.grid, p.threads, shared, s>>>(a, p.n);
+    kernel<<<p.grid, p.threads, kBytes * p.threads, s>>>(a, p.n);
     return cudaGetLastError();
+}
+template <typename T> cudaError_t launch_backward(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
+    if (p.vpt == 1) return launch_backward_t<T, 1, 128>(p, a, s);
+    if (p.threads <= 128) return launch_backward_t<T, 2, 128>(p, a, s);
+    if (p.threads <= kInRegisters) return launch_backward_t<T, 2, kInRegisters>(p, a, s);
+    return launch_backward_t<T, 2, 1024>(p, a, s);
 }
 
 }  // namespace
