@@ -14,12 +14,13 @@
 // [p (x - m)] + (m - mean) [p] over the warps.  Rows of one warp take no barrier.
 //
 // Measured on a GB300, bf16 (floors at 6.77 TB/s): forward with residual 16384 x 2304
-// 53 us (44.6), 16384 x 2048 48 (39.7), 32768 x 1024 47, 4096 x 8192 48; backward with
-// the residual's gradient 16384 x 2048 57 (39.7), 32768 x 1024 56, 4096 x 8192 74, 8192 x
-// 2048 in float32 51.  Rows loaded when their turn came took 66 us for the first and 95
-// for the backward.  The backward's rows wait in shared memory, so that what a row keeps
+// 51 us (44.6), 16384 x 2048 46 (39.7), 32768 x 1024 47, 4096 x 8192 48, without
+// residual 16384 x 2048 29 (19.8), 65536 x 512 25; backward with the residual's gradient
+// 16384 x 2048 57 (39.7), 32768 x 1024 56, 4096 x 8192 74, 8192 x 2048 in float32 52.
+// Rows loaded when their turn came took 66 us for the first and 95 for the backward.
+// The backward's rows wait in shared memory, so that what a row keeps
 // over its sums is there and not in registers, and the columns' weights are in registers:
-// 16 warps on an SM instead of 12 and no loads of weights, 66 -> 57 us (either alone 68).
+// 16 warps on an SM instead of 12 and no loads of weights, 66 -> 57 us (the first alone 68).
 #include "quad.cuh"
 
 namespace sse {
@@ -142,13 +143,14 @@ template <typename T, int VPT, int TENSORS, int DEPTH> struct Ahead {
     __device__ __forceinline__ uint32_t word(int slot, int tensor, int i) const {
         return at + ((slot * TENSORS + tensor) * VPT + i) * blockDim.x * 16;
     }
-    // Zeros where there is no word.
+    // Nothing for a row that is not there (nobody reads it), zeros where the row has no word.
     __device__ __forceinline__ void copy(const LnShape &n, int slot, int tensor, const void *p, int64_t stride, int64_t row, int first,
                                          bool ok) const {
-        const T *from = static_cast<const T *>(p) + (ok ? row * stride + first * Word<T>::kE : 0);
+        if (!ok) return;
+        const T *from = static_cast<const T *>(p) + row * stride + first * Word<T>::kE;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const bool live = ok && first + i * 32 < n.nv;
+            const bool live = first + i * 32 < n.nv;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(word(slot, tensor, i)),
                          "l"(live ? static_cast<const void *>(from + i * 32 * Word<T>::kE) : p), "r"(live ? 16 : 0) : "memory");
         }
@@ -176,37 +178,75 @@ template <typename T> __device__ __forceinline__ void vector_word(const float *p
 // Threads of a row up to which the backward has its column sums in registers: 128 a thread.
 constexpr int kInRegisters = 512;
 
+// Threads of an SM that the forward's registers allow: 64 a thread for one word, 96 (float32 80) for two, else 128.
+constexpr int forward_threads(int vpt, int bytes) { return vpt == 1 ? 1024 : vpt > 2 ? 512 : bytes == 2 ? 640 : 768; }
+
 // Rows that the backward has on their way: two, or one where shared memory has the column sums.
 constexpr int rows_ahead(int threads) { return threads > kInRegisters ? 1 : 2; }
 
-// The next row's words are loaded while this one's are at work.
+// Rows of up to two words a thread have the columns' weights and bias in registers and two rows under way in shared memory
+// (without residual: 65536 x 512 33 -> 25 us, 16384 x 2048 34.5 -> 29); wider ones load the vectors from L1 row by row and
+// the next row to registers (4096 x 8192 48 us; through shared memory 53).
 template <typename T, int VPT, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1) layer_norm_kernel(LayerNormArgs a, LnShape n) {
+__global__ void __launch_bounds__(MAXT, forward_threads(VPT, sizeof(T)) / MAXT) layer_norm_kernel(LayerNormArgs a, LnShape n) {
     constexpr int E = Word<T>::kE, P = Word<T>::kP;
+    constexpr bool HELD = VPT <= 2;
     __shared__ float4 words[64];
+    extern __shared__ __align__(16) float ring[];
+    using Rows = Ahead<T, VPT, 2, 2>;
+    const Rows ahead(ring);
+    Words<T, VPT> x, r;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     const int warp = n.warps == 1 ? 0 : wid, j0 = warp * VPT * 32 + lane;
     const int64_t rows_on = n.warps == 1 ? (int64_t)gridDim.x * (blockDim.x >> 5) : gridDim.x;
     const int64_t first = n.warps == 1 ? (int64_t)blockIdx.x * (blockDim.x >> 5) + wid : blockIdx.x;
-    const float mine = (float)warp_elements(n, warp, VPT, E), inv_mine = 1.f / mine;
+    const float inv_mine = 1.f / (float)warp_elements(n, warp, VPT, E);
+    auto fetch = [&](int slot, int64_t row) {
+        const bool ok = row < a.T;
+        if constexpr (HELD) {
+            ahead.copy(n, slot, 0, a.x, a.x_stride, row, j0, ok);
+            if (a.r) ahead.copy(n, slot, 1, a.r, a.r_stride, row, j0, ok);
+            Rows::commit();
+        } else {
+            x.load(n, a.x, a.x_stride, row, j0, ok);
+            if (a.r) r.load(n, a.r, a.r_stride, row, j0, ok);
+        }
+    };
+    fetch(0, first);
+    if constexpr (HELD) fetch(1, first + rows_on);
+    F2 w[HELD ? VPT : 1][P], b[HELD ? VPT : 1][P];
+    auto vectors = [&](int i, int j) {
+        if (a.weight) vector_word<T>(a.weight, j, w[i]);
+        if (a.bias) vector_word<T>(a.bias, j, b[i]);
+    };
+#pragma unroll
+    for (int i = 0; i < (HELD ? VPT : 1); ++i) {
+#pragma unroll
+        for (int k = 0; k < P; ++k) w[i][k] = both(1.f), b[i][k] = both(0.f);
+        if (HELD && j0 + i * 32 < n.nv) vectors(i, j0 + i * 32);
+    }
     int turn = 0;
-    Words<T, VPT> x, r;
-    x.load(n, a.x, a.x_stride, first, j0, first < a.T);
-    r.load(n, a.r, a.r_stride, first, j0, a.r && first < a.T);
     for (int64_t row = first; row < a.T; row += rows_on) {
         F2 v[VPT][P];
+        if constexpr (HELD) {
+            Rows::wait();
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                x.u[i] = ahead.read(turn, 0, i);
+                if (a.r) r.u[i] = ahead.read(turn, 1, i);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             Word<T>::unpack(x.u[i], v[i]);
             if (a.r) {
-                F2 w[P];
-                Word<T>::unpack(r.u[i], w);
+                F2 f[P];
+                Word<T>::unpack(r.u[i], f);
 #pragma unroll
-                for (int k = 0; k < P; ++k) v[i][k] = add2(v[i][k], w[k]);
+                for (int k = 0; k < P; ++k) v[i][k] = add2(v[i][k], f[k]);
             }
         }
-        x.load(n, a.x, a.x_stride, row + rows_on, j0, row + rows_on < a.T);
-        if (a.r) r.load(n, a.r, a.r_stride, row + rows_on, j0, row + rows_on < a.T);
+        fetch(turn, row + (HELD ? 2 : 1) * rows_on);
         F2 t = both(0.f);
 #pragma unroll
         for (int i = 0; i < VPT; ++i)
@@ -228,19 +268,13 @@ __global__ void __launch_bounds__(MAXT, MAXT == 128 ? 4 : 1) layer_norm_kernel(L
         const float rstd = rsqrt_ftz(fmaf(m.y, n.inv_width, n.eps));
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            const int j = j0 + i * 32;
+            const int j = j0 + i * 32, h = HELD ? i : 0;
             if (j >= n.nv) continue;
             const int64_t at = row * n.width + j * E;
             if (a.r_out) *reinterpret_cast<uint4 *>(static_cast<T *>(a.r_out) + at) = Word<T>::pack(v[i]);
-            F2 w[P], b[P];
-            if (a.weight) vector_word<T>(a.weight, j, w);
-            if (a.bias) vector_word<T>(a.bias, j, b);
+            if (!HELD) vectors(0, j);
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                v[i][k] = mul2(add2(v[i][k], both(-m.x)), both(rstd));
-                if (a.weight) v[i][k] = mul2(v[i][k], w[k]);
-                if (a.bias) v[i][k] = add2(v[i][k], b[k]);
-            }
+            for (int k = 0; k < P; ++k) v[i][k] = fma2(mul2(add2(v[i][k], both(-m.x)), both(rstd)), w[h][k], b[h][k]);
             *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + at) = Word<T>::pack(v[i]);
         }
     }
@@ -427,36 +461,47 @@ struct LnPlan {
     int grid;
 };
 
-// Up to `most` words per thread.  Rows of one warp share a CTA of four.
-LnPlan plan(const sse_layer_norm_config_t &c, int64_t T, bool backward) {
+// Up to `most` words per thread.  Rows of one warp share a CTA of four.  With a residual 384 threads of an SM (512 in
+// larger CTAs) are enough for HBM, and more in the way of each other (16384 x 2048: 45 us with 384, 48 with 512, 50 with 640;
+// 16384 x 2304 51 with 480, 56 with 640); without, 29 us with 640 and 35 with 384.
+LnPlan plan(const sse_layer_norm_config_t &c, int64_t T, bool backward, bool residual) {
     LnPlan p{};
-    const int most = backward ? 2 : 4;
     p.n.width = c.width;
     p.n.nv = c.width / (c.dtype == SSE_BF16 ? 8 : 4);
     p.n.eps = c.eps;
+    const int most = backward || p.n.nv <= 512 ? 2 : 4;
     p.n.inv_width = 1.f / c.width;
     p.n.warps = (p.n.nv + 32 * most - 1) / (32 * most);
     p.vpt = (p.n.nv + 32 * p.n.warps - 1) / (32 * p.n.warps);
     p.n.warps = (p.n.nv + 32 * p.vpt - 1) / (32 * p.vpt);
     p.teams = p.n.warps == 1 ? 4 : 1;
     p.threads = 32 * p.n.warps * p.teams;
-    // as many as an SM holds: 128 registers a thread; backward 96 for rows of few words, 64 with more than 512 threads
-    const bool small = backward && p.threads <= 128 && (p.vpt == 1 || c.dtype == SSE_F32);
-    int per_sm = (small ? 640 : p.threads <= 512 ? 512 : 1024) / p.threads;
+    // as many as an SM holds; backward: 96 registers a thread for rows of few words, 128, 64 with more than 512 threads
+    const bool small = p.threads <= 128 && (p.vpt == 1 || c.dtype == SSE_F32);
+    const int hold_threads = !backward ? forward_threads(p.vpt, c.dtype == SSE_BF16 ? 2 : 4) : small ? 640 : p.threads <= 512 ? 512 : 1024;
+    int per_sm = hold_threads / p.threads;
     if (per_sm < 1) per_sm = 1;
+    const int enough = (p.threads <= 128 ? 384 : 512) / p.threads;
+    if (!backward && residual && p.vpt <= 2 && per_sm > enough) per_sm = enough;
     const int64_t need = (T + p.teams - 1) / p.teams, hold = (int64_t)kSms * per_sm;
     p.grid = (int)(need < hold ? need : hold);
     return p;
 }
 
-template <typename T> cudaError_t launch_forward(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
-    const auto kernel = p.threads > 128 ? layer_norm_kernel<T, 4, 512>  // more than 512 words: four a thread
-                        : p.vpt == 1    ? layer_norm_kernel<T, 1, 128>
-                        : p.vpt == 2    ? layer_norm_kernel<T, 2, 128>
-                        : p.vpt == 3    ? layer_norm_kernel<T, 3, 128>
-                                        : layer_norm_kernel<T, 4, 128>;
-    kernel<<<p.grid, p.threads, 0, s>>>(a, p.n);
+template <typename T, int VPT, int MAXT> cudaError_t launch_forward_t(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
+    const auto kernel = layer_norm_kernel<T, VPT, MAXT>;
+    constexpr int kBytes = VPT <= 2 ? Ahead<T, VPT, 2, 2>::kBytes : 0;  // of a thread
+    if constexpr (kBytes * MAXT > 47 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes * MAXT);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<p.grid, p.threads, kBytes * p.threads, s>>>(a, p.n);
     return cudaGetLastError();
+}
+template <typename T> cudaError_t launch_forward(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
+    if (p.vpt == 1) return launch_forward_t<T, 1, 128>(p, a, s);
+    if (p.vpt > 2) return launch_forward_t<T, 4, 512>(p, a, s);
+    return p.threads <= 128 ? launch_forward_t<T, 2, 128>(p, a, s) : launch_forward_t<T, 2, 320>(p, a, s);
 }
 
 template <typename T, int VPT, int MAXT> cudaError_t launch_backward_t(const LnPlan &p, const LayerNormArgs &a, cudaStream_t s) {
@@ -481,17 +526,17 @@ template <typename T> cudaError_t launch_backward(const LnPlan &p, const LayerNo
 }  // namespace
 
 int64_t layer_norm_partial_rows(const sse_layer_norm_config_t &cfg, int64_t T) {
-    const LnPlan p = plan(cfg, T, true);
+    const LnPlan p = plan(cfg, T, true, true);
     return (int64_t)p.grid * p.teams;
 }
 
 cudaError_t launch_layer_norm(const sse_layer_norm_config_t &cfg, const LayerNormArgs &a, cudaStream_t stream) {
-    const LnPlan p = plan(cfg, a.T, false);
+    const LnPlan p = plan(cfg, a.T, false, a.r != nullptr);
     return cfg.dtype == SSE_BF16 ? launch_forward<__nv_bfloat16>(p, a, stream) : launch_forward<float>(p, a, stream);
 }
 
 cudaError_t launch_layer_norm_backward(const sse_layer_norm_config_t &cfg, const LayerNormArgs &a, cudaStream_t stream) {
-    const LnPlan p = plan(cfg, a.T, true);
+    const LnPlan p = plan(cfg, a.T, true, true);
     if (a.T > 0) {
         const cudaError_t e = cfg.dtype == SSE_BF16 ? launch_backward<__nv_bfloat16>(p, a, stream)
                                                     : launch_backward<float>(p, a, stream);
