@@ -14,10 +14,11 @@
 // pairs (the exponent, D x B, the state, C h), two exponentials and a 16-byte load:
 // 32 exponentials a clock and SM are 115 us, and the pairs, whose three distinct
 // operands take the register ports three cycles, about 280.
-// Measured on a GB300 in bf16, 16 states, gate and skip: 8 x 4096 x 2048 517 us, one
-// sequence of 32768 531 (of which 100 are the ranges' states), 24001 x 2048 in 16
-// ragged ones 412, a prompt of 500 x 1024 27; issue 61 %, FMA pipe 47 %, exponentials
-// 38 % busy.  Token by token with a lane per four states: 8 x 4096 x 2048 about 5 ms.
+// Measured on a GB300 in bf16, 16 states, gate and skip: 8 x 4096 x 2048 526 us, one
+// sequence of 32768 514 (of either 200 are the ranges' states), 16 x 2048 x 2048, whose
+// sequences need no such states, 387, 24001 x 2048 in 16 ragged ones 399, a prompt of 500
+// x 1024 27; issue 61 %, FMA pipe 47 %, exponentials 38 % busy.  Token by token with a
+// lane per four states: 8 x 4096 x 2048 about 5 ms.
 #include <type_traits>
 
 #include "selective.cuh"
@@ -48,9 +49,10 @@ template <int L> __device__ __forceinline__ float lanes_sum(float v) {
 // now).  Two warps to a CTA, a warp that only copies, and half of the states or of the
 // channels to a lane were slower or the same.
 // ---------------------------------------------------------------------------
-constexpr int kCols = 32;     // channels of a warp
-constexpr int kAlone = 2000;  // warps that sequences make by themselves, for a range each
-constexpr int kBlock = 4;     // tokens at a time
+constexpr int kCols = 32;           // channels of a warp
+constexpr int kAlone = 1000;        // warps that sequences make by themselves, for a range each
+constexpr int kQuarters = 4 * 152;  // of the SMs
+constexpr int kBlock = 4;           // tokens at a time
 
 // What a kernel makes: the states that later ranges start from, the forward without and with a gate.
 enum { kStates, kPlain, kGated };
@@ -80,7 +82,7 @@ __global__ void __launch_bounds__(32, 1) selective_forward_kernel(SelectiveArgs 
     extern __shared__ __align__(16) char smem[];
     const int lane = threadIdx.x, r = blockIdx.y;
     const Columns cols(sh, blockIdx.x, kCols);
-    const Ranges rg(a, sh.ranges);
+    const Ranges rg(a, sh, [](const int32_t *cu, int S, int end) { return even_sequences(cu, S, end); });
     int t0 = rg.start(r);
     const int t1 = rg.start(r + 1);
     const bool live = lane < cols.left;
@@ -371,8 +373,17 @@ __global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, ss
 
 enum What { kForward, kStep };
 
+// Warps of an SM quarter, by the registers that N states take: 4, 3, 2, 2.
+SelectiveShape forward_shape(const sse_selective_config_t &c, int64_t T, int32_t S) {
+    SelectiveShape s = selective_shape(c, kCols);
+    const double held = c.state == 8 ? 4 : c.state == 16 ? 3 : 2;
+    const Waves choices[] = {{2 * held, 400}, {held, 256}, {2, 96}, {1, 4 * kTile}};
+    set_ranges(s, ranges_that_fill(s.tiles * c.groups, kQuarters, choices, T), kAlone, S);
+    return s;
+}
+
 template <typename T, int N> cudaError_t launch_forward(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
-    const SelectiveShape sh = selective_shape(c, kCols, kAlone, a.total_tokens, a.num_seqs);
+    const SelectiveShape sh = forward_shape(c, a.total_tokens, a.num_seqs);
     ForwardWork wk;
     wk.q = reinterpret_cast<float *>(a.workspace);
     wk.steps = wk.q + (int64_t)sh.ranges * c.width * N;
@@ -417,7 +428,7 @@ cudaError_t launch(What what, const sse_selective_config_t &c, const SelectiveAr
 }  // namespace
 
 size_t selective_forward_workspace(const sse_selective_config_t &c, int64_t T, int32_t S) {
-    const SelectiveShape s = selective_shape(c, kCols, kAlone, T, S);
+    const SelectiveShape s = forward_shape(c, T, S);
     return s.ranges > 1 ? sizeof(float) * (size_t)s.ranges * c.width * (c.state + 1) : 0;
 }
 cudaError_t launch_selective_forward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {

@@ -13,26 +13,44 @@ static_assert(kTile == kSelectiveCheckpoint, "a checkpoint is the state before a
 
 struct SelectiveShape {
     int width, groups, per, tiles;  // channels; groups; channels and tiles of a group
-    int ranges;                     // of the token axis
+    int ranges;                     // of the token axis, at most: CTAs along it
+    int fill;                       // ranges that fill the GPU
+    bool alone;                     // sequences that fill it by themselves, if they are even
 };
 
-// Warps of a call, `cols` channels each, and ranges of the token axis.  A range that begins inside a sequence costs a
-// pass of its own over the range before it, so there are no more than fill the GPU: about 1024 warps for short calls
-// (8192 tokens x 512 in one sequence: forward 59 us with 64 ranges, 109 with 16 and 84 with 128), about 4096 where ranges
-// have 512 tokens at least (32768 x 2048: 531 us with 64 ranges, 615 with 16).  Sequences that make `alone` warps by
-// themselves have a range each, which even lengths need no such pass for (32 x 1024 x 2048: forward 374 us with 32 ranges,
-// 470 with 64; the backward of 8 x 4096 x 2048: 1543 with 8, 1640 with 32), although uneven ones lose by it (24001 x
-// 2048 in 16: forward 467 with 16 and 388 with 64, backward 1385 and 1234 with 32).
-inline SelectiveShape selective_shape(const sse_selective_config_t &c, int cols, int alone, int64_t T, int32_t S) {
-    SelectiveShape s{c.width, c.groups, c.width / c.groups, 0, 1};
+// Ranges of the token axis for `ctas` along the channels, of which the GPU holds `slots`.  A range that begins inside a
+// sequence costs a pass of its own over the range before it and the last wave of CTAs is as long as the others, so ranges
+// make whole waves: as many of `waves` (most first) as leave a range `tokens` of each.  One sequence of 32768 x 2048: forward
+// with 1, 2 and 3 waves of three warps per SM quarter 519, 515 and 538 us, between two of them 523 to 538; backward with 2
+// and 4 1562 and 1567, between them 1598 and 1635.  8192 x 512: forward with two warps per quarter 58, with one 60, with
+// three 69; backward with 1 and 2 waves 125 and 134.
+struct Waves {
+    double waves;
+    int tokens;
+};
+template <int M> inline int ranges_that_fill(int64_t ctas, int slots, const Waves (&choices)[M], int64_t T) {
+    const int64_t most = T / (4 * kTile) < kMaxRanges ? T / (4 * kTile) : kMaxRanges;
+    int64_t r = 0;
+    for (const Waves &w : choices) {
+        r = (int64_t)(w.waves * slots / ctas);
+        if (r <= kMaxRanges && r * w.tokens <= T) break;
+    }
+    r = r < most ? r : most;
+    return r < 1 ? 1 : (int)r;
+}
+
+inline SelectiveShape selective_shape(const sse_selective_config_t &c, int cols) {
+    SelectiveShape s{c.width, c.groups, c.width / c.groups, 0, 1, 1, false};
     s.tiles = (s.per + cols - 1) / cols;
-    const int64_t tiles = (int64_t)s.tiles * c.groups;
-    auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
-    auto most = [](int64_t a, int64_t b) { return a > b ? a : b; };
-    const int64_t few = least((1023 + tiles) / tiles, T / (4 * kTile)), many = least((4095 + tiles) / tiles, T / 512);
-    s.ranges = (int)least(most(most(few, many), 1), kMaxRanges);
-    if (S < s.ranges && S * tiles >= alone) s.ranges = S < 1 ? 1 : S;
     return s;
+}
+// Sequences that make `enough` warps by themselves have a range each where the kernels find them even: no range then needs a
+// pass of its own (32 x 1024 x 2048: forward 377 us with 32 ranges, 523 with 57, 16 x 2048 x 2048 395 with 16 and 539 with 57; the backward of 8 x 4096 x 2048 1507 with 8,
+// 1597 with 38; of 24001 x 2048 in 16 ragged sequences 1364 with 16, 1219 with 38).
+inline void set_ranges(SelectiveShape &s, int fill, int enough, int32_t S) {
+    s.fill = fill;
+    s.alone = S > 1 && S <= kMaxRanges && (int64_t)S * s.tiles * s.groups >= enough;
+    s.ranges = s.alone && S > fill ? S : fill;
 }
 
 // log2 e and what float32 leaves of it.
@@ -82,12 +100,25 @@ template <bool SLOPE> __device__ __forceinline__ F2 softplus2(F2 v, F2 &slope) {
 // of a sequence that is no further than a quarter of a range from there; one that
 // begins inside a sequence takes the state that the ranges before it hand on.
 // ---------------------------------------------------------------------------
+// Whether every sequence starts a sixteenth of a sequence at most from its place; all lanes of a warp ask.
+__device__ __forceinline__ bool even_sequences(const int32_t *cu, int S, int end) {
+    bool even = true;
+    for (int q = threadIdx.x & 31; q < S; q += 32) {
+        const int64_t off = (int64_t)__ldg(cu + q) * S - (int64_t)end * q;
+        even = even && off * 16 <= end && off * 16 >= -end;
+    }
+    return __all_sync(0xffffffffu, even);
+}
+
 struct Ranges {
     const int32_t *cu;
     int S, end, n;  // sequences, their last token's successor, ranges with tokens
-    __device__ __forceinline__ Ranges(const SelectiveArgs &a, int ranges) : cu(a.cu_seqlens), S(a.num_seqs) {
+    // All lanes of a warp, with the same arguments; `even` is even_sequences.
+    template <typename Even>
+    __device__ __forceinline__ Ranges(const SelectiveArgs &a, const SelectiveShape &sh, Even even) : cu(a.cu_seqlens), S(a.num_seqs) {
         end = clamp_token(__ldg(cu + S), a.total_tokens);
-        n = max(1, min(ranges, end / (4 * kTile)));  // of 64 tokens and more: starts are in order
+        n = max(1, min(sh.fill, end / (4 * kTile)));  // of 64 tokens and more: starts are in order
+        if (sh.alone && end / S >= 4 * kTile && even(cu, S, end)) n = S;
     }
     __device__ __forceinline__ int start(int r) const {
         if (r <= 0) return 0;

@@ -21,8 +21,8 @@
 // Bound by instructions: about 48 of a warp for 64 (token, channel, state), 19 of them
 // arithmetic of pairs and 9 the sums over channels, against 14 bytes and 16
 // exponentials for a token and channel (159 us of HBM, 115 of exponentials for 8 x 4096
-// x 2048 with 16 states).  Measured on a GB300, bf16: 1510 us there, 1632 as one
-// sequence of 32768, 24001 x 2048 in 16 ragged sequences 1363, 64 x 512 x 512 414;
+// x 2048 with 16 states).  Measured on a GB300, bf16: 1515 us there, 1565 as one
+// sequence of 32768, 24001 x 2048 in 16 ragged sequences 1220, 64 x 512 x 512 418;
 // issue 46 %, shared memory's pipe 57 %, FMA 41 %.  255 registers leave eight warps to
 // an SM.  Spans of 4 tokens, whose 168 registers let twelve in, took 2623 us (1.75
 // passes forwards instead of 1.5, and what did not fit in registers went to L2, shared
@@ -67,6 +67,9 @@ struct BackwardWork {
     int parts;          // CTAs of a group
 };
 
+// Not inline: the kernel's registers would be given out worse for it (8 x 4096 x 2048 1546 us instead of 1515).
+__device__ __noinline__ bool even_sequences_called(const int32_t *cu, int S, int end) { return even_sequences(cu, S, end); }
+
 // FULL: the gradients.  Otherwise what an earlier range starts from: e at the range's first token from nothing behind it
 // (or from the sequence that ends in it), and the sum of its steps.
 template <typename T, int N, bool FULL>
@@ -81,7 +84,7 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     const int g = blockIdx.x / (FULL ? wk.parts : sh.tiles), part = blockIdx.x - g * (FULL ? wk.parts : sh.tiles);
     const int first = (FULL ? part * kWarps + warp : part) * kCols;
     const int left = max(0, min(kCols, sh.per - first)), c0 = g * sh.per + (left ? first : 0);
-    const Ranges rg(a, sh.ranges);
+    const Ranges rg(a, sh, even_sequences_called);
     const int t0 = rg.start(r);
     int t1 = rg.start(r + 1);
     const int pair = c0 + 2 * cl;
@@ -536,6 +539,15 @@ __global__ void __launch_bounds__(128) selective_weights_kernel(SelectiveArgs a,
         a.d_delta_bias[c] = s;
 }
 
+// CTAs that the GPU holds: two on an SM, one with 64 states, whose stages fill shared memory.
+SelectiveShape backward_shape(const sse_selective_config_t &c, int64_t T, int32_t S) {
+    SelectiveShape s = selective_shape(c, kCols);
+    const int parts = (s.tiles + 3) / 4;
+    const Waves choices[] = {{4, 400}, {2, 128}, {1, 4 * kTile}};
+    set_ranges(s, ranges_that_fill((int64_t)parts * c.groups, c.state == 64 ? 152 : 304, choices, T), kAlone, S);
+    return s;
+}
+
 // The workspace: what ranges hand on, the tokens' rows, the ranges' weights.
 size_t carve(const sse_selective_config_t &c, const SelectiveShape &s, int64_t T, char *base, BackwardWork &wk) {
     const size_t N = c.state;
@@ -557,7 +569,7 @@ size_t carve(const sse_selective_config_t &c, const SelectiveShape &s, int64_t T
 }
 
 template <typename T, int N> cudaError_t launch_t(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
-    const SelectiveShape sh = selective_shape(c, kCols, kAlone, a.total_tokens, a.num_seqs);
+    const SelectiveShape sh = backward_shape(c, a.total_tokens, a.num_seqs);
     BackwardWork wk;
     carve(c, sh, a.total_tokens, a.workspace, wk);
     const auto states = selective_backward_kernel<T, N, false>, full = selective_backward_kernel<T, N, true>;
@@ -587,7 +599,7 @@ template <typename T> cudaError_t launch_state(const sse_selective_config_t &c, 
 
 size_t selective_backward_workspace(const sse_selective_config_t &c, int64_t T, int32_t S) {
     BackwardWork wk;
-    return carve(c, selective_shape(c, kCols, kAlone, T, S), T, nullptr, wk);
+    return carve(c, backward_shape(c, T, S), T, nullptr, wk);
 }
 cudaError_t launch_selective_backward(const sse_selective_config_t &cfg, const SelectiveArgs &a, cudaStream_t stream) {
     return cfg.dtype == SSE_BF16 ? launch_state<__nv_bfloat16>(cfg, a, stream) : launch_state<float>(cfg, a, stream);

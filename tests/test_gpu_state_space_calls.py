@@ -183,3 +183,25 @@ def test_more_than_32_ranges(b, lens):
     assert b.sse_selective_forward_workspace_size(cfg, sum(lens), len(lens)) > 100 * 4 * 8 * 9  # a hundred ranges and more
     f, g = run(b, c, "f32")
     check(c, "f32", f, g)
+
+
+@pytest.mark.parametrize("lens,tail", [([66] * 16, 0), ([70, 62] * 8, 0), ([71, 61] * 8, 0), ([60] * 16, 0), ([0, 132] + [66] * 14, 0),
+                                       ([80] * 16, 300), ([64] * 15 + [84], 7), ([128, 127, 129], 0)])
+def test_even_and_uneven_sequences(b, lens, tail):
+    """Sequences that make enough warps have a range each where they are even (every start within a sixteenth of its place);
+    the others are cut.  Nothing that the workspaces held matters."""
+    W = 2048 if len(lens) > 3 else 16384
+    c = make(lens, W, 8, 1, "bf16", 6, tail=tail)
+    f, g = run(b, c, "bf16")
+    check(c, "bf16", f, g)
+    cfg, T, S = b.make_selective_config(W, 8), sum(lens) + tail, len(lens)
+    nan = lambda n: torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")  # noqa: E731
+    args = (c["x"], c["delta"], c["A"], c["B"], c["C"], c["cu"])
+    parts = dict(delta_bias=c["bias"], skip=c["skip"], gate=c["gate"], initial_state=c["init"])
+    f2 = b.selective_forward(cfg, *args, want_checkpoints=True, workspace=nan(b.sse_selective_forward_workspace_size(cfg, T, S)), **parts)
+    g2 = b.selective_backward(cfg, *args, f2["checkpoints"], c["d_out"], d_final_state=c["d_final"],
+                              workspace=nan(b.sse_selective_backward_workspace_size(cfg, T, S)), **parts)
+    n = sum(lens)
+    assert torch.equal(f["out"][:n], f2["out"][:n]) and torch.equal(f["final_state"], f2["final_state"])
+    assert all(torch.equal(g[k][:n], g2[k][:n]) for k in ("dx", "d_delta", "d_gate", "d_B", "d_C"))
+    assert all(torch.equal(g[k], g2[k]) for k in ("d_A", "d_skip", "d_delta_bias", "d_initial_state"))
