@@ -477,6 +477,7 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
         }
     }
     if constexpr (FULL) {
+        griddep_launch_dependents();
         float *w = wk.weights + (int64_t)r * sh.width * (N + 2);
         for (int s = 0; s < SL; ++s) {
             recall(s);
@@ -505,38 +506,39 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     }
 }
 
-// dB and dC from the CTAs' rows, four values per thread.
+// dB and dC from the CTAs' rows, four values per thread, in the first `tokens` CTAs; in those behind them the weights'
+// gradients from the ranges' sums.  Launched as a dependent of the gradients' kernel.
 template <typename T>
-__global__ void __launch_bounds__(256) selective_tokens_kernel(SelectiveArgs a, int groups, int N, const float *sums, int parts) {
-    const int row = groups * N / 2;
+__global__ void __launch_bounds__(256) selective_sums_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk, int N, unsigned tokens) {
+    griddep_wait();
+    if (blockIdx.x >= tokens) {
+        const int i = (blockIdx.x - tokens) * 256 + threadIdx.x, c = i / (N + 2), n = i % (N + 2);
+        if (c >= sh.width) return;
+        float s = 0.f;
+#pragma unroll 8
+        for (int r = 0; r < sh.ranges; ++r) s += wk.weights[(int64_t)r * sh.width * (N + 2) + i];
+        if (n < N)
+            a.d_A[(int64_t)c * N + n] = s;
+        else if (n == N && a.d_skip)
+            a.d_skip[c] = s;
+        else if (n == N + 1 && a.d_delta_bias)
+            a.d_delta_bias[c] = s;
+        return;
+    }
+    const int groups = sh.groups, row = groups * N / 2;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / row;
     if (t >= clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens)) return;
     const int at = (int)(i - t * row) * 4, g = at / (2 * N), n = at % (2 * N);
     const int64_t part = (int64_t)a.total_tokens * groups * 2 * N;
-    const float *from = sums + (t * groups + g) * 2 * N + n;
+    const float *from = wk.tokens + (t * groups + g) * 2 * N + n;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 16
-    for (int p = 0; p < parts; ++p) {
+    for (int p = 0; p < wk.parts; ++p) {
         const float4 v = *reinterpret_cast<const float4 *>(from + p * part);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
     }
     const F2 f[2] = {f2(s.x, s.y), f2(s.z, s.w)};
     *reinterpret_cast<typename Quad<T>::Raw *>(static_cast<T *>(n < N ? a.d_B : a.d_C) + (t * groups + g) * N + n % N) = Quad<T>::pack(f);
-}
-
-// The weights' gradients from the ranges' sums.
-__global__ void __launch_bounds__(128) selective_weights_kernel(SelectiveArgs a, int width, int N, const float *sums, int ranges) {
-    const int i = blockIdx.x * 128 + threadIdx.x, c = i / (N + 2), n = i % (N + 2);
-    if (c >= width) return;
-    float s = 0.f;
-#pragma unroll 8
-    for (int r = 0; r < ranges; ++r) s += sums[(int64_t)r * width * (N + 2) + i];
-    if (n < N)
-        a.d_A[(int64_t)c * N + n] = s;
-    else if (n == N && a.d_skip)
-        a.d_skip[c] = s;
-    else if (n == N + 1 && a.d_delta_bias)
-        a.d_delta_bias[c] = s;
 }
 
 // CTAs that the GPU holds: two on an SM, one with 64 states, whose stages fill shared memory.
@@ -575,15 +577,15 @@ template <typename T, int N> cudaError_t launch_t(const sse_selective_config_t &
     const auto states = selective_backward_kernel<T, N, false>, full = selective_backward_kernel<T, N, true>;
     constexpr int kStates = Layout<T, N, false>::kBytes, kFull = Layout<T, N, true>::kBytes;
     static_assert(Layout<T, N, true>::kWarps == 4 && kStates <= 48 * 1024 && kFull <= 227 * 1024, "shared memory");
-    const cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
+    cudaError_t e = cudaFuncSetAttribute(full, cudaFuncAttributeMaxDynamicSharedMemorySize, kFull);
     if (e != cudaSuccess) return e;
+    // (The gradients as a dependent of the states would have their CTAs placed beside those: 500 x 1024 51 -> 55 us.)
     if (sh.ranges > 1) states<<<dim3(sh.tiles * c.groups, sh.ranges), 32, kStates, s>>>(a, sh, wk);
     full<<<dim3(wk.parts * c.groups, sh.ranges), 32 * Layout<T, N, true>::kWarps, kFull, s>>>(a, sh, wk);
-    const int64_t rows = (int64_t)a.total_tokens * c.groups * N / 2;
-    if (rows > 0)
-        selective_tokens_kernel<T><<<(unsigned)((rows + 255) / 256), 256, 0, s>>>(a, c.groups, N, wk.tokens, wk.parts);
-    selective_weights_kernel<<<(c.width * (N + 2) + 127) / 128, 128, 0, s>>>(a, c.width, N, wk.weights, sh.ranges);
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const unsigned tokens = (unsigned)(((int64_t)a.total_tokens * c.groups * N / 2 + 255) / 256);
+    return launch_dependent(selective_sums_kernel<T>, dim3(tokens + (c.width * (N + 2) + 255) / 256), dim3(256), 0, s, a, sh, wk, N,
+                            tokens);
 }
 
 template <typename T> cudaError_t launch_state(const sse_selective_config_t &c, const SelectiveArgs &a, cudaStream_t s) {
