@@ -109,13 +109,25 @@ template <typename T, int K> struct Window {
     }
 };
 
+// A sequence's state as it is; zeros where there is none.
+template <typename T, int K>
+__device__ __forceinline__ void copy_state(T *to, const T *from, int q, int width, int col) {
+    using Raw = typename Quad<T>::Raw;
+    Raw row[K - 1];
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i)
+        row[i] = from ? *reinterpret_cast<const Raw *>(from + Window<T, K>::state_at(q, i, width, col)) : Quad<T>::zero();
+#pragma unroll
+    for (int i = 0; i < K - 1; ++i) *reinterpret_cast<Raw *>(to + Window<T, K>::state_at(q, i, width, col)) = row[i];
+}
+
 // Runs: gridDim.y CTAs of kWarps warps, `run` tokens each.
 template <typename T, int K, bool SILU>
 __global__ void __launch_bounds__(32 * kWarps, 6) conv_forward_kernel(ConvArgs a, int width, int run) {
     using Raw = typename Quad<T>::Raw;
     using Rows = Ring<T, 1>;
     const int lane = threadIdx.x & 31;
-    const int col = (blockIdx.x * 32 + lane) * 4;
+    const int col = (blockIdx.x * 32 + lane) * 4, lanes = min(32, (width - blockIdx.x * 128) / 4);  // of the warp, with columns
     if (col >= width) return;
     const int id = blockIdx.y * kWarps + (threadIdx.x >> 5), runs = gridDim.y * kWarps;
     const int end_of_all = clamp_token(__ldg(a.cu_seqlens + a.num_seqs), a.total_tokens);
@@ -130,9 +142,10 @@ __global__ void __launch_bounds__(32 * kWarps, 6) conv_forward_kernel(ConvArgs a
         win.before(a, t, q, start, width, col);
         while (t < t1) {
             if (t == end) {  // the next sequence that has tokens
-                while (end <= t && q + 1 < a.num_seqs) {
-                    ++q;
-                    start = end;
+                for (bool next = true; end <= t && q + 1 < a.num_seqs; next = false) {
+                    const int s = next ? 0 : sequence_of(a.cu_seqlens, a.num_seqs, t);  // past a row of empty ones
+                    q = s > q ? s : q + 1;
+                    start = __ldg(a.cu_seqlens + q);
                     end = __ldg(a.cu_seqlens + q + 1);
                 }
                 win.before(a, t, q, start, width, col);
@@ -196,14 +209,9 @@ __global__ void __launch_bounds__(32 * kWarps, 6) conv_forward_kernel(ConvArgs a
         }
     }
     if (a.final_state)  // empty sequences keep their state
-        for (int q = id; q < a.num_seqs; q += runs)
-            if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1))
-#pragma unroll
-                for (int i = 0; i < K - 1; ++i) {
-                    const int64_t at = Window<T, K>::state_at(q, i, width, col);
-                    *reinterpret_cast<Raw *>(static_cast<T *>(a.final_state) + at) =
-                        a.init ? *reinterpret_cast<const Raw *>(static_cast<const T *>(a.init) + at) : Quad<T>::zero();
-                }
+        each_empty(a.cu_seqlens, a.num_seqs, id, runs, lane, lanes, [&](int q) {
+            copy_state<T, K>(static_cast<T *>(a.final_state), static_cast<const T *>(a.init), q, width, col);
+        });
 }
 
 template <typename T, int K, bool SILU>
@@ -229,7 +237,10 @@ __global__ void __launch_bounds__(32 * kWarps, 4) conv_backward_kernel(ConvArgs 
         // state where the sequence begins in the run.  Row p is complete with g_{p + K - 1}.
         for (int s0 = t0; s0 < t1 && q < a.num_seqs; ++q) {
             const int start = __ldg(a.cu_seqlens + q), end = __ldg(a.cu_seqlens + q + 1);
-            if (end <= s0) continue;
+            if (end <= s0) {  // past a row of empty ones
+                q = max(q, sequence_of(a.cu_seqlens, a.num_seqs, s0) - 1);
+                continue;
+            }
             const int s1 = min(end, t1);
             Window<T, K> win;
             win.before(a, s0, q, start, width, col);
@@ -346,14 +357,9 @@ __global__ void __launch_bounds__(32 * kWarps, 4) conv_backward_kernel(ConvArgs 
         }
     }
     if (live && a.d_init)  // empty sequences hand the final state's gradient through
-        for (int q = id; q < a.num_seqs; q += runs)
-            if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1))
-#pragma unroll
-                for (int i = 0; i < K - 1; ++i) {
-                    const int64_t at = Window<T, K>::state_at(q, i, width, col);
-                    *reinterpret_cast<Raw *>(static_cast<T *>(a.d_init) + at) =
-                        a.d_final ? *reinterpret_cast<const Raw *>(static_cast<const T *>(a.d_final) + at) : Quad<T>::zero();
-                }
+        each_empty(a.cu_seqlens, a.num_seqs, id, runs, lane, min(32, (width - blockIdx.x * 128) / 4), [&](int q) {
+            copy_state<T, K>(static_cast<T *>(a.d_init), static_cast<const T *>(a.d_final), q, width, col);
+        });
     griddep_launch_dependents();
 #pragma unroll
     for (int j = 0; j <= K; ++j) {

@@ -90,13 +90,10 @@ __global__ void __launch_bounds__(32, 1) selective_forward_kernel(SelectiveArgs 
     const int64_t states = (int64_t)ch * N;  // this thread's first state
     if constexpr (FULL) {
         if (a.final_state)  // empty sequences keep their state
-            for (int q = r; q < a.num_seqs; q += sh.ranges)
-                if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1) && live)
-                    for (int i = 0; i < N; i += 4) {
-                        const int64_t at = (int64_t)q * sh.width * N + states + i;
-                        *reinterpret_cast<float4 *>(a.final_state + at) =
-                            a.init ? *reinterpret_cast<const float4 *>(a.init + at) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
+            each_empty(a.cu_seqlens, a.num_seqs, r, sh.ranges, lane, 32, [&](int q) {
+                const int64_t at = (int64_t)q * sh.width * N + states;
+                if (live) copy_words<N / 4, 1>(a.final_state + at, a.init ? a.init + at : nullptr);
+            });
     } else {
         const int from = rg.origin(t1);
         if (t1 >= rg.end || from == t1) return;  // the next range begins a sequence

@@ -92,12 +92,10 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     const int64_t states = (int64_t)pair * N + j * NT;
     if constexpr (FULL) {
         if (a.d_init)  // empty sequences hand the final state's gradient through
-            for (int q = r; q < a.num_seqs; q += sh.ranges)
-                if (__ldg(a.cu_seqlens + q) >= __ldg(a.cu_seqlens + q + 1) && live)
-                    for (int i = j; i < 2 * N; i += kL) {
-                        const int64_t at = ((int64_t)q * sh.width + pair) * N + i;
-                        a.d_init[at] = a.d_final ? a.d_final[at] : 0.f;
-                    }
+            each_empty(a.cu_seqlens, a.num_seqs, r, sh.ranges, lane, 32, [&](int q) {
+                const int64_t at = ((int64_t)q * sh.width + pair) * N + 4 * j;
+                if (live) copy_words<N / 8, kL>(a.d_init + at, a.d_final ? a.d_final + at : nullptr);
+            });
     } else {
         if (t0 >= t1 || rg.origin(t0) == t0) return;  // the range begins a sequence
         t1 = min(t1, clamp_token(__ldg(a.cu_seqlens + sequence_of(rg.cu, rg.S, t0) + 1), rg.end));

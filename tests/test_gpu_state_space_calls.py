@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 
 from oracle import selective as scan_oracle
+from tests import test_gpu_conv as conv
 from tests.test_gpu_selective import check, make, run
 
 pytestmark = pytest.mark.gpu
@@ -205,3 +206,28 @@ def test_even_and_uneven_sequences(b, lens, tail):
     assert torch.equal(f["out"][:n], f2["out"][:n]) and torch.equal(f["final_state"], f2["final_state"])
     assert all(torch.equal(g[k][:n], g2[k][:n]) for k in ("dx", "d_delta", "d_gate", "d_B", "d_C"))
     assert all(torch.equal(g[k], g2[k]) for k in ("d_A", "d_skip", "d_delta_bias", "d_initial_state"))
+
+
+EMPTY = [[5] + [0] * 300 + [7] + [0] * 90 + [40, 3], [0] * 70 + [2], [1] + [0] * 33, [0] * 129]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", EMPTY)
+def test_many_empty_sequences(b, dtype, lens):
+    """Empty sequences by the hundred, in a row, at both ends, alone: their states go through."""
+    for W, K in ((40, 4), (136, 2)):
+        c = conv.make(lens, W, K, dtype, 11)
+        f, g = conv.run(b, c, "silu", dtype)
+        if sum(lens):
+            conv.check(c, "silu", dtype, f, g)
+        empty = [q for q, n in enumerate(lens) if n == 0]
+        assert torch.equal(f["final_state"][empty], c["init"][empty]) and torch.equal(g["d_initial_state"][empty], c["d_final"][empty])
+    for N in (8, 64):
+        c = make(lens, 24, N, 1, dtype, 12)
+        f, g = run(b, c, dtype)
+        if sum(lens):
+            check(c, dtype, f, g)
+        assert torch.equal(f["final_state"][empty], c["init"][empty]) and torch.equal(g["d_initial_state"][empty], c["d_final"][empty])
+    c = make(lens, 24, 16, 1, dtype, 13, states=False)
+    f, g = run(b, c, dtype)
+    assert not f["final_state"][empty].any() and not g["d_initial_state"][empty].any()
