@@ -516,7 +516,8 @@ sse_status_t sse_block_norm_backward(const sse_norm_config_t *cfg, int64_t total
  *   x, d_out             [total_tokens, width] in cfg->dtype; x takes a row
  *                        stride in elements (>= width, whole 16-byte words);
  *                        d_out and every output are packed.
- *   weight               float32 [width, taps]; weight[taps - 1] meets x_t
+ *   weight               float32 [width, taps]; weight[taps - 1] meets x_t; given
+ *                        without tokens, too
  *   bias                 float32 [width], may be NULL (zero)
  *   initial_state        [num_seqs, taps - 1, width] in cfg->dtype, the newest
  *                        row last, may be NULL (zero)
@@ -581,7 +582,7 @@ sse_status_t sse_conv_step(const sse_conv_config_t *cfg, const void *x, int64_t 
  *                        words).  gate may be NULL (none: out = y).
  *   B, C                 [total_tokens, groups, state] in cfg->dtype, each with
  *                        its own row stride (>= groups * state, whole words)
- *   A                    float32 [width, state]
+ *   A                    float32 [width, state]; given without tokens, too
  *   delta_bias, skip     float32 [width], may be NULL (zero)
  *   initial_state        float32 [num_seqs, width, state], may be NULL (zero)
  *   final_state          likewise, may be NULL (not written).  An empty

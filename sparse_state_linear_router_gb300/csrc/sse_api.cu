@@ -882,7 +882,7 @@ sse_status_t sse_conv_forward(const sse_conv_config_t *cfg, const void *x, int64
     SSE_RANGE("sse_conv_forward");
     const sse_status_t st = check_conv(cfg, total_tokens, num_seqs);
     if (st != SSE_OK) return st;
-    if (!cu_seqlens || (total_tokens > 0 && (!x || !weight || !out))) return SSE_ERR_INVALID_ARG;
+    if (!cu_seqlens || (num_seqs > 0 && !weight) || (total_tokens > 0 && (!x || !out))) return SSE_ERR_INVALID_ARG;
     if (!stride_ok(x_stride, cfg->width, cfg->dtype == SSE_BF16 ? 2 : 4)) return SSE_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, initial_state, final_state, out})) return SSE_ERR_INVALID_ARG;
     if (final_state && final_state == initial_state) return SSE_ERR_INVALID_ARG;
@@ -906,7 +906,7 @@ sse_status_t sse_conv_backward(const sse_conv_config_t *cfg, const void *x, int6
     SSE_RANGE("sse_conv_backward");
     const sse_status_t st = check_conv(cfg, total_tokens, num_seqs);
     if (st != SSE_OK) return st;
-    if (!cu_seqlens || !d_weight || (total_tokens > 0 && (!x || !weight || !d_out || !dx))) return SSE_ERR_INVALID_ARG;
+    if (!cu_seqlens || !weight || !d_weight || (total_tokens > 0 && (!x || !d_out || !dx))) return SSE_ERR_INVALID_ARG;
     if (!stride_ok(x_stride, cfg->width, cfg->dtype == SSE_BF16 ? 2 : 4)) return SSE_ERR_INVALID_ARG;
     if (!all_aligned16({x, weight, bias, initial_state, d_out, d_final_state, dx, d_weight, d_bias, d_initial_state}))
         return SSE_ERR_INVALID_ARG;
@@ -1010,7 +1010,7 @@ sse_status_t sse_selective_forward(const sse_selective_config_t *cfg, const void
     sse::SelectiveArgs a = selective_args(x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride,
                                           skip, gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state);
     if ((st = check_selective_inputs(*cfg, a, total_tokens)) != SSE_OK) return st;
-    if (!cu_seqlens || (total_tokens > 0 && !out)) return SSE_ERR_INVALID_ARG;
+    if (!cu_seqlens || (num_seqs > 0 && !A) || (total_tokens > 0 && !out)) return SSE_ERR_INVALID_ARG;
     if (!all_aligned16({final_state, out, checkpoints})) return SSE_ERR_INVALID_ARG;
     if (final_state && final_state == initial_state) return SSE_ERR_INVALID_ARG;
     if (!workspace_ok(workspace, workspace_bytes, sse_selective_forward_workspace_size(cfg, total_tokens, num_seqs)))
@@ -1045,7 +1045,7 @@ sse_status_t sse_selective_backward(const sse_selective_config_t *cfg, const voi
     sse::SelectiveArgs a = selective_args(x, x_stride, delta, delta_stride, delta_bias, A, B, b_stride, C, c_stride,
                                           skip, gate, gate_stride, cu_seqlens, num_seqs, total_tokens, initial_state);
     if ((st = check_selective_inputs(*cfg, a, total_tokens)) != SSE_OK) return st;
-    if (!cu_seqlens || !d_A || (d_skip && !skip)) return SSE_ERR_INVALID_ARG;
+    if (!cu_seqlens || !A || !d_A || (d_skip && !skip)) return SSE_ERR_INVALID_ARG;
     if (total_tokens > 0 && (!checkpoints || !d_out || !dx || !d_delta || !d_B || !d_C ||
                              (gate != nullptr) != (d_gate != nullptr)))
         return SSE_ERR_INVALID_ARG;

@@ -133,3 +133,19 @@ def test_layer_norm_refuses(b):
 def test_configs_have_the_headers_layout(b):
     assert ctypes.sizeof(b.sse_conv_config_t) == 16 and ctypes.sizeof(b.sse_selective_config_t) == 16
     assert ctypes.sizeof(b.sse_layer_norm_config_t) == 12
+
+
+def test_weights_are_asked_for_without_tokens(b):
+    """The kernels that pass states of empty sequences on read the weights: none is refused on the host, tokens or not."""
+    I, cv, sc = b.SSE_ERR_INVALID_ARG, b.make_conv_config(64), b.make_selective_config(64)
+    for T, S in ((0, 1), (0, 3), (16, 1)):
+        assert b.sse_conv_forward(cv, FAKE, 64, None, None, FAKE, S, T, FAKE, None, FAKE, None) == I
+        assert b.sse_conv_backward(cv, FAKE, 64, None, None, FAKE, S, T, FAKE, FAKE, None, FAKE, FAKE, None, None, FAKE, ROOM, None) == I
+        inputs = (FAKE, 64, FAKE, 64, None, None, FAKE, 16, FAKE, 16, None, None, 64, FAKE, S, T, FAKE)
+        assert b.sse_selective_forward(sc, *inputs, None, FAKE, None, FAKE, ROOM, None) == I
+        assert b.sse_selective_backward(sc, *inputs, FAKE, FAKE, None, FAKE, FAKE, None, FAKE, FAKE, FAKE, None, None, None, FAKE,
+                                        ROOM, None) == I
+    # the gradients' kernel runs without sequences, too: d_A is zeroed
+    inputs = (FAKE, 64, FAKE, 64, None, None, FAKE, 16, FAKE, 16, None, None, 64, FAKE, 0, 0, None)
+    assert b.sse_selective_backward(sc, *inputs, None, None, None, None, None, None, FAKE, None, None, None, None, None, FAKE,
+                                    ROOM, None) == I
