@@ -408,6 +408,9 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
                     const int i = from + b;
                     const Operands o = next;
                     if (b) next = operands(i - 1);
+                    // A row of no token adds nothing to dA (its decay is 1 and its step 0, but an infinite or NaN state or
+                    // gradient beside it is not) and passes e on; what it would leave for the other sums nobody reads.
+                    if (EDGES && (row0 + i < t0 || row0 + i >= t1)) continue;
                     if (EDGES && ((ed.ends >> i) & 1u)) get(a.d_final, __shfl_sync(0xffffffffu, ed.seq, i), s, e);
                     const F2 d = f2(o.d.x, o.d.y), x = f2(o.d.z, o.d.w), dy = f2(o.dy.x, o.dy.y);
                     F2 sum[3] = {both(0.f), both(0.f), both(0.f)};
