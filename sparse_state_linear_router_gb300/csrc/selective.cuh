@@ -96,9 +96,12 @@ template <bool SLOPE> __device__ __forceinline__ F2 softplus2(F2 v, F2 &slope) {
 }
 
 // ---------------------------------------------------------------------------
-// Ranges of the token axis.  A range begins at a multiple of 16, or at the start
-// of a sequence that is no further than a quarter of a range from there; one that
-// begins inside a sequence takes the state that the ranges before it hand on.
+// Ranges of the token axis, of 64 tokens and more.  Range r of n begins at the
+// start of a sequence that is no further than a quarter of a range from the
+// r-th n-th of the tokens, or at the multiple of 16 below that; one that begins
+// inside a sequence takes the state that the ranges before it hand on.  Starts
+// are in order: from their places, 64 tokens apart, they are a quarter of that off,
+// or 15 to the left.  Even sequences, a sixteenth off at most, have a range each.
 // ---------------------------------------------------------------------------
 // Whether every sequence starts a sixteenth of a sequence at most from its place; all lanes of a warp ask.
 __device__ __forceinline__ bool even_sequences(const int32_t *cu, int S, int end) {
@@ -123,10 +126,10 @@ struct Ranges {
     __device__ __forceinline__ int start(int r) const {
         if (r <= 0) return 0;
         if (r >= n) return end;
-        const int t = (int)((int64_t)end * r / n) & ~(kTile - 1), near = end / (4 * n);
+        const int t = (int)((int64_t)end * r / n), near = end / (4 * n);
         const int s = sequence_of(cu, S, t), lo = clamp_token(__ldg(cu + s), end), hi = clamp_token(__ldg(cu + s + 1), end);
-        if (t - lo <= hi - t) return t - lo <= near ? lo : t;
-        return hi - t <= near ? hi : t;
+        const int to = t - lo <= hi - t ? lo : hi;
+        return abs(t - to) <= near ? to : t & ~(kTile - 1);
     }
     // The first token of the sequence that token t continues; t itself where t begins one, or is the end.
     __device__ __forceinline__ int origin(int t) const {

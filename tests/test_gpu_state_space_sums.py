@@ -1,5 +1,6 @@
 """What the sums and the ranges of the selective scan promise beyond ordinary
-values (marked gpu): the gradient of A beside rows of no token."""
+values (marked gpu): the gradient of A beside rows of no token, even sequences
+that have a range each."""
 import numpy as np
 import pytest
 
@@ -47,3 +48,33 @@ def test_an_infinite_gradient_of_a_first_token(b):
         assert bool(torch.isinf(g["d_A"][3]).all())
         keep = [i for i in range(8) if i != 3]
         assert torch.equal(g["d_A"][keep], fine["d_A"][keep])
+
+
+@pytest.mark.parametrize("lens", [[70, 62] * 8, [67, 65] * 8, [69, 63, 66] * 6, [66] * 16, [80] * 16])
+def test_even_sequences_have_a_range_each(b, lens):
+    """Nothing is handed on between ranges: where the workspaces keep the states and the sums of steps of ranges they stay as
+    they were, and every sequence gives bit for bit what it gives in a call of its own (one range)."""
+    W, N, S = 2048, 8, len(lens)
+    c = make(lens, W, N, 1, "f32", 6)
+    cfg, args = cfg_of(b, c, "f32"), (c["x"], c["delta"], c["A"], c["B"], c["C"], c["cu"])
+    kw = dict(delta_bias=c["bias"], skip=c["skip"], gate=c["gate"], initial_state=c["init"])
+    marked = lambda n: torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")  # noqa: E731
+    room = marked(b.sse_selective_forward_workspace_size(cfg, sum(lens), S))
+    handed = 4 * S * W * (N + 1)  # a row of states and a step for each of at least S ranges
+    assert room.numel() >= handed
+    f = b.selective_forward(cfg, *args, want_checkpoints=True, workspace=room, **kw)
+    assert bool((room == 0xFF).all())
+    room = marked(b.sse_selective_backward_workspace_size(cfg, sum(lens), S))
+    g = b.selective_backward(cfg, *args, f["checkpoints"], c["d_out"], d_final_state=c["d_final"], workspace=room, **kw)
+    assert bool((room[-handed:] == 0xFF).all()) and not bool((room[:-handed] == 0xFF).all())
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    for q in range(len(lens)):
+        s = slice(cu[q], cu[q + 1])
+        one = {k: v[s] if k in ("x", "delta", "B", "C", "gate", "d_out") else v for k, v in c.items()}
+        one.update(cu=torch.tensor([0, lens[q]], dtype=torch.int32, device="cuda"), init=c["init"][q:q + 1],
+                   d_final=c["d_final"][q:q + 1], n=lens[q])
+        assert b.sse_selective_forward_workspace_size(cfg_of(b, one, "f32"), lens[q], 1) == 0
+        f1, g1 = run(b, one, "f32")
+        assert torch.equal(f["out"][s], f1["out"]) and torch.equal(f["final_state"][q], f1["final_state"][0]), q
+        assert torch.equal(g["dx"][s], g1["dx"]) and torch.equal(g["d_delta"][s], g1["d_delta"]), q
+        assert torch.equal(g["d_initial_state"][q], g1["d_initial_state"][0]), q
