@@ -37,6 +37,7 @@ namespace {
 constexpr int kL = 4, kCols = 16;
 constexpr int kAlone = 1000;  // warps that sequences make by themselves, for a range each
 constexpr int kSpan = 8;      // tokens whose states are held in registers, and of an epilogue
+constexpr int kPart = 1024;   // tokens of a sum for the weights
 
 template <typename T, int N, bool FULL> struct Layout {
     static constexpr int NT = N == 8 ? 2 : 4, SL = N / (kL * NT);
@@ -119,20 +120,26 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     auto put = [&](float *p, int64_t i, int s, const F2 (&from)[NT]) {
         if (live) write_states(p + i * sh.width * N + states + s * kL * NT, N, swap, from);
     };
-    // a slice's e and dA between tiles: registers with one slice, else shared memory
+    // a slice's e between tiles and its dA: registers with one slice, else shared memory
     float *kept = reinterpret_cast<float *>(smem + Lay::kKept) + lane * 4;
     auto keep = [&](int s) {
-        if constexpr (SL > 1) {
-            write_states(kept + s * 512, 128, 0, e);
-            write_states(kept + s * 512 + 256, 128, 0, dA);
-        }
+        if constexpr (SL > 1) write_states(kept + s * 512, 128, 0, e);
     };
     auto recall = [&](int s) {
         if constexpr (SL > 1) {
             read_states(kept + s * 512, 128, 0, e);
-            read_states(kept + s * 512 + 256, 128, 0, dA);
             load_A(s);
         }
+    };
+    auto add_dA = [&](int s, const F2 (&half)[NT]) {
+        if constexpr (SL > 1) read_states(kept + s * 512 + 256, 128, 0, dA);
+#pragma unroll
+        for (int k = 0; k < NT; ++k) dA[k] = add2(dA[k], half[k]);
+        if constexpr (SL > 1) write_states(kept + s * 512 + 256, 128, 0, dA);
+    };
+    auto no_dA = [&](int s) {
+        no_states(dA);
+        if constexpr (SL > 1) write_states(kept + s * 512 + 256, 128, 0, dA);
     };
     auto decays = [&](F2 d, F2 (&to)[NT]) {
 #pragma unroll
@@ -162,7 +169,7 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
 #pragma unroll
             for (int k = 0; k < NT; ++k) e[k] = fma2(dec[k], e[k], q[k]);
         }
-        no_states(dA);
+        no_dA(s);
         keep(s);
     }
 
@@ -217,8 +224,43 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     Edges ed;
     int stage = 0, turn = 0;
     const int row_last = (t1 - 1) & ~(kTile - 1);
+    // The weights' sums go to the range's row every kPart tokens, which it then has the sum of: one chain of additions over
+    // a long range would lose as many bits as its length has (131072 equal tokens in one range: d_A 2.3e-4 off, with the
+    // parts 3e-6; it costs the other registers 1 % with 16 states).  `from`: the first token that is in them.  Every value
+    // of the row is one thread's.
+    auto leave_weights = [&](int from) {
+        const bool more = (row_last & ~(kPart - 1)) > from;  // what was left behind `from`
+        float *w = wk.weights + (int64_t)r * sh.width * (N + 2);
+        for (int s = 0; s < SL; ++s) {
+            float *to = w + (int64_t)pair * (N + 2) + s * kL * NT + j * NT;
+            F2 was[NT];
+            no_states(was);
+            if (more && live) read_states(to, N + 2, swap, was);
+            add_dA(s, was);
+            if (live) write_states(to, N + 2, swap, dA);
+            no_dA(s);
+        }
+        // the vectors' sums over the tokens of the eight lanes of a quad
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float2 u = f2_get(d_skip[p]), v = f2_get(d_bias[p]);
+#pragma unroll
+            for (int o = kQuads; o < 32; o <<= 1) {
+                u.x += __shfl_xor_sync(0xffffffffu, u.x, o), u.y += __shfl_xor_sync(0xffffffffu, u.y, o);
+                v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+            }
+            if (tq == 0 && quad_live) {
+                float *to = w + (int64_t)(c0 + qd * 4 + 2 * p) * (N + 2) + N;
+                if (more) u.x += to[0], v.x += to[1], u.y += to[N + 2], v.y += to[N + 3];
+                to[0] = u.x, to[1] = v.x, to[N + 2] = u.y, to[N + 3] = v.y;
+            }
+            d_skip[p] = d_bias[p] = both(0.f);
+        }
+    };
     if (t0 < t1) fetch(row_last, 0);
     for (int row0 = row_last; t0 < t1 && row0 + kTile > t0; row0 -= kTile, stage ^= 1) {
+        if constexpr (FULL)
+            if ((row0 + kTile) % kPart == 0 && row0 < row_last) leave_weights(row0 + kTile);
         fetch(row0 - kTile, stage ^ 1);
         ed.find(rg, row0, t0, t1, lane);
         copies_wait<1>();
@@ -401,7 +443,7 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
                     return o;
                 };
                 Operands next = operands(from + kSpan - 1);
-                F2 dA_half[NT];  // a sum of its own: 4096 terms one after the other would lose four bits
+                F2 dA_half[NT];  // a sum of its own
                 no_states(dA_half);
 #pragma unroll
                 for (int b = kSpan - 1; b >= 0; --b) {
@@ -459,8 +501,7 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
                         if (a.d_init) put(a.d_init, q, s, e);
                     }
                 }
-#pragma unroll
-                for (int k = 0; k < NT; ++k) dA[k] = add2(dA[k], dA_half[k]);
+                add_dA(s, dA_half);
                 keep(s);
             };
 #pragma unroll 1
@@ -479,25 +520,7 @@ selective_backward_kernel(SelectiveArgs a, SelectiveShape sh, BackwardWork wk) {
     }
     if constexpr (FULL) {
         griddep_launch_dependents();
-        float *w = wk.weights + (int64_t)r * sh.width * (N + 2);
-        for (int s = 0; s < SL; ++s) {
-            recall(s);
-            if (live) write_states(w + (int64_t)pair * (N + 2) + s * kL * NT + j * NT, N + 2, swap, dA);
-        }
-        // the vectors' sums over the tokens of the eight lanes of a quad
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            float2 u = f2_get(d_skip[p]), v = f2_get(d_bias[p]);
-#pragma unroll
-            for (int o = kQuads; o < 32; o <<= 1) {
-                u.x += __shfl_xor_sync(0xffffffffu, u.x, o), u.y += __shfl_xor_sync(0xffffffffu, u.y, o);
-                v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
-            }
-            if (tq == 0 && quad_live) {
-                float *to = w + (int64_t)(c0 + qd * 4 + 2 * p) * (N + 2) + N;
-                to[0] = u.x, to[1] = v.x, to[N + 2] = u.y, to[N + 3] = v.y;
-            }
-        }
+        leave_weights(t0);
     } else {
         for (int s = 0; s < SL; ++s) {
             recall(s);

@@ -1,10 +1,12 @@
 """What the sums and the ranges of the selective scan promise beyond ordinary
 values (marked gpu): the gradient of A beside rows of no token, even sequences
-that have a range each."""
+that have a range each, long float32 sums."""
 import numpy as np
 import pytest
 
-from tests.test_gpu_selective import cfg_of, make, run
+from oracle import selective as oracle
+from tests._bounds import ROUND
+from tests.test_gpu_selective import bounds, cfg_of, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -78,3 +80,43 @@ def test_even_sequences_have_a_range_each(b, lens):
         assert torch.equal(f["out"][s], f1["out"]) and torch.equal(f["final_state"][q], f1["final_state"][0]), q
         assert torch.equal(g["dx"][s], g1["dx"]) and torch.equal(g["d_delta"][s], g1["d_delta"]), q
         assert torch.equal(g["d_initial_state"][q], g1["d_initial_state"][0]), q
+
+
+def test_long_sums_of_the_weights_gradients(b):
+    """d_A, d_skip and d_delta_bias over 131072 tokens in one range: the same inputs at every token, so that the float32
+    additions of one long chain would all be off in the same direction."""
+    T, N, per, G = 1 << 17, 8, 8, 610
+    W = per * G
+    r = torch.Generator().manual_seed(3)
+    row = {k: torch.rand(n, generator=r) + 0.5 for k, n in (("x", per), ("delta", per), ("B", N), ("C", N), ("d_out", per))}
+    row = {k: v.bfloat16() for k, v in row.items()}
+    A, bias, skip = -torch.rand(per, N, generator=r) - 1, torch.rand(per, generator=r), torch.rand(per, generator=r)
+    wide = lambda k, n: row[k].repeat(G).cuda().expand(n, -1).contiguous()  # noqa: E731
+    v = {k: wide(k, T) for k in ("x", "delta", "d_out")}
+    B, C = (wide(k, T).unflatten(1, (G, N)) for k in ("B", "C"))
+    cfg, cu = b.make_selective_config(W, N, G), torch.tensor([0, T], dtype=torch.int32, device="cuda")
+    args = (v["x"], v["delta"], A.repeat(G, 1).cuda(), B, C, cu)
+    kw = dict(delta_bias=bias.repeat(G).cuda(), skip=skip.repeat(G).cuda())
+    ck = b.selective_forward(cfg, *args, want_checkpoints=True, want_final_state=False, **kw)["checkpoints"]
+    g = b.selective_backward(cfg, *args, ck, v["d_out"], want_d_initial_state=False, **kw)
+    torch.cuda.synchronize()
+
+    # Decays of at most exp(-0.9): behind 100 tokens every token gives the same terms (to 1e-39), which 300 tokens and 301 show.
+    n64 = lambda t: t.double().numpy()  # noqa: E731
+
+    def some(n):
+        e = lambda k: np.tile(n64(row[k]), (n, 1))  # noqa: E731
+        return oracle.backward(e("x"), e("delta"), n64(A), e("B")[:, None], e("C")[:, None], [0, n], e("d_out"), n64(bias), n64(skip))
+
+    few, more = some(300), some(301)
+    # The error of one token's terms: that of 60 tokens' sum, a factor of 60 above at most what 60 additions add to it.
+    small = {k: row[k].expand(60, -1) for k in ("x", "delta", "d_out")}
+    small.update({k: row[k].expand(60, -1).unflatten(1, (1, N)) for k in ("B", "C")})
+    small.update(A=A, bias=bias, skip=skip, gate=None, init=None, d_final=None, n=60, cu=torch.tensor([0, 60], dtype=torch.int32))
+    bd = bounds(small)
+    chain = 2 * 64 + T // 1024 + 64  # halves of a tile in 1024 tokens, the parts, and what is within a half and behind them
+    for k in ("d_A", "d_skip", "d_delta_bias"):
+        want = few[k] + (T - 300) * (more[k] - few[k])
+        off = np.abs(n64(g[k].cpu()).reshape(G, *want.shape) - want).max(0)
+        tol = (np.abs(bd[k].e / bd[k].v) + chain * ROUND) * np.abs(want)
+        assert (off <= tol).all(), (k, (off / np.abs(want)).max(), (tol / np.abs(want)).max())
