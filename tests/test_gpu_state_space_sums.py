@@ -1,12 +1,13 @@
 """What the sums and the ranges of the selective scan promise beyond ordinary
 values (marked gpu): the gradient of A beside rows of no token, even sequences
-that have a range each, long float32 sums."""
+that have a range each, long float32 sums, and states handed on between ranges with
+every number of states."""
 import numpy as np
 import pytest
 
 from oracle import selective as oracle
 from tests._bounds import ROUND
-from tests.test_gpu_selective import bounds, cfg_of, make, run
+from tests.test_gpu_selective import bounds, cfg_of, check, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +121,15 @@ def test_long_sums_of_the_weights_gradients(b):
         off = np.abs(n64(g[k].cpu()).reshape(G, *want.shape) - want).max(0)
         tol = (np.abs(bd[k].e / bd[k].v) + chain * ROUND) * np.abs(want)
         assert (off <= tol).all(), (k, (off / np.abs(want)).max(), (tol / np.abs(want)).max())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N,G", [(32, 1), (32, 3), (64, 1), (64, 2), (8, 3)])
+@pytest.mark.parametrize("lens", [[300], [140, 0, 170, 3], [5, 331]])
+def test_states_handed_on(b, dtype, N, G, lens):
+    """Sequences over several ranges with every number of states and groups."""
+    c = make(lens, 24 * G, N, G, dtype, N + len(lens))
+    cfg = cfg_of(b, c, dtype)
+    assert b.sse_selective_forward_workspace_size(cfg, sum(lens), len(lens)) >= 4 * 4 * 24 * G * N  # four ranges
+    f, g = run(b, c, dtype)
+    check(c, dtype, f, g)
