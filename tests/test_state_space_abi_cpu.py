@@ -149,3 +149,18 @@ def test_weights_are_asked_for_without_tokens(b):
     inputs = (FAKE, 64, FAKE, 64, None, None, FAKE, 16, FAKE, 16, None, None, 64, FAKE, 0, 0, None)
     assert b.sse_selective_backward(sc, *inputs, None, None, None, None, None, None, FAKE, None, None, None, None, None, FAKE,
                                     ROOM, None) == I
+
+
+def test_selective_forward_asks_for_its_workspace(b):
+    """A missing, misaligned or short workspace of the forward is refused; a million tokens of 64 channels need one."""
+    cfg, W = b.make_selective_config(64), b.SSE_ERR_WORKSPACE
+    size = b.sse_selective_forward_workspace_size(cfg, 1 << 20, 1)
+    assert size > 0
+
+    def fwd(ws, n):
+        return b.sse_selective_forward(cfg, FAKE, 64, FAKE, 64, None, FAKE, FAKE, 16, FAKE, 16, None, None, 64, FAKE, 1, 1 << 20,
+                                       None, None, FAKE, None, ws, n, None)
+
+    assert fwd(None, 0) == W and fwd(None, size) == W
+    assert fwd(FAKE + 16, ROOM) == W and fwd(FAKE + 128, ROOM) == W
+    assert fwd(FAKE, size - 256) == W and fwd(FAKE, 0) == W
