@@ -602,7 +602,10 @@ sse_status_t sse_conv_step(const sse_conv_config_t *cfg, const void *x, int64_t 
  * when there are none.
  * Workspaces: sse_selective_forward_workspace_size and
  * sse_selective_backward_workspace_size bytes, 256-byte aligned, contents
- * undefined on entry and exit; NULL where the size is 0.
+ * undefined on entry and exit; NULL where the size is 0.  The backward's grows
+ * with the call: for every token, group and 64 of a group's channels it holds
+ * 2 * state floats (134 MB for 32768 tokens of 2048 channels with 16 states, as
+ * much as a bfloat16 tensor of the call; 537 MB with 64).
  *
  * sse_selective_step is one token of each of `batch` sequences: state
  * float32 [batch, width, state] is replaced, out [batch, width].
@@ -611,8 +614,13 @@ sse_status_t sse_conv_step(const sse_conv_config_t *cfg, const void *x, int64_t 
  * initial_state is refused.  Tokens at and past cu_seqlens[num_seqs] (a padded
  * batch) belong to no sequence: their rows are not read and the outputs' rows
  * stay as they were.  Sums and states are float32, rounded once to cfg->dtype,
- * formed in a fixed order (deterministic).  A NaN stays in its own sequence and
- * channel, in the gradients of B, C and the weights in its own token or channel.
+ * formed in a fixed order (deterministic).  A NaN or an infinity goes where the
+ * formulas take it and no further: out of a channel's x, delta, gate or d_out it
+ * stays in its sequence and channel, and d_B and d_C, which sum over a group's
+ * channels, have it at every token that it reaches there (a NaN in x: d_C of its
+ * token and all later ones of the sequence, d_B of its token).  Out of B or C it
+ * goes to every channel of its group.  d_A does not have it from the x of a
+ * sequence's last token, which is in no earlier state.
  * state is 8, 16, 32 or 64; width at most 65536, width / groups and the row
  * strides whole 16-byte words of cfg->dtype; total_tokens and num_seqs are below
  * 2^30.
