@@ -181,6 +181,16 @@ constexpr int kInRegisters = 512;
 // Threads of an SM that the forward's registers allow: 64 a thread for one word, 96 (float32 80) for two, else 128.
 constexpr int forward_threads(int vpt, int bytes) { return vpt == 1 ? 1024 : vpt > 2 ? 512 : bytes == 2 ? 640 : 768; }
 
+constexpr int kPart = 256;  // rows of a team in one sum
+
+// Four column sums of a thread's own, added to what is there with `more`.
+__device__ __forceinline__ void leave_quad(float *to, const F2 (&sum)[2], bool more) {
+    F2 was[2] = {both(0.f), both(0.f)};
+    if (more) read_quad(to, was);
+    const F2 now[2] = {add2(sum[0], was[0]), add2(sum[1], was[1])};
+    write_quad(to, now);
+}
+
 // Rows that the backward has on their way: two, or one where shared memory has the column sums.
 constexpr int rows_ahead(int threads) { return threads > kInRegisters ? 1 : 2; }
 
@@ -297,18 +307,21 @@ layer_norm_backward_kernel(LayerNormArgs a, LnShape n) {
     const Rows ahead(sums + (SHARED ? VPT * P * 4 * blockDim.x : 0));
     F2 sum_w[SHARED ? 1 : VPT][P], sum_b[SHARED ? 1 : VPT][P];
     auto mine = [&](int which, int i, int k) { return sums + (((which * VPT + i) * (P / 2) + k / 2) * blockDim.x + threadIdx.x) * 4; };
+    auto no_sums = [&] {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+        for (int i = 0; i < VPT; ++i)
 #pragma unroll
-        for (int k = 0; k < P; k += 2) {
-            const F2 none[2] = {both(0.f), both(0.f)};
-            if constexpr (SHARED) {
-                write_quad(mine(0, i, k), none);
-                write_quad(mine(1, i, k), none);
-            } else {
-                sum_w[i][k] = sum_w[i][k + 1] = sum_b[i][k] = sum_b[i][k + 1] = both(0.f);
+            for (int k = 0; k < P; k += 2) {
+                const F2 none[2] = {both(0.f), both(0.f)};
+                if constexpr (SHARED) {
+                    write_quad(mine(0, i, k), none);
+                    write_quad(mine(1, i, k), none);
+                } else {
+                    sum_w[i][k] = sum_w[i][k + 1] = sum_b[i][k] = sum_b[i][k + 1] = both(0.f);
+                }
             }
-        }
+    };
+    no_sums();
     int turn = 0;
     auto copy = [&](int slot, int64_t row) {
         ahead.copy(n, slot, 0, a.x, a.x_stride, row, j0, row < a.T);
@@ -331,103 +344,112 @@ layer_norm_backward_kernel(LayerNormArgs a, LnShape n) {
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) copy(k, first + k * rows_on);
     int slot = 0;
-    for (int64_t row = first; row < a.T; row += rows_on) {
-        F2 v[VPT][P];
-        Rows::wait();
+    int64_t row = first;
+    // This team's column sums go to its partial row of each every kPart rows, which it then has the sum of: one chain of
+    // additions over a long batch would lose as many bits as its length has (2^19 equal rows of 8192 columns: d_weight
+    // 5.8e-5 off, with the parts 2.5e-5, which its terms are).
+    bool more = false;  // the partial rows have something already
+    do {
+        const int64_t stop = min(a.T, row + kPart * rows_on);
+        for (; row < stop; row += rows_on) {
+            F2 v[VPT][P];
+            Rows::wait();
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) Word<T>::unpack(ahead.read(slot, 0, i), v[i]);
-        F2 t = both(0.f);
+            for (int i = 0; i < VPT; ++i) Word<T>::unpack(ahead.read(slot, 0, i), v[i]);
+            F2 t = both(0.f);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
+            for (int i = 0; i < VPT; ++i)
 #pragma unroll
-            for (int k = 0; k < P; ++k) t = add2(t, v[i][k]);
-        float4 m;
-        m.x = warp_sum(fold(t)) * inv_mine;
-        F2 sq = both(0.f), sp = both(0.f), sx = both(0.f);
+                for (int k = 0; k < P; ++k) t = add2(t, v[i][k]);
+            float4 m;
+            m.x = warp_sum(fold(t)) * inv_mine;
+            F2 sq = both(0.f), sp = both(0.f), sx = both(0.f);
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int j = j0 + i * 32;
-            if (j >= n.nv) continue;
-            F2 d[P];
-            weights(i, j);
-            Word<T>::unpack(ahead.read(slot, 1, i), d);
+            for (int i = 0; i < VPT; ++i) {
+                const int j = j0 + i * 32;
+                if (j >= n.nv) continue;
+                F2 d[P];
+                weights(i, j);
+                Word<T>::unpack(ahead.read(slot, 1, i), d);
 #pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const F2 c = add2(v[i][k], both(-m.x));
-                const F2 p = mul2(d[k], w[SHARED ? 0 : i][k]);
-                sq = fma2(c, c, sq);
-                sp = add2(sp, p);
-                sx = fma2(p, c, sx);
-            }
-        }
-        m.y = warp_sum(fold(sq));
-        m.z = warp_sum(fold(sp));
-        m.w = warp_sum(fold(sx));
-        join<4, VPT, E, MAXT / 32>(n, m, warp, lane, turn, words);
-        turn ^= 1;
-        const float rstd = rsqrt_ftz(fmaf(m.y, n.inv_width, n.eps));
-        const float mean_p = m.z * n.inv_width, slope = m.w * n.inv_width * rstd * rstd;  // mean(p x_hat) rstd
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int j = j0 + i * 32;
-            if (j >= n.nv) continue;
-            F2 v[P], d[P], e[P];
-            weights(i, j);
-            Word<T>::unpack(ahead.read(slot, 0, i), v);
-            Word<T>::unpack(ahead.read(slot, 1, i), d);
-            if (a.d_r_out) Word<T>::unpack(ahead.read(slot, 2, i), e);
-#pragma unroll
-            for (int k = 0; k < P; ++k) {
-                const F2 c = add2(v[k], both(-m.x));
-                v[k] = mul2(c, both(rstd));  // x_hat
-                if constexpr (!SHARED) {
-                    sum_w[i][k] = fma2(d[k], v[k], sum_w[i][k]);
-                    sum_b[i][k] = add2(sum_b[i][k], d[k]);
+                for (int k = 0; k < P; ++k) {
+                    const F2 c = add2(v[i][k], both(-m.x));
+                    const F2 p = mul2(d[k], w[SHARED ? 0 : i][k]);
+                    sq = fma2(c, c, sq);
+                    sp = add2(sp, p);
+                    sx = fma2(p, c, sx);
                 }
-                F2 p = mul2(d[k], w[SHARED ? 0 : i][k]);
-                p = mul2(fma2(c, both(-slope), add2(p, both(-mean_p))), both(rstd));
-                e[k] = a.d_r_out ? add2(p, e[k]) : p;
             }
-            *reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * n.width + j * E) = Word<T>::pack(e);
-            if constexpr (SHARED) {
+            m.y = warp_sum(fold(sq));
+            m.z = warp_sum(fold(sp));
+            m.w = warp_sum(fold(sx));
+            join<4, VPT, E, MAXT / 32>(n, m, warp, lane, turn, words);
+            turn ^= 1;
+            const float rstd = rsqrt_ftz(fmaf(m.y, n.inv_width, n.eps));
+            const float mean_p = m.z * n.inv_width, slope = m.w * n.inv_width * rstd * rstd;  // mean(p x_hat) rstd
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int j = j0 + i * 32;
+                if (j >= n.nv) continue;
+                F2 v[P], d[P], e[P];
+                weights(i, j);
+                Word<T>::unpack(ahead.read(slot, 0, i), v);
+                Word<T>::unpack(ahead.read(slot, 1, i), d);
+                if (a.d_r_out) Word<T>::unpack(ahead.read(slot, 2, i), e);
+#pragma unroll
+                for (int k = 0; k < P; ++k) {
+                    const F2 c = add2(v[k], both(-m.x));
+                    v[k] = mul2(c, both(rstd));  // x_hat
+                    if constexpr (!SHARED) {
+                        sum_w[i][k] = fma2(d[k], v[k], sum_w[i][k]);
+                        sum_b[i][k] = add2(sum_b[i][k], d[k]);
+                    }
+                    F2 p = mul2(d[k], w[SHARED ? 0 : i][k]);
+                    p = mul2(fma2(c, both(-slope), add2(p, both(-mean_p))), both(rstd));
+                    e[k] = a.d_r_out ? add2(p, e[k]) : p;
+                }
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + row * n.width + j * E) = Word<T>::pack(e);
+                if constexpr (SHARED) {
+#pragma unroll
+                    for (int k = 0; k < P; k += 2) {
+                        F2 w[2], b[2];
+                        read_quad(mine(0, i, k), w);
+                        read_quad(mine(1, i, k), b);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            w[q] = fma2(d[k + q], v[k + q], w[q]);
+                            b[q] = add2(b[q], d[k + q]);
+                        }
+                        write_quad(mine(0, i, k), w);
+                        write_quad(mine(1, i, k), b);
+                    }
+                }
+            }
+            copy(slot, row + kDepth * rows_on);
+            slot = slot + 1 == kDepth ? 0 : slot + 1;
+        }
+        if (row >= a.T) griddep_launch_dependents();
+        if (first < rows_on)
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) {
+                const int j = j0 + i * 32;
+                if (j >= n.nv) continue;
 #pragma unroll
                 for (int k = 0; k < P; k += 2) {
                     F2 w[2], b[2];
-                    read_quad(mine(0, i, k), w);
-                    read_quad(mine(1, i, k), b);
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        w[q] = fma2(d[k + q], v[k + q], w[q]);
-                        b[q] = add2(b[q], d[k + q]);
+                    if constexpr (SHARED) {
+                        read_quad(mine(0, i, k), w);
+                        read_quad(mine(1, i, k), b);
+                    } else {
+                        w[0] = sum_w[i][k], w[1] = sum_w[i][k + 1], b[0] = sum_b[i][k], b[1] = sum_b[i][k + 1];
                     }
-                    write_quad(mine(0, i, k), w);
-                    write_quad(mine(1, i, k), b);
+                    if (a.d_weight) leave_quad(a.partials + first * n.width + j * E + 2 * k, w, more);
+                    if (a.d_bias) leave_quad(a.partials + (rows_on + first) * n.width + j * E + 2 * k, b, more);
                 }
             }
-        }
-        copy(slot, row + kDepth * rows_on);
-        slot = slot + 1 == kDepth ? 0 : slot + 1;
-    }
-    griddep_launch_dependents();
-    // this team's column sums: one partial row of each
-    if (first < rows_on)
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int j = j0 + i * 32;
-            if (j >= n.nv) continue;
-#pragma unroll
-            for (int k = 0; k < P; k += 2) {
-                F2 w[2], b[2];
-                if constexpr (SHARED) {
-                    read_quad(mine(0, i, k), w);
-                    read_quad(mine(1, i, k), b);
-                } else {
-                    w[0] = sum_w[i][k], w[1] = sum_w[i][k + 1], b[0] = sum_b[i][k], b[1] = sum_b[i][k + 1];
-                }
-                if (a.d_weight) write_quad(a.partials + first * n.width + j * E + 2 * k, w);
-                if (a.d_bias) write_quad(a.partials + (rows_on + first) * n.width + j * E + 2 * k, b);
-            }
-        }
+        no_sums();
+        more = true;
+    } while (row < a.T);
 }
 
 // The weights' gradients from the partial rows, in a fixed order: 32 columns of

@@ -233,3 +233,18 @@ def test_helpers_refuse(b):
         with pytest.raises(b.SSEError) as e:
             call()
         assert e.value.status == b.SSE_ERR_INVALID_ARG
+
+
+def test_long_sums_of_the_weights_gradients(b):
+    """Column sums over 2^19 equal rows, of which a team of threads has some 3450: float32 additions in one chain would all be
+    off in the same direction."""
+    T, W = 1 << 19, 8192
+    c = make(1, W, "bf16", 12)
+    x, d_out = (c[k].expand(T, -1).contiguous() for k in ("x", "d_out"))
+    g = b.layer_norm_backward(b.make_layer_norm_config(W, EPS), x, c["w"], d_out)
+    d, rstd = _moments(R(_f64(c["x"])), W)
+    chain = 256 + T // 152 // 256 + 8 + 64  # rows of a part, parts, teams in 32 runs, runs
+    for k, one in (("d_weight", R(_f64(c["d_out"])) * (d * rstd)), ("d_bias", R(_f64(c["d_out"])))):
+        want, tol = T * one.v[0], T * (one.e[0] + chain * ROUND * np.abs(one.v[0]))
+        off = np.abs(_f64(g[k]) - want)
+        assert (off <= tol).all(), (k, (off / np.abs(want)).max(), (tol / np.abs(want)).max())
