@@ -15,10 +15,10 @@
 // sequence come in batches of four by asynchronous copies, two or three batches
 // ahead.
 //
-// Measured on a GB300, K = 4 with SiLU, 32768 x 2048 in bf16: forward 50 us (HBM
+// Measured on a GB300, K = 4 with SiLU, 32768 x 2048 in bf16: forward 47 to 50 us (HBM
 // floor at 6.77 TB/s: 40), backward 94 (59), of which the activation is 18.  One row
 // after another took 290 us together, batches loaded to registers 52 and 116.
-// float32, 16384 x 2048: 53 and 82 (40, 59); a fourth batch in the backward's ring
+// float32, 16384 x 2048: 53 to 58 and 83 (40, 59); a fourth batch in the backward's ring
 // leaves it two CTAs less on an SM, and 103 us.
 #include "quad.cuh"
 

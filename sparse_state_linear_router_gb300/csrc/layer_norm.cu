@@ -15,8 +15,9 @@
 //
 // Measured on a GB300, bf16 (floors at 6.77 TB/s): forward with residual 16384 x 2304
 // 51 us (44.6), 16384 x 2048 46 (39.7), 32768 x 1024 47, 4096 x 8192 48, without
-// residual 16384 x 2048 29 (19.8), 65536 x 512 25; backward with the residual's gradient
-// 16384 x 2048 57 (39.7), 32768 x 1024 56, 4096 x 8192 74, 8192 x 2048 in float32 52.
+// residual 16384 x 2048 29 (19.8), 65536 x 512 25, in float32 16384 x 2048 52 (39.7); backward
+// with the residual's gradient 16384 x 2048 57 (39.7), 32768 x 1024 56, 4096 x 8192 73, 2048 x
+// 16384 130, 8192 x 2048 in float32 51, 4096 x 8192 174 (79).
 // Rows loaded when their turn came took 66 us for the first and 95 for the backward.
 // The backward's rows wait in shared memory, so that what a row keeps
 // over its sums is there and not in registers, and the columns' weights are in registers:

@@ -14,10 +14,11 @@
 // pairs (the exponent, D x B, the state, C h), two exponentials and a 16-byte load:
 // 32 exponentials a clock and SM are 115 us, and the pairs, whose three distinct
 // operands take the register ports three cycles, about 280.
-// Measured on a GB300 in bf16, 16 states, gate and skip: 8 x 4096 x 2048 526 us, one
-// sequence of 32768 514 (of either 200 are the ranges' states), 16 x 2048 x 2048, whose
+// Measured on a GB300 in bf16, 16 states, gate and skip: 8 x 4096 x 2048 529 us, one
+// sequence of 32768 514 (of either some 200 are the ranges' states), 16 x 2048 x 2048, whose
 // sequences need no such states, 387, 24001 x 2048 in 16 ragged ones 399, a prompt of 500
-// x 1024 27; issue 61 %, FMA pipe 47 %, exponentials 38 % busy.  Token by token with a
+// x 1024 27; checkpoints are 8 to 11 us of 32768 x 2048; issue 62 %, FMA pipe 51 %,
+// exponentials 41 % busy.  Token by token with a
 // lane per four states: 8 x 4096 x 2048 about 5 ms.
 #include <type_traits>
 
@@ -316,8 +317,10 @@ __global__ void __launch_bounds__(32, 1) selective_forward_kernel(SelectiveArgs 
     }
 }
 
-// One token of each sequence: L lanes for a pair of channels, four states of both each.  Bound by HBM (the states in and
-// out): 256 x 2048 with 16 states 16.6 us (floor 10.5); one channel and library functions per thread took 25.
+// One token of each sequence: L lanes for a pair of channels, four states of both each.  The states in and out are what it
+// has to move; bound by their loads, one word of each a thread.  256 x 2048 with 16 states, more than L2 holds in turn, 18.1
+// us (floor 10.6), the same state again and again 16.6 (one channel and library functions per thread 25), 8 states 10.4,
+// 512 x 2048 with 64 133 (80).
 template <typename T, int L>
 __global__ void __launch_bounds__(256) selective_step_kernel(SelectiveArgs a, sse_selective_config_t cfg) {
     constexpr int N = 4 * L;

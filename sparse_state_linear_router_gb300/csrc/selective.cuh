@@ -45,8 +45,12 @@ inline SelectiveShape selective_shape(const sse_selective_config_t &c, int cols)
     return s;
 }
 // Sequences that make `enough` warps by themselves have a range each where the kernels find them even: no range then needs a
-// pass of its own (32 x 1024 x 2048: forward 377 us with 32 ranges, 523 with 57, 16 x 2048 x 2048 395 with 16 and 539 with 57; the backward of 8 x 4096 x 2048 1507 with 8,
-// 1597 with 38; of 24001 x 2048 in 16 ragged sequences 1364 with 16, 1219 with 38).
+// pass of its own.  Measured at a range each against ranges that fill the GPU, 8 x 2048 tokens in bf16 with 8, 16 and 32
+// states: forward with 512 warps 289, 391, 644 against 207, 273, 509 us, 832 warps 291, 396, 668 against 322, 437, 836, 1024
+// warps 293, 398, 692 against 377, 525, 997; backward with 512 warps 566, 767, 1690 against 320, 429, 938, 1024 warps 572,
+// 780, 1718 against 617, 824, 1775, 1664 warps 964, 1261, 2934 against 994, 1331, 2870, 2048 warps 1127, 1526, 3394 against
+// 1189, 1588, 3391.  The one limit of 1000 is on the right side of these but for the forward's 832 warps; between two whole
+// waves it is not: backward with 1280 warps 957, 1237, 2835 against 777, 1030, 2234.  float32 and 64 states go the same way.
 inline void set_ranges(SelectiveShape &s, int fill, int enough, int32_t S) {
     s.fill = fill;
     s.alone = S > 1 && S <= kMaxRanges && (int64_t)S * s.tiles * s.groups >= enough;

@@ -21,9 +21,9 @@
 // Bound by instructions: about 48 of a warp for 64 (token, channel, state), 19 of them
 // arithmetic of pairs and 9 the sums over channels, against 14 bytes and 16
 // exponentials for a token and channel (159 us of HBM, 115 of exponentials for 8 x 4096
-// x 2048 with 16 states).  Measured on a GB300, bf16: 1515 us there, 1565 as one
-// sequence of 32768, 24001 x 2048 in 16 ragged sequences 1220, 64 x 512 x 512 418;
-// issue 46 %, shared memory's pipe 57 %, FMA 41 %.  255 registers leave eight warps to
+// x 2048 with 16 states).  Measured on a GB300, bf16: 1523 us there, 1567 as one
+// sequence of 32768, 24001 x 2048 in 16 ragged sequences 1222, 64 x 512 x 512 421;
+// issue 46 %, shared memory's pipe 56 %, FMA 41 %.  255 registers leave eight warps to
 // an SM.  Spans of 4 tokens, whose 168 registers let twelve in, took 2623 us (1.75
 // passes forwards instead of 1.5, and what did not fit in registers went to L2, shared
 // memory having taken the L1); every step of a tile through shared memory 1655.
